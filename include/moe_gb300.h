@@ -85,6 +85,17 @@ enum moe_epilogue {
                                    out_scale: fp32 [rp_cap, n_out/256] */
 };
 
+enum moe_dtype {
+    MOE_DT_F32 = 0,  /* fp32 */
+    MOE_DT_BF16 = 1, /* bfloat16 */
+    MOE_DT_F16 = 2,  /* IEEE binary16 */
+};
+
+enum moe_scoring {
+    MOE_SCORE_SOFTMAX = 0, /* score of expert e: exp(l_e) / sum over all experts of exp(l) */
+    MOE_SCORE_SIGMOID = 1, /* score of expert e: 1 / (1 + exp(-l_e)) */
+};
+
 /* Text of a status code (static storage). */
 MOE_API const char* moe_status_string(int status);
 
@@ -339,6 +350,126 @@ MOE_API int moe_forward_host_i64(const void* hidden_states_host, const int64_t* 
 /* Makes `stream` wait until every output copy moe_forward_host has enqueued on the
  * current device so far has completed. */
 MOE_API int moe_host_wait(moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------------
+ * One training step of a pre-norm MoE block with 16-bit expert weights: the norm in
+ * front of the layer, the router that chooses the experts, the experts' products with
+ * their gradients, and the clipping of the gradients. (moe_scatter with MOE_QUANT_NONE
+ * and moe_gather_weight_reduce permute between them in both directions.)
+ * All sums, statistics and products are held in fp32 (the norm of a list of tensors
+ * partly in fp64) and rounded once where a result is stored in 16 bits. */
+
+/* Layer norm over the last dimension of x [M, K]:
+ *   mean = sum x / K;  rstd = 1 / sqrt(sum (x - mean)^2 / K + eps)
+ *   y = (x - mean) * rstd * weight + bias
+ *   x, y     `dtype` [M, K], contiguous; y may be x itself
+ *   weight   `param_dtype` [K];  bias `param_dtype` [K] or NULL (none)
+ *   mean, rstd  fp32 [M], written (the backward pass reads them); both may be NULL
+ *   param_dtype is `dtype` or MOE_DT_F32. 1 <= K. eps >= 0. Every pointer is aligned to
+ *   its element only; rows that start on 16-byte boundaries are moved 16 bytes at a time.
+ * M = 0 does nothing. */
+MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const void* weight, const void* bias,
+                           int param_dtype, float eps, void* y, float* mean, float* rstd, moe_stream_t stream);
+
+/* Scratch bytes moe_layer_norm_backward needs. Returns 0 on bad arguments. */
+MOE_API size_t moe_layer_norm_workspace_size(int64_t M, int K);
+
+/* Its gradients, from x and the mean and rstd of the forward pass. With
+ * xh = (x - mean) * rstd and g = dy * weight:
+ *   dx       = rstd * (g - sum g / K - xh * sum(g * xh) / K)     `dtype` [M, K]; may be dy itself
+ *   d_weight = sum over rows of dy * xh                          `param_dtype` [K]
+ *   d_bias   = sum over rows of dy                               `param_dtype` [K] or NULL
+ * The sums over rows have a fixed order: results do not change from call to call.
+ * M = 0 writes zeros to d_weight and d_bias.
+ * workspace >= moe_layer_norm_workspace_size(M, K) bytes, 16-byte aligned. */
+MOE_API int moe_layer_norm_backward(const void* dy, const void* x, int64_t M, int K, int dtype, const void* weight,
+                                    int param_dtype, const float* mean, const float* rstd, void* dx, void* d_weight,
+                                    void* d_bias, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* The router: the topk experts of every token and their weights, from logits [M, E].
+ *   logits   `dtype` [M, E], contiguous. A NaN counts as -inf; -inf means that the expert
+ *            is not available to the token; +inf counts as the largest finite value
+ *   scoring  enum moe_scoring
+ *   bias     fp32 [E] or NULL: added to the score for the choice only (load balancing).
+ *            Without it experts are ordered by their logits, with it by score + bias;
+ *            equal ones by ascending index. A NaN bias counts as -inf.
+ *   topk_ids     int32 [M, topk]: the chosen experts, best first. A slot for which no
+ *                available expert is left holds -1 (an empty slot, dropped by every entry
+ *                point that reads ids)
+ *   topk_weights fp32 [M, topk]: scale * score, or scale * score / (sum of the chosen
+ *                scores) with renormalize != 0; 0 in empty slots
+ * 1 <= topk <= 32, topk <= E <= 1024. */
+MOE_API int moe_router_topk(const void* logits, int64_t M, int E, int dtype, int topk, int scoring, const float* bias,
+                            int renormalize, float scale, float* topk_weights, int32_t* topk_ids, moe_stream_t stream);
+/* The same with topk_ids int64 [M, topk]. */
+MOE_API int moe_router_topk_i64(const void* logits, int64_t M, int E, int dtype, int topk, int scoring,
+                                const float* bias, int renormalize, float scale, float* topk_weights,
+                                int64_t* topk_ids, moe_stream_t stream);
+
+/* Gradient of the router's weights with respect to the logits (the choice itself has
+ * none): d_logits [M, E] of `dtype` from d_topk_weights fp32 [M, topk], the logits and
+ * the chosen ids of the forward pass. Ids outside [0, E) are empty slots; an id must not
+ * appear twice in a row. d_logits may be logits itself. */
+MOE_API int moe_router_topk_backward(const void* logits, int64_t M, int E, int dtype, const int32_t* topk_ids, int topk,
+                                     int scoring, int renormalize, float scale, const float* d_topk_weights,
+                                     void* d_logits, moe_stream_t stream);
+/* The same with topk_ids int64 [M, topk]. */
+MOE_API int moe_router_topk_backward_i64(const void* logits, int64_t M, int E, int dtype, const int64_t* topk_ids,
+                                         int topk, int scoring, int renormalize, float scale,
+                                         const float* d_topk_weights, void* d_logits, moe_stream_t stream);
+
+/* Products of ragged row groups with one weight matrix per group. The rows of group l are
+ * [expert_offsets[l], expert_offsets[l+1]), or, with expert_num_tokens, the first
+ * expert_num_tokens[l] rows from expert_offsets[l] (moe_scatter's 128-aligned blocks).
+ * Groups may be empty, start anywhere and have any length; they must not overlap.
+ *   out[r] = W_l x[r]
+ *   x        `dtype` [R, k_in];  w `dtype` [El, n_out, k_in]
+ *   out      `out_dtype` [R, n_out]; rows of no group are not written
+ *   expert_offsets int32 [El+1], expert_num_tokens int32 [El] or NULL. Rows outside
+ *            [0, R) are never touched, whatever the offsets say.
+ *   dtype    MOE_DT_BF16 or MOE_DT_F16; out_dtype is `dtype` or MOE_DT_F32
+ * n_out and k_in are multiples of 8; 1 <= El <= 1024; R <= 2^31 - 1; x, w and out are
+ * 16-byte aligned and out overlaps neither. Products accumulate in fp32. */
+MOE_API int moe_grouped_matmul(const void* x, int64_t R, const void* w, int local_num_experts, int n_out, int k_in,
+                               const int32_t* expert_offsets, const int32_t* expert_num_tokens, int dtype,
+                               int out_dtype, void* out, moe_stream_t stream);
+
+/* Its gradient with respect to the rows: dx[r] = W_l^T dy[r], dy `dtype` [R, n_out],
+ * dx `out_dtype` [R, k_in]. */
+MOE_API int moe_grouped_matmul_dgrad(const void* dy, int64_t R, const void* w, int local_num_experts, int n_out,
+                                     int k_in, const int32_t* expert_offsets, const int32_t* expert_num_tokens,
+                                     int dtype, int out_dtype, void* dx, moe_stream_t stream);
+
+/* Its gradient with respect to the weights: dw[l] = sum over the rows r of group l of
+ * dy[r] x[r]^T, `out_dtype` [El, n_out, k_in]; zeros for a group without rows. Rows of no
+ * group add nothing, whatever they hold. */
+MOE_API int moe_grouped_matmul_wgrad(const void* dy, const void* x, int64_t R, int local_num_experts, int n_out,
+                                     int k_in, const int32_t* expert_offsets, const int32_t* expert_num_tokens,
+                                     int dtype, int out_dtype, void* dw, moe_stream_t stream);
+
+/* Scratch bytes moe_grad_norm and moe_clip_grad_norm need for these tensors (HOST array of
+ * n_tensors lengths). Returns 0 on bad arguments. */
+MOE_API size_t moe_grad_norm_workspace_size(const int64_t* numel, int n_tensors);
+
+/* The 2-norm of all values of a list of tensors, as of one vector.
+ *   tensors  HOST array of n_tensors DEVICE pointers, aligned to their elements
+ *   numel    HOST array of their lengths (0 allowed);  dtypes HOST array of enum moe_dtype
+ *   norm     fp32 [1], written. Squares that overflow or vanish in fp32 are taken in fp64,
+ *            so the norm is right over the whole range of fp32; inf or NaN if a value is
+ * The sum has a fixed order. n_tensors = 0 writes 0.
+ * workspace >= moe_grad_norm_workspace_size bytes, 16-byte aligned. */
+MOE_API int moe_grad_norm(const void* const* tensors, const int64_t* numel, const int32_t* dtypes, int n_tensors,
+                          float* norm, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Clipping by it: out[t] = tensors[t] * c with c = max_norm / norm where norm > max_norm,
+ * else 1; tensors are left as they are (c = 1) when the norm is inf or NaN, which the
+ * caller sees in norm[0].
+ *   outs     HOST array of n_tensors DEVICE pointers of the tensors' types and lengths, or
+ *            NULL: in place. outs[t] may be tensors[t]; otherwise outputs overlap nothing
+ *   max_norm >= 0 */
+MOE_API int moe_clip_grad_norm(void* const* tensors, const int64_t* numel, const int32_t* dtypes, int n_tensors,
+                               float max_norm, void* const* outs, float* norm, void* workspace,
+                               size_t workspace_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,10 @@ The layer (vLLM PRs #20903, #20725, #20392): count_expert_num_tokens ->
 ep_scatter with 1x128 FP8 quantisation -> block-scaled FP8 grouped GEMM (w13) ->
 SiLU-and-mul requantisation -> grouped GEMM (w2) -> ep_gather with the top-k
 weight-and-reduce, under a chunking loop that sizes the workspace per chunk.
+
+Beside it, the operators of one training step of a pre-norm MoE block with 16-bit expert
+weights, each with its gradient: moe_layer_norm, moe_router_topk, moe_grouped_matmul, and
+moe_clip_grad_norm over the gradients (``train.py`` runs them together under autograd).
 """
 from __future__ import annotations
 
@@ -25,6 +29,9 @@ LIB_PATH = os.path.join(_PKG, "libmoe_gb300.so")
 MOE_OK = 0
 MOE_QUANT_NONE, MOE_QUANT_FP8_1X128 = 0, 1
 MOE_EPI_BF16, MOE_EPI_F32, MOE_EPI_SILU_MUL_QUANT = 0, 1, 2
+MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+_DTYPES = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 
 _lib = None
 
@@ -49,6 +56,7 @@ def lib() -> ctypes.CDLL:
 
 
 _p, _i64, _int, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_f = ctypes.c_float
 
 SIGNATURES = {
     "moe_status_string": ([_int], ctypes.c_char_p),
@@ -81,6 +89,19 @@ SIGNATURES = {
     "moe_forward_host_i64": ([_p, _p, _p, _p, _p, _p, _p, _p, _int, _int, _i64, _int, _int, _int, _i64, _int,
                               _p, _p, _sz, _p, _p, _p], _int),
     "moe_host_wait": ([_p], _int),
+    "moe_layer_norm": ([_p, _i64, _int, _int, _p, _p, _int, _f, _p, _p, _p, _p], _int),
+    "moe_layer_norm_workspace_size": ([_i64, _int], _sz),
+    "moe_layer_norm_backward": ([_p, _p, _i64, _int, _int, _p, _int, _p, _p, _p, _p, _p, _p, _sz, _p], _int),
+    "moe_router_topk": ([_p, _i64, _int, _int, _int, _int, _p, _int, _f, _p, _p, _p], _int),
+    "moe_router_topk_i64": ([_p, _i64, _int, _int, _int, _int, _p, _int, _f, _p, _p, _p], _int),
+    "moe_router_topk_backward": ([_p, _i64, _int, _int, _p, _int, _int, _int, _f, _p, _p, _p], _int),
+    "moe_router_topk_backward_i64": ([_p, _i64, _int, _int, _p, _int, _int, _int, _f, _p, _p, _p], _int),
+    "moe_grouped_matmul": ([_p, _i64, _p, _int, _int, _int, _p, _p, _int, _int, _p, _p], _int),
+    "moe_grouped_matmul_dgrad": ([_p, _i64, _p, _int, _int, _int, _p, _p, _int, _int, _p, _p], _int),
+    "moe_grouped_matmul_wgrad": ([_p, _p, _i64, _int, _int, _int, _p, _p, _int, _int, _p, _p], _int),
+    "moe_grad_norm_workspace_size": ([_p, _int], _sz),
+    "moe_grad_norm": ([_p, _p, _p, _int, _p, _p, _sz, _p], _int),
+    "moe_clip_grad_norm": ([_p, _p, _p, _int, _f, _p, _p, _p, _sz, _p], _int),
 }
 
 
@@ -364,3 +385,223 @@ def moe_ep_combine(partials, out=None, stream=None):
     arr = (ctypes.c_void_p * len(partials))(*[_ptr(p).value for p in partials])
     _check("moe_ep_combine", lib().moe_ep_combine(arr, len(partials), M, K, _ptr(out), _stream(stream)))
     return out
+
+
+# ------------------------------------------------------ training step of an MoE block
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected torch.float32, torch.bfloat16 or torch.float16, got {t.dtype}")
+    return code
+
+
+def _same(t, shape, dtype, name):
+    """Checks an output buffer or a second operand against the shape and type it has to have."""
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """Scratch memory for a call on `stream`: the allocator keeps it until that stream is done with it."""
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def moe_layer_norm(x, weight, bias=None, eps=1e-5, out=None, mean=None, rstd=None, stream=None):
+    """Layer norm over the last dimension of x [M, K] (bf16, fp16 or fp32); weight and bias
+    [K] in x's type or fp32. Returns (y, mean, rstd), the statistics in fp32 [M]."""
+    dt = _dtype_code(x, "x")
+    pdt = _dtype_code(weight, "weight")
+    M, K = x.shape
+    _same(weight, (K,), weight.dtype, "weight")
+    _same(bias, (K,), weight.dtype, "bias")
+    if out is None:
+        out = torch.empty_like(x)
+    if mean is None:
+        mean = torch.empty(M, dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    _same(out, (M, K), x.dtype, "out")
+    _same(mean, (M,), torch.float32, "mean")
+    _same(rstd, (M,), torch.float32, "rstd")
+    _check("moe_layer_norm", lib().moe_layer_norm(
+        _ptr(x), M, K, dt, _ptr(weight), _ptr(bias), pdt, eps, _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)))
+    return out, mean, rstd
+
+
+def moe_layer_norm_workspace_size(M: int, K: int) -> int:
+    return int(lib().moe_layer_norm_workspace_size(M, K))
+
+
+def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, d_weight=None, d_bias=None, workspace=None,
+                            stream=None):
+    """Gradients of moe_layer_norm from its inputs and statistics: (dx, d_weight, d_bias)."""
+    dt = _dtype_code(x, "x")
+    pdt = _dtype_code(weight, "weight")
+    M, K = x.shape
+    _same(dy, (M, K), x.dtype, "dy")
+    _same(weight, (K,), weight.dtype, "weight")
+    _same(mean, (M,), torch.float32, "mean")
+    _same(rstd, (M,), torch.float32, "rstd")
+    if dx is None:
+        dx = torch.empty_like(x)
+    if d_weight is None:
+        d_weight = torch.empty_like(weight)
+    if d_bias is None:
+        d_bias = torch.empty_like(weight)
+    _same(dx, (M, K), x.dtype, "dx")
+    _same(d_weight, (K,), weight.dtype, "d_weight")
+    _same(d_bias, (K,), weight.dtype, "d_bias")
+    if workspace is None:
+        workspace = _scratch(moe_layer_norm_workspace_size(M, K), x.device, stream)
+    _check("moe_layer_norm_backward", lib().moe_layer_norm_backward(
+        _ptr(dy), _ptr(x), M, K, dt, _ptr(weight), pdt, _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(d_weight),
+        _ptr(d_bias), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return dx, d_weight, d_bias
+
+
+def moe_router_topk(logits, topk, scoring=MOE_SCORE_SOFTMAX, renormalize=True, scale=1.0, bias=None,
+                    topk_weights=None, topk_ids=None, stream=None):
+    """The topk experts of every token and their weights from logits [M, E] (bf16, fp16 or
+    fp32): (topk_weights fp32 [M, topk], topk_ids int32, or int64 if such a buffer is
+    given). Ties go to the lowest expert; a slot without an available expert is -1."""
+    dt = _dtype_code(logits, "logits")
+    M, E = logits.shape
+    _same(bias, (E,), torch.float32, "bias")
+    if topk_weights is None:
+        topk_weights = torch.empty(M, topk, dtype=torch.float32, device=logits.device)
+    if topk_ids is None:
+        topk_ids = torch.empty(M, topk, dtype=torch.int32, device=logits.device)
+    fn = _ids_entry("moe_router_topk", topk_ids)
+    _same(topk_weights, (M, topk), torch.float32, "topk_weights")
+    _same(topk_ids, (M, topk), topk_ids.dtype, "topk_ids")
+    _check(fn, getattr(lib(), fn)(
+        _ptr(logits), M, E, dt, topk, scoring, _ptr(bias), int(bool(renormalize)), scale, _ptr(topk_weights),
+        _ptr(topk_ids), _stream(stream)))
+    return topk_weights, topk_ids
+
+
+def moe_router_topk_backward(logits, topk_ids, d_topk_weights, scoring=MOE_SCORE_SOFTMAX, renormalize=True,
+                             scale=1.0, d_logits=None, stream=None):
+    """Gradient of the router's weights with respect to its logits: [M, E] of their type."""
+    dt = _dtype_code(logits, "logits")
+    M, E = logits.shape
+    fn = _ids_entry("moe_router_topk_backward", topk_ids)
+    topk = topk_ids.shape[1]
+    _same(topk_ids, (M, topk), topk_ids.dtype, "topk_ids")
+    _same(d_topk_weights, (M, topk), torch.float32, "d_topk_weights")
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+    _same(d_logits, (M, E), logits.dtype, "d_logits")
+    _check(fn, getattr(lib(), fn)(
+        _ptr(logits), M, E, dt, _ptr(topk_ids), topk, scoring, int(bool(renormalize)), scale, _ptr(d_topk_weights),
+        _ptr(d_logits), _stream(stream)))
+    return d_logits
+
+
+def _grouped(fn, a, b, shape, dims, expert_offsets, expert_num_tokens, out, out_dtype, stream):
+    """The three grouped products: operands a and b, the result's shape, (El, n_out, k_in)."""
+    dt = _dtype_code(a, "rows")
+    _same(b, b.shape, a.dtype, "second operand")
+    El, N, K = dims
+    _same(expert_offsets, (El + 1,), torch.int32, "expert_offsets")
+    _same(expert_num_tokens, (El,), torch.int32, "expert_num_tokens")
+    if out is None:
+        out = torch.empty(shape, dtype=a.dtype if out_dtype is None else out_dtype, device=a.device)
+    _same(out, shape, out.dtype if out_dtype is None else out_dtype, "out")
+    odt = _dtype_code(out, "out")
+    off, cnt = _ptr(expert_offsets), _ptr(expert_num_tokens)
+    if fn == "moe_grouped_matmul_wgrad":
+        st = lib().moe_grouped_matmul_wgrad(_ptr(a), _ptr(b), a.shape[0], El, N, K, off, cnt, dt, odt, _ptr(out),
+                                            _stream(stream))
+    else:
+        st = getattr(lib(), fn)(_ptr(a), a.shape[0], _ptr(b), El, N, K, off, cnt, dt, odt, _ptr(out), _stream(stream))
+    _check(fn, st)
+    return out
+
+
+def moe_grouped_matmul(x, w, expert_offsets, expert_num_tokens=None, out=None, out_dtype=None, stream=None):
+    """out[r] = w[l] @ x[r] for the rows r of every group l: x [R, k_in] and w [El, n_out,
+    k_in] in bf16 or fp16, out [R, n_out] in their type or fp32. Group l has the rows
+    [expert_offsets[l], expert_offsets[l + 1]), or the first expert_num_tokens[l] from
+    expert_offsets[l]; rows of no group are not written."""
+    El, N, K = w.shape
+    R = x.shape[0]
+    _same(x, (R, K), w.dtype, "x")
+    return _grouped("moe_grouped_matmul", x, w, (R, N), (El, N, K), expert_offsets, expert_num_tokens, out, out_dtype,
+                    stream)
+
+
+def moe_grouped_matmul_dgrad(dy, w, expert_offsets, expert_num_tokens=None, out=None, out_dtype=None, stream=None):
+    """Gradient of moe_grouped_matmul's rows: w[l].T @ dy[r], [R, k_in]."""
+    El, N, K = w.shape
+    R = dy.shape[0]
+    _same(dy, (R, N), w.dtype, "dy")
+    return _grouped("moe_grouped_matmul_dgrad", dy, w, (R, K), (El, N, K), expert_offsets, expert_num_tokens, out,
+                    out_dtype, stream)
+
+
+def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=None, out_dtype=None, stream=None):
+    """Gradient of moe_grouped_matmul's weights: sum over group l's rows of the outer
+    products dy[r] x[r], [El, n_out, k_in]; zeros for a group without rows."""
+    El = expert_offsets.shape[0] - 1
+    R, N = dy.shape
+    K = x.shape[1]
+    _same(x, (R, K), dy.dtype, "x")
+    return _grouped("moe_grouped_matmul_wgrad", dy, x, (El, N, K), (El, N, K), expert_offsets, expert_num_tokens, out,
+                    out_dtype, stream)
+
+
+def _tensor_list(tensors):
+    """C arrays of the pointers, lengths and types of a list of contiguous CUDA tensors."""
+    n = len(tensors)
+    ptrs = (ctypes.c_void_p * n)(*[_ptr(t).value for t in tensors])
+    lens = (ctypes.c_int64 * n)(*[t.numel() for t in tensors])
+    types = (ctypes.c_int32 * n)(*[_dtype_code(t, "tensors") for t in tensors])
+    return ptrs, lens, types
+
+
+def moe_grad_norm_workspace_size(numels) -> int:
+    n = len(numels)
+    return int(lib().moe_grad_norm_workspace_size((ctypes.c_int64 * n)(*numels), n))
+
+
+def moe_grad_norm(tensors, norm=None, workspace=None, stream=None):
+    """2-norm of all values of a list of tensors (bf16, fp16, fp32 mixed), as fp32 [1]."""
+    return _norm_call("moe_grad_norm", tensors, None, None, norm, workspace, stream)
+
+
+def moe_clip_grad_norm(tensors, max_norm, out=None, norm=None, workspace=None, stream=None):
+    """Scales the tensors by max_norm / norm where their common 2-norm exceeds max_norm, in
+    place or into the tensors `out`; with an infinite or NaN norm they keep their values.
+    Returns the norm before clipping, fp32 [1]."""
+    return _norm_call("moe_clip_grad_norm", tensors, float(max_norm), out, norm, workspace, stream)
+
+
+def _norm_call(fn, tensors, max_norm, out, norm, workspace, stream):
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError(f"{fn}: no tensors")
+    ptrs, lens, types = _tensor_list(tensors)
+    dev = tensors[0].device
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    _same(norm, (1,), torch.float32, "norm")
+    n = len(tensors)
+    if workspace is None:
+        workspace = _scratch(int(lib().moe_grad_norm_workspace_size(lens, n)), dev, stream)
+    if max_norm is None:
+        st = lib().moe_grad_norm(ptrs, lens, types, n, _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream))
+    else:
+        outs = None
+        if out is not None:
+            out = list(out)
+            if len(out) != n or any(o.numel() != t.numel() or o.dtype != t.dtype for o, t in zip(out, tensors)):
+                raise ValueError(f"{fn}: outputs of other lengths or types than the tensors")
+            outs = (ctypes.c_void_p * n)(*[_ptr(o).value for o in out])
+        st = lib().moe_clip_grad_norm(ptrs, lens, types, n, max_norm, outs, _ptr(norm), _ptr(workspace),
+                                      workspace.numel(), _stream(stream))
+    _check(fn, st)
+    return norm

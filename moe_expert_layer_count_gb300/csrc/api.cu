@@ -18,7 +18,8 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_dev_state[kMaxDevices];  // 0 unknown, 1 sm_103, 2 other
 std::atomic<int> g_dev_sms[kMaxDevices];
 
-// MOE_OK when the current device is compute capability 10.3; fills the SM count.
+}  // namespace
+
 int check_device(int* num_sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
@@ -37,6 +38,8 @@ int check_device(int* num_sms) {
     if (num_sms) *num_sms = g_dev_sms[dev].load(std::memory_order_relaxed);
     return st == 1 ? MOE_OK : MOE_ERR_UNSUPPORTED_DEVICE;
 }
+
+namespace {
 
 inline size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 

@@ -17,6 +17,9 @@ constexpr int kGroup = 128;  // 1x128 activation groups, 128x128 weight blocks
 // Kernel launches made by this library (read by moe_kernel_launch_count()).
 void note_launches(int n);
 
+// MOE_OK when the current device is compute capability 10.3; fills the SM count (may be NULL).
+int check_device(int* num_sms);
+
 // Launch-status helper: returns MOE_ERR_CUDA if the last launch failed.
 inline int launch_status() {
     cudaError_t e = cudaGetLastError();

@@ -1,0 +1,263 @@
+// The 2-norm of all values of a list of tensors and clipping by it:
+//   norm = sqrt(sum over tensors and values of g^2);  g' = g * (norm > max ? max / norm : 1)
+// The tensors are cut into chunks; each block adds the squares of its chunks (fp32 per
+// thread and chunk, fp64 above that) into one partial sum. The chunks go to the blocks by
+// their number alone, so the sum's order does not change from call to call. The clip pass
+// adds the partial sums in every block and scales the chunks, last chunk first: the end
+// of the list is what the first pass has left in L2.
+#include "elem.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr int kMaxBlocks = 1216;  // 152 SMs x 8 blocks of 256 threads
+constexpr int kTensors = 256;     // tensors per launch
+constexpr int64_t kChunk = 16384;
+
+struct Table {
+    const void* in[kTensors];
+    void* out[kTensors];
+    int64_t n[kTensors];
+    int64_t chunk0[kTensors + 1];  // first chunk of each tensor
+    uint8_t dtype[kTensors];
+    int count;
+};
+
+// Values before the first 16-byte boundary of a tensor.
+template <typename T>
+__host__ __device__ __forceinline__ int64_t head_of(const void* p, int64_t n) {
+    const int64_t h = (int64_t)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (int64_t)sizeof(T);
+    return h < n ? h : n;
+}
+
+// Chunk c of a tensor: [lo, hi), lo on a 16-byte boundary but for chunk 0, which has the head too.
+template <typename T>
+__device__ __forceinline__ void chunk_range(const void* p, int64_t n, int64_t c, int64_t& head, int64_t& lo, int64_t& hi) {
+    head = head_of<T>(p, n);
+    lo = c == 0 ? 0 : head + c * kChunk;
+    hi = min(head + (c + 1) * kChunk, n);
+}
+
+__device__ __forceinline__ int tensor_of(const Table& t, int64_t chunk) {
+    int lo = 0, hi = t.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.chunk0[mid] <= chunk) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Sum of the squares of this thread's values of a chunk. fp32 holds it while it neither
+// overflows nor sinks to where the squares lose bits (values below ~1e-17); otherwise the
+// thread's values are read again in fp64. `any`: the bits of all values, to tell zeros
+// from vanished squares.
+template <typename T>
+__device__ double chunk_squares(const void* p, int64_t n, int64_t c) {
+    constexpr int V = 16 / sizeof(T);
+    const T* g = static_cast<const T*>(p);
+    int64_t head, lo, hi;
+    chunk_range<T>(p, n, c, head, lo, hi);
+    const int64_t v0 = c == 0 ? head : lo;
+    const int64_t nv = (hi - v0) / V;
+    float a = 0.f, most = 0.f;
+    auto add = [&](float x) {
+        a = fmaf(x, x, a);
+        most = fmaxf(most, fabsf(x));
+    };
+    for (int64_t i = lo + threadIdx.x; i < v0; i += kNormThreads) add(to_f32(g[i]));
+    for (int64_t i = threadIdx.x; i < nv; i += kNormThreads) {
+        const Vec<T, V> r = *reinterpret_cast<const Vec<T, V>*>(g + v0 + i * V);
+#pragma unroll
+        for (int j = 0; j < V; ++j) add(to_f32(r.v[j]));
+    }
+    for (int64_t i = v0 + nv * V + threadIdx.x; i < hi; i += kNormThreads) add(to_f32(g[i]));
+    if (a >= 1e-30f && a <= 3e38f) return (double)a;
+    if (most == 0.f && a == 0.f) return 0.0;
+    double d = 0.0;
+    for (int64_t i = lo + threadIdx.x; i < v0; i += kNormThreads) d += (double)to_f32(g[i]) * to_f32(g[i]);
+    for (int64_t i = threadIdx.x; i < nv; i += kNormThreads)
+        for (int j = 0; j < V; ++j) {
+            const double x = to_f32(g[v0 + i * V + j]);
+            d += x * x;
+        }
+    for (int64_t i = v0 + nv * V + threadIdx.x; i < hi; i += kNormThreads) d += (double)to_f32(g[i]) * to_f32(g[i]);
+    return d;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* s) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int i = 0; i < kNormThreads / 32; ++i) v += s[i];
+    __syncthreads();
+    return v;
+}
+
+__global__ void __launch_bounds__(kNormThreads) squares_kernel(const __grid_constant__ Table t, double* __restrict__ parts) {
+    __shared__ double s[kNormThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    double a = 0.0;
+    for (int64_t c = blockIdx.x; c < t.chunk0[t.count]; c += gridDim.x) {
+        const int k = tensor_of(t, c);
+        const int64_t i = c - t.chunk0[k];
+        switch (t.dtype[k]) {
+            case MOE_DT_F32: a += chunk_squares<float>(t.in[k], t.n[k], i); break;
+            case MOE_DT_BF16: a += chunk_squares<bf16>(t.in[k], t.n[k], i); break;
+            default: a += chunk_squares<fp16>(t.in[k], t.n[k], i); break;
+        }
+    }
+    a = block_sum(a, s);
+    if (threadIdx.x == 0) parts[blockIdx.x] = a;
+}
+
+// The norm from the n partial sums: the same order, so the same value, in every block.
+__device__ __forceinline__ float norm_of(const double* __restrict__ parts, int n, double* s) {
+    double a = 0.0;
+    for (int i = threadIdx.x; i < n; i += kNormThreads) a += parts[i];
+    return (float)sqrt(block_sum(a, s));
+}
+
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(const double* __restrict__ parts, int n, float* __restrict__ norm) {
+    __shared__ double s[kNormThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    const float v = norm_of(parts, n, s);
+    if (threadIdx.x == 0) *norm = v;
+}
+
+template <typename T>
+__device__ void scale_chunk(const void* p, void* q, int64_t n, int64_t c, float coef) {
+    constexpr int V = 16 / sizeof(T);
+    const T* g = static_cast<const T*>(p);
+    T* o = static_cast<T*>(q);
+    int64_t head, lo, hi;
+    chunk_range<T>(p, n, c, head, lo, hi);
+    const int64_t v0 = c == 0 ? head : lo;
+    const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    const int64_t nv = same ? (hi - v0) / V : 0;
+    for (int64_t i = lo + threadIdx.x; i < v0; i += kNormThreads) o[i] = from_f32<T>(to_f32(g[i]) * coef);
+    for (int64_t i = threadIdx.x; i < nv; i += kNormThreads) {
+        Vec<T, V> r = *reinterpret_cast<const Vec<T, V>*>(g + v0 + i * V);
+#pragma unroll
+        for (int j = 0; j < V; ++j) r.v[j] = from_f32<T>(to_f32(r.v[j]) * coef);
+        *reinterpret_cast<Vec<T, V>*>(o + v0 + i * V) = r;
+    }
+    for (int64_t i = v0 + nv * V + threadIdx.x; i < hi; i += kNormThreads) o[i] = from_f32<T>(to_f32(g[i]) * coef);
+}
+
+__global__ void __launch_bounds__(kNormThreads)
+    clip_kernel(const __grid_constant__ Table t, const double* __restrict__ parts, int n, float max_norm,
+                float* __restrict__ norm) {
+    __shared__ double s[kNormThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    const float v = norm_of(parts, n, s);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+    const float coef = v > max_norm && v <= 3.402823466e38f ? max_norm / v : 1.f;
+    for (int64_t c = t.chunk0[t.count] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+        const int k = tensor_of(t, c);
+        if (coef == 1.f && t.in[k] == t.out[k]) continue;  // in place and nothing to clip
+        const int64_t i = c - t.chunk0[k];
+        switch (t.dtype[k]) {
+            case MOE_DT_F32: scale_chunk<float>(t.in[k], t.out[k], t.n[k], i, coef); break;
+            case MOE_DT_BF16: scale_chunk<bf16>(t.in[k], t.out[k], t.n[k], i, coef); break;
+            default: scale_chunk<fp16>(t.in[k], t.out[k], t.n[k], i, coef); break;
+        }
+    }
+}
+
+int launches_of(int n_tensors) { return (n_tensors + kTensors - 1) / kTensors; }
+
+// The table of tensors [first, first + kTensors); returns its number of chunks.
+int64_t fill(Table& t, const void* const* in, void* const* out, const int64_t* numel, const int32_t* dtypes, int first,
+             int n_tensors) {
+    t.count = n_tensors - first < kTensors ? n_tensors - first : kTensors;
+    int64_t chunks = 0;
+    for (int i = 0; i < t.count; ++i) {
+        const int64_t n = numel[first + i];
+        t.in[i] = in[first + i];
+        t.out[i] = out ? out[first + i] : nullptr;
+        t.n[i] = n;
+        t.dtype[i] = (uint8_t)dtypes[first + i];
+        t.chunk0[i] = chunks;
+        const int64_t head = dtypes[first + i] == MOE_DT_F32 ? head_of<float>(in[first + i], n) : head_of<bf16>(in[first + i], n);
+        if (n > 0) chunks += n - head > 0 ? (n - head + kChunk - 1) / kChunk : 1;
+    }
+    t.chunk0[t.count] = chunks;
+    return chunks;
+}
+
+int blocks_of(int64_t chunks) { return (int)(chunks < 1 ? 1 : chunks < kMaxBlocks ? chunks : kMaxBlocks); }
+
+int norm_impl(const void* const* in, const int64_t* numel, const int32_t* dtypes, int n_tensors, bool clip, float max_norm,
+              void* const* outs, float* norm, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (n_tensors < 0 || !norm || misaligned(norm, 4) || !workspace || misaligned(workspace, 16) ||
+        (n_tensors > 0 && (!in || !numel || !dtypes)) || (clip && !(max_norm >= 0.f)))
+        return MOE_ERR_INVALID_ARG;
+    for (int i = 0; i < n_tensors; ++i) {
+        const int z = dtype_bytes(dtypes[i]);
+        if (numel[i] < 0 || !z) return MOE_ERR_INVALID_ARG;
+        if (numel[i] == 0) continue;
+        const void* o = outs ? outs[i] : in[i];
+        const size_t b = (size_t)numel[i] * z;
+        if (!in[i] || !o || misaligned(in[i], z) || misaligned(o, z) || (o != in[i] && overlap(o, b, in[i], b)) ||
+            overlap(workspace, workspace_bytes, o, b) || overlap(workspace, workspace_bytes, in[i], b))
+            return MOE_ERR_INVALID_ARG;
+    }
+    if (workspace_bytes < moe_grad_norm_workspace_size(numel, n_tensors)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (int st = check_device(nullptr)) return st;
+    double* parts = static_cast<double*>(workspace);
+    int n_parts = 0;
+    Table t;
+    for (int first = 0; first < n_tensors; first += kTensors) {
+        const int grid = blocks_of(fill(t, in, outs, numel, dtypes, first, n_tensors));
+        launch_k(squares_kernel, grid, kNormThreads, 0, stream, t, parts + n_parts);
+        note_launches(1);
+        n_parts += grid;
+    }
+    if (!clip || n_tensors == 0) {
+        launch_k(norm_kernel, 1, kNormThreads, 0, stream, parts, n_parts, norm);
+        note_launches(1);
+        return launch_status();
+    }
+    for (int first = (n_tensors - 1) / kTensors * kTensors; first >= 0; first -= kTensors) {
+        const int grid = blocks_of(fill(t, in, outs ? outs : const_cast<void* const*>(in), numel, dtypes, first, n_tensors));
+        launch_k(clip_kernel, grid, kNormThreads, 0, stream, t, parts, n_parts, max_norm, norm);
+        note_launches(1);
+    }
+    return launch_status();
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+MOE_API size_t moe_grad_norm_workspace_size(const int64_t* numel, int n_tensors) {
+    if (n_tensors < 0 || (n_tensors > 0 && !numel)) return 0;
+    for (int i = 0; i < n_tensors; ++i)
+        if (numel[i] < 0) return 0;
+    return (size_t)(n_tensors ? launches_of(n_tensors) : 1) * kMaxBlocks * sizeof(double);
+}
+
+MOE_API int moe_grad_norm(const void* const* tensors, const int64_t* numel, const int32_t* dtypes, int n_tensors,
+                          float* norm, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+    return norm_impl(tensors, numel, dtypes, n_tensors, false, 0.f, nullptr, norm, workspace, workspace_bytes,
+                     (cudaStream_t)stream);
+}
+
+MOE_API int moe_clip_grad_norm(void* const* tensors, const int64_t* numel, const int32_t* dtypes, int n_tensors,
+                               float max_norm, void* const* outs, float* norm, void* workspace, size_t workspace_bytes,
+                               moe_stream_t stream) {
+    return norm_impl(const_cast<const void* const*>(tensors), numel, dtypes, n_tensors, true, max_norm, outs, norm, workspace,
+                     workspace_bytes, (cudaStream_t)stream);
+}
+
+}  // extern "C"

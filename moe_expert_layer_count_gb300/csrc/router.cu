@@ -1,0 +1,357 @@
+// The top-k router: for every token the topk experts with the largest logits (or biased
+// scores), their weights, and the gradient of the weights with respect to the logits.
+//
+//   softmax  s_j = exp(l_j) / sum_m exp(l_m)        sigmoid  s_j = 1 / (1 + exp(-l_j))
+//   w_i = scale * s_i,  or  scale * s_i / S  with S the sum over the chosen experts
+// Gradient, g_i = dL/dw_i, sums over the chosen experts:
+//   softmax               dl_j = s_j * scale * ([j chosen] g_j - sum_i s_i g_i)
+//   softmax, renormalised dl_i = scale * q_i * (g_i - sum_m q_m g_m),  q_i = s_i / S; 0 elsewhere
+//   sigmoid               dl_i = scale * g_i * s_i * (1 - s_i)
+//   sigmoid, renormalised dl_i = scale * q_i * (g_i - sum_m q_m g_m) * (1 - s_i)
+// One warp per token: lane i holds the V consecutive logits [i*V, (i+1)*V) in registers, so
+// a tie goes to the lowest lane and then to its first value.
+#include <climits>
+
+#include "elem.cuh"
+#include "route.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kRouterWarps = 8;
+constexpr int kMaxRouterExperts = 1024;
+constexpr float kFltMax = 3.402823466e38f;
+
+// A logit as the router sees it: NaN is -inf (not available), +inf the largest finite value.
+__device__ __forceinline__ float clean_logit(float l) { return l != l ? -INFINITY : fminf(l, kFltMax); }
+
+// Order-preserving key of a value; 0 (below every other) for -inf and NaN: not available.
+// -0 and +0 share a key.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.f);
+    const uint32_t k = (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    return v > -INFINITY ? k : 0u;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// 1 / (1 + exp(-l)), without overflow on either side.
+__device__ __forceinline__ float sigmoid(float l) {
+    const float e = expf(-fabsf(l));
+    return l >= 0.f ? 1.f / (1.f + e) : e / (1.f + e);
+}
+
+// The ratios s_i / S of sigmoid scores, one chosen logit per lane (-inf: none): each score
+// times exp(-m), m = min(0, largest chosen logit), so that scores too small for fp32 keep
+// their ratios. All of the warp's lanes call it.
+__device__ __forceinline__ float sigmoid_share(float l) {
+    const float m = fminf(0.f, warp_max(l));
+    const float s = l > -INFINITY ? expf(fminf(l, 0.f) - m) / (1.f + expf(-fabsf(l))) : 0.f;
+    const float S = warp_sum(s);
+    return S > 0.f ? s / S : 0.f;
+}
+
+// The V logits of this lane (absent ones -inf).
+template <typename T, int V, bool kVec>
+__device__ __forceinline__ void load_logits(const T* __restrict__ row, int lane, int E, float (&v)[V]) {
+    if constexpr (kVec) {  // E is a multiple of V and rows start on V * sizeof(T) bytes
+        Vec<T, V> r;
+        const bool in = lane * V < E;
+        if (in) r = *reinterpret_cast<const Vec<T, V>*>(row + lane * V);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = in ? clean_logit(to_f32(r.v[j])) : -INFINITY;
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int e = lane * V + j;
+            v[j] = e < E ? clean_logit(to_f32(row[e])) : -INFINITY;
+        }
+    }
+}
+
+template <typename T, typename TId, int V, bool kVec>
+__global__ void __launch_bounds__(kRouterWarps * 32)
+    router_kernel(const T* __restrict__ logits, int64_t M, int E, int topk, int scoring, const float* __restrict__ bias,
+                  int renorm, float scale, float* __restrict__ out_w, TId* __restrict__ out_id) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5);
+    if (t >= M) return;
+    float v[V];
+    load_logits<T, V, kVec>(logits + t * E, lane, E, v);
+    const bool soft = scoring == MOE_SCORE_SOFTMAX;
+    float top = 0.f, sum = 1.f;
+    if (soft && (bias || !renorm)) {
+        top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < V; ++j) top = fmaxf(top, v[j]);
+        top = warp_max(top);
+        sum = 0.f;
+        if (top > -INFINITY) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum += expf(v[j] - top);
+        }
+        sum = warp_sum(sum);
+    }
+    uint32_t key[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        float s = v[j];
+        if (bias) {
+            const int e = lane * V + j;
+            s = v[j] > -INFINITY && e < E ? (soft ? expf(v[j] - top) / sum : sigmoid(v[j])) + __ldg(bias + e) : -INFINITY;
+        }
+        key[j] = order_key(s);
+    }
+    int my_id = -1;
+    float my_logit = -INFINITY;
+    for (int i = 0; i < topk; ++i) {
+        uint32_t best = 0;
+        int at = 0;
+        float l = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (key[j] > best) {
+                best = key[j];
+                at = j;
+                l = v[j];
+            }
+        const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+        if (most == 0) break;  // no available expert is left
+        const int win = __ffs(__ballot_sync(0xffffffffu, best == most)) - 1;
+        const int id = __shfl_sync(0xffffffffu, lane * V + at, win);
+        l = __shfl_sync(0xffffffffu, l, win);
+        if (lane == i) {
+            my_id = id;
+            my_logit = l;
+        }
+        if (lane == win) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j == at) key[j] = 0;
+        }
+    }
+    // lane i: slot i
+    float w = 0.f;
+    if (soft) {
+        if (renorm) {
+            // relative to the largest chosen logit, so that small scores do not vanish first
+            const float m = warp_max(my_logit);
+            const float e = my_id >= 0 ? expf(my_logit - m) : 0.f;
+            const float S = warp_sum(e);
+            w = my_id >= 0 ? e / S : 0.f;
+        } else if (my_id >= 0) {
+            w = expf(my_logit - top) / sum;
+        }
+    } else if (renorm) {
+        w = sigmoid_share(my_logit);
+    } else if (my_id >= 0) {
+        w = sigmoid(my_logit);
+    }
+    if (lane < topk) {
+        out_w[t * topk + lane] = w * scale;
+        out_id[t * topk + lane] = (TId)my_id;
+    }
+}
+
+template <typename T, typename TId, int V, bool kVec>
+__global__ void __launch_bounds__(kRouterWarps * 32)
+    router_backward_kernel(const T* logits, int64_t M, int E, const TId* __restrict__ ids, int topk, int scoring,
+                           int renorm, float scale, const float* __restrict__ dw, T* d_logits) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5);
+    if (t >= M) return;
+    const bool soft = scoring == MOE_SCORE_SOFTMAX;
+    // lane i: slot i
+    int id = -1;
+    float g = 0.f, l = -INFINITY;
+    if (lane < topk) {
+        const TId raw = ids[t * topk + lane];
+        if (raw >= 0 && raw < TId(E)) {
+            id = (int)raw;
+            g = scale * dw[t * topk + lane];
+            l = clean_logit(to_f32(logits[t * E + id]));
+        }
+    }
+    float v[V];
+    float top = -INFINITY, sum = 0.f, dot = 0.f, d = 0.f;
+    if (soft && !renorm) {
+        load_logits<T, V, kVec>(logits + t * E, lane, E, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) top = fmaxf(top, v[j]);
+        top = warp_max(top);
+        if (top > -INFINITY) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[j] = expf(v[j] - top);
+                sum += v[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = 0.f;
+        }
+        sum = warp_sum(sum);
+        const float r = sum > 0.f ? 1.f / sum : 0.f;
+        const float s = l > -INFINITY ? expf(l - top) * r : 0.f;
+        dot = warp_sum(s * g);
+        d = s * (g - dot);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = -dot * (v[j] * r);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = 0.f;
+        if (soft) {
+            const float m = warp_max(l);
+            const float e = l > -INFINITY ? expf(l - m) : 0.f;
+            const float S = warp_sum(e);
+            const float q = S > 0.f ? e / S : 0.f;
+            dot = warp_sum(q * g);
+            d = q * (g - dot);
+        } else {
+            const float one_less = sigmoid(-l);
+            if (renorm) {
+                const float q = sigmoid_share(l);
+                dot = warp_sum(q * g);
+                d = q * (g - dot) * one_less;
+            } else {
+                d = l > -INFINITY ? g * sigmoid(l) * one_less : 0.f;
+            }
+        }
+    }
+    __syncwarp();  // every logit of the row is read: d_logits may be logits
+    T* row = d_logits + t * E;
+    if constexpr (kVec) {
+        if (lane * V < E) {
+            Vec<T, V> r;
+#pragma unroll
+            for (int j = 0; j < V; ++j) r.v[j] = from_f32<T>(v[j]);
+            *reinterpret_cast<Vec<T, V>*>(row + lane * V) = r;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (lane * V + j < E) row[lane * V + j] = from_f32<T>(v[j]);
+    }
+    __syncwarp();  // the chosen experts' values replace the ones just written
+    if (id >= 0) row[id] = from_f32<T>(d);
+}
+
+bool router_args_ok(int64_t M, int E, int dtype, int topk, int scoring) {
+    return M >= 0 && E >= 1 && E <= kMaxRouterExperts && topk >= 1 && topk <= 32 && topk <= E && M <= INT32_MAX / topk &&
+           dtype_bytes(dtype) && (scoring == MOE_SCORE_SOFTMAX || scoring == MOE_SCORE_SIGMOID);
+}
+
+// Calls f(V) with V = the smallest power of two that covers E with 32 lanes.
+template <typename F>
+int with_v(int E, F&& f) {
+    if (E <= 32) return f(std::integral_constant<int, 1>{});
+    if (E <= 64) return f(std::integral_constant<int, 2>{});
+    if (E <= 128) return f(std::integral_constant<int, 4>{});
+    if (E <= 256) return f(std::integral_constant<int, 8>{});
+    if (E <= 512) return f(std::integral_constant<int, 16>{});
+    return f(std::integral_constant<int, 32>{});
+}
+
+// Vector accesses move at most 16 bytes: a lane's V values are one vector only while they fit.
+template <typename T, int V>
+constexpr bool fits_vec() { return V > 1 && V * sizeof(T) <= 16; }
+
+template <typename TId>
+int router_impl(const void* logits, int64_t M, int E, int dtype, int topk, int scoring, const float* bias, int renorm,
+                float scale, float* w, TId* ids, moe_stream_t stream) {
+    if (!router_args_ok(M, E, dtype, topk, scoring)) return MOE_ERR_INVALID_ARG;
+    if (M == 0) return MOE_OK;
+    if (!logits || !w || !ids || misaligned(logits, dtype_bytes(dtype))) return MOE_ERR_INVALID_ARG;
+    const size_t nl = (size_t)M * E * dtype_bytes(dtype), nw = (size_t)M * topk * 4, ni = (size_t)M * topk * sizeof(TId);
+    if (overlap(w, nw, logits, nl) || overlap(ids, ni, logits, nl) || overlap(w, nw, ids, ni)) return MOE_ERR_INVALID_ARG;
+    if (int st = check_device(nullptr)) return st;
+    const unsigned grid = (unsigned)((M + kRouterWarps - 1) / kRouterWarps);
+    return with_dtype(dtype, [&](auto* p) {
+        using T = std::remove_pointer_t<decltype(p)>;
+        return with_v(E, [&](auto vc) {
+            constexpr int V = decltype(vc)::value;
+            auto go = [&](auto kernel) {
+                launch_k(kernel, grid, kRouterWarps * 32, 0, (cudaStream_t)stream, static_cast<const T*>(logits), M, E,
+                         topk, scoring, bias, renorm ? 1 : 0, scale, w, ids);
+                note_launches(1);
+                return launch_status();
+            };
+            if constexpr (fits_vec<T, V>())
+                if (E % V == 0 && !misaligned(logits, V * sizeof(T))) return go(router_kernel<T, TId, V, true>);
+            return go(router_kernel<T, TId, V, false>);
+        });
+    });
+}
+
+template <typename TId>
+int router_backward_impl(const void* logits, int64_t M, int E, int dtype, const TId* ids, int topk, int scoring,
+                         int renorm, float scale, const float* dw, void* d_logits, moe_stream_t stream) {
+    if (!router_args_ok(M, E, dtype, topk, scoring)) return MOE_ERR_INVALID_ARG;
+    if (M == 0) return MOE_OK;
+    if (!logits || !ids || !dw || !d_logits || misaligned(logits, dtype_bytes(dtype)) ||
+        misaligned(d_logits, dtype_bytes(dtype)))
+        return MOE_ERR_INVALID_ARG;
+    const size_t nl = (size_t)M * E * dtype_bytes(dtype);
+    if ((d_logits != logits && overlap(d_logits, nl, logits, nl)) ||
+        overlap(d_logits, nl, ids, (size_t)M * topk * sizeof(TId)) || overlap(d_logits, nl, dw, (size_t)M * topk * 4))
+        return MOE_ERR_INVALID_ARG;
+    if (int st = check_device(nullptr)) return st;
+    const unsigned grid = (unsigned)((M + kRouterWarps - 1) / kRouterWarps);
+    return with_dtype(dtype, [&](auto* p) {
+        using T = std::remove_pointer_t<decltype(p)>;
+        return with_v(E, [&](auto vc) {
+            constexpr int V = decltype(vc)::value;
+            auto go = [&](auto kernel) {
+                launch_k(kernel, grid, kRouterWarps * 32, 0, (cudaStream_t)stream, static_cast<const T*>(logits), M, E, ids,
+                         topk, scoring, renorm ? 1 : 0, scale, dw, static_cast<T*>(d_logits));
+                note_launches(1);
+                return launch_status();
+            };
+            if constexpr (fits_vec<T, V>())
+                if (E % V == 0 && !misaligned(logits, V * sizeof(T)) && !misaligned(d_logits, V * sizeof(T)))
+                    return go(router_backward_kernel<T, TId, V, true>);
+            return go(router_backward_kernel<T, TId, V, false>);
+        });
+    });
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+MOE_API int moe_router_topk(const void* logits, int64_t M, int E, int dtype, int topk, int scoring, const float* bias,
+                            int renormalize, float scale, float* topk_weights, int32_t* topk_ids, moe_stream_t stream) {
+    return router_impl(logits, M, E, dtype, topk, scoring, bias, renormalize, scale, topk_weights, topk_ids, stream);
+}
+
+MOE_API int moe_router_topk_i64(const void* logits, int64_t M, int E, int dtype, int topk, int scoring,
+                                const float* bias, int renormalize, float scale, float* topk_weights, int64_t* topk_ids,
+                                moe_stream_t stream) {
+    return router_impl(logits, M, E, dtype, topk, scoring, bias, renormalize, scale, topk_weights, topk_ids, stream);
+}
+
+MOE_API int moe_router_topk_backward(const void* logits, int64_t M, int E, int dtype, const int32_t* topk_ids, int topk,
+                                     int scoring, int renormalize, float scale, const float* d_topk_weights,
+                                     void* d_logits, moe_stream_t stream) {
+    return router_backward_impl(logits, M, E, dtype, topk_ids, topk, scoring, renormalize, scale, d_topk_weights, d_logits,
+                                stream);
+}
+
+MOE_API int moe_router_topk_backward_i64(const void* logits, int64_t M, int E, int dtype, const int64_t* topk_ids,
+                                         int topk, int scoring, int renormalize, float scale,
+                                         const float* d_topk_weights, void* d_logits, moe_stream_t stream) {
+    return router_backward_impl(logits, M, E, dtype, topk_ids, topk, scoring, renormalize, scale, d_topk_weights, d_logits,
+                                stream);
+}
+
+}  // extern "C"
