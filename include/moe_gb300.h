@@ -104,7 +104,7 @@ MOE_API const char* moe_status_string(int status);
 MOE_API uint64_t moe_kernel_launch_count(void);
 
 /* Device-side error word of this library's kernels on the current device: 0 when no
- * kernel has reported a problem, 1 when a grouped-GEMM pipeline wait gave up after its
+ * kernel has reported a problem, 1 when a wait in the pipeline of a grouped GEMM or product gave up after its
  * time limit (the kernel then returned early and its output is not valid). Reading it
  * synchronises the device; clear != 0 resets it to 0. Returns -1 if the read failed. */
 MOE_API int moe_device_error(int clear);

@@ -99,7 +99,10 @@ MOE_API const char* moe_status_string(int status) {
 
 MOE_API uint64_t moe_kernel_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
-MOE_API int moe_device_error(int clear) { return read_gemm_error(clear); }
+MOE_API int moe_device_error(int clear) {
+    const int a = read_gemm_error(clear), b = read_grouped_error(clear);
+    return a < 0 || b < 0 ? -1 : a | b;
+}
 
 MOE_API int64_t moe_rp_cap(int64_t chunk_M, int topk, int local_num_experts) {
     if (chunk_M < 0 || topk < 1 || local_num_experts < 1) return -1;

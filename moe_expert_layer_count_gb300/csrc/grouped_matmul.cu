@@ -1,101 +1,540 @@
 // Matrix products of ragged row groups with one 16-bit weight matrix per group (the
-// experts of an MoE layer in training, or served from 16-bit weights):
+// experts of an MoE layer in training, or served from 16-bit weights), on the
+// 5th-generation tensor cores (tcgen05, sm_103a):
 //   forward   y[r]  = W_l x[r]                     for the rows r of group l
 //   dgrad     dx[r] = W_l^T dy[r]
 //   wgrad     dW_l  = sum over the rows r of group l of dy[r] x[r]^T   (0 if it has none)
-// One 64x64 output tile per block, operands through shared memory, fp32 FMAs.
+//
+// Two CTAs (one cluster, two neighbouring SMs) work on one 256-row tile with
+// tcgen05.mma.cta_group::2; each holds 128 rows of A and half of B's columns in shared
+// memory and 128 rows of the fp32 accumulator in TMEM.
+//  * forward and dgrad compute the transposed product: the M side (256 rows) runs over the
+//    weights' outputs, which have no ragged edge, and the N side over a group's rows. N may
+//    be any multiple of 16 up to 256, so a group of c rows costs ceil(c / 16) * 16 columns
+//    and not a multiple of 128, and a group of a few rows (decode) just streams its weights.
+//  * wgrad: M over n_out, N over k_in, the sum over the group's rows in steps of 64. The
+//    last step's rows past the group's end are another group's (or anything): the warps that
+//    feed the MMAs zero them in shared memory, in both operands (0 * NaN is NaN).
+// The operand that TMA loads with its reduced index outermost (the weights of dgrad, both
+// operands of wgrad) is read as an MN-major tile: 64 x 64 boxes, no transposition in memory.
+// A persistent grid of CTA pairs; per CTA: warps 0-3 epilogue, warp 4 TMA, warp 5 MMA (issued
+// by the pair's first CTA). Two TMEM accumulators, so that a tile's epilogue runs under the
+// next tile's MMAs. Every pipeline wait gives up after 2 s, sets a device error word and ends
+// the kernel.
+#include <cudaTypedefs.h>
+
+#include <atomic>
 #include <climits>
+#include <mutex>
 
 #include "elem.cuh"
 #include "route.cuh"
+#include "sm100_ptx.cuh"
 
 namespace moe {
+
+__device__ int g_grouped_error;  // set to 1 when a pipeline wait ran out of time
+
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
 enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
-// Rows [lo, hi) of group l, never outside [0, R).
-__device__ __forceinline__ void group_rows(const int32_t* off, const int32_t* cnt, int l, int R, int& lo, int& hi) {
-    lo = min(max(off[l], 0), R);
-    const int end = cnt ? (int)min((int64_t)lo + max(cnt[l], 0), (int64_t)R) : off[l + 1];
-    hi = max(min(end, R), lo);
+constexpr int kPairM = 256;        // rows of a tile (both CTAs)
+constexpr int kMaxN = 256;         // columns of a tile
+constexpr int kDepth = 64;         // reduced index per stage: 64 16-bit values = one 128-byte swizzled row
+constexpr int kOperandBytes = 128 * kDepth * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kMaxStages = 6;
+constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 192;
+constexpr int kBoxBytes = 4096;    // wgrad output box: 32 rows x 128 bytes
+constexpr int kStagingBytes = kEpiWarps * 2 * kBoxBytes;
+constexpr int kSmemLimit = 232448;
+constexpr int kRowBoxes = 5;       // boxes of 8, 16, 32, 64, 128 rows
+constexpr int kMaxDevices = 64;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+struct Maps {
+    CUtensorMap a;             // M side: weights (forward, dgrad) or dy (wgrad)
+    CUtensorMap b[kRowBoxes];  // N side: rows in boxes of 8 << i (forward, dgrad); b[0]: x (wgrad)
+    CUtensorMap o;             // wgrad's output
+};
+
+struct __align__(8) Tail {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t ready[kMaxStages];  // wgrad, first CTA: the second CTA's half of a stage is in place
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort;
+};
+
+size_t fixed_smem(int El) { return 1024 + kStagingBytes + sizeof(Tail) + 16 + (size_t)(3 * El + 1) * sizeof(int32_t); }
+
+// ------------------------------------------------------------------ PTX of the CTA pair
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared variable `a` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t map_to(uint32_t a, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Tile loads whose completion may count on the barrier of the pair's other CTA.
+__device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void store_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t t, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(cols) : "memory");
+}
+// D[tmem of both CTAs] (+)= A * B^T over 16 values of the reduced index, 16-bit operands.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on `bar` of both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
 
-template <int MODE, typename T, typename O>
-__global__ void __launch_bounds__(256)
-    grouped_simple_kernel(const T* __restrict__ a, const T* __restrict__ b, const int32_t* __restrict__ off,
-                          const int32_t* __restrict__ cnt, int El, int R, int N, int K, O* __restrict__ out) {
-    __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
+// Shared-memory descriptor of an MN-major tile with the 128-byte swizzle: boxes of 64 values
+// x `kDepth` rows of 128 bytes, boxes 8192 bytes apart (leading offset), groups of 8 rows
+// 1024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(kOperandBytes / 2 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Instruction descriptor of kind::f16 for M = 256 without N (N / 8 goes to bit 17).
+uint32_t idesc_base(int mode, int dtype) {
+    const uint32_t f = dtype == MOE_DT_BF16 ? 1u : 0u;
+    return 1u << 4 | f << 7 | f << 10 | (mode != kFwd ? 1u << 15 : 0u) | (mode == kWgrad ? 1u << 16 : 0u) |
+           (uint32_t)(kPairM >> 4) << 24;
+}
+
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, bool check_abort = true) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if ((i & 31) == 0) {
+            if (check_abort && *abort) return false;
+            if (ptx::globaltimer_ns() - t0 > kTimeoutNs) {
+                *abort = 1;
+                atomicExch(&g_grouped_error, 1);
+                return false;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ tiles
+struct Groups {
+    const int32_t* start;  // first tile of each group (forward, dgrad), El + 1
+    const int32_t* lo;     // first row
+    const int32_t* rows;   // row count
+};
+
+// Where a tile lies. forward, dgrad: outputs [m0, m0 + 256) x rows [lo, lo + rows) of group
+// l, n = rows rounded up to 16. wgrad: [m0, m0 + 256) x [n0, n0 + 256) of dW_l, summed over
+// rows [lo, lo + rows). steps: stages of the reduced index.
+struct Tile {
+    int l, lo, rows, m0, n0, n, steps;
+};
+
+template <int MODE>
+__device__ __forceinline__ Tile tile_at(int tile, const Groups& g, int El, int m_tiles, int n_tiles, int depth) {
+    Tile t;
+    if (MODE == kWgrad) {
+        t.l = tile / (m_tiles * n_tiles);
+        const int i = tile - t.l * m_tiles * n_tiles;
+        t.m0 = i % m_tiles * kPairM;
+        t.n0 = i / m_tiles * kMaxN;
+        t.n = kMaxN;
+        t.lo = g.lo[t.l];
+        t.rows = g.rows[t.l];
+        t.steps = (t.rows + kDepth - 1) / kDepth;
+    } else {
+        int a = 0, b = El - 1;
+        while (a < b) {
+            const int mid = (a + b + 1) >> 1;
+            if (g.start[mid] <= tile) a = mid; else b = mid - 1;
+        }
+        t.l = a;
+        const int i = tile - g.start[a], count = g.rows[a];
+        const int parts = (count + kMaxN - 1) / kMaxN;          // equal parts of the group, whole 16s
+        const int per = ((count + parts - 1) / parts + 15) & ~15;
+        const int p = i / m_tiles;
+        t.m0 = (i - p * m_tiles) * kPairM;
+        t.lo = g.lo[a] + p * per;
+        t.rows = min(per, count - p * per);
+        t.n = (t.rows + 15) & ~15;
+        t.n0 = 0;
+        t.steps = (depth + kDepth - 1) / kDepth;
+    }
+    return t;
+}
+
+template <int MODE, typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ off, const int32_t* __restrict__ cnt,
+                   int El, int R, int N, int K, uint32_t idesc0, int stages, O* __restrict__ out) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* staging = smem + stages * kStageBytes;
+    Tail* st = reinterpret_cast<Tail*>(staging + kStagingBytes);
+    int32_t* s_lo = reinterpret_cast<int32_t*>(st + 1);
+    int32_t* s_rows = s_lo + El;
+    int32_t* s_start = s_rows + El;
+    volatile int* abort = &st->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    const Groups groups{s_start, s_lo, s_rows};
+    const int P = MODE == kDgrad ? K : N;                 // length of the M side
+    const int depth = MODE == kDgrad ? N : K;             // reduced index (forward, dgrad)
+    const int m_tiles = (P + kPairM - 1) / kPairM;
+    const int n_tiles = (K + kMaxN - 1) / kMaxN;          // wgrad
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&st->full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&st->empty[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&st->ready[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(ptx::smem_addr(&st->tfull[b]), 1);
+            ptx::mbar_init(ptx::smem_addr(&st->tempty[b]), 2 * kEpiWarps);
+        }
+        ptx::mbar_init(ptx::smem_addr(&st->mma_done), 1);
+        st->abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc_pair(ptx::smem_addr(&st->tmem_base), 512);
+        tmem_relinquish_pair();
+        ptx::tc_fence_before();
+    }
     pdl_wait();
     pdl_trigger();
-    // this block's group and its tile within the group
-    int l, lo, hi, m0;
-    if (MODE == kWgrad) {
-        l = blockIdx.z;
-        group_rows(off, cnt, l, R, lo, hi);
-        m0 = blockIdx.x * kTile;
+    // the groups' rows, never outside [0, R), and the prefix sums of their tiles
+    for (int l = threadIdx.x; l < El; l += kThreads) {
+        const int lo = min(max(__ldg(off + l), 0), R);
+        const int end = cnt ? (int)min((int64_t)lo + max(__ldg(cnt + l), 0), (int64_t)R) : min(__ldg(off + l + 1), R);
+        s_lo[l] = lo;
+        s_rows[l] = max(end - lo, 0);
+    }
+    __syncthreads();
+    if (MODE != kWgrad && warp == 0) {
+        int base = 0;
+        for (int l0 = 0; l0 < El; l0 += 32) {
+            const int l = l0 + lane;
+            const int mine = l < El ? (s_rows[l] + kMaxN - 1) / kMaxN * m_tiles : 0;
+            int sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (l < El) s_start[l] = base + sum - mine;
+            base += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) s_start[El] = base;
+    }
+    __syncthreads();
+    cluster_sync();  // barriers and TMEM of both CTAs are in place
+    ptx::tc_fence_after();
+    const uint32_t tmem = st->tmem_base;
+    const int tiles = MODE == kWgrad ? El * m_tiles * n_tiles : s_start[El];
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            int s = 0;
+            uint32_t ph = 0, loads = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < tiles; tile += step) {
+                const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
+                int box = 0;  // the smallest box that holds this CTA's half of the columns
+                while (MODE != kWgrad && (8 << box) < t.n / 2) ++box;
+                const int row = t.lo + (int)rank * (t.n / 2);
+                const int m = t.m0 + (int)rank * 128;
+                for (int k = 0; k < t.steps; ++k) {
+                    if (!wait_phase(ptx::smem_addr(&st->empty[s]), ph ^ 1, abort)) { ok = false; break; }
+                    const uint32_t a = ptx::smem_addr(smem + s * kStageBytes), b = a + kOperandBytes;
+                    const uint32_t mine = ptx::smem_addr(&st->full[s]);
+                    const int d = k * kDepth;
+                    if (MODE == kWgrad) {
+                        ptx::mbar_arrive_expect_tx(mine, kStageBytes);
+                        const int n = t.n0 + (int)rank * 128, r = t.lo + d;
+                        ptx::tma_load_2d(a, &maps.a, m, r, mine);
+                        ptx::tma_load_2d(a + kOperandBytes / 2, &maps.a, m + 64, r, mine);
+                        ptx::tma_load_2d(b, &maps.b[0], n, r, mine);
+                        ptx::tma_load_2d(b + kOperandBytes / 2, &maps.b[0], n + 64, r, mine);
+                    } else {
+                        // both CTAs' loads count on the first CTA's barrier
+                        const uint32_t bar = map_to(mine, 0);
+                        if (rank == 0) ptx::mbar_arrive_expect_tx(mine, 2 * (kOperandBytes + (1024u << box)));
+                        if (MODE == kFwd) {
+                            load_3d_pair(a, &maps.a, d, m, t.l, bar);
+                        } else {
+                            load_3d_pair(a, &maps.a, m, d, t.l, bar);
+                            load_3d_pair(a + kOperandBytes / 2, &maps.a, m + 64, d, t.l, bar);
+                        }
+                        load_2d_pair(b, &maps.b[box], d, row, bar);
+                    }
+                    ++loads;
+                    if (++s == stages) s = 0, ph ^= 1;
+                }
+            }
+            // never leave with copies in flight: the last stages' loads must have landed (the
+            // first CTA's barriers count both CTAs' in forward and dgrad)
+            if (MODE == kWgrad || rank == 0) {
+                const int n = loads < (uint32_t)stages ? (int)loads : stages;
+                for (int i = 0; i < n; ++i) {
+                    if (--s < 0) s = stages - 1, ph ^= 1;
+                    wait_phase(ptx::smem_addr(&st->full[s]), ph, abort, false);
+                }
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        int s = 0, b = 0;
+        uint32_t ph = 0, tph = 0;
+        bool ok = true;
+        for (int tile = first; ok && tile < tiles; tile += step) {
+            if (MODE != kWgrad && (rank != 0 || lane != 0)) break;
+            const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
+            if (t.steps == 0) continue;
+            const uint32_t idesc = idesc0 | (uint32_t)(t.n >> 3) << 17;
+            const uint32_t d = tmem + (uint32_t)(b * kMaxN);
+            if (rank == 0 && lane == 0) ok = wait_phase(ptx::smem_addr(&st->tempty[b]), tph ^ 1, abort);
+            if (MODE == kWgrad) ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            for (int k = 0; k < t.steps; ++k) {
+                ok = wait_phase(ptx::smem_addr(&st->full[s]), ph, abort);
+                const uint32_t a_base = ptx::smem_addr(smem + s * kStageBytes), b_base = a_base + kOperandBytes;
+                const int left = (MODE == kWgrad ? t.rows : depth) - k * kDepth;
+                const int slices = left >= kDepth ? kDepth / 16 : (left + 15) / 16;
+                if (MODE == kWgrad) {
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (left < slices * 16) {
+                        // rows past the group's end within the last 16: zeros in all four boxes
+                        uint8_t* p = smem + s * kStageBytes;
+                        const int n = (slices * 16 - left) * 8;  // 16-byte pieces of a box
+                        for (int i = lane; i < 4 * n; i += 32)
+                            *reinterpret_cast<uint4*>(p + i / n * (kOperandBytes / 2) + left * 128 + i % n * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        ptx::fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank != 0)
+                            arrive_cluster(map_to(ptx::smem_addr(&st->ready[s]), 0));
+                        else
+                            ok = wait_phase(ptx::smem_addr(&st->ready[s]), ph, abort);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                }
+                if (!ok) break;
+                if (rank == 0 && lane == 0) {
+                    ptx::tc_fence_after();
+                    for (int i = 0; i < slices; ++i)
+                        mma_pair(d,
+                                 MODE == kFwd ? ptx::smem_desc_sw128(a_base + 32 * i, 1024) : desc_mn(a_base + 2048 * i),
+                                 MODE == kWgrad ? desc_mn(b_base + 2048 * i) : ptx::smem_desc_sw128(b_base + 32 * i, 1024),
+                                 idesc, (k | i) ? 1u : 0u);
+                    commit_pair(ptx::smem_addr(&st->empty[s]));
+                    if (k + 1 == t.steps) commit_pair(ptx::smem_addr(&st->tfull[b]));
+                }
+                if (++s == stages) s = 0, ph ^= 1;
+            }
+            if (++b == 2) b = 0, tph ^= 1;
+        }
+        // never leave with MMAs in flight
+        if (rank == 0 && lane == 0) {
+            commit_pair(ptx::smem_addr(&st->mma_done));
+            wait_phase(ptx::smem_addr(&st->mma_done), 0, abort, false);
+        }
     } else {
-        int t = blockIdx.x;
-        for (l = 0; l < El; ++l) {
-            group_rows(off, cnt, l, R, lo, hi);
-            const int n = (hi - lo + kTile - 1) / kTile;
-            if (t < n) break;
-            t -= n;
+        // ---------------------------------------------------------------- epilogue
+        int b = 0, boxes = 0;
+        uint32_t tph = 0;
+        const uint32_t slab = (uint32_t)(warp * 32) << 16;
+        for (int tile = first; tile < tiles; tile += step) {
+            const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
+            const int m = t.m0 + (int)rank * 128 + warp * 32;  // this warp's first row of the tile
+            if (t.steps > 0) {
+                bool ok = wait_phase(ptx::smem_addr(&st->tfull[b]), tph, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ptx::tc_fence_after();
+            }
+            const uint32_t acc = tmem + slab + (uint32_t)(b * kMaxN);
+            if constexpr (MODE == kWgrad) {
+                constexpr int kCols = 128 / sizeof(O);  // columns of a 128-byte-wide box
+                for (int c = 0; c < kMaxN && t.n0 + c < K; c += kCols) {
+                    float v[kCols];
+#pragma unroll
+                    for (int h = 0; h < kCols; h += 32) {
+                        uint32_t r[32];
+                        if (t.steps > 0) {
+                            ptx::tmem_ld_32x32b_x32(acc + c + h, r);
+                            ptx::tmem_wait_ld_regs32(r);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[h + j] = t.steps > 0 ? __uint_as_float(r[j]) : 0.f;
+                    }
+                    // 32 rows x 128 bytes in TMA's 128-byte swizzle, two boxes in turn
+                    uint8_t* box = staging + (warp * 2 + (boxes & 1)) * kBoxBytes;
+                    ++boxes;
+                    if (lane == 0) ptx::bulk_wait_read1();
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        Vec<O, 16 / sizeof(O)> w;
+#pragma unroll
+                        for (int j = 0; j < 16 / (int)sizeof(O); ++j) w.v[j] = from_f32<O>(v[q * (16 / sizeof(O)) + j]);
+                        *reinterpret_cast<Vec<O, 16 / sizeof(O)>*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (m < P) store_3d(&maps.o, ptx::smem_addr(box), t.n0 + c, m, t.l);
+                        ptx::bulk_commit();
+                    }
+                }
+            } else {
+                const bool in = m + lane < P;
+                O* o = out + (int64_t)t.lo * P + m + lane;
+                for (int c = 0; c < t.rows; c += 32) {
+                    uint32_t r[32];
+                    __syncwarp();
+                    ptx::tmem_ld_32x32b_x32(acc + c, r);
+                    ptx::tmem_wait_ld_regs32(r);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (in && c + j < t.rows) o[(int64_t)(c + j) * P] = from_f32<O>(__uint_as_float(r[j]));
+                }
+            }
+            if (t.steps > 0) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(map_to(ptx::smem_addr(&st->tempty[b]), 0));
+                if (++b == 2) b = 0, tph ^= 1;
+            }
         }
-        if (l == El) return;
-        m0 = lo + t * kTile;
+        if (MODE == kWgrad && lane == 0) ptx::bulk_wait0();
     }
-    const int n0 = blockIdx.y * kTile;
-    const int m_end = MODE == kWgrad ? N : hi, n_end = MODE == kFwd ? N : K;
-    const int d0 = MODE == kWgrad ? lo : 0, d_end = MODE == kWgrad ? hi : MODE == kFwd ? K : N;
-    const T* w = b + (MODE == kWgrad ? 0 : (int64_t)l * N * K);
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int d = d0; d < d_end; d += kDepth) {
-        for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-            // the fastest index runs along each operand's contiguous direction
-            int m = MODE == kWgrad ? i % kTile : i / kDepth, k = MODE == kWgrad ? i / kTile : i % kDepth;
-            float v = 0.f;
-            if (m0 + m < m_end && d + k < d_end)
-                v = MODE == kFwd     ? to_f32(a[(int64_t)(m0 + m) * K + d + k])
-                    : MODE == kDgrad ? to_f32(a[(int64_t)(m0 + m) * N + d + k])
-                                     : to_f32(a[(int64_t)(d + k) * N + m0 + m]);
-            sa[k][m] = v;
-            m = MODE == kFwd ? i / kDepth : i % kTile, k = MODE == kFwd ? i % kDepth : i / kTile;
-            v = 0.f;
-            if (n0 + m < n_end && d + k < d_end)
-                v = MODE == kFwd ? to_f32(w[(int64_t)(n0 + m) * K + d + k]) : to_f32(w[(int64_t)(d + k) * K + n0 + m]);
-            sb[k][m] = v;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
-        __syncthreads();
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while the other still signals its barriers or uses its TMEM
+    if (warp == kMmaWarp) {
+        ptx::tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
     }
-    O* o = out + (MODE == kWgrad ? (int64_t)l * N * K : 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < m_end && n < n_end) o[(int64_t)m * n_end + n] = from_f32<O>(acc[i][j]);
-        }
 }
 
-template <int MODE, typename T, typename O>
-int launch_simple(const void* a, const void* b, const int32_t* off, const int32_t* cnt, int El, int64_t R, int N, int K,
-                  void* out, cudaStream_t stream) {
-    const int64_t tiles = MODE == kWgrad ? (N + kTile - 1) / kTile : (R + kTile - 1) / kTile + El;
-    const int n_out = MODE == kFwd ? N : K;
-    if (n_out > 65535 * kTile) return MOE_ERR_INVALID_ARG;
-    const dim3 grid((unsigned)tiles, (unsigned)((n_out + kTile - 1) / kTile), MODE == kWgrad ? (unsigned)El : 1u);
-    launch_k(grouped_simple_kernel<MODE, T, O>, grid, 256, 0, stream, static_cast<const T*>(a), static_cast<const T*>(b), off,
-             cnt, El, (int)R, N, K, static_cast<O*>(out));
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// Tensor [z, y, x] (z = 1: two dimensions) of 2- or 4-byte elements, boxes of box_y rows x 128
+// bytes with the 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, int esize, uint64_t x, uint64_t y, uint64_t z, uint32_t box_y, int dims) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t size[3] = {x, y, z}, stride[2] = {x * esize, x * y * esize};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / esize), box_y, 1}, one[3] = {1, 1, 1};
+    return fn(m, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (cuuint32_t)dims,
+              const_cast<void*>(base), size, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, typename O>
+int launch_grouped(const void* a, const void* b, const int32_t* off, const int32_t* cnt, int El, int64_t R, int N, int K,
+                   int dtype, void* out, int num_sms, cudaStream_t stream) {
+    Maps maps{};
+    bool ok = true;
+    if (MODE == kWgrad) {
+        const uint64_t rows = R > 0 ? (uint64_t)R : 1;  // R = 0: nothing is loaded
+        const void* any = out;
+        ok = make_map(&maps.a, R > 0 ? a : any, 2, N, rows, 1, kDepth, 2) &&
+             make_map(&maps.b[0], R > 0 ? b : any, 2, K, rows, 1, kDepth, 2) &&
+             make_map(&maps.o, out, sizeof(O), K, N, El, 32, 3);
+    } else {
+        ok = make_map(&maps.a, b, 2, K, N, El, MODE == kFwd ? 128 : kDepth, 3);
+        for (int i = 0; i < kRowBoxes; ++i) ok = ok && make_map(&maps.b[i], a, 2, MODE == kFwd ? K : N, R, 1, 8u << i, 2);
+    }
+    if (!ok) return MOE_ERR_CUDA;
+    int dev = 0;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(grouped_kernel<MODE, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
+            cudaSuccess)
+            return MOE_ERR_CUDA;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    const int stages = (int)((kSmemLimit - fixed_smem(El)) / kStageBytes);
+    const size_t smem = fixed_smem(El) + (size_t)(stages < kMaxStages ? stages : kMaxStages) * kStageBytes;
+    // no more pairs than tiles (an upper bound: the groups' sizes are not known here)
+    const int64_t m_tiles = ((MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;
+    const int64_t most = MODE == kWgrad ? El * m_tiles * ((K + kMaxN - 1) / kMaxN)
+                                        : (R / kMaxN + (R < El ? R : El)) * m_tiles;
+    const int pairs = (int)(most < num_sms / 2 ? most : num_sms / 2);
+    launch_k(grouped_kernel<MODE, O>, 2 * pairs, kThreads, smem, stream, maps, off, cnt, El, (int)R, N, K,
+             idesc_base(MODE, dtype), stages < kMaxStages ? stages : kMaxStages, static_cast<O*>(out));
     note_launches(1);
     return launch_status();
 }
@@ -107,23 +546,39 @@ int grouped_impl(const void* a, const void* b, const int32_t* off, const int32_t
     if (El < 1 || El > kMaxLocalExperts || R < 0 || R > INT32_MAX || N < 8 || K < 8 || N % 8 || K % 8 || !off ||
         (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16) || (out_dtype != dtype && out_dtype != MOE_DT_F32))
         return MOE_ERR_INVALID_ARG;
-    if (((R > 0 || MODE == kWgrad) && !out) || (R > 0 && (!a || !b)) || misaligned(a, 16) || misaligned(b, 16) || misaligned(out, 16)) return MOE_ERR_INVALID_ARG;
+    if (((R > 0 || MODE == kWgrad) && !out) || (R > 0 && (!a || !b)) || misaligned(a, 16) || misaligned(b, 16) ||
+        misaligned(out, 16))
+        return MOE_ERR_INVALID_ARG;
+    // tiles are counted in 32 bits
+    const int64_t m_tiles = ((MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;
+    if ((MODE == kWgrad ? El * m_tiles * ((K + kMaxN - 1) / kMaxN) : (R / kMaxN + El) * m_tiles) > INT32_MAX / 2)
+        return MOE_ERR_INVALID_ARG;
     if (R == 0 && MODE != kWgrad) return MOE_OK;
     const size_t wn = (size_t)El * N * K;
     const size_t a_bytes = (size_t)R * (MODE == kFwd ? K : N) * 2;
     const size_t b_bytes = MODE == kWgrad ? (size_t)R * K * 2 : wn * 2;
     const size_t o_bytes = (MODE == kWgrad ? wn : (size_t)R * (MODE == kFwd ? N : K)) * dtype_bytes(out_dtype);
     if (overlap(out, o_bytes, a, a_bytes) || overlap(out, o_bytes, b, b_bytes)) return MOE_ERR_INVALID_ARG;
-    if (int st = check_device(nullptr)) return st;
+    int sms = 0;
+    if (int st = check_device(&sms)) return st;
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == MOE_DT_BF16)
-        return out_dtype == MOE_DT_F32 ? launch_simple<MODE, bf16, float>(a, b, off, cnt, El, R, N, K, out, s)
-                                       : launch_simple<MODE, bf16, bf16>(a, b, off, cnt, El, R, N, K, out, s);
-    return out_dtype == MOE_DT_F32 ? launch_simple<MODE, fp16, float>(a, b, off, cnt, El, R, N, K, out, s)
-                                   : launch_simple<MODE, fp16, fp16>(a, b, off, cnt, El, R, N, K, out, s);
+    if (out_dtype == MOE_DT_F32) return launch_grouped<MODE, float>(a, b, off, cnt, El, R, N, K, dtype, out, sms, s);
+    if (dtype == MOE_DT_BF16) return launch_grouped<MODE, bf16>(a, b, off, cnt, El, R, N, K, dtype, out, sms, s);
+    return launch_grouped<MODE, fp16>(a, b, off, cnt, El, R, N, K, dtype, out, sms, s);
 }
 
 }  // namespace
+
+int read_grouped_error(int clear) {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_grouped_error, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_grouped_error, &z, sizeof(int));
+    }
+    return v;
+}
+
 }  // namespace moe
 
 using namespace moe;
