@@ -13,12 +13,12 @@
 //    be any multiple of 16 up to 256, so a group of c rows costs ceil(c / 16) * 16 columns
 //    and not a multiple of 128, and a group of a few rows (decode) just streams its weights.
 //  * wgrad: M over n_out, N over k_in, the sum over the group's rows in steps of 64. The
-//    last step's rows past the group's end are another group's (or anything): the warps that
-//    feed the MMAs zero them in shared memory, in both operands (0 * NaN is NaN).
+//    last step's rows past the group's end are another group's (or anything): a warp of each
+//    CTA zeroes them in shared memory, in both operands (0 * NaN is NaN).
 // The operand that TMA loads with its reduced index outermost (the weights of dgrad, both
 // operands of wgrad) is read as an MN-major tile: 64 x 64 boxes, no transposition in memory.
 // A persistent grid of CTA pairs; per CTA: warps 0-3 epilogue, warp 4 TMA, warp 5 MMA (issued
-// by the pair's first CTA). Two TMEM accumulators, so that a tile's epilogue runs under the
+// by the pair's first CTA), warp 6 wgrad's ragged ends. Two TMEM accumulators, so that a tile's epilogue runs under the
 // next tile's MMAs. Every pipeline wait gives up after 2 s, sets a device error word and ends
 // the kernel.
 #include <cudaTypedefs.h>
@@ -45,12 +45,13 @@ constexpr int kDepth = 64;         // reduced index per stage: 64 16-bit values 
 constexpr int kOperandBytes = 128 * kDepth * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxStages = 6;
-constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kTailWarp = 6;
 constexpr int kBoxBytes = 4096;    // wgrad output box: 32 rows x 128 bytes
 constexpr int kStagingBytes = kEpiWarps * 2 * kBoxBytes;
 constexpr int kSmemLimit = 232448;
 constexpr int kRowBoxes = 5;       // boxes of 8, 16, 32, 64, 128 rows
+template <int MODE>
+__host__ __device__ constexpr int threads_of() { return MODE == kWgrad ? 224 : 192; }  // the tail warp is wgrad's
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -61,9 +62,10 @@ struct Maps {
 };
 
 struct __align__(8) Tail {
-    uint64_t full[kMaxStages];
+    uint64_t full[kMaxStages];   // first CTA: both CTAs' loads of a stage have landed
     uint64_t empty[kMaxStages];
-    uint64_t ready[kMaxStages];  // wgrad, first CTA: the second CTA's half of a stage is in place
+    uint64_t land[kMaxStages];   // wgrad: this CTA's loads of a group's ragged last stage have landed
+    uint64_t ready[kMaxStages];  // wgrad, first CTA: both CTAs have zeroed what the stage must not hold
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t mma_done;
@@ -216,8 +218,12 @@ __device__ __forceinline__ Tile tile_at(int tile, const Groups& g, int El, int m
     return t;
 }
 
+// wgrad: whether stage k of a tile ends between two multiples of 16 rows, so that the MMAs
+// would read rows past the group's end.
+__device__ __forceinline__ bool ragged(const Tile& t, int k) { return k + 1 == t.steps && (t.rows & 15) != 0; }
+
 template <int MODE, typename O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 1)
     grouped_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ off, const int32_t* __restrict__ cnt,
                    int El, int R, int N, int K, uint32_t idesc0, int stages, O* __restrict__ out) {
     extern __shared__ uint8_t smem_raw[];
@@ -240,7 +246,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int s = 0; s < stages; ++s) {
             ptx::mbar_init(ptx::smem_addr(&st->full[s]), 1);
             ptx::mbar_init(ptx::smem_addr(&st->empty[s]), 1);
-            ptx::mbar_init(ptx::smem_addr(&st->ready[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&st->land[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&st->ready[s]), 2);
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(ptx::smem_addr(&st->tfull[b]), 1);
@@ -258,7 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_trigger();
     // the groups' rows, never outside [0, R), and the prefix sums of their tiles
-    for (int l = threadIdx.x; l < El; l += kThreads) {
+    for (int l = threadIdx.x; l < El; l += threads_of<MODE>()) {
         const int lo = min(max(__ldg(off + l), 0), R);
         const int end = cnt ? (int)min((int64_t)lo + max(__ldg(cnt + l), 0), (int64_t)R) : min(__ldg(off + l + 1), R);
         s_lo[l] = lo;
@@ -291,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == kTmaWarp) {
         if (lane == 0) {
             int s = 0;
-            uint32_t ph = 0, loads = 0;
+            uint32_t ph = 0, filled = 0, landed = 0;
             bool ok = true;
             for (int tile = first; ok && tile < tiles; tile += step) {
                 const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
@@ -303,17 +310,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (!wait_phase(ptx::smem_addr(&st->empty[s]), ph ^ 1, abort)) { ok = false; break; }
                     const uint32_t a = ptx::smem_addr(smem + s * kStageBytes), b = a + kOperandBytes;
                     const uint32_t mine = ptx::smem_addr(&st->full[s]);
+                    const uint32_t bar = map_to(mine, 0);  // both CTAs' loads count on the first CTA's barrier
                     const int d = k * kDepth;
                     if (MODE == kWgrad) {
-                        ptx::mbar_arrive_expect_tx(mine, kStageBytes);
                         const int n = t.n0 + (int)rank * 128, r = t.lo + d;
-                        ptx::tma_load_2d(a, &maps.a, m, r, mine);
-                        ptx::tma_load_2d(a + kOperandBytes / 2, &maps.a, m + 64, r, mine);
-                        ptx::tma_load_2d(b, &maps.b[0], n, r, mine);
-                        ptx::tma_load_2d(b + kOperandBytes / 2, &maps.b[0], n + 64, r, mine);
+                        if (ragged(t, k)) {  // this CTA's tail warp comes first
+                            const uint32_t land = ptx::smem_addr(&st->land[s]);
+                            ptx::mbar_arrive_expect_tx(land, kStageBytes);
+                            ptx::tma_load_2d(a, &maps.a, m, r, land);
+                            ptx::tma_load_2d(a + kOperandBytes / 2, &maps.a, m + 64, r, land);
+                            ptx::tma_load_2d(b, &maps.b[0], n, r, land);
+                            ptx::tma_load_2d(b + kOperandBytes / 2, &maps.b[0], n + 64, r, land);
+                            landed ^= 1u << s;
+                        } else {
+                            if (rank == 0) ptx::mbar_arrive_expect_tx(mine, 2 * kStageBytes);
+                            load_2d_pair(a, &maps.a, m, r, bar);
+                            load_2d_pair(a + kOperandBytes / 2, &maps.a, m + 64, r, bar);
+                            load_2d_pair(b, &maps.b[0], n, r, bar);
+                            load_2d_pair(b + kOperandBytes / 2, &maps.b[0], n + 64, r, bar);
+                            filled ^= 1u << s;
+                        }
                     } else {
-                        // both CTAs' loads count on the first CTA's barrier
-                        const uint32_t bar = map_to(mine, 0);
                         if (rank == 0) ptx::mbar_arrive_expect_tx(mine, 2 * (kOperandBytes + (1024u << box)));
                         if (MODE == kFwd) {
                             load_3d_pair(a, &maps.a, d, m, t.l, bar);
@@ -322,79 +339,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             load_3d_pair(a + kOperandBytes / 2, &maps.a, m + 64, d, t.l, bar);
                         }
                         load_2d_pair(b, &maps.b[box], d, row, bar);
+                        filled ^= 1u << s;
                     }
-                    ++loads;
                     if (++s == stages) s = 0, ph ^= 1;
                 }
             }
-            // never leave with copies in flight: the last stages' loads must have landed (the
-            // first CTA's barriers count both CTAs' in forward and dgrad)
-            if (MODE == kWgrad || rank == 0) {
-                const int n = loads < (uint32_t)stages ? (int)loads : stages;
-                for (int i = 0; i < n; ++i) {
-                    if (--s < 0) s = stages - 1, ph ^= 1;
-                    wait_phase(ptx::smem_addr(&st->full[s]), ph, abort, false);
-                }
+            // never leave with copies in flight: every stage's last loads must have landed
+            // (`filled`, `landed`: the parity of each barrier's uses, odd after the first)
+            for (int i = 0; i < stages; ++i) {
+                if (rank == 0) wait_phase(ptx::smem_addr(&st->full[i]), (filled >> i & 1) ^ 1, abort, false);
+                if (MODE == kWgrad) wait_phase(ptx::smem_addr(&st->land[i]), (landed >> i & 1) ^ 1, abort, false);
             }
         }
     } else if (warp == kMmaWarp) {
-        int s = 0, b = 0;
-        uint32_t ph = 0, tph = 0;
-        bool ok = true;
-        for (int tile = first; ok && tile < tiles; tile += step) {
-            if (MODE != kWgrad && (rank != 0 || lane != 0)) break;
-            const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
-            if (t.steps == 0) continue;
-            const uint32_t idesc = idesc0 | (uint32_t)(t.n >> 3) << 17;
-            const uint32_t d = tmem + (uint32_t)(b * kMaxN);
-            if (rank == 0 && lane == 0) ok = wait_phase(ptx::smem_addr(&st->tempty[b]), tph ^ 1, abort);
-            if (MODE == kWgrad) ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            for (int k = 0; k < t.steps; ++k) {
-                ok = wait_phase(ptx::smem_addr(&st->full[s]), ph, abort);
-                const uint32_t a_base = ptx::smem_addr(smem + s * kStageBytes), b_base = a_base + kOperandBytes;
-                const int left = (MODE == kWgrad ? t.rows : depth) - k * kDepth;
-                const int slices = left >= kDepth ? kDepth / 16 : (left + 15) / 16;
-                if (MODE == kWgrad) {
-                    ok = __all_sync(0xffffffffu, ok);
+        if (rank == 0 && lane == 0) {
+            int s = 0, b = 0;
+            uint32_t tph = 0, filled = 0, landed = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < tiles; tile += step) {
+                const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
+                if (t.steps == 0) continue;
+                const uint32_t idesc = idesc0 | (uint32_t)(t.n >> 3) << 17;
+                const uint32_t d = tmem + (uint32_t)(b * kMaxN);
+                if (!(ok = wait_phase(ptx::smem_addr(&st->tempty[b]), tph ^ 1, abort))) break;
+                for (int k = 0; k < t.steps; ++k) {
+                    if (MODE == kWgrad && ragged(t, k)) {
+                        ok = wait_phase(ptx::smem_addr(&st->ready[s]), landed >> s & 1, abort);
+                        landed ^= 1u << s;
+                    } else {
+                        ok = wait_phase(ptx::smem_addr(&st->full[s]), filled >> s & 1, abort);
+                        filled ^= 1u << s;
+                    }
                     if (!ok) break;
-                    if (left < slices * 16) {
-                        // rows past the group's end within the last 16: zeros in all four boxes
-                        uint8_t* p = smem + s * kStageBytes;
-                        const int n = (slices * 16 - left) * 8;  // 16-byte pieces of a box
-                        for (int i = lane; i < 4 * n; i += 32)
-                            *reinterpret_cast<uint4*>(p + i / n * (kOperandBytes / 2) + left * 128 + i % n * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        ptx::fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (rank != 0)
-                            arrive_cluster(map_to(ptx::smem_addr(&st->ready[s]), 0));
-                        else
-                            ok = wait_phase(ptx::smem_addr(&st->ready[s]), ph, abort);
-                    }
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                }
-                if (!ok) break;
-                if (rank == 0 && lane == 0) {
                     ptx::tc_fence_after();
+                    const uint32_t a_base = ptx::smem_addr(smem + s * kStageBytes), b_base = a_base + kOperandBytes;
+                    const int left = (MODE == kWgrad ? t.rows : depth) - k * kDepth;
+                    const int slices = left >= kDepth ? kDepth / 16 : (left + 15) / 16;
                     for (int i = 0; i < slices; ++i)
                         mma_pair(d,
                                  MODE == kFwd ? ptx::smem_desc_sw128(a_base + 32 * i, 1024) : desc_mn(a_base + 2048 * i),
                                  MODE == kWgrad ? desc_mn(b_base + 2048 * i) : ptx::smem_desc_sw128(b_base + 32 * i, 1024),
                                  idesc, (k | i) ? 1u : 0u);
                     commit_pair(ptx::smem_addr(&st->empty[s]));
-                    if (k + 1 == t.steps) commit_pair(ptx::smem_addr(&st->tfull[b]));
+                    if (++s == stages) s = 0;
                 }
-                if (++s == stages) s = 0, ph ^= 1;
+                if (ok) commit_pair(ptx::smem_addr(&st->tfull[b]));
+                if (++b == 2) b = 0, tph ^= 1;
             }
-            if (++b == 2) b = 0, tph ^= 1;
-        }
-        // never leave with MMAs in flight
-        if (rank == 0 && lane == 0) {
+            // never leave with MMAs in flight
             commit_pair(ptx::smem_addr(&st->mma_done));
             wait_phase(ptx::smem_addr(&st->mma_done), 0, abort, false);
+        }
+    } else if (MODE == kWgrad && warp == kTailWarp) {
+        // a group's last stage: the rows past the group's end within the last 16 that the MMAs
+        // read become zeros in all four boxes of this CTA
+        int s = 0;
+        uint32_t landed = 0;
+        for (int tile = first; tile < tiles; tile += step) {
+            const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
+            if (t.steps == 0) continue;
+            s = (s + t.steps - 1) % stages;
+            if (ragged(t, t.steps - 1)) {
+                const bool ok = wait_phase(ptx::smem_addr(&st->land[s]), landed >> s & 1, abort);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                landed ^= 1u << s;
+                uint8_t* p = smem + s * kStageBytes;
+                const int left = t.rows - (t.steps - 1) * kDepth;
+                const int n = (-left & 15) * 8;  // 16-byte pieces of a box
+                for (int i = lane; i < 4 * n; i += 32)
+                    *reinterpret_cast<uint4*>(p + i / n * (kOperandBytes / 2) + left * 128 + i % n * 16) =
+                        make_uint4(0, 0, 0, 0);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(map_to(ptx::smem_addr(&st->ready[s]), 0));
+            }
+            if (++s == stages) s = 0;
         }
     } else {
         // ---------------------------------------------------------------- epilogue
@@ -533,7 +552,7 @@ int launch_grouped(const void* a, const void* b, const int32_t* off, const int32
     const int64_t most = MODE == kWgrad ? El * m_tiles * ((K + kMaxN - 1) / kMaxN)
                                         : (R / kMaxN + (R < El ? R : El)) * m_tiles;
     const int pairs = (int)(most < num_sms / 2 ? most : num_sms / 2);
-    launch_k(grouped_kernel<MODE, O>, 2 * pairs, kThreads, smem, stream, maps, off, cnt, El, (int)R, N, K,
+    launch_k(grouped_kernel<MODE, O>, 2 * pairs, threads_of<MODE>(), smem, stream, maps, off, cnt, El, (int)R, N, K,
              idesc_base(MODE, dtype), stages < kMaxStages ? stages : kMaxStages, static_cast<O*>(out));
     note_launches(1);
     return launch_status();
