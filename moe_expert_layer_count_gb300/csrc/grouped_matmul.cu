@@ -140,12 +140,22 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
         : "memory");
 }
 
-// Shared-memory descriptor of an MN-major tile with the 128-byte swizzle: boxes of 64 values
-// x `kDepth` rows of 128 bytes, boxes 8192 bytes apart (leading offset), groups of 8 rows
-// 1024 bytes apart (stride offset).
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(kOperandBytes / 2 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Shared-memory descriptor of 16 values of the reduced index (the i-th) of an operand tile with
+// the 128-byte swizzle; `addr`: its address / 16. K-major (the reduced index innermost): rows
+// of 128 bytes, groups of 8 rows 1024 bytes apart (stride offset). MN-major: boxes of 64
+// values x kDepth rows of 128 bytes, the boxes 8192 bytes apart (leading offset), groups of 8
+// rows of the reduced index 1024 bytes apart.
+template <bool kMn>
+__device__ __forceinline__ uint64_t operand(uint32_t addr, int i) {
+    const uint32_t lo = addr + (uint32_t)i * (kMn ? 2048 >> 4 : 32 >> 4) | (kMn ? kOperandBytes / 2 >> 4 : 1u) << 16;
+    constexpr uint32_t hi = 1024 >> 4 | 1u << 14 | 2u << 29;  // stride offset, version, 128-byte swizzle
+    return (uint64_t)hi << 32 | lo;
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Instruction descriptor of kind::f16 for M = 256 without N (N / 8 goes to bit 17).
@@ -234,7 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
     int32_t* s_rows = s_lo + El;
     int32_t* s_start = s_rows + El;
     volatile int* abort = &st->abort;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
     const Groups groups{s_start, s_lo, s_rows};
     const int P = MODE == kDgrad ? K : N;                 // length of the M side
@@ -352,7 +362,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             }
         }
     } else if (warp == kMmaWarp) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            // the whole warp runs the loop, so that what the MMAs take stays in uniform registers;
+            // one elected lane issues
+            const bool lead = elect_one();
+            const uint32_t base = ptx::smem_addr(smem) >> 4;
             int s = 0, b = 0;
             uint32_t tph = 0, filled = 0, landed = 0;
             bool ok = true;
@@ -361,34 +375,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 if (t.steps == 0) continue;
                 const uint32_t idesc = idesc0 | (uint32_t)(t.n >> 3) << 17;
                 const uint32_t d = tmem + (uint32_t)(b * kMaxN);
-                if (!(ok = wait_phase(ptx::smem_addr(&st->tempty[b]), tph ^ 1, abort))) break;
+                ok = __all_sync(0xffffffffu, wait_phase(ptx::smem_addr(&st->tempty[b]), tph ^ 1, abort));
+                if (!ok) break;
                 for (int k = 0; k < t.steps; ++k) {
+                    bool got;
                     if (MODE == kWgrad && ragged(t, k)) {
-                        ok = wait_phase(ptx::smem_addr(&st->ready[s]), landed >> s & 1, abort);
+                        got = wait_phase(ptx::smem_addr(&st->ready[s]), landed >> s & 1, abort);
                         landed ^= 1u << s;
                     } else {
-                        ok = wait_phase(ptx::smem_addr(&st->full[s]), filled >> s & 1, abort);
+                        got = wait_phase(ptx::smem_addr(&st->full[s]), filled >> s & 1, abort);
                         filled ^= 1u << s;
                     }
+                    ok = __all_sync(0xffffffffu, got);
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t a_base = ptx::smem_addr(smem + s * kStageBytes), b_base = a_base + kOperandBytes;
+                    const uint32_t a = base + (uint32_t)s * (kStageBytes >> 4), w = a + (kOperandBytes >> 4);
                     const int left = (MODE == kWgrad ? t.rows : depth) - k * kDepth;
-                    const int slices = left >= kDepth ? kDepth / 16 : (left + 15) / 16;
-                    for (int i = 0; i < slices; ++i)
-                        mma_pair(d,
-                                 MODE == kFwd ? ptx::smem_desc_sw128(a_base + 32 * i, 1024) : desc_mn(a_base + 2048 * i),
-                                 MODE == kWgrad ? desc_mn(b_base + 2048 * i) : ptx::smem_desc_sw128(b_base + 32 * i, 1024),
-                                 idesc, (k | i) ? 1u : 0u);
-                    commit_pair(ptx::smem_addr(&st->empty[s]));
+                    if (left > kDepth - 16) {
+                        if (lead) {
+#pragma unroll
+                            for (int i = 0; i < kDepth / 16; ++i)
+                                mma_pair(d, operand<MODE != kFwd>(a, i), operand<MODE == kWgrad>(w, i), idesc,
+                                         i > 0 || k > 0 ? 1u : 0u);
+                            commit_pair(ptx::smem_addr(&st->empty[s]));
+                        }
+                    } else if (lead) {
+                        for (int i = 0; i * 16 < left; ++i)
+                            mma_pair(d, operand<MODE != kFwd>(a, i), operand<MODE == kWgrad>(w, i), idesc, (i | k) ? 1u : 0u);
+                        commit_pair(ptx::smem_addr(&st->empty[s]));
+                    }
                     if (++s == stages) s = 0;
                 }
-                if (ok) commit_pair(ptx::smem_addr(&st->tfull[b]));
+                if (ok && lead) commit_pair(ptx::smem_addr(&st->tfull[b]));
                 if (++b == 2) b = 0, tph ^= 1;
             }
             // never leave with MMAs in flight
-            commit_pair(ptx::smem_addr(&st->mma_done));
-            wait_phase(ptx::smem_addr(&st->mma_done), 0, abort, false);
+            if (lead) {
+                commit_pair(ptx::smem_addr(&st->mma_done));
+                wait_phase(ptx::smem_addr(&st->mma_done), 0, abort, false);
+            }
         }
     } else if (MODE == kWgrad && warp == kTailWarp) {
         // a group's last stage: the rows past the group's end within the last 16 that the MMAs
