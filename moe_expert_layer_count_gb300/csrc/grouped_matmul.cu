@@ -47,7 +47,8 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kTailWarp = 6;
 constexpr int kBoxBytes = 4096;    // wgrad output box: 32 rows x 128 bytes
-constexpr int kStagingBytes = kEpiWarps * 2 * kBoxBytes;
+constexpr int kBoxes = 4;          // boxes of a warp in turn
+constexpr int kStagingBytes = kEpiWarps * kBoxes * kBoxBytes;
 constexpr int kSmemLimit = 232448;
 constexpr int kRowBoxes = 5;       // boxes of 8, 16, 32, 64, 128 rows
 template <int MODE>
@@ -150,6 +151,53 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, int i) {
     const uint32_t lo = addr + (uint32_t)i * (kMn ? 2048 >> 4 : 32 >> 4) | (kMn ? kOperandBytes / 2 >> 4 : 1u) << 16;
     constexpr uint32_t hi = 1024 >> 4 | 1u << 14 | 2u << 29;  // stride offset, version, 128-byte swizzle
     return (uint64_t)hi << 32 | lo;
+}
+
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// TMEM columns [t, t + N) of this warp's 32 lanes: thread i gets lane i.
+__device__ __forceinline__ void load_columns(uint32_t t, uint32_t (&r)[32]) { ptx::tmem_ld_32x32b_x32(t, r); }
+__device__ __forceinline__ void load_columns(uint32_t t, uint32_t (&r)[64]) {
+    ptx::tmem_ld_32x32b_x32(t, *reinterpret_cast<uint32_t(*)[32]>(r));
+    ptx::tmem_ld_32x32b_x32(t + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+}
+__device__ __forceinline__ void wait_columns(uint32_t (&r)[32]) { ptx::tmem_wait_ld_regs32(r); }
+__device__ __forceinline__ void wait_columns(uint32_t (&r)[64]) {
+    ptx::tmem_wait_ld_regs32(*reinterpret_cast<uint32_t(*)[32]>(r));
+    ptx::tmem_wait_ld_regs32(*reinterpret_cast<uint32_t(*)[32]>(r + 32));
+}
+// 16 lanes x 32 columns as 8 x 8 fragments: registers 4i .. 4i + 3 of thread T hold columns
+// 8i + 2 (T % 4) and the next of lane T / 4, then of lane T / 4 + 8.
+__device__ __forceinline__ void load_fragments16(uint32_t t, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+}
+// The warp's 32 lanes x 32 columns: lanes 0-15 in r[0..15], lanes 16-31 in r[16..31].
+__device__ __forceinline__ void load_fragments(uint32_t t, uint32_t (&r)[32]) {
+    load_fragments16(t, r);
+    load_fragments16(t + (16u << 16), r + 16);
+}
+// Four 8 x 8 fragments of 16-bit values, transposed; lane i addresses row i % 8 of fragment i / 8.
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+// Two fp32 rounded to O, the first in the low half.
+template <typename O>
+__device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) {
+    Vec<O, 2> v;
+    v.v[0] = from_f32<O>(__uint_as_float(lo));
+    v.v[1] = from_f32<O>(__uint_as_float(hi));
+    return *reinterpret_cast<uint32_t*>(&v);
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -455,30 +503,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 ptx::tc_fence_after();
             }
             const uint32_t acc = tmem + slab + (uint32_t)(b * kMaxN);
+            // the accumulator is free for the MMAs once this warp has read its last columns
+            auto release = [&] {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(map_to(ptx::smem_addr(&st->tempty[b]), 0));
+            };
             if constexpr (MODE == kWgrad) {
                 constexpr int kCols = 128 / sizeof(O);  // columns of a 128-byte-wide box
-                for (int c = 0; c < kMaxN && t.n0 + c < K; c += kCols) {
-                    float v[kCols];
-#pragma unroll
-                    for (int h = 0; h < kCols; h += 32) {
-                        uint32_t r[32];
-                        if (t.steps > 0) {
-                            ptx::tmem_ld_32x32b_x32(acc + c + h, r);
-                            ptx::tmem_wait_ld_regs32(r);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[h + j] = t.steps > 0 ? __uint_as_float(r[j]) : 0.f;
-                    }
-                    // 32 rows x 128 bytes in TMA's 128-byte swizzle, two boxes in turn
-                    uint8_t* box = staging + (warp * 2 + (boxes & 1)) * kBoxBytes;
-                    ++boxes;
-                    if (lane == 0) ptx::bulk_wait_read1();
+                const int cols = min(kMaxN, K - t.n0);
+                // 32 rows x 128 bytes in TMA's 128-byte swizzle, kBoxes boxes in turn
+                auto put = [&](const uint32_t (&v)[kCols], int c) {
+                    uint8_t* box = staging + (warp * kBoxes + boxes) * kBoxBytes;
+                    if (++boxes == kBoxes) boxes = 0;
+                    if (lane == 0) bulk_wait_read<kBoxes - 1>();
                     __syncwarp();
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         Vec<O, 16 / sizeof(O)> w;
 #pragma unroll
-                        for (int j = 0; j < 16 / (int)sizeof(O); ++j) w.v[j] = from_f32<O>(v[q * (16 / sizeof(O)) + j]);
+                        for (int j = 0; j < 16 / (int)sizeof(O); ++j)
+                            w.v[j] = from_f32<O>(__uint_as_float(v[q * (16 / sizeof(O)) + j]));
                         *reinterpret_cast<Vec<O, 16 / sizeof(O)>*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
                     }
                     ptx::fence_proxy_async_smem();
@@ -487,26 +532,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                         if (m < P) store_3d(&maps.o, ptx::smem_addr(box), t.n0 + c, m, t.l);
                         ptx::bulk_commit();
                     }
+                };
+                uint32_t u[kCols], v[kCols];
+                if (t.steps == 0) {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) u[j] = 0;
+                    for (int c = 0; c < cols; c += kCols) put(u, c);
+                } else {
+                    // the next box's columns are on their way while this one's are stored
+                    auto step_box = [&](uint32_t (&now)[kCols], uint32_t (&next)[kCols], int c) {
+                        wait_columns(now);
+                        if (c + kCols < cols)
+                            load_columns(acc + c + kCols, next);
+                        else
+                            release();
+                        put(now, c);
+                    };
+                    load_columns(acc, u);
+                    for (int c = 0; c < cols; c += 2 * kCols) {
+                        step_box(u, v, c);
+                        if (c + kCols < cols) step_box(v, u, c + kCols);
+                    }
                 }
-            } else {
+            } else if constexpr (sizeof(O) == 4) {
+                // lane = output column: 128 bytes of one row per store
                 const bool in = m + lane < P;
                 O* o = out + (int64_t)t.lo * P + m + lane;
-                for (int c = 0; c < t.rows; c += 32) {
-                    uint32_t r[32];
+                uint32_t u[32], v[32];
+                auto step_rows = [&](uint32_t (&now)[32], uint32_t (&next)[32], int c) {
                     __syncwarp();
-                    ptx::tmem_ld_32x32b_x32(acc + c, r);
-                    ptx::tmem_wait_ld_regs32(r);
+                    wait_columns(now);
+                    if (c + 32 < t.rows)
+                        load_columns(acc + c + 32, next);
+                    else
+                        release();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (in && c + j < t.rows) o[(int64_t)(c + j) * P] = from_f32<O>(__uint_as_float(r[j]));
+                        if (in && c + j < t.rows) o[(int64_t)(c + j) * P] = __uint_as_float(now[j]);
+                };
+                load_columns(acc, u);
+                for (int c = 0; c < t.rows; c += 64) {
+                    step_rows(u, v, c);
+                    if (c + 32 < t.rows) step_rows(v, u, c + 32);
                 }
-            }
-            if (t.steps > 0) {
-                ptx::tc_fence_before();
+            } else {
+                // 32 rows of the result x this warp's 32 outputs at a time: read as 8 x 8 fragments,
+                // transposed into shared memory (64 bytes a row, 16-byte pieces swizzled so that
+                // neither side has bank conflicts), stored as 64-byte pieces of rows
+                uint8_t* stage = staging + warp * kBoxes * kBoxBytes;
+                const int piece = lane & 3;
+                const bool in = m + piece * 8 < P;
+                O* o = out + ((int64_t)t.lo + (lane >> 2)) * P + m + piece * 8;
+                const uint32_t put_at = (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
+                const uint32_t get_at = (uint32_t)((lane >> 2) * 64 + ((piece ^ ((lane >> 3) & 3)) << 4));
+                uint32_t u[32], v[32];
+                auto step_rows = [&](uint32_t (&now)[32], uint32_t (&next)[32], int c) {
+                    __syncwarp();
+                    wait_columns(now);
+                    if (c + 32 < t.rows)
+                        load_fragments(acc + c + 32, next);
+                    else
+                        release();
+                    uint8_t* buf = stage + (c & 32) * 64;
+                    const uint32_t to = ptx::smem_addr(buf) + put_at;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        store_transposed(to + i * 512, pack2<O>(now[4 * i], now[4 * i + 1]),
+                                         pack2<O>(now[4 * i + 2], now[4 * i + 3]), pack2<O>(now[16 + 4 * i], now[16 + 4 * i + 1]),
+                                         pack2<O>(now[16 + 4 * i + 2], now[16 + 4 * i + 3]));
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(buf + get_at + i * 512);
+                        if (in && c + i * 8 + (lane >> 2) < t.rows) *reinterpret_cast<uint4*>(o + (int64_t)(c + i * 8) * P) = w;
+                    }
+                };
+                load_fragments(acc, u);
+                for (int c = 0; c < t.rows; c += 64) {
+                    step_rows(u, v, c);
+                    if (c + 32 < t.rows) step_rows(v, u, c + 32);
+                }
                 __syncwarp();
-                if (lane == 0) arrive_cluster(map_to(ptx::smem_addr(&st->tempty[b]), 0));
-                if (++b == 2) b = 0, tph ^= 1;
             }
+            if (t.steps > 0)
+                if (++b == 2) b = 0, tph ^= 1;
         }
         if (MODE == kWgrad && lane == 0) ptx::bulk_wait0();
     }
