@@ -48,7 +48,9 @@ constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kTailWarp = 6;
 constexpr int kBoxBytes = 4096;    // wgrad output box: 32 rows x 128 bytes
 constexpr int kBoxes = 4;          // boxes of a warp in turn
-constexpr int kStagingBytes = kEpiWarps * kBoxes * kBoxBytes;
+// forward and dgrad stage two 32-row x 64-byte buffers per warp
+template <int MODE>
+__host__ __device__ constexpr int staging_bytes() { return kEpiWarps * kBoxBytes * (MODE == kWgrad ? kBoxes : 1); }
 constexpr int kSmemLimit = 232448;
 constexpr int kRowBoxes = 5;       // boxes of 8, 16, 32, 64, 128 rows
 template <int MODE>
@@ -72,9 +74,13 @@ struct __align__(8) Tail {
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
+    int tiles;
 };
 
-size_t fixed_smem(int El) { return 1024 + kStagingBytes + sizeof(Tail) + 16 + (size_t)(3 * El + 1) * sizeof(int32_t); }
+// Shared memory without the stages: alignment, staging, the groups, barriers.
+template <int MODE>
+size_t fixed_smem(int El) { return 1024 + staging_bytes<MODE>() + sizeof(Tail) + (size_t)El * 16; }
+
 
 // ------------------------------------------------------------------ PTX of the CTA pair
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -92,7 +98,7 @@ __device__ __forceinline__ uint32_t map_to(uint32_t a, uint32_t rank) {
     return r;
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Tile loads whose completion may count on the barrier of the pair's other CTA.
 __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
@@ -230,10 +236,28 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 }
 
 // ------------------------------------------------------------------ tiles
-struct Groups {
-    const int32_t* start;  // first tile of each group (forward, dgrad), El + 1
-    const int32_t* lo;     // first row
-    const int32_t* rows;   // row count
+// A group of rows: its first row, its row count and, forward and dgrad, its first tile and the
+// rows of each of its tiles (equal parts of at most 256, whole 16s).
+struct __align__(16) Group {
+    int start, lo, rows, per;
+};
+
+// i / d for 0 <= i < 2^31 by a multiplication; magic_of(d) = floor(2^32 / d) + 1 overshoots by
+// less than one.
+uint32_t magic_of(int64_t d) { return d == 1 ? 0 : (uint32_t)((1ull << 32) / (uint64_t)d + 1); }
+struct Divisor {
+    int d;
+    uint32_t magic;
+    __device__ __forceinline__ int of(int i) const {
+        if (d == 1) return i;
+        const int q = (int)__umulhi((uint32_t)i, magic);
+        return q * (int64_t)d > i ? q - 1 : q;
+    }
+};
+struct Shape {
+    Divisor m_tiles;      // tiles along the M side
+    Divisor group_tiles;  // wgrad: tiles of a group
+    int depth;            // forward, dgrad: the reduced length
 };
 
 // Where a tile lies. forward, dgrad: outputs [m0, m0 + 256) x rows [lo, lo + rows) of group
@@ -243,35 +267,38 @@ struct Tile {
     int l, lo, rows, m0, n0, n, steps;
 };
 
+// All lanes of a warp call it together (forward and dgrad look the group up with two votes).
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(int tile, const Groups& g, int El, int m_tiles, int n_tiles, int depth) {
+__device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, const Shape& sh) {
     Tile t;
     if (MODE == kWgrad) {
-        t.l = tile / (m_tiles * n_tiles);
-        const int i = tile - t.l * m_tiles * n_tiles;
-        t.m0 = i % m_tiles * kPairM;
-        t.n0 = i / m_tiles * kMaxN;
+        t.l = sh.group_tiles.of(tile);
+        const int i = tile - t.l * sh.group_tiles.d;
+        const int p = sh.m_tiles.of(i);
+        const Group g = groups[t.l];
+        t.m0 = (i - p * sh.m_tiles.d) * kPairM;
+        t.n0 = p * kMaxN;
         t.n = kMaxN;
-        t.lo = g.lo[t.l];
-        t.rows = g.rows[t.l];
+        t.lo = g.lo;
+        t.rows = g.rows;
         t.steps = (t.rows + kDepth - 1) / kDepth;
     } else {
-        int a = 0, b = El - 1;
-        while (a < b) {
-            const int mid = (a + b + 1) >> 1;
-            if (g.start[mid] <= tile) a = mid; else b = mid - 1;
-        }
-        t.l = a;
-        const int i = tile - g.start[a], count = g.rows[a];
-        const int parts = (count + kMaxN - 1) / kMaxN;          // equal parts of the group, whole 16s
-        const int per = ((count + parts - 1) / parts + 15) & ~15;
-        const int p = i / m_tiles;
-        t.m0 = (i - p * m_tiles) * kPairM;
-        t.lo = g.lo[a] + p * per;
-        t.rows = min(per, count - p * per);
+        // the last group whose first tile is not past this one (an empty group starts where
+        // the next one does): the block of `stride` groups, then the group
+        const int lane = threadIdx.x & 31, stride = (El + 31) >> 5;
+        int l = lane * stride;
+        l = __popc(__ballot_sync(0xffffffffu, l < El && groups[l].start <= tile)) * stride - stride;
+        l += __popc(__ballot_sync(0xffffffffu, lane < stride && l + lane < El && groups[l + lane].start <= tile)) - 1;
+        t.l = l;
+        const Group g = groups[l];
+        const int i = tile - g.start;
+        const int p = sh.m_tiles.of(i);
+        t.m0 = (i - p * sh.m_tiles.d) * kPairM;
+        t.lo = g.lo + p * g.per;
+        t.rows = min(g.per, g.rows - p * g.per);
         t.n = (t.rows + 15) & ~15;
         t.n0 = 0;
-        t.steps = (depth + kDepth - 1) / kDepth;
+        t.steps = (sh.depth + kDepth - 1) / kDepth;
     }
     return t;
 }
@@ -283,22 +310,16 @@ __device__ __forceinline__ bool ragged(const Tile& t, int k) { return k + 1 == t
 template <int MODE, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 1)
     grouped_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ off, const int32_t* __restrict__ cnt,
-                   int El, int R, int N, int K, uint32_t idesc0, int stages, O* __restrict__ out) {
+                   int El, int R, int N, int K, Shape sh, uint32_t idesc0, int stages, O* __restrict__ out) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* staging = smem + stages * kStageBytes;
-    Tail* st = reinterpret_cast<Tail*>(staging + kStagingBytes);
-    int32_t* s_lo = reinterpret_cast<int32_t*>(st + 1);
-    int32_t* s_rows = s_lo + El;
-    int32_t* s_start = s_rows + El;
+    Group* groups = reinterpret_cast<Group*>(staging + staging_bytes<MODE>());
+    Tail* st = reinterpret_cast<Tail*>(groups + El);
     volatile int* abort = &st->abort;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
-    const Groups groups{s_start, s_lo, s_rows};
-    const int P = MODE == kDgrad ? K : N;                 // length of the M side
-    const int depth = MODE == kDgrad ? N : K;             // reduced index (forward, dgrad)
-    const int m_tiles = (P + kPairM - 1) / kPairM;
-    const int n_tiles = (K + kMaxN - 1) / kMaxN;          // wgrad
+    const int P = MODE == kDgrad ? K : N;  // length of the M side
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
@@ -322,92 +343,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
     }
     pdl_wait();
     pdl_trigger();
-    // the groups' rows, never outside [0, R), and the prefix sums of their tiles
+    // the groups' rows, never outside [0, R), their tiles and the tiles' prefix sums
     for (int l = threadIdx.x; l < El; l += threads_of<MODE>()) {
         const int lo = min(max(__ldg(off + l), 0), R);
         const int end = cnt ? (int)min((int64_t)lo + max(__ldg(cnt + l), 0), (int64_t)R) : min(__ldg(off + l + 1), R);
-        s_lo[l] = lo;
-        s_rows[l] = max(end - lo, 0);
+        const int rows = max(end - lo, 0);
+        const int parts = max((rows + kMaxN - 1) / kMaxN, 1);
+        groups[l] = Group{(rows + kMaxN - 1) / kMaxN * sh.m_tiles.d, lo, rows, ((rows + parts - 1) / parts + 15) & ~15};
     }
     __syncthreads();
     if (MODE != kWgrad && warp == 0) {
         int base = 0;
         for (int l0 = 0; l0 < El; l0 += 32) {
             const int l = l0 + lane;
-            const int mine = l < El ? (s_rows[l] + kMaxN - 1) / kMaxN * m_tiles : 0;
+            const int mine = l < El ? groups[l].start : 0;
             int sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += v;
             }
-            if (l < El) s_start[l] = base + sum - mine;
+            if (l < El) groups[l].start = base + sum - mine;
             base += __shfl_sync(0xffffffffu, sum, 31);
         }
-        if (lane == 0) s_start[El] = base;
+        if (lane == 0) st->tiles = base;
     }
     __syncthreads();
     cluster_sync();  // barriers and TMEM of both CTAs are in place
     ptx::tc_fence_after();
     const uint32_t tmem = st->tmem_base;
-    const int tiles = MODE == kWgrad ? El * m_tiles * n_tiles : s_start[El];
+    const int tiles = MODE == kWgrad ? El * sh.group_tiles.d : st->tiles;
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
     if (warp == kTmaWarp) {
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0, filled = 0, landed = 0;
-            bool ok = true;
-            for (int tile = first; ok && tile < tiles; tile += step) {
-                const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
-                int box = 0;  // the smallest box that holds this CTA's half of the columns
-                while (MODE != kWgrad && (8 << box) < t.n / 2) ++box;
-                const int row = t.lo + (int)rank * (t.n / 2);
-                const int m = t.m0 + (int)rank * 128;
-                for (int k = 0; k < t.steps; ++k) {
-                    if (!wait_phase(ptx::smem_addr(&st->empty[s]), ph ^ 1, abort)) { ok = false; break; }
-                    const uint32_t a = ptx::smem_addr(smem + s * kStageBytes), b = a + kOperandBytes;
-                    const uint32_t mine = ptx::smem_addr(&st->full[s]);
-                    const uint32_t bar = map_to(mine, 0);  // both CTAs' loads count on the first CTA's barrier
-                    const int d = k * kDepth;
-                    if (MODE == kWgrad) {
-                        const int n = t.n0 + (int)rank * 128, r = t.lo + d;
-                        if (ragged(t, k)) {  // this CTA's tail warp comes first
-                            const uint32_t land = ptx::smem_addr(&st->land[s]);
-                            ptx::mbar_arrive_expect_tx(land, kStageBytes);
-                            ptx::tma_load_2d(a, &maps.a, m, r, land);
-                            ptx::tma_load_2d(a + kOperandBytes / 2, &maps.a, m + 64, r, land);
-                            ptx::tma_load_2d(b, &maps.b[0], n, r, land);
-                            ptx::tma_load_2d(b + kOperandBytes / 2, &maps.b[0], n + 64, r, land);
-                            landed ^= 1u << s;
-                        } else {
-                            if (rank == 0) ptx::mbar_arrive_expect_tx(mine, 2 * kStageBytes);
-                            load_2d_pair(a, &maps.a, m, r, bar);
-                            load_2d_pair(a + kOperandBytes / 2, &maps.a, m + 64, r, bar);
-                            load_2d_pair(b, &maps.b[0], n, r, bar);
-                            load_2d_pair(b + kOperandBytes / 2, &maps.b[0], n + 64, r, bar);
-                            filled ^= 1u << s;
-                        }
-                    } else {
-                        if (rank == 0) ptx::mbar_arrive_expect_tx(mine, 2 * (kOperandBytes + (1024u << box)));
-                        if (MODE == kFwd) {
-                            load_3d_pair(a, &maps.a, d, m, t.l, bar);
-                        } else {
-                            load_3d_pair(a, &maps.a, m, d, t.l, bar);
-                            load_3d_pair(a + kOperandBytes / 2, &maps.a, m + 64, d, t.l, bar);
-                        }
-                        load_2d_pair(b, &maps.b[box], d, row, bar);
-                        filled ^= 1u << s;
+        const bool lead = elect_one();
+        const uint32_t pair_full = map_to(ptx::smem_addr(&st->full[0]), 0);  // both CTAs' loads count on the first's
+        int s = 0;
+        uint32_t ph = 0, filled = 0, landed = 0;
+        bool ok = true;
+        for (int tile = first; ok && tile < tiles; tile += step) {
+            const Tile t = tile_at<MODE>(tile, groups, El, sh);
+            int box = 0;  // the smallest box that holds this CTA's half of the columns
+            while (MODE != kWgrad && (8 << box) < t.n / 2) ++box;
+            const int row = t.lo + (int)rank * (t.n / 2);
+            const int m = t.m0 + (int)rank * 128, n = t.n0 + (int)rank * 128;
+            for (int k = 0; k < t.steps; ++k) {
+                ok = __all_sync(0xffffffffu, wait_phase(ptx::smem_addr(&st->empty[s]), ph ^ 1, abort));
+                if (!ok) break;
+                const uint32_t a = ptx::smem_addr(smem + s * kStageBytes), b = a + kOperandBytes;
+                const uint32_t full = ptx::smem_addr(&st->full[s]), bar = pair_full + 8 * s;
+                const int d = k * kDepth;
+                if (MODE == kWgrad && ragged(t, k)) {  // this CTA's tail warp comes first
+                    if (lead) {
+                        const uint32_t land = ptx::smem_addr(&st->land[s]);
+                        ptx::mbar_arrive_expect_tx(land, kStageBytes);
+                        ptx::tma_load_2d(a, &maps.a, m, t.lo + d, land);
+                        ptx::tma_load_2d(a + kOperandBytes / 2, &maps.a, m + 64, t.lo + d, land);
+                        ptx::tma_load_2d(b, &maps.b[0], n, t.lo + d, land);
+                        ptx::tma_load_2d(b + kOperandBytes / 2, &maps.b[0], n + 64, t.lo + d, land);
                     }
-                    if (++s == stages) s = 0, ph ^= 1;
+                    landed ^= 1u << s;
+                } else {
+                    if (lead) {
+                        if (rank == 0)
+                            ptx::mbar_arrive_expect_tx(full, MODE == kWgrad ? 2 * kStageBytes : 2 * (kOperandBytes + (1024u << box)));
+                        if (MODE == kWgrad) {
+                            load_2d_pair(a, &maps.a, m, t.lo + d, bar);
+                            load_2d_pair(a + kOperandBytes / 2, &maps.a, m + 64, t.lo + d, bar);
+                            load_2d_pair(b, &maps.b[0], n, t.lo + d, bar);
+                            load_2d_pair(b + kOperandBytes / 2, &maps.b[0], n + 64, t.lo + d, bar);
+                        } else {
+                            if (MODE == kFwd) {
+                                load_3d_pair(a, &maps.a, d, m, t.l, bar);
+                            } else {
+                                load_3d_pair(a, &maps.a, m, d, t.l, bar);
+                                load_3d_pair(a + kOperandBytes / 2, &maps.a, m + 64, d, t.l, bar);
+                            }
+                            load_2d_pair(b, &maps.b[box], d, row, bar);
+                        }
+                    }
+                    filled ^= 1u << s;
                 }
+                if (++s == stages) s = 0, ph ^= 1;
             }
-            // never leave with copies in flight: every stage's last loads must have landed
-            // (`filled`, `landed`: the parity of each barrier's uses, odd after the first)
-            for (int i = 0; i < stages; ++i) {
-                if (rank == 0) wait_phase(ptx::smem_addr(&st->full[i]), (filled >> i & 1) ^ 1, abort, false);
-                if (MODE == kWgrad) wait_phase(ptx::smem_addr(&st->land[i]), (landed >> i & 1) ^ 1, abort, false);
-            }
+        }
+        // never leave with copies in flight: every stage's last loads must have landed
+        // (`filled`, `landed`: the parity of each barrier's uses, odd after the first)
+        for (int i = 0; i < stages; ++i) {
+            if (rank == 0) wait_phase(ptx::smem_addr(&st->full[i]), (filled >> i & 1) ^ 1, abort, false);
+            if (MODE == kWgrad) wait_phase(ptx::smem_addr(&st->land[i]), (landed >> i & 1) ^ 1, abort, false);
         }
     } else if (warp == kMmaWarp) {
         if (rank == 0) {
@@ -419,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             uint32_t tph = 0, filled = 0, landed = 0;
             bool ok = true;
             for (int tile = first; ok && tile < tiles; tile += step) {
-                const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
+                const Tile t = tile_at<MODE>(tile, groups, El, sh);
                 if (t.steps == 0) continue;
                 const uint32_t idesc = idesc0 | (uint32_t)(t.n >> 3) << 17;
                 const uint32_t d = tmem + (uint32_t)(b * kMaxN);
@@ -438,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint32_t a = base + (uint32_t)s * (kStageBytes >> 4), w = a + (kOperandBytes >> 4);
-                    const int left = (MODE == kWgrad ? t.rows : depth) - k * kDepth;
+                    const int left = (MODE == kWgrad ? t.rows : sh.depth) - k * kDepth;
                     if (left > kDepth - 16) {
                         if (lead) {
 #pragma unroll
@@ -469,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         int s = 0;
         uint32_t landed = 0;
         for (int tile = first; tile < tiles; tile += step) {
-            const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
+            const Tile t = tile_at<MODE>(tile, groups, El, sh);
             if (t.steps == 0) continue;
             s = (s + t.steps - 1) % stages;
             if (ragged(t, t.steps - 1)) {
@@ -494,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         uint32_t tph = 0;
         const uint32_t slab = (uint32_t)(warp * 32) << 16;
         for (int tile = first; tile < tiles; tile += step) {
-            const Tile t = tile_at<MODE>(tile, groups, El, m_tiles, n_tiles, depth);
+            const Tile t = tile_at<MODE>(tile, groups, El, sh);
             const int m = t.m0 + (int)rank * 128 + warp * 32;  // this warp's first row of the tile
             if (t.steps > 0) {
                 bool ok = wait_phase(ptx::smem_addr(&st->tfull[b]), tph, abort);
@@ -579,7 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 // 32 rows of the result x this warp's 32 outputs at a time: read as 8 x 8 fragments,
                 // transposed into shared memory (64 bytes a row, 16-byte pieces swizzled so that
                 // neither side has bank conflicts), stored as 64-byte pieces of rows
-                uint8_t* stage = staging + warp * kBoxes * kBoxBytes;
+                uint8_t* stage = staging + warp * kBoxBytes;
                 const int piece = lane & 3;
                 const bool in = m + piece * 8 < P;
                 O* o = out + ((int64_t)t.lo + (lane >> 2)) * P + m + piece * 8;
@@ -679,15 +703,17 @@ int launch_grouped(const void* a, const void* b, const int32_t* off, const int32
             return MOE_ERR_CUDA;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    const int stages = (int)((kSmemLimit - fixed_smem(El)) / kStageBytes);
-    const size_t smem = fixed_smem(El) + (size_t)(stages < kMaxStages ? stages : kMaxStages) * kStageBytes;
-    // no more pairs than tiles (an upper bound: the groups' sizes are not known here)
+    int stages = (int)((kSmemLimit - fixed_smem<MODE>(El)) / kStageBytes);
+    if (stages > kMaxStages) stages = kMaxStages;
+    const size_t smem = fixed_smem<MODE>(El) + (size_t)stages * kStageBytes;
     const int64_t m_tiles = ((MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;
-    const int64_t most = MODE == kWgrad ? El * m_tiles * ((K + kMaxN - 1) / kMaxN)
-                                        : (R / kMaxN + (R < El ? R : El)) * m_tiles;
+    const int64_t group_tiles = m_tiles * ((K + kMaxN - 1) / kMaxN);
+    const Shape sh{{(int)m_tiles, magic_of(m_tiles)}, {(int)group_tiles, magic_of(group_tiles)}, MODE == kDgrad ? N : K};
+    // no more pairs than tiles (an upper bound: the groups' sizes are not known here)
+    const int64_t most = MODE == kWgrad ? El * group_tiles : (R / kMaxN + (R < El ? R : El)) * m_tiles;
     const int pairs = (int)(most < num_sms / 2 ? most : num_sms / 2);
     launch_k(grouped_kernel<MODE, O>, 2 * pairs, threads_of<MODE>(), smem, stream, maps, off, cnt, El, (int)R, N, K,
-             idesc_base(MODE, dtype), stages < kMaxStages ? stages : kMaxStages, static_cast<O*>(out));
+             sh, idesc_base(MODE, dtype), stages, static_cast<O*>(out));
     note_launches(1);
     return launch_status();
 }
