@@ -47,7 +47,7 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kTailWarp = 6;
 constexpr int kBoxBytes = 4096;    // wgrad output box: 32 rows x 128 bytes
-constexpr int kBoxes = 4;          // boxes of a warp in turn
+constexpr int kBoxes = 2;          // boxes of a warp in turn (four would cost two stages: 302 against 289 us)
 // forward and dgrad stage two 32-row x 64-byte buffers per warp
 template <int MODE>
 __host__ __device__ constexpr int staging_bytes() { return kEpiWarps * kBoxBytes * (MODE == kWgrad ? kBoxes : 1); }
@@ -55,6 +55,7 @@ constexpr int kSmemLimit = 232448;
 constexpr int kRowBoxes = 5;       // boxes of 8, 16, 32, 64, 128 rows
 template <int MODE>
 __host__ __device__ constexpr int threads_of() { return MODE == kWgrad ? 224 : 192; }  // the tail warp is wgrad's
+constexpr int kBuckets = 128;      // steps of cost that the groups are sorted by
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -75,6 +76,7 @@ struct __align__(8) Tail {
     uint32_t tmem_base;
     int abort;
     int tiles;
+    int bucket[kBuckets];
 };
 
 // Shared memory without the stages: alignment, staging, the groups, barriers.
@@ -236,11 +238,17 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 }
 
 // ------------------------------------------------------------------ tiles
-// A group of rows: its first row, its row count and, forward and dgrad, its first tile and the
-// rows of each of its tiles (equal parts of at most 256, whole 16s).
+// A group of rows: its first row, its row count, its number (low 16 bits of `id`) and, forward
+// and dgrad, its first tile and the rows of each of its tiles (high 16 bits of `id`; equal
+// parts of at most 256, whole 16s). wgrad has the groups in falling order of rows.
 struct __align__(16) Group {
-    int start, lo, rows, per;
+    int start, lo, rows;
+    uint32_t id;
 };
+// wgrad: the bucket of a group of so many rows, four buckets an octave, the largest first.
+__device__ __forceinline__ int bucket_of(int rows) {
+    return kBuckets - 1 - ((int)(__float_as_uint((float)rows + 1.f) >> 21) - 508);
+}
 
 // i / d for 0 <= i < 2^31 by a multiplication; magic_of(d) = floor(2^32 / d) + 1 overshoots by
 // less than one.
@@ -272,10 +280,11 @@ template <int MODE>
 __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, const Shape& sh) {
     Tile t;
     if (MODE == kWgrad) {
-        t.l = sh.group_tiles.of(tile);
-        const int i = tile - t.l * sh.group_tiles.d;
+        const int at = sh.group_tiles.of(tile);
+        const int i = tile - at * sh.group_tiles.d;
         const int p = sh.m_tiles.of(i);
-        const Group g = groups[t.l];
+        const Group g = groups[at];
+        t.l = g.id & 0xffff;
         t.m0 = (i - p * sh.m_tiles.d) * kPairM;
         t.n0 = p * kMaxN;
         t.n = kMaxN;
@@ -289,13 +298,13 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, c
         int l = lane * stride;
         l = __popc(__ballot_sync(0xffffffffu, l < El && groups[l].start <= tile)) * stride - stride;
         l += __popc(__ballot_sync(0xffffffffu, lane < stride && l + lane < El && groups[l + lane].start <= tile)) - 1;
-        t.l = l;
         const Group g = groups[l];
-        const int i = tile - g.start;
+        const int i = tile - g.start, per = g.id >> 16;
         const int p = sh.m_tiles.of(i);
+        t.l = g.id & 0xffff;
         t.m0 = (i - p * sh.m_tiles.d) * kPairM;
-        t.lo = g.lo + p * g.per;
-        t.rows = min(g.per, g.rows - p * g.per);
+        t.lo = g.lo + p * per;
+        t.rows = min(per, g.rows - p * per);
         t.n = (t.rows + 15) & ~15;
         t.n0 = 0;
         t.steps = (sh.depth + kDepth - 1) / kDepth;
@@ -306,6 +315,15 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, c
 // wgrad: whether stage k of a tile ends between two multiples of 16 rows, so that the MMAs
 // would read rows past the group's end.
 __device__ __forceinline__ bool ragged(const Tile& t, int k) { return k + 1 == t.steps && (t.rows & 15) != 0; }
+
+__device__ __forceinline__ int warp_prefix(int v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)(threadIdx.x & 31) >= o) v += w;
+    }
+    return v;
+}
 
 template <int MODE, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 1)
@@ -343,37 +361,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
     }
     pdl_wait();
     pdl_trigger();
-    // the groups' rows, never outside [0, R), their tiles and the tiles' prefix sums
+    // the groups' rows, never outside [0, R)
+    Group* unsorted = MODE == kWgrad ? reinterpret_cast<Group*>(smem) : groups;  // in the still unused stages
+    if (MODE == kWgrad) {
+        for (int i = threadIdx.x; i < kBuckets; i += threads_of<MODE>()) st->bucket[i] = 0;
+        __syncthreads();
+    }
     for (int l = threadIdx.x; l < El; l += threads_of<MODE>()) {
         const int lo = min(max(__ldg(off + l), 0), R);
         const int end = cnt ? (int)min((int64_t)lo + max(__ldg(cnt + l), 0), (int64_t)R) : min(__ldg(off + l + 1), R);
         const int rows = max(end - lo, 0);
         const int parts = max((rows + kMaxN - 1) / kMaxN, 1);
-        groups[l] = Group{(rows + kMaxN - 1) / kMaxN * sh.m_tiles.d, lo, rows, ((rows + parts - 1) / parts + 15) & ~15};
+        const int per = ((rows + parts - 1) / parts + 15) & ~15;
+        const int b = MODE == kWgrad ? bucket_of(rows) : 0;
+        unsorted[l] = Group{b, lo, rows, (uint32_t)per << 16 | l};
+        if (MODE == kWgrad) atomicAdd(&st->bucket[b], 1);
     }
     __syncthreads();
-    if (MODE != kWgrad && warp == 0) {
-        int base = 0;
-        for (int l0 = 0; l0 < El; l0 += 32) {
-            const int l = l0 + lane;
-            const int mine = l < El ? groups[l].start : 0;
-            int sum = mine;
+    if (warp == 0) {
+        if (MODE == kWgrad) {
+            // a counting sort that every CTA does alike: the first place of every bucket (lane i
+            // has buckets [4i, 4i + 4)), then the groups in their order
+            int n[kBuckets / 32], sum = 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += v;
+            for (int i = 0; i < kBuckets / 32; ++i) {
+                n[i] = sum;
+                sum += st->bucket[lane * (kBuckets / 32) + i];
             }
-            if (l < El) groups[l].start = base + sum - mine;
-            base += __shfl_sync(0xffffffffu, sum, 31);
+            const int before = warp_prefix(sum) - sum;
+#pragma unroll
+            for (int i = 0; i < kBuckets / 32; ++i) st->bucket[lane * (kBuckets / 32) + i] = before + n[i];
+            __syncwarp();
+            for (int l0 = 0; l0 < El; l0 += 32) {
+                const bool in = l0 + lane < El;
+                const Group g = in ? unsorted[l0 + lane] : Group{-1, 0, 0, 0};
+                const unsigned same = __match_any_sync(0xffffffffu, g.start);
+                const int place = in ? st->bucket[g.start] + __popc(same & lanemask_lt()) : 0;
+                __syncwarp();
+                if (in) {
+                    groups[place] = g;
+                    if (same >> lane == 1u) st->bucket[g.start] = place + 1;  // the last of its bucket
+                }
+                __syncwarp();
+            }
+        } else {
+            // prefix sums of the groups' tiles
+            int base = 0;
+            for (int l0 = 0; l0 < El; l0 += 32) {
+                const int l = l0 + lane;
+                const int mine = l < El ? (groups[l].rows + kMaxN - 1) / kMaxN * sh.m_tiles.d : 0;
+                const int sum = warp_prefix(mine);
+                if (l < El) groups[l].start = base + sum - mine;
+                base += __shfl_sync(0xffffffffu, sum, 31);
+            }
+            if (lane == 0) st->tiles = base;
         }
-        if (lane == 0) st->tiles = base;
     }
+    if (MODE == kWgrad) ptx::fence_proxy_async_smem();  // TMA writes the stages next
     __syncthreads();
     cluster_sync();  // barriers and TMEM of both CTAs are in place
     ptx::tc_fence_after();
     const uint32_t tmem = st->tmem_base;
     const int tiles = MODE == kWgrad ? El * sh.group_tiles.d : st->tiles;
-    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    // Pair p takes the tiles p, p + pairs, ...; wgrad, whose tiles come from the dearest to the
+    // cheapest, p, 2 * pairs - 1 - p, 2 * pairs + p, ..., so that the pairs' sums stay close
+    // (skewed groups of 65536 rows: 378 -> 345 us). Forward and dgrad are bound by what the SMs
+    // take in from L2, not by the spread of the pairs' work: sorted, they measured no faster.
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int turn = MODE == kWgrad ? 2 * (pairs - pair) - 1 : pairs;
 
     if (warp == kTmaWarp) {
         const bool lead = elect_one();
@@ -381,7 +436,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         int s = 0;
         uint32_t ph = 0, filled = 0, landed = 0;
         bool ok = true;
-        for (int tile = first; ok && tile < tiles; tile += step) {
+        for (int tile = pair, gap = turn; ok && tile < tiles; tile += gap, gap = 2 * pairs - gap) {
             const Tile t = tile_at<MODE>(tile, groups, El, sh);
             int box = 0;  // the smallest box that holds this CTA's half of the columns
             while (MODE != kWgrad && (8 << box) < t.n / 2) ++box;
@@ -442,7 +497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             int s = 0, b = 0;
             uint32_t tph = 0, filled = 0, landed = 0;
             bool ok = true;
-            for (int tile = first; ok && tile < tiles; tile += step) {
+            for (int tile = pair, gap = turn; ok && tile < tiles; tile += gap, gap = 2 * pairs - gap) {
                 const Tile t = tile_at<MODE>(tile, groups, El, sh);
                 if (t.steps == 0) continue;
                 const uint32_t idesc = idesc0 | (uint32_t)(t.n >> 3) << 17;
@@ -492,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         // read become zeros in all four boxes of this CTA
         int s = 0;
         uint32_t landed = 0;
-        for (int tile = first; tile < tiles; tile += step) {
+        for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
             const Tile t = tile_at<MODE>(tile, groups, El, sh);
             if (t.steps == 0) continue;
             s = (s + t.steps - 1) % stages;
@@ -517,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         int b = 0, boxes = 0;
         uint32_t tph = 0;
         const uint32_t slab = (uint32_t)(warp * 32) << 16;
-        for (int tile = first; tile < tiles; tile += step) {
+        for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
             const Tile t = tile_at<MODE>(tile, groups, El, sh);
             const int m = t.m0 + (int)rank * 128 + warp * 32;  // this warp's first row of the tile
             if (t.steps > 0) {
