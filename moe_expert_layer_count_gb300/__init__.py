@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from typing import Optional
 
 import torch
@@ -123,8 +124,20 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(_raw_stream(stream))
+
+
+# The handle of the current device's current stream without a torch.cuda.Stream object around
+# it (2.9 us a call).
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream=None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _current_raw(torch.cuda.current_device())
 
 
 def _check(fn: str, status: int):
@@ -395,18 +408,30 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
     return code
 
 
+def _addr(t: Optional[torch.Tensor]):
+    """The device address of a contiguous CUDA tensor (None for None)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
 def _same(t, shape, dtype, name):
     """Checks an output buffer or a second operand against the shape and type it has to have."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """Scratch memory for a call on `stream`: the allocator keeps it until that stream is done with it."""
-    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream` (None: the current one), from that stream's own pool: no
+    work of another stream that is still under way has it in use."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def moe_layer_norm(x, weight, bias=None, eps=1e-5, out=None, mean=None, rstd=None, stream=None):
@@ -418,16 +443,16 @@ def moe_layer_norm(x, weight, bias=None, eps=1e-5, out=None, mean=None, rstd=Non
     _same(weight, (K,), weight.dtype, "weight")
     _same(bias, (K,), weight.dtype, "bias")
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     if mean is None:
-        mean = torch.empty(M, dtype=torch.float32, device=x.device)
+        mean = _empty(M, torch.float32, x.device, stream)
     if rstd is None:
-        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+        rstd = _empty(M, torch.float32, x.device, stream)
     _same(out, (M, K), x.dtype, "out")
     _same(mean, (M,), torch.float32, "mean")
     _same(rstd, (M,), torch.float32, "rstd")
     _check("moe_layer_norm", lib().moe_layer_norm(
-        _ptr(x), M, K, dt, _ptr(weight), _ptr(bias), pdt, eps, _ptr(out), _ptr(mean), _ptr(rstd), _stream(stream)))
+        _addr(x), M, K, dt, _addr(weight), _addr(bias), pdt, eps, _addr(out), _addr(mean), _addr(rstd), _raw_stream(stream)))
     return out, mean, rstd
 
 
@@ -446,19 +471,19 @@ def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, d_weight=None, d
     _same(mean, (M,), torch.float32, "mean")
     _same(rstd, (M,), torch.float32, "rstd")
     if dx is None:
-        dx = torch.empty_like(x)
+        dx = _empty(x.shape, x.dtype, x.device, stream)
     if d_weight is None:
-        d_weight = torch.empty_like(weight)
+        d_weight = _empty(weight.shape, weight.dtype, weight.device, stream)
     if d_bias is None:
-        d_bias = torch.empty_like(weight)
+        d_bias = _empty(weight.shape, weight.dtype, weight.device, stream)
     _same(dx, (M, K), x.dtype, "dx")
     _same(d_weight, (K,), weight.dtype, "d_weight")
     _same(d_bias, (K,), weight.dtype, "d_bias")
     if workspace is None:
-        workspace = _scratch(moe_layer_norm_workspace_size(M, K), x.device, stream)
+        workspace = _empty(moe_layer_norm_workspace_size(M, K), torch.uint8, x.device, stream)
     _check("moe_layer_norm_backward", lib().moe_layer_norm_backward(
-        _ptr(dy), _ptr(x), M, K, dt, _ptr(weight), pdt, _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(d_weight),
-        _ptr(d_bias), _ptr(workspace), workspace.numel(), _stream(stream)))
+        _addr(dy), _addr(x), M, K, dt, _addr(weight), pdt, _addr(mean), _addr(rstd), _addr(dx), _addr(d_weight),
+        _addr(d_bias), _addr(workspace), workspace.numel(), _raw_stream(stream)))
     return dx, d_weight, d_bias
 
 
@@ -471,15 +496,15 @@ def moe_router_topk(logits, topk, scoring=MOE_SCORE_SOFTMAX, renormalize=True, s
     M, E = logits.shape
     _same(bias, (E,), torch.float32, "bias")
     if topk_weights is None:
-        topk_weights = torch.empty(M, topk, dtype=torch.float32, device=logits.device)
+        topk_weights = _empty((M, topk), torch.float32, logits.device, stream)
     if topk_ids is None:
-        topk_ids = torch.empty(M, topk, dtype=torch.int32, device=logits.device)
+        topk_ids = _empty((M, topk), torch.int32, logits.device, stream)
     fn = _ids_entry("moe_router_topk", topk_ids)
     _same(topk_weights, (M, topk), torch.float32, "topk_weights")
     _same(topk_ids, (M, topk), topk_ids.dtype, "topk_ids")
     _check(fn, getattr(lib(), fn)(
-        _ptr(logits), M, E, dt, topk, scoring, _ptr(bias), int(bool(renormalize)), scale, _ptr(topk_weights),
-        _ptr(topk_ids), _stream(stream)))
+        _addr(logits), M, E, dt, topk, scoring, _addr(bias), int(bool(renormalize)), scale, _addr(topk_weights),
+        _addr(topk_ids), _raw_stream(stream)))
     return topk_weights, topk_ids
 
 
@@ -493,11 +518,11 @@ def moe_router_topk_backward(logits, topk_ids, d_topk_weights, scoring=MOE_SCORE
     _same(topk_ids, (M, topk), topk_ids.dtype, "topk_ids")
     _same(d_topk_weights, (M, topk), torch.float32, "d_topk_weights")
     if d_logits is None:
-        d_logits = torch.empty_like(logits)
+        d_logits = _empty(logits.shape, logits.dtype, logits.device, stream)
     _same(d_logits, (M, E), logits.dtype, "d_logits")
     _check(fn, getattr(lib(), fn)(
-        _ptr(logits), M, E, dt, _ptr(topk_ids), topk, scoring, int(bool(renormalize)), scale, _ptr(d_topk_weights),
-        _ptr(d_logits), _stream(stream)))
+        _addr(logits), M, E, dt, _addr(topk_ids), topk, scoring, int(bool(renormalize)), scale, _addr(d_topk_weights),
+        _addr(d_logits), _raw_stream(stream)))
     return d_logits
 
 
@@ -509,15 +534,15 @@ def _grouped(fn, a, b, shape, dims, expert_offsets, expert_num_tokens, out, out_
     _same(expert_offsets, (El + 1,), torch.int32, "expert_offsets")
     _same(expert_num_tokens, (El,), torch.int32, "expert_num_tokens")
     if out is None:
-        out = torch.empty(shape, dtype=a.dtype if out_dtype is None else out_dtype, device=a.device)
+        out = _empty(shape, a.dtype if out_dtype is None else out_dtype, a.device, stream)
     _same(out, shape, out.dtype if out_dtype is None else out_dtype, "out")
     odt = _dtype_code(out, "out")
-    off, cnt = _ptr(expert_offsets), _ptr(expert_num_tokens)
+    off, cnt = _addr(expert_offsets), _addr(expert_num_tokens)
     if fn == "moe_grouped_matmul_wgrad":
-        st = lib().moe_grouped_matmul_wgrad(_ptr(a), _ptr(b), a.shape[0], El, N, K, off, cnt, dt, odt, _ptr(out),
-                                            _stream(stream))
+        st = lib().moe_grouped_matmul_wgrad(_addr(a), _addr(b), a.shape[0], El, N, K, off, cnt, dt, odt, _addr(out),
+                                            _raw_stream(stream))
     else:
-        st = getattr(lib(), fn)(_ptr(a), a.shape[0], _ptr(b), El, N, K, off, cnt, dt, odt, _ptr(out), _stream(stream))
+        st = getattr(lib(), fn)(_addr(a), a.shape[0], _addr(b), El, N, K, off, cnt, dt, odt, _addr(out), _raw_stream(stream))
     _check(fn, st)
     return out
 
@@ -554,13 +579,13 @@ def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=
                     out_dtype, stream)
 
 
-def _tensor_list(tensors):
-    """C arrays of the pointers, lengths and types of a list of contiguous CUDA tensors."""
-    n = len(tensors)
-    ptrs = (ctypes.c_void_p * n)(*[_ptr(t).value for t in tensors])
-    lens = (ctypes.c_int64 * n)(*[t.numel() for t in tensors])
-    types = (ctypes.c_int32 * n)(*[_dtype_code(t, "tensors") for t in tensors])
-    return ptrs, lens, types
+def _addresses(tensors) -> array:
+    """The device addresses of a list of contiguous CUDA tensors."""
+    if not all([t.is_cuda for t in tensors]):
+        raise ValueError("expected CUDA tensors")
+    if not all([t.is_contiguous() for t in tensors]):
+        raise ValueError("expected contiguous tensors")
+    return array("Q", [t.data_ptr() for t in tensors])
 
 
 def moe_grad_norm_workspace_size(numels) -> int:
@@ -582,26 +607,36 @@ def moe_clip_grad_norm(tensors, max_norm, out=None, norm=None, workspace=None, s
 
 def _norm_call(fn, tensors, max_norm, out, norm, workspace, stream):
     tensors = list(tensors)
-    if not tensors:
+    n = len(tensors)
+    if n == 0:
         raise ValueError(f"{fn}: no tensors")
-    ptrs, lens, types = _tensor_list(tensors)
+    dtypes = [t.dtype for t in tensors]
+    try:
+        types = array("i", [_DTYPES[d] for d in dtypes])
+    except KeyError as e:
+        raise TypeError(f"{fn}: expected torch.float32, torch.bfloat16 or torch.float16, got {e.args[0]}") from None
+    sizes = [t.numel() for t in tensors]
+    lens = array("q", sizes)
+    ptrs = _addresses(tensors)
     dev = tensors[0].device
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        norm = _empty(1, torch.float32, dev, stream)
     _same(norm, (1,), torch.float32, "norm")
-    n = len(tensors)
+    lens_at = lens.buffer_info()[0]
     if workspace is None:
-        workspace = _scratch(int(lib().moe_grad_norm_workspace_size(lens, n)), dev, stream)
+        workspace = _empty(int(lib().moe_grad_norm_workspace_size(lens_at, n)), torch.uint8, dev, stream)
+    ptrs_at, types_at = ptrs.buffer_info()[0], types.buffer_info()[0]
     if max_norm is None:
-        st = lib().moe_grad_norm(ptrs, lens, types, n, _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream))
+        st = lib().moe_grad_norm(ptrs_at, lens_at, types_at, n, _addr(norm), _addr(workspace), workspace.numel(),
+                                 _raw_stream(stream))
     else:
         outs = None
         if out is not None:
             out = list(out)
-            if len(out) != n or any(o.numel() != t.numel() or o.dtype != t.dtype for o, t in zip(out, tensors)):
+            if [o.numel() for o in out] != sizes or [o.dtype for o in out] != dtypes:
                 raise ValueError(f"{fn}: outputs of other lengths or types than the tensors")
-            outs = (ctypes.c_void_p * n)(*[_ptr(o).value for o in out])
-        st = lib().moe_clip_grad_norm(ptrs, lens, types, n, max_norm, outs, _ptr(norm), _ptr(workspace),
-                                      workspace.numel(), _stream(stream))
+            outs = _addresses(out)
+        st = lib().moe_clip_grad_norm(ptrs_at, lens_at, types_at, n, max_norm, outs.buffer_info()[0] if outs else None,
+                                      _addr(norm), _addr(workspace), workspace.numel(), _raw_stream(stream))
     _check(fn, st)
     return norm

@@ -8,8 +8,9 @@
 //   softmax, renormalised dl_i = scale * q_i * (g_i - sum_m q_m g_m),  q_i = s_i / S; 0 elsewhere
 //   sigmoid               dl_i = scale * g_i * s_i * (1 - s_i)
 //   sigmoid, renormalised dl_i = scale * q_i * (g_i - sum_m q_m g_m) * (1 - s_i)
-// One warp per token: lane i holds the V consecutive logits [i*V, (i+1)*V) in registers, so
-// a tie goes to the lowest lane and then to its first value.
+// The general kernels take one warp per token: lane i holds the V consecutive logits
+// [i*V, (i+1)*V) in registers, so a tie goes to the lowest lane and then to its first value.
+// Without a bias and up to 16 choices the forward pass runs as router_list_kernel.
 #include <climits>
 
 #include "elem.cuh"
@@ -159,6 +160,193 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
     }
 }
 
+// ------------------------------------------------------------------ unbiased choice
+// Four lanes per token, eight tokens per warp. A lane takes 8 of every 32 logits, turns each into
+// a key that holds the logit's order and, below it, the index (so that keys are distinct and a
+// tie goes to the lower index), keeps the L largest keys in a sorted list by sorting networks, and
+// merges its list with its neighbours' (two exchanges). A 16-bit logit has 13 or 16 zero bits
+// below its fp32 form: its key is 32 bits and a comparator is two instructions; fp32 takes 64.
+// What bounds it is the issue of these instructions, not memory: about 70 per token of 128
+// 16-bit logits against 256 bytes read.
+constexpr int kListThreads = 128;
+constexpr int kLanes = 4;             // per token
+constexpr uint32_t kIndexMask = 0x3ff;
+
+template <typename T>
+struct KeyOf {
+    using type = uint32_t;
+    static __device__ __forceinline__ uint32_t make(uint32_t order, int e) { return (order & ~kIndexMask) | (kIndexMask - e); }
+    static __device__ __forceinline__ int index(uint32_t k) { return kIndexMask - (k & kIndexMask); }
+    // the logit; NaN for key 0 (no logit)
+    static __device__ __forceinline__ float logit(uint32_t k) {
+        return __uint_as_float(k & 0x80000000u ? (k & ~kIndexMask) ^ 0x80000000u : ~(k | kIndexMask));
+    }
+};
+template <>
+struct KeyOf<float> {
+    using type = uint64_t;
+    static __device__ __forceinline__ uint64_t make(uint32_t order, int e) { return (uint64_t)order << 32 | (kIndexMask - e); }
+    static __device__ __forceinline__ int index(uint64_t k) { return kIndexMask - ((uint32_t)k & kIndexMask); }
+    static __device__ __forceinline__ float logit(uint64_t k) {
+        const uint32_t o = (uint32_t)(k >> 32);
+        return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+    }
+};
+
+// a >= b afterwards.
+template <typename K>
+__device__ __forceinline__ void order2(K& a, K& b) {
+    const K hi = a > b ? a : b, lo = a > b ? b : a;
+    a = hi;
+    b = lo;
+}
+
+// Batcher's odd-even merge sort, descending (L a power of two).
+template <typename K, int L>
+__device__ __forceinline__ void sort_list(K (&a)[L]) {
+#pragma unroll
+    for (int p = 1; p < L; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < L; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < L && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order2(a[i + j], a[i + j + k]);
+}
+
+// The L largest of two descending lists, descending: the larger of a[i] and b[L - 1 - i] are
+// they, as a bitonic sequence.
+template <typename K, int L>
+__device__ __forceinline__ void merge_lists(K (&a)[L], const K (&b)[L]) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) a[i] = a[i] > b[L - 1 - i] ? a[i] : b[L - 1 - i];
+#pragma unroll
+    for (int s = L / 2; s >= 1; s /= 2)
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            if (!(i & s)) order2(a[i], a[i + s]);
+}
+
+// 8 logits of one lane of a 32-logit chunk and their experts. kVec: 8 in a row (E a multiple
+// of 8, rows on 16-byte boundaries), else every fourth.
+template <bool kVec>
+__device__ __forceinline__ int expert_at(int chunk, int lane, int j) {
+    return kVec ? chunk * 32 + lane * 8 + j : chunk * 32 + j * kLanes + lane;
+}
+template <typename T, bool kVec>
+__device__ __forceinline__ void load8(const T* __restrict__ row, int chunk, int lane, int E, float (&v)[8]) {
+    if constexpr (kVec) {
+        constexpr int N = 16 / sizeof(T);
+        if (chunk * 32 + lane * 8 < E) {
+#pragma unroll
+            for (int h = 0; h < 8; h += N) {
+                const Vec<T, N> r = *reinterpret_cast<const Vec<T, N>*>(row + chunk * 32 + lane * 8 + h);
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[h + j] = to_f32(r.v[j]);
+            }
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = -INFINITY;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = expert_at<false>(chunk, lane, j);
+            v[j] = e < E ? to_f32(row[e]) : -INFINITY;
+        }
+    }
+}
+
+template <typename T, typename TId, int L, bool kVec>
+__global__ void __launch_bounds__(kListThreads)
+    router_list_kernel(const T* __restrict__ logits, int64_t M, int E, int topk, int scoring, int renorm, float scale,
+                       float* __restrict__ out_w, TId* __restrict__ out_id) {
+    using Key = KeyOf<T>;
+    using K = typename Key::type;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & (kLanes - 1);
+    int64_t t = (int64_t)blockIdx.x * (kListThreads / kLanes) + threadIdx.x / kLanes;
+    const bool real = t < M;  // the lanes past the last token go along on the last one's row
+    if (!real) t = M - 1;
+    const T* row = logits + t * E;
+    const int chunks = (E + 31) / 32;  // absent logits are -inf: they cannot displace a real one, nor be chosen
+    K best[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) best[i] = 0;
+#pragma unroll 4
+    for (int c = 0; c < chunks; c += L / 8) {
+        K now[L];
+#pragma unroll
+        for (int h = 0; h < L; h += 8) {
+            float v[8];
+            load8<T, kVec>(row, c + h / 8, lane, E, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                // -0 becomes +0, NaN -inf
+                const uint32_t u = __float_as_uint(fmaxf(v[j] + 0.f, -INFINITY));
+                const uint32_t order = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+                now[h + j] = Key::make(order, expert_at<kVec>(c + h / 8, lane, j) & kIndexMask);
+            }
+        }
+        sort_list(now);
+        merge_lists(best, now);
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o *= 2) {
+        K other[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) other[i] = __shfl_xor_sync(0xffffffffu, best[i], o);
+        merge_lists(best, other);
+    }
+    // all four lanes have the list; lane q takes places q, q + 4, ...
+    const bool soft = scoring == MOE_SCORE_SOFTMAX;
+    const float top = fminf(Key::logit(best[0]), kFltMax);
+    float w[L / kLanes], sum = 0.f;
+    int id[L / kLanes];
+#pragma unroll
+    for (int i = 0; i < L / kLanes; ++i) {
+        K k = best[i * kLanes];
+#pragma unroll
+        for (int q = 1; q < kLanes; ++q)
+            if (lane == q) k = best[i * kLanes + q];
+        const float l = fminf(Key::logit(k), kFltMax);
+        const bool chosen = l > -INFINITY && i * kLanes + lane < topk;  // false for NaN: no such logit
+        id[i] = chosen ? Key::index(k) : -1;
+        if (soft)
+            w[i] = chosen ? expf(l - top) : 0.f;
+        else if (renorm)  // as sigmoid_share has it
+            w[i] = chosen ? expf(fminf(l, 0.f) - fminf(0.f, top)) / (1.f + expf(-fabsf(l))) : 0.f;
+        else
+            w[i] = chosen ? sigmoid(l) : 0.f;
+        sum += w[i];
+    }
+    if (soft && !renorm) {
+        sum = 0.f;
+        for (int c = 0; c < chunks; ++c) {
+            float v[8];
+            load8<T, kVec>(row, c, lane, E, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += __expf(clean_logit(v[j]) - top);
+        }
+    }
+    if (soft || renorm) {
+#pragma unroll
+        for (int o = 1; o < kLanes; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        scale = sum > 0.f ? scale / sum : 0.f;  // 0 or NaN: nothing was chosen, all w are 0
+    }
+    if (!real) return;
+#pragma unroll
+    for (int i = 0; i < L / kLanes; ++i) {
+        const int at = i * kLanes + lane;
+        if (at < topk) {
+            out_w[t * topk + at] = w[i] * scale;
+            out_id[t * topk + at] = (TId)id[i];
+        }
+    }
+}
+
 template <typename T, typename TId, int V, bool kVec>
 __global__ void __launch_bounds__(kRouterWarps * 32)
     router_backward_kernel(const T* logits, int64_t M, int E, const TId* __restrict__ ids, int topk, int scoring,
@@ -275,6 +463,18 @@ int router_impl(const void* logits, int64_t M, int E, int dtype, int topk, int s
     const unsigned grid = (unsigned)((M + kRouterWarps - 1) / kRouterWarps);
     return with_dtype(dtype, [&](auto* p) {
         using T = std::remove_pointer_t<decltype(p)>;
+        if (!bias && topk <= 16) {
+            auto go = [&](auto kernel) {
+                constexpr int per = kListThreads / kLanes;
+                launch_k(kernel, (unsigned)((M + per - 1) / per), kListThreads, 0, (cudaStream_t)stream,
+                         static_cast<const T*>(logits), M, E, topk, scoring, renorm ? 1 : 0, scale, w, ids);
+                note_launches(1);
+                return launch_status();
+            };
+            const bool vec = E % 8 == 0 && !misaligned(logits, 16);
+            if (topk <= 8) return vec ? go(router_list_kernel<T, TId, 8, true>) : go(router_list_kernel<T, TId, 8, false>);
+            return vec ? go(router_list_kernel<T, TId, 16, true>) : go(router_list_kernel<T, TId, 16, false>);
+        }
         return with_v(E, [&](auto vc) {
             constexpr int V = decltype(vc)::value;
             auto go = [&](auto kernel) {
