@@ -11,8 +11,10 @@
 //  * backward: each block takes every G-th row and keeps the sums of d_weight and d_bias for its
 //    columns in registers, the next row's loads under way during the current row's sums; G
 //    partial sums are added in a fixed order by a second kernel.
-// Rows too long for registers (over 8 vectors in 1024 threads; backward over 8192 values)
+// Rows too long for registers (over 8 vectors in 1024 threads; backward over 16 values in each)
 // take the looping kernels, which read them again from L2.
+#include <type_traits>
+
 #include "elem.cuh"
 
 namespace moe {
@@ -21,39 +23,11 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kColParts = 152;  // row ranges of the looping kernels' partial sums
 
-// Partial sums of the backward kernel (its blocks): four an SM while a row is short, so that
-// enough loads are under way; each partial sum is 2 K floats that the fold reads again.
-int most_parts(int K) { return K <= 2048 ? 608 : K <= 4096 ? 304 : 152; }
-
-// V values from p; `vec`: p lies on a vector's boundary (else one load per value, the same values
-// to the same threads: results do not depend on the alignment).
-template <typename P, int V>
-__device__ __forceinline__ Vec<P, V> load_vec(const P* __restrict__ p, bool vec) {
-    Vec<P, V> r;
-    if (!vec) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) r.v[j] = p[j];
-    } else if constexpr (V * sizeof(P) <= 16) {
-        r = *reinterpret_cast<const Vec<P, V>*>(p);
-    } else {  // 8 fp32 values: two loads
-        constexpr int N = 16 / sizeof(P);
-#pragma unroll
-        for (int i = 0; i < V; i += N) {
-            const Vec<P, N> h = *reinterpret_cast<const Vec<P, N>*>(p + i);
-#pragma unroll
-            for (int j = 0; j < N; ++j) r.v[i + j] = h.v[j];
-        }
-    }
-    return r;
-}
-template <typename P, int V>
-__device__ __forceinline__ void store_vec(P* p, const Vec<P, V>& v, bool vec) {
-    if (vec) {
-        *reinterpret_cast<Vec<P, V>*>(p) = v;
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) p[j] = v.v[j];
-    }
+// Partial sums of the backward kernel (its blocks): as many per SM as keep enough loads under
+// way, up to eight; each partial sum is 2 K floats that the fold reads again, 10 MB in all.
+int most_parts(int K) {
+    const int n = 1250000 / K / 152;
+    return 152 * (n < 1 ? 1 : n > 8 ? 8 : n);
 }
 
 // Sum over the block, the same value in every thread. `s`: one float per warp.
@@ -66,83 +40,158 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
     return v;
 }
 
-// kThreads: the most threads of a block, 256 or 1024 (which leaves 64 registers a thread).
+// Two fp32 values; the arithmetic on them is packed (one instruction for both).
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+template <typename T>
+__device__ __forceinline__ uint32_t bits_of(T v) {
+    if constexpr (sizeof(T) == 4)
+        return __float_as_uint(v);
+    else
+        return *reinterpret_cast<const uint16_t*>(&v);
+}
 
-// The raw values of one thread's share of a row: IT vectors, `threads` vectors apart.
+// One thread's share of a row: IT vectors of V values, `threads` vectors apart, held as the
+// 32-bit words they are loaded in (V = 1: as fp32). The share is used as pairs of values,
+// whichever vectors these lie in.
 template <typename T, int V, int IT>
 struct Share {
-    Vec<T, V> v[IT];
-    // vectors at or past K are zero; `vec`: the row starts on a vector's boundary
+    static constexpr int kPairs = V * IT / 2;
+    static constexpr int kWords = V > 1 ? V * (int)sizeof(T) / 4 : 1;  // of a vector
+    uint32_t w[IT * kWords];
+    // values at or past K are zero; `vec`: the row starts on a 16-byte boundary (else one load
+    // per value, the same values to the same threads: results do not depend on the alignment)
     __device__ __forceinline__ void load(const T* __restrict__ row, int K, int tx, int threads, bool vec) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = (i * threads + tx) * V;
-            if (c < K) {
-                v[i] = load_vec<T, V>(row + c, vec);
+            uint32_t* o = w + i * kWords;
+            if (c >= K) {
+#pragma unroll
+                for (int j = 0; j < kWords; ++j) o[j] = 0;
+            } else if constexpr (V == 1) {
+                o[0] = __float_as_uint(to_f32(row[c]));
+            } else if (vec) {
+#pragma unroll
+                for (int j = 0; j < kWords; j += 4) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(row + c) + j);
+                    o[j] = u.x, o[j + 1] = u.y, o[j + 2] = u.z, o[j + 3] = u.w;
+                }
             } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[i].v[j] = from_f32<T>(0.f);
+                for (int j = 0; j < kWords; ++j)
+                    o[j] = sizeof(T) == 4 ? bits_of(row[c + j]) : bits_of(row[c + 2 * j]) | bits_of(row[c + 2 * j + 1]) << 16;
             }
         }
     }
+    __device__ __forceinline__ void store(T* __restrict__ row, int K, int tx, int threads, bool vec) const {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * threads + tx) * V;
+            const uint32_t* o = w + i * kWords;
+            if (c >= K) continue;
+            if constexpr (V == 1) {
+                row[c] = from_f32<T>(__uint_as_float(o[0]));
+            } else if (vec) {
+                *reinterpret_cast<uint4*>(row + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    if constexpr (sizeof(T) == 4)
+                        row[c + j] = __uint_as_float(o[j]);
+                    else
+                        reinterpret_cast<uint16_t*>(row)[c + j] = (uint16_t)(o[j / 2] >> (j % 2 * 16));
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float2 get(int p) const {
+        if constexpr (V == 1 || sizeof(T) == 4)
+            return make_float2(__uint_as_float(w[2 * p]), __uint_as_float(w[2 * p + 1]));
+        else if constexpr (std::is_same<T, bf16>::value)
+            return make_float2(__uint_as_float(w[p] << 16), __uint_as_float(w[p] & 0xffff0000u));
+        else
+            return __half22float2(*reinterpret_cast<const __half2*>(&w[p]));
+    }
+    __device__ __forceinline__ void set(int p, float2 f) {
+        if constexpr (V == 1 || sizeof(T) == 4) {
+            w[2 * p] = __float_as_uint(f.x);
+            w[2 * p + 1] = __float_as_uint(f.y);
+        } else if constexpr (std::is_same<T, bf16>::value) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+            w[p] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(f.x, f.y);
+            w[p] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    // the column of the pair's first value (the second: the next, or `threads` on where V is 1)
+    static __device__ __forceinline__ int column(int p, int tx, int threads) {
+        return V > 1 ? (2 * p / V * threads + tx) * V + 2 * p % V : 2 * p * threads + tx;
+    }
 };
 
-// Sum over the threads of a row (blockDim.x of them, a row per threadIdx.y), the same in all.
-// `s`: 32 floats per row; called in turn with two buffers, so that one barrier is enough.
-__device__ __forceinline__ float row_sum(float v, float* s) {
-    v = warp_sum(v);
+// Sums over the threads of a row (blockDim.x of them, a row per threadIdx.y), the same in all.
+// `s`: 32 places per row, another one at the next call, so that one barrier is enough.
+__device__ __forceinline__ float2 row_sum(float2 v, float2* s) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v = __fadd2_rn(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
     if (blockDim.x == 32) return v;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) s[threadIdx.y * 32 + (threadIdx.x >> 5)] = v;
+    s += threadIdx.y * 32;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    return warp_sum(lane < (blockDim.x >> 5) ? s[threadIdx.y * 32 + lane] : 0.f);
+    v = s[0];
+    for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v = __fadd2_rn(v, s[i]);
+    return v;
 }
 
+// kThreads, here and below: the most threads of a block. The number of blocks that an SM is
+// to hold bounds the registers, so that enough rows are under way.
 template <typename T, typename P, int V, int IT, int kThreads>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 6 : 1)
     layer_norm_rows_kernel(const T* x, int64_t M, int K, const P* __restrict__ weight, const P* __restrict__ bias, float eps,
                            T* y, float* __restrict__ mean_out, float* __restrict__ rstd_out, bool vec) {
-    __shared__ float s[2][8 * 32];
+    using S = Share<T, V, IT>;
+    __shared__ float2 s[2][4 * 32];
     pdl_wait();
     pdl_trigger();
     const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool in = r < M;  // threads of absent rows keep the barriers company
     const int tx = threadIdx.x, threads = blockDim.x;
-    Share<T, V, IT> xs;
+    S xs;
     xs.load(x + (in ? r : 0) * K, in ? K : 0, tx, threads, vec);
-    float a = 0.f;
+    float2 a = both(0.f);
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
+    for (int p = 0; p < S::kPairs; ++p) a = __fadd2_rn(a, xs.get(p));
+    a = row_sum(both(a.x + a.y), s[0]);
+    const float mean = a.x / K;
+    a = both(0.f);
 #pragma unroll
-        for (int j = 0; j < V; ++j) a += to_f32(xs.v[i].v[j]);
-    const float mean = row_sum(a, s[0]) / K;
-    a = 0.f;
-#pragma unroll
-    for (int i = 0; i < IT; ++i)
-        if ((i * threads + tx) * V < K) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = to_f32(xs.v[i].v[j]) - mean;
-                a = fmaf(d, d, a);
-            }
-        }
-    const float rstd = 1.f / sqrtf(row_sum(a, s[1]) / K + eps);
+    for (int p = 0; p < S::kPairs; ++p) {
+        float2 d = __fadd2_rn(xs.get(p), both(-mean));
+        if (S::column(p, tx, threads) >= K) d = both(0.f);
+        if (V == 1 && S::column(p, tx, threads) + threads >= K) d.y = 0.f;
+        a = __ffma2_rn(d, d, a);
+    }
+    a = row_sum(both(a.x + a.y), s[1]);
+    const float rstd = 1.f / sqrtf(a.x / K + eps);
     if (!in) return;
-    T* out = y + r * K;
+    // a vector (V = 1: a pair) of parameters at a time
+    constexpr int kStep = V > 1 ? V / 2 : 1;
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int c = (i * threads + tx) * V;
-        if (c < K) {
-            const Vec<P, V> w = load_vec<P, V>(weight + c, vec);
-            Vec<P, V> b = {};
-            if (bias) b = load_vec<P, V>(bias + c, vec);
-            Vec<T, V> o;
+    for (int p0 = 0; p0 < S::kPairs; p0 += kStep) {
+        const int c = S::column(p0, tx, threads);
+        if (c >= K) break;
+        Share<P, V, (V > 1 ? 1 : 2)> w, b;
+        w.load(weight + c, K - c, 0, threads, vec);
+        if (bias) b.load(bias + c, K - c, 0, threads, vec);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                o.v[j] = from_f32<T>(fmaf((to_f32(xs.v[i].v[j]) - mean) * rstd, to_f32(w.v[j]), bias ? to_f32(b.v[j]) : 0.f));
-            store_vec(out + c, o, vec);
+        for (int q = 0; q < kStep; ++q) {
+            const float2 h = __fmul2_rn(__fadd2_rn(xs.get(p0 + q), both(-mean)), both(rstd));
+            xs.set(p0 + q, __ffma2_rn(h, w.get(q), bias ? b.get(q) : both(0.f)));
         }
     }
+    xs.store(y + r * K, K, tx, threads, vec);
     if (tx == 0) {
         if (mean_out) mean_out[r] = mean;
         if (rstd_out) rstd_out[r] = rstd;
@@ -150,31 +199,26 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Block b takes the rows b * blockDim.y + threadIdx.y, then gridDim.x * blockDim.y further on.
+// (x - mean) * rstd is taken as x * rstd - mean * rstd in one rounding.
 template <typename T, typename P, int V, int IT, int kThreads>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : V * IT > 8 ? 2 : 3)
     layer_norm_backward_kernel(const T* dy, const T* __restrict__ x, int64_t M, int K, const P* __restrict__ weight,
                                const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* dx,
                                float* __restrict__ parts, bool vec) {
-    __shared__ float s[4][8 * 32];
+    using S = Share<T, V, IT>;
+    __shared__ float2 s[2][8 * 32];
     extern __shared__ float cols[];  // 2 * K, where the block has several rows at a time
     pdl_wait();
     pdl_trigger();
     const int tx = threadIdx.x, threads = blockDim.x;
-    float w[IT][V], dw[IT][V], db[IT][V];
+    Share<P, V, IT> w;
+    w.load(weight, K, tx, threads, vec);
+    float2 dw[S::kPairs], db[S::kPairs];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int c = (i * threads + tx) * V;
-        Vec<P, V> p = {};
-        if (c < K) p = load_vec<P, V>(weight + c, vec);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            w[i][j] = c < K ? to_f32(p.v[j]) : 0.f;
-            dw[i][j] = db[i][j] = 0.f;
-        }
-    }
+    for (int p = 0; p < S::kPairs; ++p) dw[p] = db[p] = both(0.f);
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    Share<T, V, IT> xs, ds, xn, dn;
-    float mean = 0.f, rstd = 0.f, mean_n = 0.f, rstd_n = 0.f;
+    S xs, ds, xn, dn;
+    float mean_n = 0.f, rstd_n = 0.f;
     auto fetch = [&](int64_t r) {
         const bool in = r < M;
         xn.load(x + (in ? r : 0) * K, in ? K : 0, tx, threads, vec);
@@ -186,85 +230,54 @@ __global__ void __launch_bounds__(kThreads)
     fetch(r);
     int turn = 0;
     // all rows of the block take the same number of turns (absent ones are zeros)
-    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < M; r0 += step, r += step, turn ^= 2) {
+    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < M; r0 += step, r += step, turn ^= 1) {
         xs = xn;
         ds = dn;
-        mean = mean_n;
-        rstd = rstd_n;
+        const float rstd = rstd_n, shift = -mean_n * rstd_n;
         if (r0 + step < M) fetch(r + step);
-        float a = 0.f, b = 0.f;
+        float2 a = both(0.f), b = both(0.f);
 #pragma unroll
-        for (int i = 0; i < IT; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = to_f32(ds.v[i].v[j]), h = (to_f32(xs.v[i].v[j]) - mean) * rstd, g = d * w[i][j];
-                a += g;
-                b = fmaf(g, h, b);
-                dw[i][j] = fmaf(d, h, dw[i][j]);
-                db[i][j] += d;
-            }
-        a = warp_sum(a);
-        b = warp_sum(b);
-        if (threads > 32) {
-            const int lane = tx & 31, n = threads >> 5, base = threadIdx.y * 32;
-            if (lane == 0) {
-                s[turn][base + (tx >> 5)] = a;
-                s[turn + 1][base + (tx >> 5)] = b;
-            }
-            __syncthreads();
-            a = warp_sum(lane < n ? s[turn][base + lane] : 0.f);
-            b = warp_sum(lane < n ? s[turn + 1][base + lane] : 0.f);
+        for (int p = 0; p < S::kPairs; ++p) {
+            const float2 d = ds.get(p), h = __ffma2_rn(xs.get(p), both(rstd), both(shift)), g = __fmul2_rn(d, w.get(p));
+            a = __fadd2_rn(a, g);
+            b = __ffma2_rn(g, h, b);
+            dw[p] = __ffma2_rn(d, h, dw[p]);
+            db[p] = __fadd2_rn(db[p], d);
         }
-        a /= K;
-        b /= K;
+        a = row_sum(make_float2(a.x + a.y, b.x + b.y), s[turn]);
         if (r < M) {
+            // rstd * (g - a - h b)
+            const float2 c = both(-a.x / K * rstd), e = both(-a.y / K);
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int c = (i * threads + tx) * V;
-                if (c < K) {
-                    Vec<T, V> o;
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float h = (to_f32(xs.v[i].v[j]) - mean) * rstd;
-                        o.v[j] = from_f32<T>(rstd * (to_f32(ds.v[i].v[j]) * w[i][j] - a - h * b));
-                    }
-                    store_vec(dx + r * K + c, o, vec);
-                }
+            for (int p = 0; p < S::kPairs; ++p) {
+                const float2 h = __ffma2_rn(xs.get(p), both(rstd), both(shift)), g = __fmul2_rn(ds.get(p), w.get(p));
+                xs.set(p, __ffma2_rn(__ffma2_rn(h, e, g), both(rstd), c));
             }
+            xs.store(dx + r * K, K, tx, threads, vec);
         }
     }
     float* out = parts + (int64_t)blockIdx.x * 2 * K;
-    if (blockDim.y == 1) {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int c = (i * threads + tx) * V;
-            if (c < K) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    out[c + j] = dw[i][j];
-                    out[K + c + j] = db[i][j];
-                }
-            }
-        }
-        return;
-    }
+    if (blockDim.y > 1) out = cols;
     for (int y = 0; y < blockDim.y; ++y) {  // the block's rows one after the other
-        __syncthreads();
+        if (y) __syncthreads();
         if (threadIdx.y == y) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int c = (i * threads + tx) * V;
+            for (int p = 0; p < S::kPairs; ++p) {
+                const int c = S::column(p, tx, threads), c2 = V > 1 ? c + 1 : c + threads;
                 if (c < K) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        cols[c + j] = dw[i][j] + (y ? cols[c + j] : 0.f);
-                        cols[K + c + j] = db[i][j] + (y ? cols[K + c + j] : 0.f);
-                    }
+                    out[c] = dw[p].x + (y ? out[c] : 0.f);
+                    out[K + c] = db[p].x + (y ? out[K + c] : 0.f);
+                }
+                if (c2 < K) {
+                    out[c2] = dw[p].y + (y ? out[c2] : 0.f);
+                    out[K + c2] = db[p].y + (y ? out[K + c2] : 0.f);
                 }
             }
         }
     }
+    if (blockDim.y == 1) return;
     __syncthreads();
+    out = parts + (int64_t)blockIdx.x * 2 * K;
     for (int c = threadIdx.y * threads + tx; c < 2 * K; c += threads * blockDim.y) out[c] = cols[c];
 }
 
@@ -373,13 +386,13 @@ bool norm_args_ok(int64_t M, int K, int dtype, int param_dtype) {
     return M >= 0 && M <= INT32_MAX && K >= 1 && dtype_bytes(dtype) && (param_dtype == dtype || param_dtype == MOE_DT_F32);
 }
 
-// Calls f with `it` (1, 2, 4 or 8) as a constant.
-template <typename F>
+// Calls f with `it` (a power of two up to kMost) as a constant.
+template <int kMost, typename F>
 void with_it(int it, F&& f) {
-    if (it == 1) f(std::integral_constant<int, 1>{});
-    if (it == 2) f(std::integral_constant<int, 2>{});
-    if (it == 4) f(std::integral_constant<int, 4>{});
-    if (it == 8) f(std::integral_constant<int, 8>{});
+    if (it == kMost)
+        f(std::integral_constant<int, kMost>{});
+    else if constexpr (kMost > 1)
+        with_it<kMost / 2>(it, f);
 }
 
 // Calls f(T*, P*) with the element types of x and of the parameters.
@@ -419,13 +432,15 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
             constexpr int W = decltype(vc)::value;
             const int nv = (K + W - 1) / W;
             if (nv > 8 * 1024) return false;
-            const int it = nv > 128 ? 8 : nv > 64 ? 4 : nv > 32 ? 2 : 1;
+            const int it = nv > 128 ? 8 : nv > 64 ? 4 : nv > 32 || W == 1 ? 2 : 1;
             const int threads = nv <= 256 ? 32 : ((nv + 7) / 8 + 31) / 32 * 32;
             const dim3 block(threads, threads == 32 ? 4 : 1);
-            with_it(it, [&](auto ic) {
+            with_it<8>(it, [&](auto ic) {
                 constexpr int IT = decltype(ic)::value;
-                launch_k(threads <= 256 ? layer_norm_rows_kernel<T, P, W, IT, 256> : layer_norm_rows_kernel<T, P, W, IT, 1024>,
-                         (unsigned)((M + block.y - 1) / block.y), block, 0,
+                auto kernel = layer_norm_rows_kernel<T, P, W, (IT * W > 1 ? IT : 2), 128>;
+                if constexpr (IT == 8)  // more than a warp per row: always 8 vectors a thread
+                    if (threads > 128) kernel = layer_norm_rows_kernel<T, P, W, IT, 1024>;
+                launch_k(kernel, (unsigned)((M + block.y - 1) / block.y), block, 0,
                          (cudaStream_t)stream, static_cast<const T*>(x), M, K, static_cast<const P*>(weight),
                          static_cast<const P*>(bias), eps, static_cast<T*>(y), mean, rstd, vec);
             });
@@ -471,23 +486,27 @@ MOE_API int moe_layer_norm_backward(const void* dy, const void* x, int64_t M, in
         auto rows = [&](auto vc) -> bool {
             constexpr int W = decltype(vc)::value;
             const int nv = (K + W - 1) / W;
-            // 8 columns a thread at most: their weights and two sums each stay in registers
-            constexpr int kMostIt = 8 / W;
+            // up to 16 columns a thread: their weights and two sums each stay in registers
+            constexpr int kMostIt = 16 / W;
             if (nv > kMostIt * 1024) return false;
-            int it = 1;
-            while (it < kMostIt && nv > 128 * it) it *= 2;
+            int it = W == 1 ? 2 : 1;
+            while (it < kMostIt && nv > 256 * it) it *= 2;
             const int threads = ((nv + it - 1) / it + 31) / 32 * 32;
             const dim3 block(threads, threads <= 128 ? 256 / threads : 1);
             const int64_t blocks = (M + block.y - 1) / block.y;
             n_parts = (int)(blocks < most_parts(K) ? blocks : most_parts(K));
-            with_it(it, [&](auto ic) {
+            with_it<kMostIt>(it, [&](auto ic) {
                 constexpr int IT = decltype(ic)::value;
-                if constexpr (IT * W <= 8)
-                    launch_k(threads <= 256 ? layer_norm_backward_kernel<T, P, W, IT, 256>
-                                            : layer_norm_backward_kernel<T, P, W, IT, 1024>,
-                             (unsigned)n_parts, block,
+                if constexpr (IT * W <= 16 && IT * W > 1) {
+                    auto kernel = layer_norm_backward_kernel<T, P, W, IT, 256>;
+                    if constexpr (IT == kMostIt)
+                        if (threads > 256)
+                            kernel = threads > 512 ? layer_norm_backward_kernel<T, P, W, IT, 1024>
+                                                   : layer_norm_backward_kernel<T, P, W, IT, 512>;
+                    launch_k(kernel, (unsigned)n_parts, block,
                              block.y > 1 ? 2 * K * sizeof(float) : 0, s, static_cast<const T*>(dy), static_cast<const T*>(x), M,
                              K, static_cast<const P*>(weight), mean, rstd, static_cast<T*>(dx), parts, vec);
+                }
             });
             note_launches(1);
             return true;
