@@ -7,12 +7,12 @@
 // Both are bound by memory: x (and dy) are read once, kept in registers in their own type
 // while the row's sums are taken, and written from there. Rows that start on 16-byte
 // boundaries move 16 bytes at a time (V values), others one value at a time.
-//  * forward: a warp per row up to 8 vectors a lane (no barriers), else a block per row.
-//  * backward: each block takes every G-th row and keeps the sums of d_weight and d_bias for its
-//    columns in registers, the next row's loads under way during the current row's sums; G
-//    partial sums are added in a fixed order by a second kernel.
-// Rows too long for registers (over 8 vectors in 1024 threads; backward over 16 values in each)
-// take the looping kernels, which read them again from L2.
+// A thread has 16 columns, their parameters in registers; a row takes K / 16 threads, and a
+// block every G-th row, the next ones on their way to shared memory while a row is summed.
+// The backward pass keeps the sums of d_weight and d_bias for its columns in registers; the
+// blocks' partial sums are added in a fixed order by a second kernel.
+// Rows longer than 1024 threads' columns (or the ring) take the looping kernels, which read
+// them again from L2.
 #include <type_traits>
 
 #include "elem.cuh"
@@ -23,12 +23,33 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kColParts = 152;  // row ranges of the looping kernels' partial sums
 
-// Partial sums of the backward kernel (its blocks): as many per SM as keep enough loads under
-// way, up to eight; each partial sum is 2 K floats that the fold reads again, 10 MB in all.
-int most_parts(int K) {
-    const int n = 1250000 / K / 152;
-    return 152 * (n < 1 ? 1 : n > 8 ? 8 : n);
-}
+// Columns of a thread: their weights (and biases, or the two column sums) stay in registers.
+template <int V>
+constexpr int cols_of = V == 1 ? 8 : 16;
+
+// How the row kernels divide rows of K values: the threads of a row, the rows of a block (as many
+// as fill `block` threads) and the blocks that an SM holds at once with `resident` threads.
+struct Rows {
+    int threads, per_block, per_sm;
+    Rows(int K, int columns, int block, int resident) {
+        threads = ((K + columns - 1) / columns + 31) / 32 * 32;
+        per_block = threads < block ? block / threads : 1;
+        const int n = resident / (threads * per_block);
+        per_sm = n > 1 ? n : 1;
+    }
+};
+// The most threads of the small variant of the forward kernel.
+template <int V>
+constexpr int most_threads = V == 1 ? 256 : 128;
+template <int V>
+Rows forward_rows(int K) { return Rows(K, cols_of<V>, V == 1 ? 1 : 128, V == 1 ? 1280 : 640); }
+template <int V>
+Rows backward_rows(int K) { return Rows(K, cols_of<V>, V == 1 ? 1 : 256, V == 1 ? 1120 : 512); }
+
+constexpr int kSms = 152;
+// Partial sums of the backward kernel, its blocks: each is 2 K floats that the fold reads again.
+template <int V>
+int parts_of(int K) { return kSms * backward_rows<V>(K).per_sm; }
 
 // Sum over the block, the same value in every thread. `s`: one float per warp.
 __device__ __forceinline__ float block_sum(float v, float* s) {
@@ -131,7 +152,17 @@ struct Share {
 };
 
 // Sums over the threads of a row (blockDim.x of them, a row per threadIdx.y), the same in all.
-// `s`: 32 places per row, another one at the next call, so that one barrier is enough.
+// `s`: 32 places per row, other ones at the next call, so that one barrier is enough.
+__device__ __forceinline__ float row_sum(float v, float* s) {
+    v = warp_sum(v);
+    if (blockDim.x == 32) return v;
+    s += threadIdx.y * 32;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = s[0];
+    for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v += s[i];
+    return v;
+}
 __device__ __forceinline__ float2 row_sum(float2 v, float2* s) {
 #pragma unroll
     for (int o = 16; o; o >>= 1)
@@ -145,125 +176,270 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2* s) {
     return v;
 }
 
-// kThreads, here and below: the most threads of a block. The number of blocks that an SM is
-// to hold bounds the registers, so that enough rows are under way.
-template <typename T, typename P, int V, int IT, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 6 : 1)
-    layer_norm_rows_kernel(const T* x, int64_t M, int K, const P* __restrict__ weight, const P* __restrict__ bias, float eps,
-                           T* y, float* __restrict__ mean_out, float* __restrict__ rstd_out, bool vec) {
-    using S = Share<T, V, IT>;
-    __shared__ float2 s[2][4 * 32];
-    pdl_wait();
-    pdl_trigger();
-    const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const bool in = r < M;  // threads of absent rows keep the barriers company
-    const int tx = threadIdx.x, threads = blockDim.x;
-    S xs;
-    xs.load(x + (in ? r : 0) * K, in ? K : 0, tx, threads, vec);
-    float2 a = both(0.f);
-#pragma unroll
-    for (int p = 0; p < S::kPairs; ++p) a = __fadd2_rn(a, xs.get(p));
-    a = row_sum(both(a.x + a.y), s[0]);
-    const float mean = a.x / K;
-    a = both(0.f);
-#pragma unroll
-    for (int p = 0; p < S::kPairs; ++p) {
-        float2 d = __fadd2_rn(xs.get(p), both(-mean));
-        if (S::column(p, tx, threads) >= K) d = both(0.f);
-        if (V == 1 && S::column(p, tx, threads) + threads >= K) d.y = 0.f;
-        a = __ffma2_rn(d, d, a);
-    }
-    a = row_sum(both(a.x + a.y), s[1]);
-    const float rstd = 1.f / sqrtf(a.x / K + eps);
-    if (!in) return;
-    // a vector (V = 1: a pair) of parameters at a time
-    constexpr int kStep = V > 1 ? V / 2 : 1;
-#pragma unroll
-    for (int p0 = 0; p0 < S::kPairs; p0 += kStep) {
-        const int c = S::column(p0, tx, threads);
-        if (c >= K) break;
-        Share<P, V, (V > 1 ? 1 : 2)> w, b;
-        w.load(weight + c, K - c, 0, threads, vec);
-        if (bias) b.load(bias + c, K - c, 0, threads, vec);
-#pragma unroll
-        for (int q = 0; q < kStep; ++q) {
-            const float2 h = __fmul2_rn(__fadd2_rn(xs.get(p0 + q), both(-mean)), both(rstd));
-            xs.set(p0 + q, __ffma2_rn(h, w.get(q), bias ? b.get(q) : both(0.f)));
-        }
-    }
-    xs.store(y + r * K, K, tx, threads, vec);
-    if (tx == 0) {
-        if (mean_out) mean_out[r] = mean;
-        if (rstd_out) rstd_out[r] = rstd;
-    }
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ring_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
+// A block's next rows, some of them in turn, on their way from global to shared memory by
+// cp.async. V > 1: every thread copies and reads only its own share, no barrier is needed.
+template <typename T, int V, int IT>
+struct Ring {
+    static constexpr int kBytes = V * (int)sizeof(T);  // of a vector
+    uint8_t* mine;  // this thread's first vector; the others `stride` bytes apart
+    int stride;
+    __device__ __forceinline__ Ring(uint8_t* smem, int stages, const T*, int64_t, int K) {
+        const int n = blockDim.x * blockDim.y;
+        mine = smem + (threadIdx.y * blockDim.x + threadIdx.x) * kBytes;
+        stride = n * kBytes;
+        for (int i = 0; i < stages * IT; ++i)
+            if ((int)(i % IT * blockDim.x + threadIdx.x) * V >= K)  // what no column fills is zero
+                for (int j = 0; j < kBytes / 4; ++j) reinterpret_cast<uint32_t*>(mine + i * stride)[j] = 0;
+    }
+    // bytes of a stage
+    static __host__ __device__ size_t bytes(int K, int threads, int per_block) {
+        return (size_t)threads * per_block * IT * kBytes;
+    }
+    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, bool vec) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = (i * blockDim.x + threadIdx.x) * V;
+            if (c >= K) continue;
+            uint8_t* to = mine + (stage * IT + i) * stride;
+            if (vec)
+                copy16(to, row + c);
+            else
+                for (int j = 0; j < V; ++j) reinterpret_cast<T*>(to)[j] = row[c + j];
+        }
+    }
+    __device__ __forceinline__ void read(int stage, const T*, int, Share<T, V, IT>& s) const {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4*>(mine + (stage * IT + i) * stride);
+            s.w[4 * i] = u.x, s.w[4 * i + 1] = u.y, s.w[4 * i + 2] = u.z, s.w[4 * i + 3] = u.w;
+        }
+    }
+    static __device__ __forceinline__ void landed() {}
+};
+// V = 1: the threads of a row copy the 16-byte pieces that it lies in together (a row may start
+// anywhere), and read single values from there after a barrier. A piece that is not wholly inside
+// the tensor is copied value by value.
+template <typename T, int IT>
+struct Ring<T, 1, IT> {
+    uint8_t* mine;  // this row's first stage
+    int stride;     // bytes of a stage of the block
+    const T *first, *last;
+    __device__ __forceinline__ Ring(uint8_t* smem, int stages, const T* x, int64_t n, int K) : first(x), last(x + n) {
+        const int row = row_bytes(K);
+        mine = smem + threadIdx.y * row;
+        stride = row * blockDim.y;
+    }
+    static __host__ __device__ int row_bytes(int K) { return (K * (int)sizeof(T) + 15) / 16 * 16 + 16; }
+    static __host__ __device__ size_t bytes(int K, int threads, int per_block) { return (size_t)row_bytes(K) * per_block; }
+    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, bool) {
+        const T* from = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(row) & ~uintptr_t(15));
+        constexpr int N = 16 / sizeof(T);
+        T* to = reinterpret_cast<T*>(mine + stage * stride);
+        for (int c = threadIdx.x * N; from + c < row + K; c += blockDim.x * N) {
+            if (from + c >= first && from + c + N <= last)
+                copy16(to + c, from + c);
+            else
+                for (int j = 0; j < N; ++j)
+                    if (from + c + j >= row && from + c + j < row + K) to[c + j] = from[c + j];
+        }
+    }
+    __device__ __forceinline__ void read(int stage, const T* row, int K, Share<T, 1, IT>& s) const {
+        const T* at = reinterpret_cast<const T*>(mine + stage * stride + (reinterpret_cast<uintptr_t>(row) & 15));
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int c = i * blockDim.x + threadIdx.x;
+            s.w[i] = c < K ? __float_as_uint(to_f32(at[c])) : 0u;
+        }
+    }
+    static __device__ __forceinline__ void landed() {
+        if (blockDim.x == 32)
+            __syncwarp();
+        else
+            __syncthreads();
+    }
+};
+
+template <int V>
+constexpr int its = cols_of<V> / V;  // vectors of a thread
+// S, below: the stages of a block's ring. 0: none -- single fp32 values, coalesced as they are, are
+// loaded straight into registers, forward by a block per row, backward one row ahead (30011 x 1111,
+// backward: 97 us, with a ring 112).
+
 // Block b takes the rows b * blockDim.y + threadIdx.y, then gridDim.x * blockDim.y further on.
-// (x - mean) * rstd is taken as x * rstd - mean * rstd in one rounding.
-template <typename T, typename P, int V, int IT, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : V * IT > 8 ? 2 : 3)
-    layer_norm_backward_kernel(const T* dy, const T* __restrict__ x, int64_t M, int K, const P* __restrict__ weight,
-                               const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* dx,
-                               float* __restrict__ parts, bool vec) {
-    using S = Share<T, V, IT>;
-    __shared__ float2 s[2][8 * 32];
-    extern __shared__ float cols[];  // 2 * K, where the block has several rows at a time
+// kThreads, here and below: the most threads of a block.
+template <typename T, typename P, int V, int S, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 256 ? 5 : 1)
+    layer_norm_rows_kernel(const T* x, int64_t M, int K, float inv_k, const P* __restrict__ weight, const P* __restrict__ bias,
+                           float eps, T* y, float* __restrict__ mean_out, float* __restrict__ rstd_out, bool vec) {
+    using Sh = Share<T, V, its<V>>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float2 s[4][4 * 32];
     pdl_wait();
     pdl_trigger();
     const int tx = threadIdx.x, threads = blockDim.x;
-    Share<P, V, IT> w;
+    Share<P, V, its<V>> w, bs;
     w.load(weight, K, tx, threads, vec);
-    float2 dw[S::kPairs], db[S::kPairs];
-#pragma unroll
-    for (int p = 0; p < S::kPairs; ++p) dw[p] = db[p] = both(0.f);
+    if (bias)
+        bs.load(bias, K, tx, threads, vec);
+    else
+        bs.load(weight, 0, tx, threads, vec);  // zeros
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    S xs, ds, xn, dn;
-    float mean_n = 0.f, rstd_n = 0.f;
-    auto fetch = [&](int64_t r) {
-        const bool in = r < M;
-        xn.load(x + (in ? r : 0) * K, in ? K : 0, tx, threads, vec);
-        dn.load(dy + (in ? r : 0) * K, in ? K : 0, tx, threads, vec);
-        mean_n = in ? __ldg(mean_in + r) : 0.f;
-        rstd_n = in ? __ldg(rstd_in + r) : 0.f;
-    };
     int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    fetch(r);
-    int turn = 0;
-    // all rows of the block take the same number of turns (absent ones are zeros)
-    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < M; r0 += step, r += step, turn ^= 1) {
-        xs = xn;
-        ds = dn;
-        const float rstd = rstd_n, shift = -mean_n * rstd_n;
-        if (r0 + step < M) fetch(r + step);
-        float2 a = both(0.f), b = both(0.f);
-#pragma unroll
-        for (int p = 0; p < S::kPairs; ++p) {
-            const float2 d = ds.get(p), h = __ffma2_rn(xs.get(p), both(rstd), both(shift)), g = __fmul2_rn(d, w.get(p));
-            a = __fadd2_rn(a, g);
-            b = __ffma2_rn(g, h, b);
-            dw[p] = __ffma2_rn(d, h, dw[p]);
-            db[p] = __fadd2_rn(db[p], d);
+    const int64_t rows = M - (int64_t)blockIdx.x * blockDim.y;  // from the block's first row on
+    const int turns = (int)((rows + step - 1) / step);
+    Sh xs;
+    Ring<T, V, its<V>> ring(smem, S, x, M * K, K);
+    auto fetch = [&](int i) {
+        const int64_t q = r + (int64_t)i * step;
+        if (q < M) ring.fetch(i % (S > 0 ? S : 1), x + q * K, K, vec);
+        ring_commit();
+    };
+    if constexpr (S > 0)
+        for (int i = 0; i < S - 1; ++i) fetch(i);
+    int at = 0;
+    for (int i = 0; i < turns; ++i) {
+        const int64_t q = r + (int64_t)i * step;
+        if constexpr (S > 0) {
+            fetch(i + S - 1);
+            ring_wait<S - 1>();
+            ring.landed();
+            ring.read(i % S, x + q * K, K, xs);
+        } else {
+            xs.load(x + (q < M ? q : 0) * K, q < M ? K : 0, tx, threads, false);
         }
-        a = row_sum(make_float2(a.x + a.y, b.x + b.y), s[turn]);
-        if (r < M) {
-            // rstd * (g - a - h b)
-            const float2 c = both(-a.x / K * rstd), e = both(-a.y / K);
+        float2 a = both(0.f);
 #pragma unroll
-            for (int p = 0; p < S::kPairs; ++p) {
+        for (int p = 0; p < Sh::kPairs; ++p) a = __fadd2_rn(a, xs.get(p));
+        const float mean = row_sum(a.x + a.y, &s[at][0].x) * inv_k;
+        a = both(0.f);
+#pragma unroll
+        for (int p = 0; p < Sh::kPairs; ++p) {
+            float2 d = __fadd2_rn(xs.get(p), both(-mean));
+            if (Sh::column(p, tx, threads) >= K) d = both(0.f);
+            if (V == 1 && Sh::column(p, tx, threads) + threads >= K) d.y = 0.f;
+            a = __ffma2_rn(d, d, a);
+        }
+        const float rstd = 1.f / sqrtf(fmaf(row_sum(a.x + a.y, &s[at + 1][0].x), inv_k, eps));
+        at ^= 2;
+        if (q < M) {
+#pragma unroll
+            for (int p = 0; p < Sh::kPairs; ++p) {
+                const float2 h = __fmul2_rn(__fadd2_rn(xs.get(p), both(-mean)), both(rstd));
+                xs.set(p, __ffma2_rn(h, w.get(p), bs.get(p)));
+            }
+            xs.store(y + q * K, K, tx, threads, vec);
+            if (tx == 0) {
+                if (mean_out) mean_out[q] = mean;
+                if (rstd_out) rstd_out[q] = rstd;
+            }
+        }
+    }
+    if constexpr (S > 0) ring_wait<0>();
+}
+
+// (x - mean) * rstd is taken as x * rstd - mean * rstd in one rounding.
+template <typename T, typename P, int V, int S, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : V == 1 ? 3 : 2)
+    layer_norm_backward_kernel(const T* dy, const T* __restrict__ x, int64_t M, int K, float inv_k,
+                               const P* __restrict__ weight, const float* __restrict__ mean_in,
+                               const float* __restrict__ rstd_in, T* dx, float* __restrict__ parts, bool vec) {
+    using Sh = Share<T, V, its<V>>;
+    __shared__ float2 s[2][8 * 32];
+    extern __shared__ __align__(16) uint8_t smem[];  // the ring; at the end 2 K floats where a block has several rows
+    pdl_wait();
+    pdl_trigger();
+    const int tx = threadIdx.x, threads = blockDim.x;
+    Share<P, V, its<V>> w;
+    w.load(weight, K, tx, threads, vec);
+    float2 dw[Sh::kPairs], db[Sh::kPairs];
+#pragma unroll
+    for (int p = 0; p < Sh::kPairs; ++p) dw[p] = db[p] = both(0.f);
+    const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t rows = M - (int64_t)blockIdx.x * blockDim.y;
+    const int turns = (int)((rows + step - 1) / step);
+    Sh xs, ds;
+    float mean_n = 0.f, rstd_n = 0.f;
+    using R = Ring<T, V, its<V>>;
+    R rx(smem, S, x, M * K, K), rd(smem + S * R::bytes(K, threads, blockDim.y), S, dy, M * K, K);
+    Sh xn, dn;  // S = 0
+    auto fetch = [&](int i) {
+        const int64_t q = r + (int64_t)i * step;
+        if constexpr (S > 0) {
+            if (q < M) {
+                rx.fetch(i % S, x + q * K, K, vec);
+                rd.fetch(i % S, dy + q * K, K, vec);
+            }
+            ring_commit();
+        } else {
+            xn.load(x + (q < M ? q : 0) * K, q < M ? K : 0, tx, threads, false);
+            dn.load(dy + (q < M ? q : 0) * K, q < M ? K : 0, tx, threads, false);
+        }
+    };
+    auto statistics = [&](int i) {
+        const int64_t q = r + (int64_t)i * step;
+        mean_n = q < M ? __ldg(mean_in + q) : 0.f;
+        rstd_n = q < M ? __ldg(rstd_in + q) : 0.f;
+    };
+    for (int i = 0; i < (S > 0 ? S - 1 : 1); ++i) fetch(i);
+    statistics(0);
+    for (int i = 0; i < turns; ++i) {
+        const int64_t q = r + (int64_t)i * step;
+        if constexpr (S > 0) {
+            fetch(i + S - 1);
+            ring_wait<S - 1>();
+            R::landed();
+            rx.read(i % S, x + q * K, K, xs);
+            rd.read(i % S, dy + q * K, K, ds);
+        } else {
+            xs = xn;
+            ds = dn;
+            if (i + 1 < turns) fetch(i + 1);
+        }
+        const bool in = q < M;
+        const float rstd = rstd_n, shift = -mean_n * rstd_n;
+        statistics(i + 1);
+        float2 a = both(0.f), b = both(0.f);
+        if (in) {
+#pragma unroll
+            for (int p = 0; p < Sh::kPairs; ++p) {
+                const float2 d = ds.get(p), h = __ffma2_rn(xs.get(p), both(rstd), both(shift)), g = __fmul2_rn(d, w.get(p));
+                a = __fadd2_rn(a, g);
+                b = __ffma2_rn(g, h, b);
+                dw[p] = __ffma2_rn(d, h, dw[p]);
+                db[p] = __fadd2_rn(db[p], d);
+            }
+        }
+        a = row_sum(make_float2(a.x + a.y, b.x + b.y), s[i & 1]);
+        if (in) {
+            // rstd * (g - a - h b)
+            const float2 c = both(-a.x * inv_k * rstd), e = both(-a.y * inv_k);
+#pragma unroll
+            for (int p = 0; p < Sh::kPairs; ++p) {
                 const float2 h = __ffma2_rn(xs.get(p), both(rstd), both(shift)), g = __fmul2_rn(ds.get(p), w.get(p));
                 xs.set(p, __ffma2_rn(__ffma2_rn(h, e, g), both(rstd), c));
             }
-            xs.store(dx + r * K, K, tx, threads, vec);
+            xs.store(dx + q * K, K, tx, threads, vec);
         }
     }
-    float* out = parts + (int64_t)blockIdx.x * 2 * K;
-    if (blockDim.y > 1) out = cols;
+    if constexpr (S > 0) ring_wait<0>();
+    float* cols = reinterpret_cast<float*>(smem);
+    float* out = blockDim.y > 1 ? cols : parts + (int64_t)blockIdx.x * 2 * K;
     for (int y = 0; y < blockDim.y; ++y) {  // the block's rows one after the other
-        if (y) __syncthreads();
+        if (blockDim.y > 1) __syncthreads();
         if (threadIdx.y == y) {
 #pragma unroll
-            for (int p = 0; p < S::kPairs; ++p) {
-                const int c = S::column(p, tx, threads), c2 = V > 1 ? c + 1 : c + threads;
+            for (int p = 0; p < Sh::kPairs; ++p) {
+                const int c = Sh::column(p, tx, threads), c2 = V > 1 ? c + 1 : c + threads;
                 if (c < K) {
                     out[c] = dw[p].x + (y ? out[c] : 0.f);
                     out[K + c] = db[p].x + (y ? out[K + c] : 0.f);
@@ -372,7 +548,7 @@ __global__ void __launch_bounds__(1024)
     const int c = blockIdx.x * 32 + tx;
     float a = 0.f;
     if (c < K) {
-#pragma unroll 4
+#pragma unroll 8
         for (int p = ty; p < n; p += 32) a += parts[((int64_t)p * 2 + blockIdx.y) * K + c];
     }
     s[ty][tx] = a;
@@ -386,13 +562,26 @@ bool norm_args_ok(int64_t M, int K, int dtype, int param_dtype) {
     return M >= 0 && M <= INT32_MAX && K >= 1 && dtype_bytes(dtype) && (param_dtype == dtype || param_dtype == MOE_DT_F32);
 }
 
-// Calls f with `it` (a power of two up to kMost) as a constant.
-template <int kMost, typename F>
-void with_it(int it, F&& f) {
-    if (it == kMost)
-        f(std::integral_constant<int, kMost>{});
-    else if constexpr (kMost > 1)
-        with_it<kMost / 2>(it, f);
+// Calls f with the stages of a ring that has `bytes` a stage in each of `per_sm` blocks, as a
+// constant; false where not even two fit.
+template <bool kRing, typename F>
+bool with_stages(size_t bytes, int per_sm, F&& f) {
+    if constexpr (!kRing) {
+        f(std::integral_constant<int, 0>{});
+        return true;
+    }
+    const size_t room = 200 * 1024 / per_sm;
+    if (4 * bytes <= room) f(std::integral_constant<int, 4>{});
+    else if (3 * bytes <= room) f(std::integral_constant<int, 3>{});
+    else if (2 * bytes <= room) f(std::integral_constant<int, 2>{});
+    else return false;
+    return true;
+}
+template <typename... KArgs, typename... Args>
+void launch_ring(void (*kernel)(KArgs...), unsigned grid, dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
+    if (smem + 4096 > 48 * 1024)  // with the kernels' own static arrays
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    launch_k(kernel, grid, block, smem, stream, std::forward<Args>(args)...);
 }
 
 // Calls f(T*, P*) with the element types of x and of the parameters.
@@ -422,7 +611,8 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
     if ((y != x && overlap(y, n, x, n)) || overlap(y, n, weight, (size_t)K * zp) ||
         overlap(y, n, bias, bias ? (size_t)K * zp : 0))
         return MOE_ERR_INVALID_ARG;
-    if (int st = check_device(nullptr)) return st;
+    int sms = 0;
+    if (int st = check_device(&sms)) return st;
     return with_types(dtype, param_dtype, [&](auto* t, auto* p) {
         using T = std::remove_pointer_t<decltype(t)>;
         using P = std::remove_pointer_t<decltype(p)>;
@@ -430,21 +620,20 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
         const bool vec = !misaligned(x, 16) && !misaligned(y, 16) && !misaligned(weight, 16) && !misaligned(bias, 16);
         auto rows = [&](auto vc) -> bool {
             constexpr int W = decltype(vc)::value;
-            const int nv = (K + W - 1) / W;
-            if (nv > 8 * 1024) return false;
-            const int it = nv > 128 ? 8 : nv > 64 ? 4 : nv > 32 || W == 1 ? 2 : 1;
-            const int threads = nv <= 256 ? 32 : ((nv + 7) / 8 + 31) / 32 * 32;
-            const dim3 block(threads, threads == 32 ? 4 : 1);
-            with_it<8>(it, [&](auto ic) {
-                constexpr int IT = decltype(ic)::value;
-                auto kernel = layer_norm_rows_kernel<T, P, W, (IT * W > 1 ? IT : 2), 128>;
-                if constexpr (IT == 8)  // more than a warp per row: always 8 vectors a thread
-                    if (threads > 128) kernel = layer_norm_rows_kernel<T, P, W, IT, 1024>;
-                launch_k(kernel, (unsigned)((M + block.y - 1) / block.y), block, 0,
-                         (cudaStream_t)stream, static_cast<const T*>(x), M, K, static_cast<const P*>(weight),
-                         static_cast<const P*>(bias), eps, static_cast<T*>(y), mean, rstd, vec);
+            const Rows g = forward_rows<W>(K);
+            if (g.threads > 1024) return false;
+            const int64_t blocks = (M + g.per_block - 1) / g.per_block, most = (int64_t)sms * g.per_sm;
+            const dim3 block(g.threads, g.per_block);
+            const size_t bytes = Ring<T, W, its<W>>::bytes(K, g.threads, g.per_block);
+            return with_stages<(W * sizeof(T) != 4)>(bytes, g.per_sm, [&](auto sc) {
+                constexpr int S = decltype(sc)::value;
+                auto kernel = g.threads <= most_threads<W> ? layer_norm_rows_kernel<T, P, W, S, most_threads<W>>
+                              : g.threads <= 512              ? layer_norm_rows_kernel<T, P, W, S, 512>
+                                                              : layer_norm_rows_kernel<T, P, W, S, 1024>;
+                launch_ring(kernel, (unsigned)(S == 0 || blocks < most ? blocks : most), block, bytes * S, (cudaStream_t)stream,
+                            static_cast<const T*>(x), M, K, 1.f / K, static_cast<const P*>(weight),
+                            static_cast<const P*>(bias), eps, static_cast<T*>(y), mean, rstd, vec);
             });
-            return true;
         };
         if (!(K % V == 0 ? rows(std::integral_constant<int, V>{}) : rows(std::integral_constant<int, 1>{})))
             launch_k(layer_norm_kernel<T, P>, (unsigned)M, kRowThreads, 0, (cudaStream_t)stream, static_cast<const T*>(x), K,
@@ -456,7 +645,10 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
 
 MOE_API size_t moe_layer_norm_workspace_size(int64_t M, int K) {
     if (M < 0 || K < 1) return 0;
-    return (size_t)most_parts(K) * 2 * K * sizeof(float);
+    // whichever way the rows are divided (by their type and alignment), the looping kernels too
+    int n = parts_of<1>(K) > parts_of<8>(K) ? parts_of<1>(K) : parts_of<8>(K);
+    if (n < kColParts) n = kColParts;
+    return (size_t)n * 2 * K * sizeof(float);
 }
 
 MOE_API int moe_layer_norm_backward(const void* dy, const void* x, int64_t M, int K, int dtype, const void* weight,
@@ -485,31 +677,23 @@ MOE_API int moe_layer_norm_backward(const void* dy, const void* x, int64_t M, in
         const bool vec = !misaligned(x, 16) && !misaligned(dy, 16) && !misaligned(dx, 16) && !misaligned(weight, 16);
         auto rows = [&](auto vc) -> bool {
             constexpr int W = decltype(vc)::value;
-            const int nv = (K + W - 1) / W;
-            // up to 16 columns a thread: their weights and two sums each stay in registers
-            constexpr int kMostIt = 16 / W;
-            if (nv > kMostIt * 1024) return false;
-            int it = W == 1 ? 2 : 1;
-            while (it < kMostIt && nv > 256 * it) it *= 2;
-            const int threads = ((nv + it - 1) / it + 31) / 32 * 32;
-            const dim3 block(threads, threads <= 128 ? 256 / threads : 1);
-            const int64_t blocks = (M + block.y - 1) / block.y;
-            n_parts = (int)(blocks < most_parts(K) ? blocks : most_parts(K));
-            with_it<kMostIt>(it, [&](auto ic) {
-                constexpr int IT = decltype(ic)::value;
-                if constexpr (IT * W <= 16 && IT * W > 1) {
-                    auto kernel = layer_norm_backward_kernel<T, P, W, IT, 256>;
-                    if constexpr (IT == kMostIt)
-                        if (threads > 256)
-                            kernel = threads > 512 ? layer_norm_backward_kernel<T, P, W, IT, 1024>
-                                                   : layer_norm_backward_kernel<T, P, W, IT, 512>;
-                    launch_k(kernel, (unsigned)n_parts, block,
-                             block.y > 1 ? 2 * K * sizeof(float) : 0, s, static_cast<const T*>(dy), static_cast<const T*>(x), M,
-                             K, static_cast<const P*>(weight), mean, rstd, static_cast<T*>(dx), parts, vec);
-                }
+            const Rows g = backward_rows<W>(K);
+            if (g.threads > 1024) return false;
+            const dim3 block(g.threads, g.per_block);
+            const int64_t blocks = (M + g.per_block - 1) / g.per_block;
+            n_parts = (int)(blocks < parts_of<W>(K) ? blocks : parts_of<W>(K));
+            const size_t bytes = 2 * Ring<T, W, its<W>>::bytes(K, g.threads, g.per_block);
+            return with_stages<(W * sizeof(T) != 4)>(bytes, g.per_sm, [&](auto sc) {
+                constexpr int S = decltype(sc)::value;
+                auto kernel = g.threads <= 256   ? layer_norm_backward_kernel<T, P, W, S, 256>
+                              : g.threads <= 512 ? layer_norm_backward_kernel<T, P, W, S, 512>
+                                                 : layer_norm_backward_kernel<T, P, W, S, 1024>;
+                const size_t sums = g.per_block > 1 ? 2 * K * sizeof(float) : 0;
+                launch_ring(kernel, (unsigned)n_parts, block, bytes * S < sums ? sums : bytes * S, s, static_cast<const T*>(dy),
+                            static_cast<const T*>(x), M, K, 1.f / K, static_cast<const P*>(weight), mean, rstd,
+                            static_cast<T*>(dx), parts, vec);
+                note_launches(1);
             });
-            note_launches(1);
-            return true;
         };
         if (M > 0 && !(K % V == 0 ? rows(std::integral_constant<int, V>{}) : rows(std::integral_constant<int, 1>{}))) {
             n_parts = (int)(M < kColParts ? M : kColParts);
