@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import os
 from array import array
+from operator import attrgetter
 from typing import Optional
 
 import torch
@@ -579,13 +580,16 @@ def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=
                     out_dtype, stream)
 
 
+_dtype_of, _is_cuda = attrgetter("dtype"), attrgetter("is_cuda")
+
+
 def _addresses(tensors) -> array:
     """The device addresses of a list of contiguous CUDA tensors."""
-    if not all([t.is_cuda for t in tensors]):
+    if not all(map(_is_cuda, tensors)):
         raise ValueError("expected CUDA tensors")
-    if not all([t.is_contiguous() for t in tensors]):
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
         raise ValueError("expected contiguous tensors")
-    return array("Q", [t.data_ptr() for t in tensors])
+    return array("Q", map(torch.Tensor.data_ptr, tensors))
 
 
 def moe_grad_norm_workspace_size(numels) -> int:
@@ -610,13 +614,12 @@ def _norm_call(fn, tensors, max_norm, out, norm, workspace, stream):
     n = len(tensors)
     if n == 0:
         raise ValueError(f"{fn}: no tensors")
-    dtypes = [t.dtype for t in tensors]
+    dtypes = list(map(_dtype_of, tensors))
     try:
-        types = array("i", [_DTYPES[d] for d in dtypes])
+        types = array("i", map(_DTYPES.__getitem__, dtypes))
     except KeyError as e:
         raise TypeError(f"{fn}: expected torch.float32, torch.bfloat16 or torch.float16, got {e.args[0]}") from None
-    sizes = [t.numel() for t in tensors]
-    lens = array("q", sizes)
+    lens = array("q", map(torch.Tensor.numel, tensors))
     ptrs = _addresses(tensors)
     dev = tensors[0].device
     if norm is None:
@@ -633,7 +636,7 @@ def _norm_call(fn, tensors, max_norm, out, norm, workspace, stream):
         outs = None
         if out is not None:
             out = list(out)
-            if [o.numel() for o in out] != sizes or [o.dtype for o in out] != dtypes:
+            if array("q", map(torch.Tensor.numel, out)) != lens or list(map(_dtype_of, out)) != dtypes:
                 raise ValueError(f"{fn}: outputs of other lengths or types than the tensors")
             outs = _addresses(out)
         st = lib().moe_clip_grad_norm(ptrs_at, lens_at, types_at, n, max_norm, outs.buffer_info()[0] if outs else None,
