@@ -8,10 +8,12 @@
 //   softmax, renormalised dl_i = scale * q_i * (g_i - sum_m q_m g_m),  q_i = s_i / S; 0 elsewhere
 //   sigmoid               dl_i = scale * g_i * s_i * (1 - s_i)
 //   sigmoid, renormalised dl_i = scale * q_i * (g_i - sum_m q_m g_m) * (1 - s_i)
-// The general kernels take one warp per token: lane i holds the V consecutive logits
+// The general forward kernel takes one warp per token: lane i holds the V consecutive logits
 // [i*V, (i+1)*V) in registers, so a tie goes to the lowest lane and then to its first value.
-// Without a bias and up to 16 choices the forward pass runs as router_list_kernel.
+// Without a bias and up to 16 choices the forward pass runs as router_list_kernel or, for large
+// batches of 16-bit logits, as router_pair_kernel.
 #include <climits>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "route.cuh"
@@ -166,8 +168,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
 // tie goes to the lower index), keeps the L largest keys in a sorted list by sorting networks, and
 // merges its list with its neighbours' (two exchanges). A 16-bit logit has 13 or 16 zero bits
 // below its fp32 form: its key is 32 bits and a comparator is two instructions; fp32 takes 64.
-// What bounds it is the issue of these instructions, not memory: about 70 per token of 128
-// 16-bit logits against 256 bytes read.
+// What bounds it is the ALU pipe (minima and maxima), not memory: about 110 instructions per
+// token of 128 16-bit logits against 256 bytes read.
 constexpr int kListThreads = 128;
 constexpr int kLanes = 4;             // per token
 constexpr uint32_t kIndexMask = 0x3ff;
@@ -347,88 +349,300 @@ __global__ void __launch_bounds__(kListThreads)
     }
 }
 
-template <typename T, typename TId, int V, bool kVec>
-__global__ void __launch_bounds__(kRouterWarps * 32)
-    router_backward_kernel(const T* logits, int64_t M, int E, const TId* __restrict__ ids, int topk, int scoring,
-                           int renorm, float scale, const float* __restrict__ dw, T* d_logits) {
+// The same for large batches of up to 128 16-bit logits and 8 choices: two lanes per token, so that
+// less of the work is merging, and keys made from packed pairs. Order and tie rules are those of
+// router_list_kernel. Bound by the ALU pipe like it: 2^20 tokens of 128 bf16 logits take 98.5 us
+// (3.4 TB/s, half of the copy rate) against its 141.
+constexpr int kPairThreads = 128;
+constexpr int kPairExperts = 128;
+// Smaller batches do not fill the SMs with two lanes a token.
+constexpr int64_t kPairTokens = 16384;
+
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b, const bf16*) {
+    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b, const fp16*) {
+    const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b, const bf16*) {
+    const __nv_bfloat162 r = __hadd2_rn(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b, const fp16*) {
+    const __half2 r = __hadd2_rn(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <typename T, typename TId>
+__global__ void __launch_bounds__(kPairThreads)
+    router_pair_kernel(const T* __restrict__ logits, int64_t M, int E, int topk, int scoring, int renorm, float scale,
+                       float* __restrict__ out_w, TId* __restrict__ out_id) {
+    constexpr uint32_t kLow = std::is_same<T, bf16>::value ? 0xff80ff80u : 0xfc00fc00u;  // a pair of -inf
+    constexpr T* kType = nullptr;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5);
-    if (t >= M) return;
+    const int lane = threadIdx.x & 1;
+    int64_t t = (int64_t)blockIdx.x * (kPairThreads / 2) + threadIdx.x / 2;
+    const bool real = t < M;
+    if (!real) t = M - 1;
+    const T* row = logits + t * E + lane * 8;  // this lane's 8 of every 16 logits
+    uint4 raw[kPairExperts / 16];
+#pragma unroll
+    for (int c = 0; c < kPairExperts / 16; ++c) {
+        raw[c] = make_uint4(kLow, kLow, kLow, kLow);
+        if (c * 16 + lane * 8 < E) raw[c] = *reinterpret_cast<const uint4*>(row + c * 16);
+    }
+    uint32_t best[8];
+#pragma unroll
+    for (int c = 0; c < kPairExperts / 16; ++c) {
+        if (c > 0 && c * 16 >= E) break;
+        uint32_t now[8];
+        const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // NaN becomes -inf, -0 becomes +0, then each half the order of its value
+            const uint32_t w = hadd2(hmax2(w4[j], kLow, kType), 0u, kType);
+            const uint32_t order = w ^ ((w >> 15 & 0x00010001u) * 0x7fffu + 0x80008000u);
+            const uint32_t index = kIndexMask - (c * 16 + 2 * j);
+            now[2 * j] = order * 65536u + index;
+            now[2 * j + 1] = (order & 0xffff0000u) | (index - 1);
+        }
+        sort_list(now);
+        if (c == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) best[i] = now[i];
+        } else {
+            merge_lists(best, now);
+        }
+    }
+    uint32_t other[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) best[i] -= lane * 8;  // the index counted from the row's start
+#pragma unroll
+    for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(0xffffffffu, best[i], 1);
+    merge_lists(best, other);
+    // lane q has places 4q to 4q + 3
     const bool soft = scoring == MOE_SCORE_SOFTMAX;
-    // lane i: slot i
-    int id = -1;
-    float g = 0.f, l = -INFINITY;
-    if (lane < topk) {
-        const TId raw = ids[t * topk + lane];
-        if (raw >= 0 && raw < TId(E)) {
-            id = (int)raw;
-            g = scale * dw[t * topk + lane];
-            l = clean_logit(to_f32(logits[t * E + id]));
-        }
+    auto logit_of = [&](uint32_t k) {
+        const uint32_t o = k >> 16;
+        const uint16_t u = (uint16_t)(o & 0x8000u ? o ^ 0x8000u : ~o);
+        return fminf(to_f32(*reinterpret_cast<const T*>(&u)), kFltMax);
+    };
+    const float top = logit_of(best[0]);
+    float w[4], sum = 0.f;
+    int id[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t k = lane ? best[4 + i] : best[i];
+        const float l = logit_of(k);
+        const bool chosen = l > -INFINITY && lane * 4 + i < topk;
+        id[i] = chosen ? (int)(kIndexMask - (k & kIndexMask)) : -1;
+        if (soft)
+            w[i] = chosen ? expf(l - top) : 0.f;
+        else if (renorm)  // as sigmoid_share has it
+            w[i] = chosen ? expf(fminf(l, 0.f) - fminf(0.f, top)) / (1.f + expf(-fabsf(l))) : 0.f;
+        else
+            w[i] = chosen ? sigmoid(l) : 0.f;
+        sum += w[i];
     }
-    float v[V];
-    float top = -INFINITY, sum = 0.f, dot = 0.f, d = 0.f;
     if (soft && !renorm) {
-        load_logits<T, V, kVec>(logits + t * E, lane, E, v);
+        sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) top = fmaxf(top, v[j]);
-        top = warp_max(top);
-        if (top > -INFINITY) {
+        for (int c = 0; c < kPairExperts / 16; ++c) {
+            if (c * 16 >= E) break;
+            const uint32_t w4[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                v[j] = expf(v[j] - top);
-                sum += v[j];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) v[j] = 0.f;
-        }
-        sum = warp_sum(sum);
-        const float r = sum > 0.f ? 1.f / sum : 0.f;
-        const float s = l > -INFINITY ? expf(l - top) * r : 0.f;
-        dot = warp_sum(s * g);
-        d = s * (g - dot);
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = -dot * (v[j] * r);
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = 0.f;
-        if (soft) {
-            const float m = warp_max(l);
-            const float e = l > -INFINITY ? expf(l - m) : 0.f;
-            const float S = warp_sum(e);
-            const float q = S > 0.f ? e / S : 0.f;
-            dot = warp_sum(q * g);
-            d = q * (g - dot);
-        } else {
-            const float one_less = sigmoid(-l);
-            if (renorm) {
-                const float q = sigmoid_share(l);
-                dot = warp_sum(q * g);
-                d = q * (g - dot) * one_less;
-            } else {
-                d = l > -INFINITY ? g * sigmoid(l) * one_less : 0.f;
+            for (int j = 0; j < 8; ++j) {
+                const uint16_t u = (uint16_t)(w4[j / 2] >> (j % 2 * 16));
+                sum += __expf(clean_logit(to_f32(*reinterpret_cast<const T*>(&u))) - top);
             }
         }
     }
-    __syncwarp();  // every logit of the row is read: d_logits may be logits
-    T* row = d_logits + t * E;
-    if constexpr (kVec) {
-        if (lane * V < E) {
-            Vec<T, V> r;
+    if (soft || renorm) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        scale = sum > 0.f ? scale / sum : 0.f;  // 0 or NaN: nothing was chosen, all w are 0
+    }
+    if (!real) return;
 #pragma unroll
-            for (int j = 0; j < V; ++j) r.v[j] = from_f32<T>(v[j]);
-            *reinterpret_cast<Vec<T, V>*>(row + lane * V) = r;
+    for (int i = 0; i < 4; ++i) {
+        const int at = lane * 4 + i;
+        if (at < topk) {
+            out_w[t * topk + at] = w[i] * scale;
+            out_id[t * topk + at] = (TId)id[i];
         }
-    } else {
+    }
+}
+
+// ------------------------------------------------------------------ gradient
+// Eight lanes per token. A lane takes the slots lane, lane + 8, ... and 8 of every 64 logits. The
+// row is read twice where its softmax is needed (the second time from L1): once for the maximum
+// and the sum, once for the values that are written.
+constexpr int kGradThreads = 128;
+constexpr int kGradLanes = 8;
+constexpr int kSlots = 32 / kGradLanes;
+
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (lane * V + j < E) row[lane * V + j] = from_f32<T>(v[j]);
+    for (int o = 1; o < kGradLanes; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = 1; o < kGradLanes; o *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// V = 8: in a row (E a multiple of 8, rows on 16-byte boundaries); else every eighth.
+template <bool kVec>
+__device__ __forceinline__ int grad_expert(int chunk, int lane, int j) {
+    return kVec ? chunk * 64 + lane * 8 + j : chunk * 64 + j * kGradLanes + lane;
+}
+
+template <typename T, typename TId, bool kVec>
+__global__ void __launch_bounds__(kGradThreads)
+    router_backward_kernel(const T* logits, int64_t M, int E, const TId* __restrict__ ids, int topk, int scoring,
+                           int renorm, float scale, const float* __restrict__ dw, T* d_logits) {
+    constexpr int N = 16 / sizeof(T);
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & (kGradLanes - 1);
+    int64_t t = (int64_t)blockIdx.x * (kGradThreads / kGradLanes) + threadIdx.x / kGradLanes;
+    const bool real = t < M;  // the lanes past the last token go along on the last one's row, and write nothing
+    if (!real) t = M - 1;
+    const bool soft = scoring == MOE_SCORE_SOFTMAX;
+    const T* row = logits + t * E;
+    // this lane's slots
+    int id[kSlots];
+    float g[kSlots], l[kSlots];
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        const int at = i * kGradLanes + lane;
+        id[i] = -1;
+        g[i] = 0.f;
+        l[i] = -INFINITY;
+        if (at < topk) {
+            const TId raw = ids[t * topk + at];
+            if (raw >= 0 && raw < TId(E)) {
+                id[i] = (int)raw;
+                g[i] = scale * dw[t * topk + at];
+                l[i] = clean_logit(to_f32(row[id[i]]));
+            }
+        }
+    }
+    auto load = [&](int c, float (&v)[8]) {
+        if constexpr (kVec) {
+            if (c * 64 + lane * 8 < E) {
+#pragma unroll
+                for (int h = 0; h < 8; h += N) {
+                    const Vec<T, N> r = *reinterpret_cast<const Vec<T, N>*>(row + c * 64 + lane * 8 + h);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) v[h + j] = clean_logit(to_f32(r.v[j]));
+                }
+                return;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = grad_expert<kVec>(c, lane, j);
+            v[j] = !kVec && e < E ? clean_logit(to_f32(row[e])) : -INFINITY;
+        }
+    };
+    const int chunks = (E + 63) / 64;
+    float d[kSlots];
+    float top = 0.f, rest = 0.f;  // what an expert that was not chosen gets: rest * exp(logit - top)
+    if (soft && !renorm) {
+        float m = -INFINITY, sum = 0.f;
+#pragma unroll 2
+        for (int c = 0; c < chunks; ++c) {
+            float v[8], most = m;
+            load(c, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = fmaxf(most, v[j]);
+            if (most > -INFINITY) {
+                sum *= __expf(m - most);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum += __expf(v[j] - most);
+                m = most;
+            }
+        }
+        top = group_max(m);
+        sum = group_sum(m > -INFINITY ? sum * __expf(m - top) : 0.f);
+        const float r = sum > 0.f ? 1.f / sum : 0.f;
+        float s[kSlots], dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            s[i] = l[i] > -INFINITY ? expf(l[i] - top) * r : 0.f;
+            dot = fmaf(s[i], g[i], dot);
+        }
+        dot = group_sum(dot);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) d[i] = s[i] * (g[i] - dot);
+        rest = -dot * r;
+    } else {
+        // the share of a chosen score in the chosen scores' sum, each taken times exp(-low) so that
+        // scores too small for fp32 keep their ratios (renormalised), or the score itself
+        float m = -INFINITY, S = 0.f, dot = 0.f, q[kSlots];
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) m = fmaxf(m, l[i]);
+        m = group_max(m);
+        if (!soft) m = renorm ? fminf(0.f, m) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            const bool in = l[i] > -INFINITY;
+            q[i] = !in ? 0.f : soft ? expf(l[i] - m) : expf(fminf(l[i], 0.f) - m) / (1.f + expf(-fabsf(l[i])));
+            S += q[i];
+        }
+        if (renorm) {
+            S = group_sum(S);
+            const float r = S > 0.f ? 1.f / S : 0.f;
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                q[i] *= r;
+                dot = fmaf(q[i], g[i], dot);
+            }
+            dot = group_sum(dot);
+        }
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) d[i] = q[i] * (g[i] - dot) * (soft ? 1.f : sigmoid(-l[i]));
+    }
+    __syncwarp();  // the chosen logits are read: d_logits may be logits
+    T* out = d_logits + t * E;
+#pragma unroll 2
+    for (int c = 0; c < chunks; ++c) {
+        float v[8];
+        if (rest != 0.f) {
+            load(c, v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = rest * __expf(v[j] - top);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        }
+        if (!real) continue;
+        if constexpr (kVec) {
+            if (c * 64 + lane * 8 < E) {
+#pragma unroll
+                for (int h = 0; h < 8; h += N) {
+                    Vec<T, N> r;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) r.v[j] = from_f32<T>(v[h + j]);
+                    *reinterpret_cast<Vec<T, N>*>(out + c * 64 + lane * 8 + h) = r;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int e = grad_expert<false>(c, lane, j);
+                if (e < E) out[e] = from_f32<T>(v[j]);
+            }
+        }
     }
     __syncwarp();  // the chosen experts' values replace the ones just written
-    if (id >= 0) row[id] = from_f32<T>(d);
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+        if (real && id[i] >= 0) out[id[i]] = from_f32<T>(d[i]);
 }
 
 bool router_args_ok(int64_t M, int E, int dtype, int topk, int scoring) {
@@ -464,14 +678,17 @@ int router_impl(const void* logits, int64_t M, int E, int dtype, int topk, int s
     return with_dtype(dtype, [&](auto* p) {
         using T = std::remove_pointer_t<decltype(p)>;
         if (!bias && topk <= 16) {
-            auto go = [&](auto kernel) {
-                constexpr int per = kListThreads / kLanes;
+            auto go = [&](auto kernel, int per = kListThreads / kLanes) {
+                static_assert(kListThreads == kPairThreads, "one block size");
                 launch_k(kernel, (unsigned)((M + per - 1) / per), kListThreads, 0, (cudaStream_t)stream,
                          static_cast<const T*>(logits), M, E, topk, scoring, renorm ? 1 : 0, scale, w, ids);
                 note_launches(1);
                 return launch_status();
             };
             const bool vec = E % 8 == 0 && !misaligned(logits, 16);
+            if constexpr (sizeof(T) == 2)
+                if (vec && topk <= 8 && E <= kPairExperts && M >= kPairTokens)
+                    return go(router_pair_kernel<T, TId>, kPairThreads / 2);
             if (topk <= 8) return vec ? go(router_list_kernel<T, TId, 8, true>) : go(router_list_kernel<T, TId, 8, false>);
             return vec ? go(router_list_kernel<T, TId, 16, true>) : go(router_list_kernel<T, TId, 16, false>);
         }
@@ -503,22 +720,15 @@ int router_backward_impl(const void* logits, int64_t M, int E, int dtype, const 
         overlap(d_logits, nl, ids, (size_t)M * topk * sizeof(TId)) || overlap(d_logits, nl, dw, (size_t)M * topk * 4))
         return MOE_ERR_INVALID_ARG;
     if (int st = check_device(nullptr)) return st;
-    const unsigned grid = (unsigned)((M + kRouterWarps - 1) / kRouterWarps);
     return with_dtype(dtype, [&](auto* p) {
         using T = std::remove_pointer_t<decltype(p)>;
-        return with_v(E, [&](auto vc) {
-            constexpr int V = decltype(vc)::value;
-            auto go = [&](auto kernel) {
-                launch_k(kernel, grid, kRouterWarps * 32, 0, (cudaStream_t)stream, static_cast<const T*>(logits), M, E, ids,
-                         topk, scoring, renorm ? 1 : 0, scale, dw, static_cast<T*>(d_logits));
-                note_launches(1);
-                return launch_status();
-            };
-            if constexpr (fits_vec<T, V>())
-                if (E % V == 0 && !misaligned(logits, V * sizeof(T)) && !misaligned(d_logits, V * sizeof(T)))
-                    return go(router_backward_kernel<T, TId, V, true>);
-            return go(router_backward_kernel<T, TId, V, false>);
-        });
+        constexpr int per = kGradThreads / kGradLanes;
+        const bool vec = E % 8 == 0 && !misaligned(logits, 16) && !misaligned(d_logits, 16);
+        launch_k(vec ? router_backward_kernel<T, TId, true> : router_backward_kernel<T, TId, false>,
+                 (unsigned)((M + per - 1) / per), kGradThreads, 0, (cudaStream_t)stream, static_cast<const T*>(logits), M, E, ids,
+                 topk, scoring, renorm ? 1 : 0, scale, dw, static_cast<T*>(d_logits));
+        note_launches(1);
+        return launch_status();
     });
 }
 

@@ -80,6 +80,22 @@ def test_masks_ties_and_extremes(scoring, renorm):
     check_forward(torch.tensor(rows, device="cuda"), 8, scoring, renorm, 1.0, ids_dtype=torch.int64)
 
 
+@pytest.mark.parametrize("E,topk", [(128, 8), (120, 5), (8, 8), (64, 1), (136, 8)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("scoring,renorm", [(SOFT, True), (SOFT, False), (SIGM, True), (SIGM, False)])
+def test_large_batches(E, topk, dtype, scoring, renorm):
+    """Many tokens, with ties (few distinct values), signed zeros, masks and NaN among them."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn(20011, E, device="cuda", generator=g)
+    logits[:5000] = (logits[:5000] * 2).round() / 2
+    logits[1000:2000] *= torch.where(torch.rand(1000, E, device="cuda", generator=g) < 0.5, 0.0, 1.0)
+    logits[3000:7000].masked_fill_(torch.rand(4000, E, device="cuda", generator=g) < 0.4, -float("inf"))
+    logits[6000:8000].masked_fill_(torch.rand(2000, E, device="cuda", generator=g) < 0.1, float("nan"))
+    logits[8000:8010] = -float("inf")
+    check_forward(logits.to(dtype), topk, scoring, renorm, 1.0)
+    check_forward(logits.to(dtype), topk, scoring, renorm, 0.5, ids_dtype=torch.int64)
+
+
 @pytest.mark.parametrize("scoring,renorm", [(SOFT, True), (SOFT, False), (SIGM, True), (SIGM, False)])
 @pytest.mark.parametrize("E", [16, 100, 256])
 def test_bias_moves_the_choice_only(scoring, renorm, E):
