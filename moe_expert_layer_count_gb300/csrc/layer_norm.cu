@@ -104,7 +104,17 @@ struct Share {
             }
         }
     }
-    __device__ __forceinline__ void store(T* __restrict__ row, int K, int tx, int threads, bool vec) const {
+    __device__ __forceinline__ void store(T* __restrict__ row, int K, int tx, int threads, bool vec, bool full) const {
+        if constexpr (V > 1) {
+            if (full) {
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    const uint32_t* o = w + i * kWords;
+                    *reinterpret_cast<uint4*>(row + (i * threads + tx) * V) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                return;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = (i * threads + tx) * V;
@@ -159,6 +169,10 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
     s += threadIdx.y * 32;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
+    if (blockDim.x == 128) {
+        const float4 f = *reinterpret_cast<const float4*>(s);
+        return (f.x + f.y) + (f.z + f.w);
+    }
     v = s[0];
     for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v += s[i];
     return v;
@@ -171,6 +185,10 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2* s) {
     s += threadIdx.y * 32;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
+    if (blockDim.x == 128) {
+        const float4 f = *reinterpret_cast<const float4*>(s), g = *reinterpret_cast<const float4*>(s + 2);
+        return make_float2((f.x + f.z) + (g.x + g.z), (f.y + f.w) + (g.y + g.w));
+    }
     v = s[0];
     for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v = __fadd2_rn(v, s[i]);
     return v;
@@ -204,7 +222,14 @@ struct Ring {
     static __host__ __device__ size_t bytes(int K, int threads, int per_block) {
         return (size_t)threads * per_block * IT * kBytes;
     }
-    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, bool vec) {
+    // `full`: every thread has IT whole vectors, and rows start on 16-byte boundaries
+    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, bool vec, bool full) {
+        if (full) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+                copy16(mine + (stage * IT + i) * stride, row + (i * blockDim.x + threadIdx.x) * V);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int c = (i * blockDim.x + threadIdx.x) * V;
@@ -240,7 +265,7 @@ struct Ring<T, 1, IT> {
     }
     static __host__ __device__ int row_bytes(int K) { return (K * (int)sizeof(T) + 15) / 16 * 16 + 16; }
     static __host__ __device__ size_t bytes(int K, int threads, int per_block) { return (size_t)row_bytes(K) * per_block; }
-    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, bool) {
+    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, bool, bool) {
         const T* from = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(row) & ~uintptr_t(15));
         constexpr int N = 16 / sizeof(T);
         T* to = reinterpret_cast<T*>(mine + stage * stride);
@@ -270,14 +295,26 @@ struct Ring<T, 1, IT> {
 
 template <int V>
 constexpr int its = cols_of<V> / V;  // vectors of a thread
-// S, below: the stages of a block's ring. 0: none -- single fp32 values, coalesced as they are, are
-// loaded straight into registers, forward by a block per row, backward one row ahead (30011 x 1111,
-// backward: 97 us, with a ring 112).
+// S, below: the stages of a block's ring. 0 (backward only): none -- single fp32 values, coalesced
+// as they are, are loaded straight into registers, one row ahead (30011 x 1111: 97 us, with a
+// ring 112).
 
 // Block b takes the rows b * blockDim.y + threadIdx.y, then gridDim.x * blockDim.y further on.
+struct Turns {
+    int64_t row, step;
+    int all, mine;  // rows of the block's first row of threads (each row of threads goes as far), of this one
+    __device__ __forceinline__ explicit Turns(int64_t M) {
+        const int64_t first = (int64_t)blockIdx.x * blockDim.y;
+        step = (int64_t)gridDim.x * blockDim.y;
+        row = first + threadIdx.y;
+        all = (int)((M - first + step - 1) / step);
+        mine = row < M ? (int)((M - row + step - 1) / step) : 0;
+    }
+};
+
 // kThreads, here and below: the most threads of a block.
 template <typename T, typename P, int V, int S, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 256 ? 5 : 1)
+__global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 256 ? 4 : 1)
     layer_norm_rows_kernel(const T* x, int64_t M, int K, float inv_k, const P* __restrict__ weight, const P* __restrict__ bias,
                            float eps, T* y, float* __restrict__ mean_out, float* __restrict__ rstd_out, bool vec) {
     using Sh = Share<T, V, its<V>>;
@@ -288,67 +325,68 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
     const int tx = threadIdx.x, threads = blockDim.x;
     Share<P, V, its<V>> w, bs;
     w.load(weight, K, tx, threads, vec);
-    if (bias)
-        bs.load(bias, K, tx, threads, vec);
-    else
-        bs.load(weight, 0, tx, threads, vec);  // zeros
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int64_t rows = M - (int64_t)blockIdx.x * blockDim.y;  // from the block's first row on
-    const int turns = (int)((rows + step - 1) / step);
+    bs.load(bias ? bias : weight, bias ? K : 0, tx, threads, vec);  // no bias: zeros
+    const Turns turn(M);
+    // every thread has whole columns (the way without checks costs registers, which 1024 threads lack)
+    const bool full = kThreads < 1024 && vec && K == threads * cols_of<V>;
     Sh xs;
     Ring<T, V, its<V>> ring(smem, S, x, M * K, K);
+    const int64_t hop = turn.step * K;
+    int64_t here = turn.row * K, ahead = here;  // this row's values, and the next row's to fetch
     auto fetch = [&](int i) {
-        const int64_t q = r + (int64_t)i * step;
-        if (q < M) ring.fetch(i % (S > 0 ? S : 1), x + q * K, K, vec);
+        if (i < turn.mine) ring.fetch(i % S, x + ahead, K, vec, full);
         ring_commit();
+        ahead += hop;
     };
-    if constexpr (S > 0)
-        for (int i = 0; i < S - 1; ++i) fetch(i);
+    for (int i = 0; i < S - 1; ++i) fetch(i);
     int at = 0;
-    for (int i = 0; i < turns; ++i) {
-        const int64_t q = r + (int64_t)i * step;
-        if constexpr (S > 0) {
-            fetch(i + S - 1);
-            ring_wait<S - 1>();
-            ring.landed();
-            ring.read(i % S, x + q * K, K, xs);
-        } else {
-            xs.load(x + (q < M ? q : 0) * K, q < M ? K : 0, tx, threads, false);
-        }
+    int64_t q = turn.row;
+    for (int i = 0; i < turn.all; ++i, q += turn.step, here += hop) {
+        fetch(i + S - 1);
+        ring_wait<S - 1>();
+        ring.landed();
+        ring.read(i % S, x + here, K, xs);
         float2 a = both(0.f);
 #pragma unroll
         for (int p = 0; p < Sh::kPairs; ++p) a = __fadd2_rn(a, xs.get(p));
         const float mean = row_sum(a.x + a.y, &s[at][0].x) * inv_k;
         a = both(0.f);
+        if (full) {
 #pragma unroll
-        for (int p = 0; p < Sh::kPairs; ++p) {
-            float2 d = __fadd2_rn(xs.get(p), both(-mean));
-            if (Sh::column(p, tx, threads) >= K) d = both(0.f);
-            if (V == 1 && Sh::column(p, tx, threads) + threads >= K) d.y = 0.f;
-            a = __ffma2_rn(d, d, a);
+            for (int p = 0; p < Sh::kPairs; ++p) {
+                const float2 d = __fadd2_rn(xs.get(p), both(-mean));
+                a = __ffma2_rn(d, d, a);
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < Sh::kPairs; ++p) {
+                float2 d = __fadd2_rn(xs.get(p), both(-mean));
+                if (Sh::column(p, tx, threads) >= K) d = both(0.f);
+                if (V == 1 && Sh::column(p, tx, threads) + threads >= K) d.y = 0.f;
+                a = __ffma2_rn(d, d, a);
+            }
         }
-        const float rstd = 1.f / sqrtf(fmaf(row_sum(a.x + a.y, &s[at + 1][0].x), inv_k, eps));
+        const float rstd = rsqrtf(fmaf(row_sum(a.x + a.y, &s[at + 1][0].x), inv_k, eps));
         at ^= 2;
-        if (q < M) {
+        if (i < turn.mine) {
 #pragma unroll
             for (int p = 0; p < Sh::kPairs; ++p) {
                 const float2 h = __fmul2_rn(__fadd2_rn(xs.get(p), both(-mean)), both(rstd));
                 xs.set(p, __ffma2_rn(h, w.get(p), bs.get(p)));
             }
-            xs.store(y + q * K, K, tx, threads, vec);
+            xs.store(y + here, K, tx, threads, vec, full);
             if (tx == 0) {
                 if (mean_out) mean_out[q] = mean;
                 if (rstd_out) rstd_out[q] = rstd;
             }
         }
     }
-    if constexpr (S > 0) ring_wait<0>();
+    ring_wait<0>();
 }
 
 // (x - mean) * rstd is taken as x * rstd - mean * rstd in one rounding.
 template <typename T, typename P, int V, int S, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : V == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
     layer_norm_backward_kernel(const T* dy, const T* __restrict__ x, int64_t M, int K, float inv_k,
                                const P* __restrict__ weight, const float* __restrict__ mean_in,
                                const float* __restrict__ rstd_in, T* dx, float* __restrict__ parts, bool vec) {
@@ -363,49 +401,51 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : V == 1 ? 3 : 2)
     float2 dw[Sh::kPairs], db[Sh::kPairs];
 #pragma unroll
     for (int p = 0; p < Sh::kPairs; ++p) dw[p] = db[p] = both(0.f);
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    const int64_t rows = M - (int64_t)blockIdx.x * blockDim.y;
-    const int turns = (int)((rows + step - 1) / step);
+    const Turns turn(M);
+    // every thread has whole columns (the way without checks costs registers, which 1024 threads lack)
+    const bool full = kThreads < 1024 && vec && K == threads * cols_of<V>;
     Sh xs, ds;
-    float mean_n = 0.f, rstd_n = 0.f;
     using R = Ring<T, V, its<V>>;
     R rx(smem, S, x, M * K, K), rd(smem + S * R::bytes(K, threads, blockDim.y), S, dy, M * K, K);
+    const int64_t hop = turn.step * K;
+    int64_t here = turn.row * K, ahead = here;  // this row's values, and the next row's to fetch
     Sh xn, dn;  // S = 0
     auto fetch = [&](int i) {
-        const int64_t q = r + (int64_t)i * step;
+        const bool in = i < turn.mine;
         if constexpr (S > 0) {
-            if (q < M) {
-                rx.fetch(i % S, x + q * K, K, vec);
-                rd.fetch(i % S, dy + q * K, K, vec);
+            if (in) {
+                rx.fetch(i % S, x + ahead, K, vec, full);
+                rd.fetch(i % S, dy + ahead, K, vec, full);
             }
             ring_commit();
         } else {
-            xn.load(x + (q < M ? q : 0) * K, q < M ? K : 0, tx, threads, false);
-            dn.load(dy + (q < M ? q : 0) * K, q < M ? K : 0, tx, threads, false);
+            xn.load(in ? x + ahead : x, in ? K : 0, tx, threads, false);
+            dn.load(in ? dy + ahead : dy, in ? K : 0, tx, threads, false);
         }
+        ahead += hop;
     };
+    float mean_n = 0.f, rstd_n = 0.f;
+    int64_t q = turn.row;
     auto statistics = [&](int i) {
-        const int64_t q = r + (int64_t)i * step;
-        mean_n = q < M ? __ldg(mean_in + q) : 0.f;
-        rstd_n = q < M ? __ldg(rstd_in + q) : 0.f;
+        mean_n = i < turn.mine ? __ldg(mean_in + q) : 0.f;
+        rstd_n = i < turn.mine ? __ldg(rstd_in + q) : 0.f;
+        q += turn.step;
     };
     for (int i = 0; i < (S > 0 ? S - 1 : 1); ++i) fetch(i);
     statistics(0);
-    for (int i = 0; i < turns; ++i) {
-        const int64_t q = r + (int64_t)i * step;
+    for (int i = 0; i < turn.all; ++i, here += hop) {
         if constexpr (S > 0) {
             fetch(i + S - 1);
             ring_wait<S - 1>();
             R::landed();
-            rx.read(i % S, x + q * K, K, xs);
-            rd.read(i % S, dy + q * K, K, ds);
+            rx.read(i % S, x + here, K, xs);
+            rd.read(i % S, dy + here, K, ds);
         } else {
             xs = xn;
             ds = dn;
-            if (i + 1 < turns) fetch(i + 1);
+            if (i + 1 < turn.all) fetch(i + 1);
         }
-        const bool in = q < M;
+        const bool in = i < turn.mine;
         const float rstd = rstd_n, shift = -mean_n * rstd_n;
         statistics(i + 1);
         float2 a = both(0.f), b = both(0.f);
@@ -428,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : V == 1 ? 3 : 2)
                 const float2 h = __ffma2_rn(xs.get(p), both(rstd), both(shift)), g = __fmul2_rn(ds.get(p), w.get(p));
                 xs.set(p, __ffma2_rn(__ffma2_rn(h, e, g), both(rstd), c));
             }
-            xs.store(dx + q * K, K, tx, threads, vec);
+            xs.store(dx + here, K, tx, threads, vec, full);
         }
     }
     if constexpr (S > 0) ring_wait<0>();
@@ -625,12 +665,12 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
             const int64_t blocks = (M + g.per_block - 1) / g.per_block, most = (int64_t)sms * g.per_sm;
             const dim3 block(g.threads, g.per_block);
             const size_t bytes = Ring<T, W, its<W>>::bytes(K, g.threads, g.per_block);
-            return with_stages<(W * sizeof(T) != 4)>(bytes, g.per_sm, [&](auto sc) {
+            return with_stages<true>(bytes, g.per_sm, [&](auto sc) {
                 constexpr int S = decltype(sc)::value;
                 auto kernel = g.threads <= most_threads<W> ? layer_norm_rows_kernel<T, P, W, S, most_threads<W>>
                               : g.threads <= 512              ? layer_norm_rows_kernel<T, P, W, S, 512>
                                                               : layer_norm_rows_kernel<T, P, W, S, 1024>;
-                launch_ring(kernel, (unsigned)(S == 0 || blocks < most ? blocks : most), block, bytes * S, (cudaStream_t)stream,
+                launch_ring(kernel, (unsigned)(blocks < most ? blocks : most), block, bytes * S, (cudaStream_t)stream,
                             static_cast<const T*>(x), M, K, 1.f / K, static_cast<const P*>(weight),
                             static_cast<const P*>(bias), eps, static_cast<T*>(y), mean, rstd, vec);
             });
