@@ -365,7 +365,7 @@ MOE_API int moe_host_wait(moe_stream_t stream);
  *   x, y     `dtype` [M, K], contiguous; y may be x itself
  *   weight   `param_dtype` [K];  bias `param_dtype` [K] or NULL (none)
  *   mean, rstd  fp32 [M], written (the backward pass reads them); both may be NULL
- *   param_dtype is `dtype` or MOE_DT_F32. 1 <= K. eps >= 0. Every pointer is aligned to
+ *   param_dtype is `dtype` or MOE_DT_F32. 1 <= K <= 2^24. eps >= 0. Every pointer is aligned to
  *   its element only; rows that start on 16-byte boundaries are moved 16 bytes at a time.
  * M = 0 does nothing. */
 MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const void* weight, const void* bias,

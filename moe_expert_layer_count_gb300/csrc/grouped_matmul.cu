@@ -261,6 +261,8 @@ struct __align__(16) Group {
     int start, lo, rows;
     uint32_t id;
 };
+// ceil(n / d) for n >= 0, without n + d overflowing.
+__device__ __forceinline__ int ceil_div(int n, int d) { return n > 0 ? (n - 1) / d + 1 : 0; }
 // wgrad: the bucket of a group of so many rows, four buckets an octave, the largest first.
 __device__ __forceinline__ int bucket_of(int rows) {
     return kBuckets - 1 - ((int)(__float_as_uint((float)rows + 1.f) >> 21) - 508);
@@ -306,7 +308,7 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, c
         t.n = kMaxN;
         t.lo = g.lo;
         t.rows = g.rows;
-        t.steps = (t.rows + kDepth - 1) / kDepth;
+        t.steps = ceil_div(t.rows, kDepth);
     } else {
         // the last group whose first tile is not past this one (an empty group starts where
         // the next one does): the block of `stride` groups, then the group
@@ -323,7 +325,7 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, c
         t.rows = min(per, g.rows - p * per);
         t.n = (t.rows + 15) & ~15;
         t.n0 = 0;
-        t.steps = (sh.depth + kDepth - 1) / kDepth;
+        t.steps = ceil_div(sh.depth, kDepth);
     }
     return t;
 }
@@ -387,8 +389,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         const int lo = min(max(__ldg(off + l), 0), R);
         const int end = cnt ? (int)min((int64_t)lo + max(__ldg(cnt + l), 0), (int64_t)R) : min(__ldg(off + l + 1), R);
         const int rows = max(end - lo, 0);
-        const int parts = max((rows + kMaxN - 1) / kMaxN, 1);
-        const int per = ((rows + parts - 1) / parts + 15) & ~15;
+        const int parts = max(ceil_div(rows, kMaxN), 1);
+        const int per = (ceil_div(rows, parts) + 15) & ~15;
         const int b = MODE == kWgrad ? bucket_of(rows) : 0;
         unsorted[l] = Group{b, lo, rows, (uint32_t)per << 16 | l};
         if (MODE == kWgrad) atomicAdd(&st->bucket[b], 1);
@@ -425,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             int base = 0;
             for (int l0 = 0; l0 < El; l0 += 32) {
                 const int l = l0 + lane;
-                const int mine = l < El ? (groups[l].rows + kMaxN - 1) / kMaxN * sh.m_tiles.d : 0;
+                const int mine = l < El ? ceil_div(groups[l].rows, kMaxN) * sh.m_tiles.d : 0;
                 const int sum = warp_prefix(mine);
                 if (l < El) groups[l].start = base + sum - mine;
                 base += __shfl_sync(0xffffffffu, sum, 31);
@@ -777,8 +779,8 @@ int launch_grouped(const void* a, const void* b, const int32_t* off, const int32
     int stages = (int)((kSmemLimit - fixed_smem<MODE>(El)) / kStageBytes);
     if (stages > kMaxStages) stages = kMaxStages;
     const size_t smem = fixed_smem<MODE>(El) + (size_t)stages * kStageBytes;
-    const int64_t m_tiles = ((MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;
-    const int64_t group_tiles = m_tiles * ((K + kMaxN - 1) / kMaxN);
+    const int64_t m_tiles = ((int64_t)(MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;
+    const int64_t group_tiles = m_tiles * (((int64_t)K + kMaxN - 1) / kMaxN);
     const Shape sh{{(int)m_tiles, magic_of(m_tiles)}, {(int)group_tiles, magic_of(group_tiles)}, MODE == kDgrad ? N : K};
     // no more pairs than tiles (an upper bound: the groups' sizes are not known here)
     const int64_t most = MODE == kWgrad ? El * group_tiles : (R / kMaxN + (R < El ? R : El)) * m_tiles;
@@ -800,8 +802,8 @@ int grouped_impl(const void* a, const void* b, const int32_t* off, const int32_t
         misaligned(out, 16))
         return MOE_ERR_INVALID_ARG;
     // tiles are counted in 32 bits
-    const int64_t m_tiles = ((MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;
-    if ((MODE == kWgrad ? El * m_tiles * ((K + kMaxN - 1) / kMaxN) : (R / kMaxN + El) * m_tiles) > INT32_MAX / 2)
+    const int64_t m_tiles = ((int64_t)(MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;
+    if ((MODE == kWgrad ? El * m_tiles * (((int64_t)K + kMaxN - 1) / kMaxN) : (R / kMaxN + El) * m_tiles) > INT32_MAX / 2)
         return MOE_ERR_INVALID_ARG;
     if (R == 0 && MODE != kWgrad) return MOE_OK;
     const size_t wn = (size_t)El * N * K;

@@ -46,6 +46,7 @@ Rows forward_rows(int K) { return Rows(K, cols_of<V>, V == 1 ? 1 : 128, V == 1 ?
 template <int V>
 Rows backward_rows(int K) { return Rows(K, cols_of<V>, V == 1 ? 1 : 256, V == 1 ? 1120 : 512); }
 
+constexpr int kMostColumns = 1 << 24;
 constexpr int kSms = 152;
 // Partial sums of the backward kernel, its blocks: each is 2 K floats that the fold reads again.
 template <int V>
@@ -71,66 +72,86 @@ __device__ __forceinline__ uint32_t bits_of(T v) {
         return *reinterpret_cast<const uint16_t*>(&v);
 }
 
-// One thread's share of a row: IT vectors of V values, `threads` vectors apart, held as the
-// 32-bit words they are loaded in (V = 1: as fp32). The share is used as pairs of values,
+// One thread's share of a row: IT vectors of V values, held as the 32-bit words they are loaded in
+// (V = 1: as fp32). A warp has 32 * IT vectors in a row; a lane every 32nd of them, from vector
+// `base` on, so that their addresses differ by constants. The share is used as pairs of values,
 // whichever vectors these lie in.
 template <typename T, int V, int IT>
 struct Share {
     static constexpr int kPairs = V * IT / 2;
     static constexpr int kWords = V > 1 ? V * (int)sizeof(T) / 4 : 1;  // of a vector
     uint32_t w[IT * kWords];
-    // values at or past K are zero; `vec`: the row starts on a 16-byte boundary (else one load
-    // per value, the same values to the same threads: results do not depend on the alignment)
-    __device__ __forceinline__ void load(const T* __restrict__ row, int K, int tx, int threads, bool vec) {
+    static __device__ __forceinline__ int base() { return (threadIdx.x & ~31u) * IT + (threadIdx.x & 31); }
+    // whether this warp's vectors all lie within K values and can be moved as such
+    static __device__ __forceinline__ bool whole(int K, bool vec) {
+        return ((int)(threadIdx.x >> 5) + 1) * 32 * IT * V <= K && (V == 1 || vec);
+    }
+    // values at or past K are zero; `vec`: the row starts on a 16-byte boundary (else one load per
+    // value, the same values to the same threads: results do not depend on the alignment); `whole`: as
+    // above, the way without checks
+    __device__ __forceinline__ void load(const T* __restrict__ row, int K, int base, bool vec, bool whole) {
+        row += base * V;
+        if (V > 1 && whole) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+#pragma unroll
+                for (int j = 0; j < kWords; j += 4) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(row + i * 32 * V) + j);
+                    uint32_t* o = w + i * kWords + j;
+                    o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w;
+                }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int c = (i * threads + tx) * V;
             uint32_t* o = w + i * kWords;
-            if (c >= K) {
+            const T* at = row + i * 32 * V;
+            if (!whole && (base + i * 32) * V >= K) {
 #pragma unroll
                 for (int j = 0; j < kWords; ++j) o[j] = 0;
             } else if constexpr (V == 1) {
-                o[0] = __float_as_uint(to_f32(row[c]));
+                o[0] = __float_as_uint(to_f32(at[0]));
             } else if (vec) {
 #pragma unroll
                 for (int j = 0; j < kWords; j += 4) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(row + c) + j);
+                    const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(at) + j);
                     o[j] = u.x, o[j + 1] = u.y, o[j + 2] = u.z, o[j + 3] = u.w;
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < kWords; ++j)
-                    o[j] = sizeof(T) == 4 ? bits_of(row[c + j]) : bits_of(row[c + 2 * j]) | bits_of(row[c + 2 * j + 1]) << 16;
+                    o[j] = sizeof(T) == 4 ? bits_of(at[j]) : bits_of(at[2 * j]) | bits_of(at[2 * j + 1]) << 16;
             }
         }
     }
-    __device__ __forceinline__ void store(T* __restrict__ row, int K, int tx, int threads, bool vec, bool full) const {
+    __device__ __forceinline__ void store(T* __restrict__ row, int K, int base, bool vec, bool whole) const {
+        row += base * V;
         if constexpr (V > 1) {
-            if (full) {
+            if (whole) {
 #pragma unroll
                 for (int i = 0; i < IT; ++i) {
                     const uint32_t* o = w + i * kWords;
-                    *reinterpret_cast<uint4*>(row + (i * threads + tx) * V) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(row + i * 32 * V) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
                 return;
             }
         }
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int c = (i * threads + tx) * V;
             const uint32_t* o = w + i * kWords;
-            if (c >= K) continue;
+            T* at = row + i * 32 * V;
+            if (!whole && (base + i * 32) * V >= K) continue;
             if constexpr (V == 1) {
-                row[c] = from_f32<T>(__uint_as_float(o[0]));
+                at[0] = from_f32<T>(__uint_as_float(o[0]));
             } else if (vec) {
-                *reinterpret_cast<uint4*>(row + c) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(at) = make_uint4(o[0], o[1], o[2], o[3]);
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     if constexpr (sizeof(T) == 4)
-                        row[c + j] = __uint_as_float(o[j]);
+                        at[j] = __uint_as_float(o[j]);
                     else
-                        reinterpret_cast<uint16_t*>(row)[c + j] = (uint16_t)(o[j / 2] >> (j % 2 * 16));
+                        reinterpret_cast<uint16_t*>(at)[j] = (uint16_t)(o[j / 2] >> (j % 2 * 16));
                 }
             }
         }
@@ -155,10 +176,11 @@ struct Share {
             w[p] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
-    // the column of the pair's first value (the second: the next, or `threads` on where V is 1)
-    static __device__ __forceinline__ int column(int p, int tx, int threads) {
-        return V > 1 ? (2 * p / V * threads + tx) * V + 2 * p % V : 2 * p * threads + tx;
+    // the columns of a pair's two values
+    static __device__ __forceinline__ int first(int p, int base) {
+        return V > 1 ? (base + 2 * p / V * 32) * V + 2 * p % V : base + 2 * p * 32;
     }
+    static __device__ __forceinline__ int second(int p, int base) { return first(p, base) + (V > 1 ? 1 : 32); }
 };
 
 // Sums over the threads of a row (blockDim.x of them, a row per threadIdx.y), the same in all.
@@ -215,33 +237,32 @@ struct Ring {
         mine = smem + (threadIdx.y * blockDim.x + threadIdx.x) * kBytes;
         stride = n * kBytes;
         for (int i = 0; i < stages * IT; ++i)
-            if ((int)(i % IT * blockDim.x + threadIdx.x) * V >= K)  // what no column fills is zero
+            if ((Share<T, V, IT>::base() + i % IT * 32) * V >= K)  // what no column fills is zero
                 for (int j = 0; j < kBytes / 4; ++j) reinterpret_cast<uint32_t*>(mine + i * stride)[j] = 0;
     }
     // bytes of a stage
     static __host__ __device__ size_t bytes(int K, int threads, int per_block) {
         return (size_t)threads * per_block * IT * kBytes;
     }
-    // `full`: every thread has IT whole vectors, and rows start on 16-byte boundaries
-    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, bool vec, bool full) {
-        if (full) {
+    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, int base, bool vec, bool whole) {
+        row += base * V;
+        if (whole) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i)
-                copy16(mine + (stage * IT + i) * stride, row + (i * blockDim.x + threadIdx.x) * V);
+            for (int i = 0; i < IT; ++i) copy16(mine + (stage * IT + i) * stride, row + i * 32 * V);
             return;
         }
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const int c = (i * blockDim.x + threadIdx.x) * V;
-            if (c >= K) continue;
+            if ((base + i * 32) * V >= K) continue;
             uint8_t* to = mine + (stage * IT + i) * stride;
+            const T* at = row + i * 32 * V;
             if (vec)
-                copy16(to, row + c);
+                copy16(to, at);
             else
-                for (int j = 0; j < V; ++j) reinterpret_cast<T*>(to)[j] = row[c + j];
+                for (int j = 0; j < V; ++j) reinterpret_cast<T*>(to)[j] = at[j];
         }
     }
-    __device__ __forceinline__ void read(int stage, const T*, int, Share<T, V, IT>& s) const {
+    __device__ __forceinline__ void read(int stage, const T*, int, int, bool, Share<T, V, IT>& s) const {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const uint4 u = *reinterpret_cast<const uint4*>(mine + (stage * IT + i) * stride);
@@ -265,7 +286,7 @@ struct Ring<T, 1, IT> {
     }
     static __host__ __device__ int row_bytes(int K) { return (K * (int)sizeof(T) + 15) / 16 * 16 + 16; }
     static __host__ __device__ size_t bytes(int K, int threads, int per_block) { return (size_t)row_bytes(K) * per_block; }
-    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, bool, bool) {
+    __device__ __forceinline__ void fetch(int stage, const T* __restrict__ row, int K, int, bool, bool) {
         const T* from = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(row) & ~uintptr_t(15));
         constexpr int N = 16 / sizeof(T);
         T* to = reinterpret_cast<T*>(mine + stage * stride);
@@ -277,13 +298,10 @@ struct Ring<T, 1, IT> {
                     if (from + c + j >= row && from + c + j < row + K) to[c + j] = from[c + j];
         }
     }
-    __device__ __forceinline__ void read(int stage, const T* row, int K, Share<T, 1, IT>& s) const {
-        const T* at = reinterpret_cast<const T*>(mine + stage * stride + (reinterpret_cast<uintptr_t>(row) & 15));
+    __device__ __forceinline__ void read(int stage, const T* row, int K, int base, bool whole, Share<T, 1, IT>& s) const {
+        const T* at = reinterpret_cast<const T*>(mine + stage * stride + (reinterpret_cast<uintptr_t>(row) & 15)) + base;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
-            s.w[i] = c < K ? __float_as_uint(to_f32(at[c])) : 0u;
-        }
+        for (int i = 0; i < IT; ++i) s.w[i] = whole || base + i * 32 < K ? __float_as_uint(to_f32(at[i * 32])) : 0u;
     }
     static __device__ __forceinline__ void landed() {
         if (blockDim.x == 32)
@@ -322,19 +340,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
     __shared__ float2 s[4][4 * 32];
     pdl_wait();
     pdl_trigger();
-    const int tx = threadIdx.x, threads = blockDim.x;
+    const int tx = threadIdx.x;
     Share<P, V, its<V>> w, bs;
-    w.load(weight, K, tx, threads, vec);
-    bs.load(bias ? bias : weight, bias ? K : 0, tx, threads, vec);  // no bias: zeros
+    const int base = Sh::base();
+    const bool whole = Sh::whole(K, vec);
+    w.load(weight, K, base, vec, whole);
+    bs.load(bias ? bias : weight, bias ? K : 0, base, vec, false);  // no bias: zeros
     const Turns turn(M);
-    // every thread has whole columns (the way without checks costs registers, which 1024 threads lack)
-    const bool full = kThreads < 1024 && vec && K == threads * cols_of<V>;
     Sh xs;
     Ring<T, V, its<V>> ring(smem, S, x, M * K, K);
     const int64_t hop = turn.step * K;
     int64_t here = turn.row * K, ahead = here;  // this row's values, and the next row's to fetch
     auto fetch = [&](int i) {
-        if (i < turn.mine) ring.fetch(i % S, x + ahead, K, vec, full);
+        if (i < turn.mine) ring.fetch(i % S, x + ahead, K, base, vec, whole);
         ring_commit();
         ahead += hop;
     };
@@ -345,13 +363,13 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
         fetch(i + S - 1);
         ring_wait<S - 1>();
         ring.landed();
-        ring.read(i % S, x + here, K, xs);
+        ring.read(i % S, x + here, K, base, whole, xs);
         float2 a = both(0.f);
 #pragma unroll
         for (int p = 0; p < Sh::kPairs; ++p) a = __fadd2_rn(a, xs.get(p));
         const float mean = row_sum(a.x + a.y, &s[at][0].x) * inv_k;
         a = both(0.f);
-        if (full) {
+        if (whole) {
 #pragma unroll
             for (int p = 0; p < Sh::kPairs; ++p) {
                 const float2 d = __fadd2_rn(xs.get(p), both(-mean));
@@ -361,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
 #pragma unroll
             for (int p = 0; p < Sh::kPairs; ++p) {
                 float2 d = __fadd2_rn(xs.get(p), both(-mean));
-                if (Sh::column(p, tx, threads) >= K) d = both(0.f);
-                if (V == 1 && Sh::column(p, tx, threads) + threads >= K) d.y = 0.f;
+                if (Sh::first(p, base) >= K) d.x = 0.f;
+                if (Sh::second(p, base) >= K) d.y = 0.f;
                 a = __ffma2_rn(d, d, a);
             }
         }
@@ -374,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
                 const float2 h = __fmul2_rn(__fadd2_rn(xs.get(p), both(-mean)), both(rstd));
                 xs.set(p, __ffma2_rn(h, w.get(p), bs.get(p)));
             }
-            xs.store(y + here, K, tx, threads, vec, full);
+            xs.store(y + here, K, base, vec, whole);
             if (tx == 0) {
                 if (mean_out) mean_out[q] = mean;
                 if (rstd_out) rstd_out[q] = rstd;
@@ -397,13 +415,13 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
     pdl_trigger();
     const int tx = threadIdx.x, threads = blockDim.x;
     Share<P, V, its<V>> w;
-    w.load(weight, K, tx, threads, vec);
+    const int base = Sh::base();
+    const bool whole = Sh::whole(K, vec);
+    w.load(weight, K, base, vec, whole);
     float2 dw[Sh::kPairs], db[Sh::kPairs];
 #pragma unroll
     for (int p = 0; p < Sh::kPairs; ++p) dw[p] = db[p] = both(0.f);
     const Turns turn(M);
-    // every thread has whole columns (the way without checks costs registers, which 1024 threads lack)
-    const bool full = kThreads < 1024 && vec && K == threads * cols_of<V>;
     Sh xs, ds;
     using R = Ring<T, V, its<V>>;
     R rx(smem, S, x, M * K, K), rd(smem + S * R::bytes(K, threads, blockDim.y), S, dy, M * K, K);
@@ -414,13 +432,15 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
         const bool in = i < turn.mine;
         if constexpr (S > 0) {
             if (in) {
-                rx.fetch(i % S, x + ahead, K, vec, full);
-                rd.fetch(i % S, dy + ahead, K, vec, full);
+                rx.fetch(i % S, x + ahead, K, base, vec, whole);
+                rd.fetch(i % S, dy + ahead, K, base, vec, whole);
             }
             ring_commit();
         } else {
-            xn.load(in ? x + ahead : x, in ? K : 0, tx, threads, false);
-            dn.load(in ? dy + ahead : dy, in ? K : 0, tx, threads, false);
+            if (in) {
+                xn.load(x + ahead, K, base, false, whole);
+                dn.load(dy + ahead, K, base, false, whole);
+            }
         }
         ahead += hop;
     };
@@ -438,8 +458,8 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
             fetch(i + S - 1);
             ring_wait<S - 1>();
             R::landed();
-            rx.read(i % S, x + here, K, xs);
-            rd.read(i % S, dy + here, K, ds);
+            rx.read(i % S, x + here, K, base, whole, xs);
+            rd.read(i % S, dy + here, K, base, whole, ds);
         } else {
             xs = xn;
             ds = dn;
@@ -468,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
                 const float2 h = __ffma2_rn(xs.get(p), both(rstd), both(shift)), g = __fmul2_rn(ds.get(p), w.get(p));
                 xs.set(p, __ffma2_rn(__ffma2_rn(h, e, g), both(rstd), c));
             }
-            xs.store(dx + here, K, tx, threads, vec, full);
+            xs.store(dx + here, K, base, vec, whole);
         }
     }
     if constexpr (S > 0) ring_wait<0>();
@@ -479,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
         if (threadIdx.y == y) {
 #pragma unroll
             for (int p = 0; p < Sh::kPairs; ++p) {
-                const int c = Sh::column(p, tx, threads), c2 = V > 1 ? c + 1 : c + threads;
+                const int c = Sh::first(p, base), c2 = Sh::second(p, base);
                 if (c < K) {
                     out[c] = dw[p].x + (y ? out[c] : 0.f);
                     out[K + c] = db[p].x + (y ? out[K + c] : 0.f);
@@ -599,7 +619,7 @@ __global__ void __launch_bounds__(1024)
 }
 
 bool norm_args_ok(int64_t M, int K, int dtype, int param_dtype) {
-    return M >= 0 && M <= INT32_MAX && K >= 1 && dtype_bytes(dtype) && (param_dtype == dtype || param_dtype == MOE_DT_F32);
+    return M >= 0 && M <= INT32_MAX && K >= 1 && K <= kMostColumns && dtype_bytes(dtype) && (param_dtype == dtype || param_dtype == MOE_DT_F32);
 }
 
 // Calls f with the stages of a ring that has `bytes` a stage in each of `per_sm` blocks, as a
@@ -684,7 +704,7 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
 }
 
 MOE_API size_t moe_layer_norm_workspace_size(int64_t M, int K) {
-    if (M < 0 || K < 1) return 0;
+    if (M < 0 || K < 1 || K > kMostColumns) return 0;
     // whichever way the rows are divided (by their type and alignment), the looping kernels too
     int n = parts_of<1>(K) > parts_of<8>(K) ? parts_of<1>(K) : parts_of<8>(K);
     if (n < kColParts) n = kColParts;

@@ -25,7 +25,7 @@ def test_layer_norm_refusals(L):
     def fwd(x=at(1), M=4, K=64, dt=BF, w=at(2), b=at(3), pdt=BF, eps=1e-5, y=at(4)):
         return L.moe_layer_norm(x, M, K, dt, w, b, pdt, eps, y, at(5), at(6), None)
     assert fwd(M=0) == 0
-    assert fwd(M=-1) == INVALID and fwd(K=0) == INVALID and fwd(dt=5) == INVALID
+    assert fwd(M=-1) == INVALID and fwd(K=0) == INVALID and fwd(dt=5) == INVALID and fwd(K=(1 << 24) + 1) == INVALID
     assert fwd(pdt=HF) == INVALID                                   # neither x's type nor fp32
     assert fwd(eps=-1.0) == INVALID and fwd(eps=float("nan")) == INVALID
     assert fwd(x=None) == INVALID and fwd(w=None) == INVALID and fwd(y=None) == INVALID
