@@ -195,14 +195,16 @@ __device__ __forceinline__ float row_sum(float v, float* s) {
         const float4 f = *reinterpret_cast<const float4*>(s);
         return (f.x + f.y) + (f.z + f.w);
     }
-    v = s[0];
-    for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v += s[i];
-    return v;
+    return warp_sum((threadIdx.x & 31) < (blockDim.x >> 5) ? s[threadIdx.x & 31] : 0.f);
 }
-__device__ __forceinline__ float2 row_sum(float2 v, float2* s) {
+__device__ __forceinline__ float2 warp_sum2(float2 v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         v = __fadd2_rn(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+    return v;
+}
+__device__ __forceinline__ float2 row_sum(float2 v, float2* s) {
+    v = warp_sum2(v);
     if (blockDim.x == 32) return v;
     s += threadIdx.y * 32;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
@@ -211,9 +213,7 @@ __device__ __forceinline__ float2 row_sum(float2 v, float2* s) {
         const float4 f = *reinterpret_cast<const float4*>(s), g = *reinterpret_cast<const float4*>(s + 2);
         return make_float2((f.x + f.z) + (g.x + g.z), (f.y + f.w) + (g.y + g.w));
     }
-    v = s[0];
-    for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v = __fadd2_rn(v, s[i]);
-    return v;
+    return warp_sum2((threadIdx.x & 31) < (blockDim.x >> 5) ? s[threadIdx.x & 31] : both(0.f));
 }
 
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
