@@ -203,17 +203,32 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
         v = __fadd2_rn(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
     return v;
 }
-__device__ __forceinline__ float2 row_sum(float2 v, float2* s) {
-    v = warp_sum2(v);
-    if (blockDim.x == 32) return v;
-    s += threadIdx.y * 32;
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+// The sums of kR rows at once: one barrier, and their exchanges overlap.
+template <int kR>
+__device__ __forceinline__ void row_sums(float2 (&v)[kR], float2* s) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < kR; ++k)
+            v[k] = __fadd2_rn(v[k], make_float2(__shfl_xor_sync(0xffffffffu, v[k].x, o), __shfl_xor_sync(0xffffffffu, v[k].y, o)));
+    if (blockDim.x == 32) return;
+    s += threadIdx.y * 32 * kR;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < kR; ++k) s[k * 32 + (threadIdx.x >> 5)] = v[k];
+    }
     __syncthreads();
     if (blockDim.x == 128) {
-        const float4 f = *reinterpret_cast<const float4*>(s), g = *reinterpret_cast<const float4*>(s + 2);
-        return make_float2((f.x + f.z) + (g.x + g.z), (f.y + f.w) + (g.y + g.w));
+#pragma unroll
+        for (int k = 0; k < kR; ++k) {
+            const float4 f = *reinterpret_cast<const float4*>(s + k * 32), g = *reinterpret_cast<const float4*>(s + k * 32 + 2);
+            v[k] = make_float2((f.x + f.z) + (g.x + g.z), (f.y + f.w) + (g.y + g.w));
+        }
+        return;
     }
-    return warp_sum2((threadIdx.x & 31) < (blockDim.x >> 5) ? s[threadIdx.x & 31] : both(0.f));
+#pragma unroll
+    for (int k = 0; k < kR; ++k) v[k] = warp_sum2(lane < (int)(blockDim.x >> 5) ? s[k * 32 + lane] : both(0.f));
 }
 
 __device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -402,6 +417,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
     ring_wait<0>();
 }
 
+// Rows that the backward pass takes at once: two where a thread has the registers for it, so that
+// the wait at the barrier is shared.
+template <typename T, int V, int S, int kThreads>
+constexpr int rows_at_once = sizeof(T) == 2 && V > 1 && S >= 4 && kThreads <= 512 ? 2 : 1;
+
 // (x - mean) * rstd is taken as x * rstd - mean * rstd in one rounding.
 template <typename T, typename P, int V, int S, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
@@ -409,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
                                const P* __restrict__ weight, const float* __restrict__ mean_in,
                                const float* __restrict__ rstd_in, T* dx, float* __restrict__ parts, bool vec) {
     using Sh = Share<T, V, its<V>>;
-    __shared__ float2 s[2][8 * 32];
+    __shared__ float2 s[2][2 * 8 * 32];
     extern __shared__ __align__(16) uint8_t smem[];  // the ring; at the end 2 K floats where a block has several rows
     pdl_wait();
     pdl_trigger();
@@ -422,7 +442,9 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
 #pragma unroll
     for (int p = 0; p < Sh::kPairs; ++p) dw[p] = db[p] = both(0.f);
     const Turns turn(M);
-    Sh xs, ds;
+    constexpr int kR = rows_at_once<T, V, S, kThreads>;
+    constexpr int kAhead = S > 0 ? S - kR : 1;  // rows fetched ahead
+    Sh xs[kR], ds[kR];
     using R = Ring<T, V, its<V>>;
     R rx(smem, S, x, M * K, K), rd(smem + S * R::bytes(K, threads, blockDim.y), S, dy, M * K, K);
     const int64_t hop = turn.step * K;
@@ -444,52 +466,73 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
         }
         ahead += hop;
     };
-    float mean_n = 0.f, rstd_n = 0.f;
+    float mean_n[kR], rstd_n[kR];
     int64_t q = turn.row;
     auto statistics = [&](int i) {
-        mean_n = i < turn.mine ? __ldg(mean_in + q) : 0.f;
-        rstd_n = i < turn.mine ? __ldg(rstd_in + q) : 0.f;
-        q += turn.step;
+#pragma unroll
+        for (int k = 0; k < kR; ++k) {
+            mean_n[k] = i + k < turn.mine ? __ldg(mean_in + q) : 0.f;
+            rstd_n[k] = i + k < turn.mine ? __ldg(rstd_in + q) : 0.f;
+            q += turn.step;
+        }
     };
-    for (int i = 0; i < (S > 0 ? S - 1 : 1); ++i) fetch(i);
+    for (int i = 0; i < kAhead; ++i) fetch(i);
     statistics(0);
-    for (int i = 0; i < turn.all; ++i, here += hop) {
+    for (int i = 0; i < turn.all; i += kR) {
         if constexpr (S > 0) {
-            fetch(i + S - 1);
-            ring_wait<S - 1>();
+#pragma unroll
+            for (int k = 0; k < kR; ++k) fetch(i + kAhead + k);
+            ring_wait<kAhead>();
             R::landed();
-            rx.read(i % S, x + here, K, base, whole, xs);
-            rd.read(i % S, dy + here, K, base, whole, ds);
+#pragma unroll
+            for (int k = 0; k < kR; ++k) {
+                rx.read((i + k) % S, x + here + k * hop, K, base, whole, xs[k]);
+                rd.read((i + k) % S, dy + here + k * hop, K, base, whole, ds[k]);
+            }
         } else {
-            xs = xn;
-            ds = dn;
+            xs[0] = xn;
+            ds[0] = dn;
             if (i + 1 < turn.all) fetch(i + 1);
         }
-        const bool in = i < turn.mine;
-        const float rstd = rstd_n, shift = -mean_n * rstd_n;
-        statistics(i + 1);
-        float2 a = both(0.f), b = both(0.f);
-        if (in) {
+        float rstd[kR], shift[kR];
+        float2 a[kR], b[kR];
 #pragma unroll
-            for (int p = 0; p < Sh::kPairs; ++p) {
-                const float2 d = ds.get(p), h = __ffma2_rn(xs.get(p), both(rstd), both(shift)), g = __fmul2_rn(d, w.get(p));
-                a = __fadd2_rn(a, g);
-                b = __ffma2_rn(g, h, b);
-                dw[p] = __ffma2_rn(d, h, dw[p]);
-                db[p] = __fadd2_rn(db[p], d);
-            }
+        for (int k = 0; k < kR; ++k) {
+            rstd[k] = rstd_n[k];
+            shift[k] = -mean_n[k] * rstd_n[k];
+            a[k] = b[k] = both(0.f);
         }
-        a = row_sum(make_float2(a.x + a.y, b.x + b.y), s[i & 1]);
-        if (in) {
-            // rstd * (g - a - h b)
-            const float2 c = both(-a.x * inv_k * rstd), e = both(-a.y * inv_k);
+        statistics(i + kR);
 #pragma unroll
-            for (int p = 0; p < Sh::kPairs; ++p) {
-                const float2 h = __ffma2_rn(xs.get(p), both(rstd), both(shift)), g = __fmul2_rn(ds.get(p), w.get(p));
-                xs.set(p, __ffma2_rn(__ffma2_rn(h, e, g), both(rstd), c));
+        for (int k = 0; k < kR; ++k)
+            if (i + k < turn.mine) {
+#pragma unroll
+                for (int p = 0; p < Sh::kPairs; ++p) {
+                    const float2 d = ds[k].get(p), h = __ffma2_rn(xs[k].get(p), both(rstd[k]), both(shift[k])),
+                                 g = __fmul2_rn(d, w.get(p));
+                    a[k] = __fadd2_rn(a[k], g);
+                    b[k] = __ffma2_rn(g, h, b[k]);
+                    dw[p] = __ffma2_rn(d, h, dw[p]);
+                    db[p] = __fadd2_rn(db[p], d);
+                }
             }
-            xs.store(dx + here, K, base, vec, whole);
-        }
+#pragma unroll
+        for (int k = 0; k < kR; ++k) a[k] = make_float2(a[k].x + a[k].y, b[k].x + b[k].y);
+        row_sums<kR>(a, s[i / kR & 1]);
+#pragma unroll
+        for (int k = 0; k < kR; ++k)
+            if (i + k < turn.mine) {
+                // rstd * (g - a - h b)
+                const float2 c = both(-a[k].x * inv_k * rstd[k]), e = both(-a[k].y * inv_k);
+#pragma unroll
+                for (int p = 0; p < Sh::kPairs; ++p) {
+                    const float2 h = __ffma2_rn(xs[k].get(p), both(rstd[k]), both(shift[k])),
+                                 g = __fmul2_rn(ds[k].get(p), w.get(p));
+                    xs[k].set(p, __ffma2_rn(__ffma2_rn(h, e, g), both(rstd[k]), c));
+                }
+                xs[k].store(dx + here + k * hop, K, base, vec, whole);
+            }
+        here += kR * hop;
     }
     if constexpr (S > 0) ring_wait<0>();
     float* cols = reinterpret_cast<float*>(smem);
