@@ -576,9 +576,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 uint8_t* p = smem + s * kStageBytes;
                 const int left = t.rows - (t.steps - 1) * kDepth;
                 const int n = (-left & 15) * 8;  // 16-byte pieces of a box
-                for (int i = lane; i < 4 * n; i += 32)
-                    *reinterpret_cast<uint4*>(p + i / n * (kOperandBytes / 2) + left * 128 + i % n * 16) =
-                        make_uint4(0, 0, 0, 0);
+                p += left * 128 + lane * 16;
+                for (int i = lane; i < n; i += 32, p += 512)
+#pragma unroll
+                    for (int box = 0; box < 4; ++box)
+                        *reinterpret_cast<uint4*>(p + box * (kOperandBytes / 2)) = make_uint4(0, 0, 0, 0);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(map_to(ptx::smem_addr(&st->ready[s]), 0));
