@@ -26,12 +26,14 @@
 // dense product: 555 us):
 //   one group of 8192 rows, 8192 x 8192      610 us forward, 597 us wgrad   1.80, 1.84 PFLOP/s
 //   128 groups of 512 rows, 1536 x 2048      250 us forward, 286 us wgrad   1.65, 1.44
-//   65536 rows over 128 groups, Zipf 1.2     285 us forward, 343 us wgrad   1.45, 1.20
+//   65536 rows over 128 groups, Zipf 1.2     285 us forward, 331 us wgrad   1.45, 1.24
 //   512 rows over 128 groups (decode)        127 us forward: 806 MB of weights at 6.3 TB/s
-// Where the time goes (variants of the forward product that leave one part out, 512 rows a
-// group): without loads 187 us, without MMAs 211 us -- DRAM gives 6 TB/s for the 1.27 GB that it has to move
-// -- and the full kernel 250 us, as the two hide each other only in part. wgrad writes 805 MB there, and
-// a plain fill of memory runs at 4.0 TB/s on this GPU (200 us for as much).
+//                                            130 us wgrad: as much written at 6.2 TB/s
+// Where the time goes (variants that leave one part out, 512 rows a group):
+//   forward: without loads 187 us, without MMAs 211 us (DRAM gives 6 TB/s for the 1.27 GB that has
+//   to move), the full kernel 250 us, as the two hide each other only in part;
+//   wgrad: without loads 190 us, without stores 216 us, without MMAs 244 us: 3.2 GB into the SMs
+//   and 0.8 GB out of them, 16.4 TB/s, which is about what they take (64 bytes a clock each).
 // What it is sensitive to: the MMA loop has to issue from uniform registers (a loop that one lane
 // runs alone takes 130 clocks an MMA: 750 us dense), the look-up of a tile is on the MMA warp's
 // way between tiles, and a signal to the other CTA must not be a cluster-wide release, which
