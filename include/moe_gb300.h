@@ -440,12 +440,19 @@ MOE_API int moe_grouped_matmul_dgrad(const void* dy, int64_t R, const void* w, i
                                      int k_in, const int32_t* expert_offsets, const int32_t* expert_num_tokens,
                                      int dtype, int out_dtype, void* dx, moe_stream_t stream);
 
+/* Scratch bytes moe_grouped_matmul_wgrad needs: 0 unless few weights meet many rows, whose sum is
+ * then split into parts that are joined in a fixed order. */
+MOE_API size_t moe_grouped_matmul_wgrad_workspace_size(int64_t R, int local_num_experts, int n_out, int k_in);
+
 /* Its gradient with respect to the weights: dw[l] = sum over the rows r of group l of
  * dy[r] x[r]^T, `out_dtype` [El, n_out, k_in]; zeros for a group without rows. Rows of no
- * group add nothing, whatever they hold. */
+ * group add nothing, whatever they hold.
+ * workspace >= moe_grouped_matmul_wgrad_workspace_size(R, El, n_out, k_in) bytes, 16-byte aligned
+ * (NULL where that is 0). */
 MOE_API int moe_grouped_matmul_wgrad(const void* dy, const void* x, int64_t R, int local_num_experts, int n_out,
                                      int k_in, const int32_t* expert_offsets, const int32_t* expert_num_tokens,
-                                     int dtype, int out_dtype, void* dw, moe_stream_t stream);
+                                     int dtype, int out_dtype, void* dw, void* workspace, size_t workspace_bytes,
+                                     moe_stream_t stream);
 
 /* Scratch bytes moe_grad_norm and moe_clip_grad_norm need for these tensors (HOST array of
  * n_tensors lengths). Returns 0 on bad arguments. */

@@ -100,7 +100,8 @@ SIGNATURES = {
     "moe_router_topk_backward_i64": ([_p, _i64, _int, _int, _p, _int, _int, _int, _f, _p, _p, _p], _int),
     "moe_grouped_matmul": ([_p, _i64, _p, _int, _int, _int, _p, _p, _int, _int, _p, _p], _int),
     "moe_grouped_matmul_dgrad": ([_p, _i64, _p, _int, _int, _int, _p, _p, _int, _int, _p, _p], _int),
-    "moe_grouped_matmul_wgrad": ([_p, _p, _i64, _int, _int, _int, _p, _p, _int, _int, _p, _p], _int),
+    "moe_grouped_matmul_wgrad": ([_p, _p, _i64, _int, _int, _int, _p, _p, _int, _int, _p, _p, _sz, _p], _int),
+    "moe_grouped_matmul_wgrad_workspace_size": ([_i64, _int, _int, _int], _sz),
     "moe_grad_norm_workspace_size": ([_p, _int], _sz),
     "moe_grad_norm": ([_p, _p, _p, _int, _p, _p, _sz, _p], _int),
     "moe_clip_grad_norm": ([_p, _p, _p, _int, _f, _p, _p, _p, _sz, _p], _int),
@@ -527,7 +528,11 @@ def moe_router_topk_backward(logits, topk_ids, d_topk_weights, scoring=MOE_SCORE
     return d_logits
 
 
-def _grouped(fn, a, b, shape, dims, expert_offsets, expert_num_tokens, out, out_dtype, stream):
+def moe_grouped_matmul_wgrad_workspace_size(R: int, local_num_experts: int, n_out: int, k_in: int) -> int:
+    return int(lib().moe_grouped_matmul_wgrad_workspace_size(R, local_num_experts, n_out, k_in))
+
+
+def _grouped(fn, a, b, shape, dims, expert_offsets, expert_num_tokens, out, out_dtype, stream, workspace=None):
     """The three grouped products: operands a and b, the result's shape, (El, n_out, k_in)."""
     dt = _dtype_code(a, "rows")
     _same(b, b.shape, a.dtype, "second operand")
@@ -540,7 +545,12 @@ def _grouped(fn, a, b, shape, dims, expert_offsets, expert_num_tokens, out, out_
     odt = _dtype_code(out, "out")
     off, cnt = _addr(expert_offsets), _addr(expert_num_tokens)
     if fn == "moe_grouped_matmul_wgrad":
+        if workspace is None:
+            need = moe_grouped_matmul_wgrad_workspace_size(a.shape[0], El, N, K)
+            if need:
+                workspace = _empty(need, torch.uint8, a.device, stream)
         st = lib().moe_grouped_matmul_wgrad(_addr(a), _addr(b), a.shape[0], El, N, K, off, cnt, dt, odt, _addr(out),
+                                            _addr(workspace), 0 if workspace is None else workspace.numel(),
                                             _raw_stream(stream))
     else:
         st = getattr(lib(), fn)(_addr(a), a.shape[0], _addr(b), El, N, K, off, cnt, dt, odt, _addr(out), _raw_stream(stream))
@@ -569,7 +579,8 @@ def moe_grouped_matmul_dgrad(dy, w, expert_offsets, expert_num_tokens=None, out=
                     out_dtype, stream)
 
 
-def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=None, out_dtype=None, stream=None):
+def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=None, out_dtype=None, stream=None,
+                             workspace=None):
     """Gradient of moe_grouped_matmul's weights: sum over group l's rows of the outer
     products dy[r] x[r], [El, n_out, k_in]; zeros for a group without rows."""
     El = expert_offsets.shape[0] - 1
@@ -577,7 +588,7 @@ def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=
     K = x.shape[1]
     _same(x, (R, K), dy.dtype, "x")
     return _grouped("moe_grouped_matmul_wgrad", dy, x, (El, N, K), (El, N, K), expert_offsets, expert_num_tokens, out,
-                    out_dtype, stream)
+                    out_dtype, stream, workspace)
 
 
 _dtype_of, _is_cuda = attrgetter("dtype"), attrgetter("is_cuda")

@@ -74,6 +74,7 @@ constexpr int kRowBoxes = 5;       // boxes of 8, 16, 32, 64, 128 rows
 template <int MODE>
 __host__ __device__ constexpr int threads_of() { return MODE == kWgrad ? 224 : 192; }  // the tail warp is wgrad's
 constexpr int kBuckets = 128;      // steps of cost that the groups are sorted by
+constexpr int kSms = 152;           // what a workspace size is computed for
 constexpr int kMaxDevices = 64;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -284,15 +285,17 @@ struct Divisor {
 };
 struct Shape {
     Divisor m_tiles;      // tiles along the M side
-    Divisor group_tiles;  // wgrad: tiles of a group
+    Divisor group_tiles;  // wgrad: tiles of a group, all its parts'
+    Divisor part_tiles;   // wgrad: tiles of one part
+    int parts;            // wgrad: parts that a group's rows are split into
     int depth;            // forward, dgrad: the reduced length
 };
 
 // Where a tile lies. forward, dgrad: outputs [m0, m0 + 256) x rows [lo, lo + rows) of group
-// l, n = rows rounded up to 16. wgrad: [m0, m0 + 256) x [n0, n0 + 256) of dW_l, summed over
-// rows [lo, lo + rows). steps: stages of the reduced index.
+// l, n = rows rounded up to 16. wgrad: [m0, m0 + 256) x [n0, n0 + 256) of the part-th sum of
+// dW_l, over rows [lo, lo + rows). steps: stages of the reduced index.
 struct Tile {
-    int l, lo, rows, m0, n0, n, steps;
+    int l, part, lo, rows, m0, n0, n, steps;
 };
 
 // All lanes of a warp call it together (forward and dgrad look the group up with two votes).
@@ -301,7 +304,9 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, c
     Tile t;
     if (MODE == kWgrad) {
         const int at = sh.group_tiles.of(tile);
-        const int i = tile - at * sh.group_tiles.d;
+        int i = tile - at * sh.group_tiles.d;
+        t.part = sh.part_tiles.of(i);
+        i -= t.part * sh.part_tiles.d;
         const int p = sh.m_tiles.of(i);
         const Group g = groups[at];
         t.l = g.id & 0xffff;
@@ -311,6 +316,12 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, c
         t.lo = g.lo;
         t.rows = g.rows;
         t.steps = ceil_div(t.rows, kDepth);
+        if (sh.parts > 1) {  // whole steps to every part
+            const int from = (int)((int64_t)t.steps * t.part / sh.parts), to = (int)((int64_t)t.steps * (t.part + 1) / sh.parts);
+            t.lo += from * kDepth;
+            t.rows = min(t.rows - from * kDepth, (to - from) * kDepth);
+            t.steps = to - from;
+        }
     } else {
         // the last group whose first tile is not past this one (an empty group starts where
         // the next one does): the block of `stride` groups, then the group
@@ -326,7 +337,7 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, c
         t.lo = g.lo + p * per;
         t.rows = min(per, g.rows - p * per);
         t.n = (t.rows + 15) & ~15;
-        t.n0 = 0;
+        t.n0 = t.part = 0;
         t.steps = ceil_div(sh.depth, kDepth);
     }
     return t;
@@ -630,7 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        if (m < P) store_3d(&maps.o, ptx::smem_addr(box), t.n0 + c, m, t.l);
+                        if (m < P) store_3d(&maps.o, ptx::smem_addr(box), t.n0 + c, m, t.part * El + t.l);
                         ptx::bulk_commit();
                     }
                 };
@@ -755,9 +766,38 @@ bool make_map(CUtensorMap* m, const void* base, int esize, uint64_t x, uint64_t 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// wgrad of few tiles over many rows (a router's gate, a few large experts): each group's rows are
+// split into parts whose tiles fill the pairs, their sums joined by fold_parts_kernel in a fixed
+// order. The parts have 512 rows or more on average; one more costs 4 bytes written and read per
+// weight (8192 rows, 128 x 2048: 38.5 us in one part, 14.7 us in nine).
+constexpr int kPartRows = 512, kMostParts = 16;
+
+int wgrad_parts(int64_t R, int El, int N, int K) {
+    const int64_t tiles = El * (((int64_t)N + kPairM - 1) / kPairM) * (((int64_t)K + kMaxN - 1) / kMaxN);
+    int64_t parts = kSms / 2 / tiles;
+    if (parts > R / El / kPartRows) parts = R / El / kPartRows;
+    return (int)(parts < 2 ? 1 : parts > kMostParts ? kMostParts : parts);
+}
+
+template <typename O>
+__global__ void __launch_bounds__(256) fold_parts_kernel(const float4* __restrict__ parts, int n, int64_t n4, O* __restrict__ out) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n4) return;
+    float4 a = parts[i];
+    for (int p = 1; p < n; ++p) {
+        const float4 v = parts[p * n4 + i];
+        a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    }
+    Vec<O, 4> o;
+    o.v[0] = from_f32<O>(a.x), o.v[1] = from_f32<O>(a.y), o.v[2] = from_f32<O>(a.z), o.v[3] = from_f32<O>(a.w);
+    reinterpret_cast<Vec<O, 4>*>(out)[i] = o;
+}
+
 template <int MODE, typename O>
 int launch_grouped(const void* a, const void* b, const int32_t* off, const int32_t* cnt, int El, int64_t R, int N, int K,
-                   int dtype, void* out, int num_sms, cudaStream_t stream) {
+                   int dtype, void* out, int parts, int num_sms, cudaStream_t stream) {
     Maps maps{};
     bool ok = true;
     if (MODE == kWgrad) {
@@ -765,7 +805,7 @@ int launch_grouped(const void* a, const void* b, const int32_t* off, const int32
         const void* any = out;
         ok = make_map(&maps.a, R > 0 ? a : any, 2, N, rows, 1, kDepth, 2) &&
              make_map(&maps.b[0], R > 0 ? b : any, 2, K, rows, 1, kDepth, 2) &&
-             make_map(&maps.o, out, sizeof(O), K, N, El, 32, 3);
+             make_map(&maps.o, out, sizeof(O), K, N, (uint64_t)El * parts, 32, 3);
     } else {
         ok = make_map(&maps.a, b, 2, K, N, El, MODE == kFwd ? 128 : kDepth, 3);
         for (int i = 0; i < kRowBoxes; ++i) ok = ok && make_map(&maps.b[i], a, 2, MODE == kFwd ? K : N, R, 1, 8u << i, 2);
@@ -784,8 +824,9 @@ int launch_grouped(const void* a, const void* b, const int32_t* off, const int32
     if (stages > kMaxStages) stages = kMaxStages;
     const size_t smem = fixed_smem<MODE>(El) + (size_t)stages * kStageBytes;
     const int64_t m_tiles = ((int64_t)(MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;
-    const int64_t group_tiles = m_tiles * (((int64_t)K + kMaxN - 1) / kMaxN);
-    const Shape sh{{(int)m_tiles, magic_of(m_tiles)}, {(int)group_tiles, magic_of(group_tiles)}, MODE == kDgrad ? N : K};
+    const int64_t part_tiles = m_tiles * (((int64_t)K + kMaxN - 1) / kMaxN), group_tiles = part_tiles * parts;
+    const Shape sh{{(int)m_tiles, magic_of(m_tiles)}, {(int)group_tiles, magic_of(group_tiles)},
+                   {(int)part_tiles, magic_of(part_tiles)}, parts, MODE == kDgrad ? N : K};
     // no more pairs than tiles (an upper bound: the groups' sizes are not known here)
     const int64_t most = MODE == kWgrad ? El * group_tiles : (R / kMaxN + (R < El ? R : El)) * m_tiles;
     const int pairs = (int)(most < num_sms / 2 ? most : num_sms / 2);
@@ -798,7 +839,7 @@ int launch_grouped(const void* a, const void* b, const int32_t* off, const int32
 // a, b: the operands (x and w; dy and w; dy and x). The checks of all three entry points.
 template <int MODE>
 int grouped_impl(const void* a, const void* b, const int32_t* off, const int32_t* cnt, int El, int64_t R, int N, int K,
-                 int dtype, int out_dtype, void* out, moe_stream_t stream) {
+                 int dtype, int out_dtype, void* out, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
     if (El < 1 || El > kMaxLocalExperts || R < 0 || R > INT32_MAX || N < 8 || K < 8 || N % 8 || K % 8 || !off ||
         (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16) || (out_dtype != dtype && out_dtype != MOE_DT_F32))
         return MOE_ERR_INVALID_ARG;
@@ -815,12 +856,36 @@ int grouped_impl(const void* a, const void* b, const int32_t* off, const int32_t
     const size_t b_bytes = MODE == kWgrad ? (size_t)R * K * 2 : wn * 2;
     const size_t o_bytes = (MODE == kWgrad ? wn : (size_t)R * (MODE == kFwd ? N : K)) * dtype_bytes(out_dtype);
     if (overlap(out, o_bytes, a, a_bytes) || overlap(out, o_bytes, b, b_bytes)) return MOE_ERR_INVALID_ARG;
+    if (MODE == kWgrad) {
+        const size_t need = moe_grouped_matmul_wgrad_workspace_size(R, El, N, K);
+        if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+        if (need > 0 && (misaligned(workspace, 16) || overlap(workspace, need, a, a_bytes) || overlap(workspace, need, b, b_bytes) ||
+                         overlap(workspace, need, out, o_bytes)))
+            return MOE_ERR_INVALID_ARG;
+    }
     int sms = 0;
     if (int st = check_device(&sms)) return st;
     cudaStream_t s = (cudaStream_t)stream;
-    if (out_dtype == MOE_DT_F32) return launch_grouped<MODE, float>(a, b, off, cnt, El, R, N, K, dtype, out, sms, s);
-    if (dtype == MOE_DT_BF16) return launch_grouped<MODE, bf16>(a, b, off, cnt, El, R, N, K, dtype, out, sms, s);
-    return launch_grouped<MODE, fp16>(a, b, off, cnt, El, R, N, K, dtype, out, sms, s);
+    if constexpr (MODE == kWgrad) {
+        const int parts = wgrad_parts(R, El, N, K);
+        if (parts > 1) {
+            if (int st = launch_grouped<kWgrad, float>(a, b, off, cnt, El, R, N, K, dtype, workspace, parts, sms, s)) return st;
+            const int64_t n4 = (int64_t)wn / 4;  // n_out and k_in are multiples of 8
+            const unsigned grid = (unsigned)((n4 + 255) / 256);
+            const float4* from = static_cast<const float4*>(workspace);
+            if (out_dtype == MOE_DT_F32)
+                launch_k(fold_parts_kernel<float>, grid, 256, 0, s, from, parts, n4, static_cast<float*>(out));
+            else if (dtype == MOE_DT_BF16)
+                launch_k(fold_parts_kernel<bf16>, grid, 256, 0, s, from, parts, n4, static_cast<bf16*>(out));
+            else
+                launch_k(fold_parts_kernel<fp16>, grid, 256, 0, s, from, parts, n4, static_cast<fp16*>(out));
+            note_launches(1);
+            return launch_status();
+        }
+    }
+    if (out_dtype == MOE_DT_F32) return launch_grouped<MODE, float>(a, b, off, cnt, El, R, N, K, dtype, out, 1, sms, s);
+    if (dtype == MOE_DT_BF16) return launch_grouped<MODE, bf16>(a, b, off, cnt, El, R, N, K, dtype, out, 1, sms, s);
+    return launch_grouped<MODE, fp16>(a, b, off, cnt, El, R, N, K, dtype, out, 1, sms, s);
 }
 
 }  // namespace
@@ -845,21 +910,27 @@ MOE_API int moe_grouped_matmul(const void* x, int64_t R, const void* w, int loca
                                const int32_t* expert_offsets, const int32_t* expert_num_tokens, int dtype, int out_dtype,
                                void* out, moe_stream_t stream) {
     return grouped_impl<kFwd>(x, w, expert_offsets, expert_num_tokens, local_num_experts, R, n_out, k_in, dtype, out_dtype,
-                              out, stream);
+                              out, nullptr, 0, stream);
 }
 
 MOE_API int moe_grouped_matmul_dgrad(const void* dy, int64_t R, const void* w, int local_num_experts, int n_out, int k_in,
                                      const int32_t* expert_offsets, const int32_t* expert_num_tokens, int dtype,
                                      int out_dtype, void* dx, moe_stream_t stream) {
     return grouped_impl<kDgrad>(dy, w, expert_offsets, expert_num_tokens, local_num_experts, R, n_out, k_in, dtype,
-                                out_dtype, dx, stream);
+                                out_dtype, dx, nullptr, 0, stream);
 }
 
 MOE_API int moe_grouped_matmul_wgrad(const void* dy, const void* x, int64_t R, int local_num_experts, int n_out, int k_in,
-                                     const int32_t* expert_offsets, const int32_t* expert_num_tokens, int dtype,
-                                     int out_dtype, void* dw, moe_stream_t stream) {
+                                     const int32_t* expert_offsets, const int32_t* expert_num_tokens, int dtype, int out_dtype,
+                                     void* dw, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
     return grouped_impl<kWgrad>(dy, x, expert_offsets, expert_num_tokens, local_num_experts, R, n_out, k_in, dtype,
-                                out_dtype, dw, stream);
+                                out_dtype, dw, workspace, workspace_bytes, stream);
+}
+
+MOE_API size_t moe_grouped_matmul_wgrad_workspace_size(int64_t R, int local_num_experts, int n_out, int k_in) {
+    if (R < 0 || local_num_experts < 1 || n_out < 1 || k_in < 1) return 0;
+    const int parts = wgrad_parts(R, local_num_experts, n_out, k_in);
+    return parts > 1 ? (size_t)parts * local_num_experts * n_out * k_in * sizeof(float) : 0;
 }
 
 }  // extern "C"

@@ -109,6 +109,17 @@ def test_neighbouring_group_holds_nan(out_dtype):
         close(dw[l], dy[rows].double().T, x[rows].double(), rows.stop - rows.start)
 
 
+@pytest.mark.parametrize("counts,N,K", [([8192], 128, 264), ([3000, 5, 0, 4099], 256, 256), ([1025], 8, 8),
+                                        ([0, 5001, 0], 136, 520), ([20000], 256, 512)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("wide", [False, True])
+def test_few_weights_and_many_rows(counts, N, K, dtype, wide):
+    """The sums over rows are split into parts here, whatever the single groups' lengths."""
+    assert moe.moe_grouped_matmul_wgrad_workspace_size(sum(counts), len(counts), N, K) > 0
+    x, dy, w, off = make(counts, N, K, dtype, seed=N)
+    check(x, dy, w, off, counts, torch.float32 if wide else None)
+
+
 def test_offsets_past_the_rows_touch_nothing():
     x, dy, w, _ = make([40, 24], 64, 64, torch.bfloat16)
     guard = torch.full((64 + 64, 64), 3.0, dtype=torch.bfloat16, device="cuda")

@@ -79,11 +79,20 @@ def test_grouped_matmul_refusals(L):
                     dict(out=at(2))):
             assert fwd(fn=fn, **bad) == INVALID, bad
 
-    def wgrad(dy=at(1), x=at(2), R=16, El=4, N=64, K=64, off=off, dt=BF, odt=FP, out=at(3)):
-        return L.moe_grouped_matmul_wgrad(dy, x, R, El, N, K, off, None, dt, odt, out, None)
+    def wgrad(dy=at(1), x=at(2), R=16, El=4, N=64, K=64, off=off, dt=BF, odt=FP, out=at(3), ws=None, nb=0):
+        return L.moe_grouped_matmul_wgrad(dy, x, R, El, N, K, off, None, dt, odt, out, ws, nb, None)
     for bad in (dict(El=0), dict(N=4), dict(K=12), dict(R=-1), dict(dt=FP), dict(odt=HF), dict(off=None), dict(dy=None),
                 dict(x=None), dict(out=None), dict(R=0, out=None), dict(out=at(1)), dict(out=at(2))):
         assert wgrad(**bad) == INVALID, bad
+    # few weights, many rows: the sum is split and needs scratch
+    size = L.moe_grouped_matmul_wgrad_workspace_size
+    assert size(16, 4, 64, 64) == 0 and size(-1, 4, 64, 64) == 0 and size(100, 0, 64, 64) == 0
+    assert size(65536, 128, 1536, 2048) == 0
+    need = size(8192, 1, 128, 2048)
+    assert need >= 2 * 128 * 2048 * 4
+    big = dict(R=8192, El=1, N=128, K=2048, dy=at(1 << 10), x=at(1 << 12), out=at(1 << 14))
+    assert wgrad(**big) == SMALL and wgrad(**big, ws=at(1 << 16), nb=need - 1) == SMALL
+    assert wgrad(**big, ws=at(1 << 12), nb=need) == INVALID and wgrad(**big, ws=ctypes.c_void_p((1 << 36) + 8), nb=need) == INVALID
 
 
 def test_grad_norm_refusals(L):
