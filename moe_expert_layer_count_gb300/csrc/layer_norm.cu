@@ -329,8 +329,8 @@ struct Ring<T, 1, IT> {
 template <int V>
 constexpr int its = cols_of<V> / V;  // vectors of a thread
 // S, below: the stages of a block's ring. 0 (backward only): none -- single fp32 values, coalesced
-// as they are, are loaded straight into registers, one row ahead (30011 x 1111: 97 us, with a
-// ring 112).
+// as they are, are loaded straight into registers, one row ahead (30011 x 1111: 92 us, with a
+// ring 109).
 
 // Block b takes the rows b * blockDim.y + threadIdx.y, then gridDim.x * blockDim.y further on.
 struct Turns {
