@@ -118,8 +118,27 @@ __device__ __forceinline__ uint32_t map_to(uint32_t a, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
+// Arrivals on a barrier of the pair's other CTA. With nothing in memory to publish (an accumulator that
+// has been read, ordered by tcgen05.fence) the arrival is relaxed; without a scope it would be a release
+// among this CTA's threads, which says nothing to the other CTA.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The arrival that makes this warp's shared-memory writes visible to the other CTA's waiter (which takes
+// wait_phase<true>). It waits for the thread's own global stores; the tail warp has none.
+__device__ __forceinline__ void arrive_cluster_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
 }
 // Tile loads whose completion may count on the barrier of the pair's other CTA.
 __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
@@ -240,11 +259,15 @@ uint32_t idesc_base(int mode, int dtype) {
            (uint32_t)(kPairM >> 4) << 24;
 }
 
+// Waits for a phase; false when the kernel was given up or the time ran out. kCluster: the barrier's
+// arrivals come from both CTAs and publish, or hand over, what the waiter uses next.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, bool check_abort = true) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+    auto done = [&] { return kCluster ? try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+    if (done()) return true;
     const uint64_t t0 = ptx::globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
-        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (done()) return true;
         if ((i & 31) == 0) {
             if (check_abort && *abort) return false;
             if (ptx::globaltimer_ns() - t0 > kTimeoutNs) {
@@ -533,12 +556,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 if (t.steps == 0) continue;
                 const uint32_t idesc = idesc0 | (uint32_t)(t.n >> 3) << 17;
                 const uint32_t d = tmem + (uint32_t)(b * kMaxN);
-                ok = __all_sync(0xffffffffu, wait_phase(ptx::smem_addr(&st->tempty[b]), tph ^ 1, abort));
+                ok = __all_sync(0xffffffffu, wait_phase<true>(ptx::smem_addr(&st->tempty[b]), tph ^ 1, abort));
                 if (!ok) break;
                 for (int k = 0; k < t.steps; ++k) {
                     bool got;
                     if (MODE == kWgrad && ragged(t, k)) {
-                        got = wait_phase(ptx::smem_addr(&st->ready[s]), landed >> s & 1, abort);
+                        got = wait_phase<true>(ptx::smem_addr(&st->ready[s]), landed >> s & 1, abort);
                         landed ^= 1u << s;
                     } else {
                         got = wait_phase(ptx::smem_addr(&st->full[s]), filled >> s & 1, abort);
@@ -596,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                         *reinterpret_cast<uint4*>(p + box * (kOperandBytes / 2)) = make_uint4(0, 0, 0, 0);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive_cluster(map_to(ptx::smem_addr(&st->ready[s]), 0));
+                if (lane == 0) arrive_cluster_release(map_to(ptx::smem_addr(&st->ready[s]), 0));
             }
             if (++s == stages) s = 0;
         }
