@@ -183,12 +183,21 @@ struct Share {
     static __device__ __forceinline__ int second(int p, int base) { return first(p, base) + (V > 1 ? 1 : 32); }
 };
 
+// The warps' sums of N rows (or rows of pairs), 32 places each: read four values at a time, so on
+// 16-byte boundaries.
+template <typename F, int N>
+struct alignas(16) WarpSums {
+    F v[N * 32];
+};
+
 // Sums over the threads of a row (blockDim.x of them, a row per threadIdx.y), the same in all.
-// `s`: 32 places per row, other ones at the next call, so that one barrier is enough.
-__device__ __forceinline__ float row_sum(float v, float* s) {
+// `sums`: a place per row, other ones at the next call, so that one barrier is enough.
+template <int N>
+__device__ __forceinline__ float row_sum(float v, WarpSums<float, N>& sums) {
+    static_assert(alignof(WarpSums<float, N>) >= alignof(float4), "read as float4");
     v = warp_sum(v);
     if (blockDim.x == 32) return v;
-    s += threadIdx.y * 32;
+    float* s = sums.v + threadIdx.y * 32;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
     if (blockDim.x == 128) {
@@ -204,15 +213,16 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
     return v;
 }
 // The sums of kR rows at once: one barrier, and their exchanges overlap.
-template <int kR>
-__device__ __forceinline__ void row_sums(float2 (&v)[kR], float2* s) {
+template <int kR, int N>
+__device__ __forceinline__ void row_sums(float2 (&v)[kR], WarpSums<float2, N>& sums) {
+    static_assert(alignof(WarpSums<float2, N>) >= alignof(float4), "read as float4");
 #pragma unroll
     for (int o = 16; o; o >>= 1)
 #pragma unroll
         for (int k = 0; k < kR; ++k)
             v[k] = __fadd2_rn(v[k], make_float2(__shfl_xor_sync(0xffffffffu, v[k].x, o), __shfl_xor_sync(0xffffffffu, v[k].y, o)));
     if (blockDim.x == 32) return;
-    s += threadIdx.y * 32 * kR;
+    float2* s = sums.v + threadIdx.y * 32 * kR;
     const int lane = threadIdx.x & 31;
     if (lane == 0) {
 #pragma unroll
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
                            float eps, T* y, float* __restrict__ mean_out, float* __restrict__ rstd_out, bool vec) {
     using Sh = Share<T, V, its<V>>;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 s[4][4 * 32];
+    __shared__ WarpSums<float, 4> s[4];  // at most four rows a block
     pdl_wait();
     pdl_trigger();
     const int tx = threadIdx.x;
@@ -382,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
         float2 a = both(0.f);
 #pragma unroll
         for (int p = 0; p < Sh::kPairs; ++p) a = __fadd2_rn(a, xs.get(p));
-        const float mean = row_sum(a.x + a.y, &s[at][0].x) * inv_k;
+        const float mean = row_sum(a.x + a.y, s[at]) * inv_k;
         a = both(0.f);
         if (whole) {
 #pragma unroll
@@ -399,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
                 a = __ffma2_rn(d, d, a);
             }
         }
-        const float rstd = rsqrtf(fmaf(row_sum(a.x + a.y, &s[at + 1][0].x), inv_k, eps));
+        const float rstd = rsqrtf(fmaf(row_sum(a.x + a.y, s[at + 1]), inv_k, eps));
         at ^= 2;
         if (i < turn.mine) {
 #pragma unroll
@@ -429,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
                                const P* __restrict__ weight, const float* __restrict__ mean_in,
                                const float* __restrict__ rstd_in, T* dx, float* __restrict__ parts, bool vec) {
     using Sh = Share<T, V, its<V>>;
-    __shared__ float2 s[2][2 * 8 * 32];
+    __shared__ WarpSums<float2, 2 * 8> s[2];  // two rows at once, at most eight rows a block
     extern __shared__ __align__(16) uint8_t smem[];  // the ring; at the end 2 K floats where a block has several rows
     pdl_wait();
     pdl_trigger();
