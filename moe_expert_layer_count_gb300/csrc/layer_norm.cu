@@ -676,25 +676,26 @@ bool norm_args_ok(int64_t M, int K, int dtype, int param_dtype) {
 }
 
 // Calls f with the stages of a ring that has `bytes` a stage in each of `per_sm` blocks, as a
-// constant; false where not even two fit.
+// constant, and returns what it returns; kNoRing where not even two fit.
+constexpr int kNoRing = -1;
 template <bool kRing, typename F>
-bool with_stages(size_t bytes, int per_sm, F&& f) {
-    if constexpr (!kRing) {
-        f(std::integral_constant<int, 0>{});
-        return true;
-    }
+int with_stages(size_t bytes, int per_sm, F&& f) {
+    if constexpr (!kRing) return f(std::integral_constant<int, 0>{});
     const size_t room = 200 * 1024 / per_sm;
-    if (4 * bytes <= room) f(std::integral_constant<int, 4>{});
-    else if (3 * bytes <= room) f(std::integral_constant<int, 3>{});
-    else if (2 * bytes <= room) f(std::integral_constant<int, 2>{});
-    else return false;
-    return true;
+    if (4 * bytes <= room) return f(std::integral_constant<int, 4>{});
+    if (3 * bytes <= room) return f(std::integral_constant<int, 3>{});
+    if (2 * bytes <= room) return f(std::integral_constant<int, 2>{});
+    return kNoRing;
 }
+// 48 KB of shared memory, the kernel's own arrays among them, need no permission; which widths stay
+// within that is not worth a rule of its own.
 template <typename... KArgs, typename... Args>
-void launch_ring(void (*kernel)(KArgs...), unsigned grid, dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
-    if (smem + 4096 > 48 * 1024)  // with the kernels' own static arrays
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    launch_k(kernel, grid, block, smem, stream, std::forward<Args>(args)...);
+int launch_ring(void (*kernel)(KArgs...), unsigned grid, dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) {
+        launch_k(kernel, grid, block, smem, stream, std::forward<Args>(args)...);
+        note_launches(1);
+    }
+    return launch_status();
 }
 
 // Calls f(T*, P*) with the element types of x and of the parameters.
@@ -731,10 +732,10 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
         using P = std::remove_pointer_t<decltype(p)>;
         constexpr int V = 16 / sizeof(T);
         const bool vec = !misaligned(x, 16) && !misaligned(y, 16) && !misaligned(weight, 16) && !misaligned(bias, 16);
-        auto rows = [&](auto vc) -> bool {
+        auto rows = [&](auto vc) -> int {
             constexpr int W = decltype(vc)::value;
             const Rows g = forward_rows<W>(K);
-            if (g.threads > 1024) return false;
+            if (g.threads > 1024) return kNoRing;
             const int64_t blocks = (M + g.per_block - 1) / g.per_block, most = (int64_t)sms * g.per_sm;
             const dim3 block(g.threads, g.per_block);
             const size_t bytes = Ring<T, W, its<W>>::bytes(K, g.threads, g.per_block);
@@ -743,14 +744,15 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
                 auto kernel = g.threads <= most_threads<W> ? layer_norm_rows_kernel<T, P, W, S, most_threads<W>>
                               : g.threads <= 512              ? layer_norm_rows_kernel<T, P, W, S, 512>
                                                               : layer_norm_rows_kernel<T, P, W, S, 1024>;
-                launch_ring(kernel, (unsigned)(blocks < most ? blocks : most), block, bytes * S, (cudaStream_t)stream,
-                            static_cast<const T*>(x), M, K, 1.f / K, static_cast<const P*>(weight),
-                            static_cast<const P*>(bias), eps, static_cast<T*>(y), mean, rstd, vec);
+                return launch_ring(kernel, (unsigned)(blocks < most ? blocks : most), block, bytes * S, (cudaStream_t)stream,
+                                   static_cast<const T*>(x), M, K, 1.f / K, static_cast<const P*>(weight),
+                                   static_cast<const P*>(bias), eps, static_cast<T*>(y), mean, rstd, vec);
             });
         };
-        if (!(K % V == 0 ? rows(std::integral_constant<int, V>{}) : rows(std::integral_constant<int, 1>{})))
-            launch_k(layer_norm_kernel<T, P>, (unsigned)M, kRowThreads, 0, (cudaStream_t)stream, static_cast<const T*>(x), K,
-                     static_cast<const P*>(weight), static_cast<const P*>(bias), eps, static_cast<T*>(y), mean, rstd);
+        const int st = K % V == 0 ? rows(std::integral_constant<int, V>{}) : rows(std::integral_constant<int, 1>{});
+        if (st != kNoRing) return st;
+        launch_k(layer_norm_kernel<T, P>, (unsigned)M, kRowThreads, 0, (cudaStream_t)stream, static_cast<const T*>(x), K,
+                 static_cast<const P*>(weight), static_cast<const P*>(bias), eps, static_cast<T*>(y), mean, rstd);
         note_launches(1);
         return launch_status();
     });
@@ -788,10 +790,10 @@ MOE_API int moe_layer_norm_backward(const void* dy, const void* x, int64_t M, in
         int n_parts = 0;
         constexpr int V = 16 / sizeof(T);
         const bool vec = !misaligned(x, 16) && !misaligned(dy, 16) && !misaligned(dx, 16) && !misaligned(weight, 16);
-        auto rows = [&](auto vc) -> bool {
+        auto rows = [&](auto vc) -> int {
             constexpr int W = decltype(vc)::value;
             const Rows g = backward_rows<W>(K);
-            if (g.threads > 1024) return false;
+            if (g.threads > 1024) return kNoRing;
             const dim3 block(g.threads, g.per_block);
             const int64_t blocks = (M + g.per_block - 1) / g.per_block;
             n_parts = (int)(blocks < parts_of<W>(K) ? blocks : parts_of<W>(K));
@@ -802,20 +804,27 @@ MOE_API int moe_layer_norm_backward(const void* dy, const void* x, int64_t M, in
                               : g.threads <= 512 ? layer_norm_backward_kernel<T, P, W, S, 512>
                                                  : layer_norm_backward_kernel<T, P, W, S, 1024>;
                 const size_t sums = g.per_block > 1 ? 2 * K * sizeof(float) : 0;
-                launch_ring(kernel, (unsigned)n_parts, block, bytes * S < sums ? sums : bytes * S, s, static_cast<const T*>(dy),
-                            static_cast<const T*>(x), M, K, 1.f / K, static_cast<const P*>(weight), mean, rstd,
-                            static_cast<T*>(dx), parts, vec);
-                note_launches(1);
+                return launch_ring(kernel, (unsigned)n_parts, block, bytes * S < sums ? sums : bytes * S, s,
+                                   static_cast<const T*>(dy), static_cast<const T*>(x), M, K, 1.f / K,
+                                   static_cast<const P*>(weight), mean, rstd, static_cast<T*>(dx), parts, vec);
             });
         };
-        if (M > 0 && !(K % V == 0 ? rows(std::integral_constant<int, V>{}) : rows(std::integral_constant<int, 1>{}))) {
-            n_parts = (int)(M < kColParts ? M : kColParts);
-            // the column sums read dy before dx, which may be the same buffer, is written
-            launch_k(layer_norm_cols_kernel<T>, dim3((unsigned)((K + 31) / 32), (unsigned)n_parts), 256, 0, s,
-                     static_cast<const T*>(dy), static_cast<const T*>(x), M, K, mean, rstd, parts);
-            launch_k(layer_norm_dx_kernel<T, P>, (unsigned)M, kRowThreads, 0, s, static_cast<const T*>(dy),
-                     static_cast<const T*>(x), K, static_cast<const P*>(weight), mean, rstd, static_cast<T*>(dx));
-            note_launches(2);
+        // a launch that was refused is not followed by one that reads its results
+        if (M > 0) {
+            int st = K % V == 0 ? rows(std::integral_constant<int, V>{}) : rows(std::integral_constant<int, 1>{});
+            if (st == kNoRing) {
+                n_parts = (int)(M < kColParts ? M : kColParts);
+                // the column sums read dy before dx, which may be the same buffer, is written
+                launch_k(layer_norm_cols_kernel<T>, dim3((unsigned)((K + 31) / 32), (unsigned)n_parts), 256, 0, s,
+                         static_cast<const T*>(dy), static_cast<const T*>(x), M, K, mean, rstd, parts);
+                note_launches(1);
+                if ((st = launch_status()) != MOE_OK) return st;
+                launch_k(layer_norm_dx_kernel<T, P>, (unsigned)M, kRowThreads, 0, s, static_cast<const T*>(dy),
+                         static_cast<const T*>(x), K, static_cast<const P*>(weight), mean, rstd, static_cast<T*>(dx));
+                note_launches(1);
+                st = launch_status();
+            }
+            if (st != MOE_OK) return st;
         }
         launch_k(layer_norm_fold_kernel<P>, dim3((unsigned)((K + 31) / 32), d_bias ? 2 : 1), dim3(32, 32), 0, s, parts, n_parts, K,
                  static_cast<P*>(d_weight), static_cast<P*>(d_bias));
