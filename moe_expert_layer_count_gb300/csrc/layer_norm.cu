@@ -13,6 +13,7 @@
 // blocks' partial sums are added in a fixed order by a second kernel.
 // Rows longer than 1024 threads' columns (or the ring) take the looping kernels, which read
 // them again from L2.
+#include <atomic>
 #include <type_traits>
 
 #include "elem.cuh"
@@ -678,23 +679,34 @@ bool norm_args_ok(int64_t M, int K, int dtype, int param_dtype) {
 // Calls f with the stages of a ring that has `bytes` a stage in each of `per_sm` blocks, as a
 // constant, and returns what it returns; kNoRing where not even two fit.
 constexpr int kNoRing = -1;
+constexpr size_t kRingRoom = 200 * 1024;
 template <bool kRing, typename F>
 int with_stages(size_t bytes, int per_sm, F&& f) {
     if constexpr (!kRing) return f(std::integral_constant<int, 0>{});
-    const size_t room = 200 * 1024 / per_sm;
+    const size_t room = kRingRoom / per_sm;
     if (4 * bytes <= room) return f(std::integral_constant<int, 4>{});
     if (3 * bytes <= room) return f(std::integral_constant<int, 3>{});
     if (2 * bytes <= room) return f(std::integral_constant<int, 2>{});
     return kNoRing;
 }
-// 48 KB of shared memory, the kernel's own arrays among them, need no permission; which widths stay
-// within that is not worth a rule of its own.
-template <typename... KArgs, typename... Args>
-int launch_ring(void (*kernel)(KArgs...), unsigned grid, dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess) {
-        launch_k(kernel, grid, block, smem, stream, std::forward<Args>(args)...);
-        note_launches(1);
+// The kernel's shared memory beyond 48 KB needs permission, which is a state of the kernel on the device: given
+// once, for the largest ring, and never lowered, so that calls of other widths beside this one do not
+// matter.
+constexpr int kMaxDevices = 64;
+template <auto kKernel, typename... Args>
+int launch_ring(unsigned grid, dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
+    static std::atomic<bool> allowed[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
+    if (!allowed[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingRoom) != cudaSuccess) {
+            launch_status();
+            return MOE_ERR_CUDA;
+        }
+        allowed[dev].store(true, std::memory_order_release);
     }
+    launch_k(kKernel, grid, block, smem, stream, std::forward<Args>(args)...);
+    note_launches(1);
     return launch_status();
 }
 
@@ -741,12 +753,15 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
             const size_t bytes = Ring<T, W, its<W>>::bytes(K, g.threads, g.per_block);
             return with_stages<true>(bytes, g.per_sm, [&](auto sc) {
                 constexpr int S = decltype(sc)::value;
-                auto kernel = g.threads <= most_threads<W> ? layer_norm_rows_kernel<T, P, W, S, most_threads<W>>
-                              : g.threads <= 512              ? layer_norm_rows_kernel<T, P, W, S, 512>
-                                                              : layer_norm_rows_kernel<T, P, W, S, 1024>;
-                return launch_ring(kernel, (unsigned)(blocks < most ? blocks : most), block, bytes * S, (cudaStream_t)stream,
-                                   static_cast<const T*>(x), M, K, 1.f / K, static_cast<const P*>(weight),
-                                   static_cast<const P*>(bias), eps, static_cast<T*>(y), mean, rstd, vec);
+                auto go = [&](auto tc) {
+                    return launch_ring<layer_norm_rows_kernel<T, P, W, S, decltype(tc)::value>>(
+                        (unsigned)(blocks < most ? blocks : most), block, bytes * S, (cudaStream_t)stream,
+                        static_cast<const T*>(x), M, K, 1.f / K, static_cast<const P*>(weight), static_cast<const P*>(bias),
+                        eps, static_cast<T*>(y), mean, rstd, vec);
+                };
+                if (g.threads <= most_threads<W>) return go(std::integral_constant<int, most_threads<W>>{});
+                if (g.threads <= 512) return go(std::integral_constant<int, 512>{});
+                return go(std::integral_constant<int, 1024>{});
             });
         };
         const int st = K % V == 0 ? rows(std::integral_constant<int, V>{}) : rows(std::integral_constant<int, 1>{});
@@ -800,13 +815,16 @@ MOE_API int moe_layer_norm_backward(const void* dy, const void* x, int64_t M, in
             const size_t bytes = 2 * Ring<T, W, its<W>>::bytes(K, g.threads, g.per_block);
             return with_stages<(W * sizeof(T) != 4)>(bytes, g.per_sm, [&](auto sc) {
                 constexpr int S = decltype(sc)::value;
-                auto kernel = g.threads <= 256   ? layer_norm_backward_kernel<T, P, W, S, 256>
-                              : g.threads <= 512 ? layer_norm_backward_kernel<T, P, W, S, 512>
-                                                 : layer_norm_backward_kernel<T, P, W, S, 1024>;
                 const size_t sums = g.per_block > 1 ? 2 * K * sizeof(float) : 0;
-                return launch_ring(kernel, (unsigned)n_parts, block, bytes * S < sums ? sums : bytes * S, s,
-                                   static_cast<const T*>(dy), static_cast<const T*>(x), M, K, 1.f / K,
-                                   static_cast<const P*>(weight), mean, rstd, static_cast<T*>(dx), parts, vec);
+                auto go = [&](auto tc) {
+                    return launch_ring<layer_norm_backward_kernel<T, P, W, S, decltype(tc)::value>>(
+                        (unsigned)n_parts, block, bytes * S < sums ? sums : bytes * S, s, static_cast<const T*>(dy),
+                        static_cast<const T*>(x), M, K, 1.f / K, static_cast<const P*>(weight), mean, rstd,
+                        static_cast<T*>(dx), parts, vec);
+                };
+                if (g.threads <= 256) return go(std::integral_constant<int, 256>{});
+                if (g.threads <= 512) return go(std::integral_constant<int, 512>{});
+                return go(std::integral_constant<int, 1024>{});
             });
         };
         // a launch that was refused is not followed by one that reads its results

@@ -1,9 +1,14 @@
-"""Layer norm launches at every width, whatever ran before it."""
+"""Layer norm launches at every width, whatever ran before it and beside it: the shared memory that
+a kernel is allowed does not depend on the widths of earlier or concurrent calls."""
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
+import torch
+
+import moe_expert_layer_count_gb300 as moe
 
 pytestmark = pytest.mark.gpu
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -26,3 +31,29 @@ def test_odd_16_bit_widths_in_a_fresh_process(dtype):
     code = FRESH.format(here=HERE, root=os.path.dirname(HERE), dtype=dtype)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "all right" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_widths_from_two_threads():
+    """Both widths run in one kernel, with 64 and with 48 KB of shared memory."""
+    wrong = []
+    go = threading.Barrier(2)
+
+    def calls(K):
+        try:
+            s = torch.cuda.Stream()
+            x = torch.randn(1, K, device="cuda").bfloat16()
+            w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+            y, mean, rstd = moe.moe_layer_norm(x, w, w)
+            torch.cuda.synchronize()
+            go.wait(60)
+            for _ in range(20000):
+                moe.moe_layer_norm(x, w, w, out=y, mean=mean, rstd=rstd, stream=s)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            wrong.append(f"K = {K}: {e}")
+    threads = [threading.Thread(target=calls, args=(K,)) for K in (8192, 6144)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
