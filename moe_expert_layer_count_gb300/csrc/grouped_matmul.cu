@@ -758,6 +758,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
     __syncthreads();
     cluster_sync();  // no CTA leaves while the other still signals its barriers or uses its TMEM
     if (warp == kMmaWarp) {
+        // The MMAs' completions are signalled to both CTAs by the hardware, outside of any thread's order: the
+        // first CTA has seen the last of them, the second may not leave before it has arrived there too (its
+        // shared memory may by then be another kernel's).
+        if (rank == 1) wait_phase(ptx::smem_addr(&st->mma_done), 0, abort, false);
+        __syncwarp();
         ptx::tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
