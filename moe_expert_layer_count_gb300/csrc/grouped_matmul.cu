@@ -18,7 +18,7 @@
 // The operand that TMA loads with its reduced index outermost (the weights of dgrad, both
 // operands of wgrad) is read as an MN-major tile: 64 x 64 boxes, no transposition in memory.
 // A persistent grid of CTA pairs; per CTA: warps 0-3 epilogue, warp 4 TMA, warp 5 MMA (issued
-// by the pair's first CTA), warp 6 wgrad's ragged ends. Two TMEM accumulators, so that a tile's
+// by the pair's first CTA), warps 6 and 7 wgrad's ragged ends. Two TMEM accumulators, so that a tile's
 // epilogue runs under the next tile's MMAs. Every pipeline wait gives up after 2 s, sets a device
 // error word and ends the kernel.
 //
@@ -72,7 +72,7 @@ __host__ __device__ constexpr int staging_bytes() { return kEpiWarps * kBoxBytes
 constexpr int kSmemLimit = 232448;
 constexpr int kRowBoxes = 5;       // boxes of 8, 16, 32, 64, 128 rows
 template <int MODE>
-__host__ __device__ constexpr int threads_of() { return MODE == kWgrad ? 224 : 192; }  // the tail warp is wgrad's
+__host__ __device__ constexpr int threads_of() { return MODE == kWgrad ? 256 : 192; }  // the tail warps are wgrad's
 constexpr int kBuckets = 128;      // steps of cost that the groups are sorted by
 constexpr int kSms = 152;           // what a workspace size is computed for
 constexpr int kMaxDevices = 64;
@@ -125,7 +125,7 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // The arrival that makes this warp's shared-memory writes visible to the other CTA's waiter (which takes
-// wait_phase<true>). It waits for the thread's own global stores; the tail warp has none.
+// wait_phase<true>). It waits for the thread's own global stores; the tail warps have none.
 __device__ __forceinline__ void arrive_cluster_release(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -502,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 const uint32_t a = ptx::smem_addr(smem + s * kStageBytes), b = a + kOperandBytes;
                 const uint32_t full = ptx::smem_addr(&st->full[s]), bar = pair_full + 8 * s;
                 const int d = k * kDepth;
-                if (MODE == kWgrad && ragged(t, k)) {  // this CTA's tail warp comes first
+                if (MODE == kWgrad && ragged(t, k)) {  // this CTA's tail warps come first
                     if (lead) {
                         const uint32_t land = ptx::smem_addr(&st->land[s]);
                         ptx::mbar_arrive_expect_tx(land, kStageBytes);
@@ -596,8 +596,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 wait_phase(ptx::smem_addr(&st->mma_done), 0, abort, false);
             }
         }
-    } else if (MODE == kWgrad && warp == kTailWarp) {
-        // a group's last stage: the rows past the group's end within the last 16 that the MMAs
+    } else if (MODE == kWgrad && warp >= kTailWarp) {
+        // a group's last stage, the first warp's where it lies in an even stage (each warp sees all phases of its
+        // stages' barriers; one warp alone, with the wait for its writes to reach the cluster, took longer than
+        // the rest of a decode-sized tile: 512 rows over 128 groups 143.8 -> 131.6 us): the rows past the group's end within the last 16 that the MMAs
         // read become zeros in all four boxes of this CTA
         int s = 0;
         uint32_t landed = 0;
@@ -605,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             const Tile t = tile_at<MODE>(tile, groups, El, sh);
             if (t.steps == 0) continue;
             s = (s + t.steps - 1) % stages;
-            if (ragged(t, t.steps - 1)) {
+            if (ragged(t, t.steps - 1) && (s & 1) == warp - kTailWarp) {
                 const bool ok = wait_phase(ptx::smem_addr(&st->land[s]), landed >> s & 1, abort);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 landed ^= 1u << s;
