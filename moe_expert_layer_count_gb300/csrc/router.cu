@@ -286,8 +286,11 @@ __global__ void __launch_bounds__(kListThreads)
             load8<T, kVec>(row, c + h / 8, lane, E, v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                // -0 becomes +0, NaN -inf
-                const uint32_t u = __float_as_uint(fmaxf(v[j] + 0.f, -INFINITY));
+                // -0 becomes +0, NaN -inf; an fp32 +inf is the largest finite value itself, while that lies above
+                // every 16-bit logit, as +inf's key does
+                float l = fmaxf(v[j] + 0.f, -INFINITY);
+                if constexpr (sizeof(T) == 4) l = fminf(l, kFltMax);
+                const uint32_t u = __float_as_uint(l);
                 const uint32_t order = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
                 now[h + j] = Key::make(order, expert_at<kVec>(c + h / 8, lane, j) & kIndexMask);
             }
