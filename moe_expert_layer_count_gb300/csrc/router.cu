@@ -316,8 +316,8 @@ __global__ void __launch_bounds__(kListThreads)
 #pragma unroll
         for (int q = 1; q < kLanes; ++q)
             if (lane == q) k = best[i * kLanes + q];
-        const float l = fminf(Key::logit(k), kFltMax);
-        const bool chosen = l > -INFINITY && i * kLanes + lane < topk;  // false for NaN: no such logit
+        const float value = Key::logit(k), l = fminf(value, kFltMax);
+        const bool chosen = value > -INFINITY && i * kLanes + lane < topk;  // not for key 0, whose logit is NaN
         id[i] = chosen ? Key::index(k) : -1;
         if (soft)
             w[i] = chosen ? expf(l - top) : 0.f;
@@ -431,16 +431,16 @@ __global__ void __launch_bounds__(kPairThreads)
     auto logit_of = [&](uint32_t k) {
         const uint32_t o = k >> 16;
         const uint16_t u = (uint16_t)(o & 0x8000u ? o ^ 0x8000u : ~o);
-        return fminf(to_f32(*reinterpret_cast<const T*>(&u)), kFltMax);
+        return to_f32(*reinterpret_cast<const T*>(&u));
     };
-    const float top = logit_of(best[0]);
+    const float top = fminf(logit_of(best[0]), kFltMax);
     float w[4], sum = 0.f;
     int id[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t k = lane ? best[4 + i] : best[i];
-        const float l = logit_of(k);
-        const bool chosen = l > -INFINITY && lane * 4 + i < topk;
+        const float value = logit_of(k), l = fminf(value, kFltMax);
+        const bool chosen = value > -INFINITY && lane * 4 + i < topk;  // not for key 0, whose logit is NaN
         id[i] = chosen ? (int)(kIndexMask - (k & kIndexMask)) : -1;
         if (soft)
             w[i] = chosen ? expf(l - top) : 0.f;
