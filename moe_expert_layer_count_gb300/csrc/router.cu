@@ -58,6 +58,17 @@ __device__ __forceinline__ float sigmoid_share(float l) {
     return S > 0.f ? s / S : 0.f;
 }
 
+// exp(x) of a softmax over logits of type T. For fp32 it is good to 2 ulp. For 16-bit logits the faster
+// form, whose relative error grows as |x| * 2^-24: what is written in 16 bits rounds by 2^-12 or more, and the fp32
+// weights only have it in their sum, where a term that is far from the maximum counts for little.
+template <typename T>
+__device__ __forceinline__ float exp_of(float x) {
+    if constexpr (sizeof(T) == 4)
+        return expf(x);
+    else
+        return __expf(x);
+}
+
 // The V logits of this lane (absent ones -inf).
 template <typename T, int V, bool kVec>
 __device__ __forceinline__ void load_logits(const T* __restrict__ row, int lane, int E, float (&v)[V]) {
@@ -333,7 +344,7 @@ __global__ void __launch_bounds__(kListThreads)
             float v[8];
             load8<T, kVec>(row, c, lane, E, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += __expf(clean_logit(v[j]) - top);
+            for (int j = 0; j < 8; ++j) sum += exp_of<T>(clean_logit(v[j]) - top);
         }
     }
     if (soft || renorm) {
@@ -459,7 +470,7 @@ __global__ void __launch_bounds__(kPairThreads)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint16_t u = (uint16_t)(w4[j / 2] >> (j % 2 * 16));
-                sum += __expf(clean_logit(to_f32(*reinterpret_cast<const T*>(&u))) - top);
+                sum += exp_of<T>(clean_logit(to_f32(*reinterpret_cast<const T*>(&u))) - top);
             }
         }
     }
@@ -564,14 +575,14 @@ __global__ void __launch_bounds__(kGradThreads)
 #pragma unroll
             for (int j = 0; j < 8; ++j) most = fmaxf(most, v[j]);
             if (most > -INFINITY) {
-                sum *= __expf(m - most);
+                sum *= exp_of<T>(m - most);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum += __expf(v[j] - most);
+                for (int j = 0; j < 8; ++j) sum += exp_of<T>(v[j] - most);
                 m = most;
             }
         }
         top = group_max(m);
-        sum = group_sum(m > -INFINITY ? sum * __expf(m - top) : 0.f);
+        sum = group_sum(m > -INFINITY ? sum * exp_of<T>(m - top) : 0.f);
         const float r = sum > 0.f ? 1.f / sum : 0.f;
         float s[kSlots], dot = 0.f;
 #pragma unroll
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(kGradThreads)
         if (rest != 0.f) {
             load(c, v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = rest * __expf(v[j] - top);
+            for (int j = 0; j < 8; ++j) v[j] = rest * exp_of<T>(v[j] - top);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = 0.f;

@@ -22,3 +22,20 @@ def test_infinity_ties_with_the_largest_finite_value(E, topk, scoring, renorm):
         row[0], row[E // 2], row[E - 1] = a, b, c
         rows.append(row)
     check_forward(torch.tensor(rows, device="cuda"), topk, scoring, renorm, 1.0)
+
+
+@pytest.mark.parametrize("E", [128, 100, 1000])
+def test_gradient_far_below_the_maximum(E):
+    """fp32 logits 0, 0 and negative multiples of 1/4, the first one chosen. Experts that were not chosen get
+    rest * exp(l), the second one rest itself: their ratios have the exponential's 2 ulp (4 * 2^-24) and
+    the product's rounding, however small they are."""
+    rng = np.random.default_rng(E)
+    l = -rng.integers(1, 320, (64, E)).astype(np.float32) / 4
+    l[:, :2] = 0.0
+    ids = torch.zeros(64, 1, dtype=torch.int32, device="cuda")
+    g = torch.ones(64, 1, device="cuda")
+    d = moe.moe_router_topk_backward(torch.from_numpy(l).cuda(), ids, g, SOFT, False, 1.5).double().cpu().numpy()
+    assert (d[:, 1] < 0).all()
+    ref = np.exp(l[:, 2:].astype(np.float64))
+    rel = np.abs(d[:, 2:] / d[:, 1:2] - ref) / ref
+    assert rel.max() <= 5.01 * 2.0 ** -24, rel.max() * 2.0 ** 24
