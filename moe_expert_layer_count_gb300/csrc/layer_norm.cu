@@ -433,7 +433,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
 template <typename T, int V, int S, int kThreads>
 constexpr int rows_at_once = sizeof(T) == 2 && V > 1 && S >= 4 && kThreads <= 512 ? 2 : 1;
 
-// (x - mean) * rstd is taken as x * rstd - mean * rstd in one rounding.
+// x - mean is one subtraction, so that its error does not grow with the mean; x * rstd - mean * rstd in one
+// rounding would save an instruction a pair (8192 x 2048 bf16: 23.8 against 23.9 us) and at a mean of 1000
+// spreads gives the weight's gradient an error of 2e-5.
 template <typename T, typename P, int V, int S, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
     layer_norm_backward_kernel(const T* dy, const T* __restrict__ x, int64_t M, int K, float inv_k,
@@ -505,12 +507,12 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
             ds[0] = dn;
             if (i + 1 < turn.all) fetch(i + 1);
         }
-        float rstd[kR], shift[kR];
+        float rstd[kR], mean[kR];
         float2 a[kR], b[kR];
 #pragma unroll
         for (int k = 0; k < kR; ++k) {
             rstd[k] = rstd_n[k];
-            shift[k] = -mean_n[k] * rstd_n[k];
+            mean[k] = mean_n[k];
             a[k] = b[k] = both(0.f);
         }
         statistics(i + kR);
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
             if (i + k < turn.mine) {
 #pragma unroll
                 for (int p = 0; p < Sh::kPairs; ++p) {
-                    const float2 d = ds[k].get(p), h = __ffma2_rn(xs[k].get(p), both(rstd[k]), both(shift[k])),
+                    const float2 d = ds[k].get(p), h = __fmul2_rn(__fadd2_rn(xs[k].get(p), both(-mean[k])), both(rstd[k])),
                                  g = __fmul2_rn(d, w.get(p));
                     a[k] = __fadd2_rn(a[k], g);
                     b[k] = __ffma2_rn(g, h, b[k]);
@@ -533,12 +535,11 @@ __global__ void __launch_bounds__(kThreads, kThreads > 256 ? 1 : 2)
 #pragma unroll
         for (int k = 0; k < kR; ++k)
             if (i + k < turn.mine) {
-                // rstd * (g - a - h b)
-                const float2 c = both(-a[k].x * inv_k * rstd[k]), e = both(-a[k].y * inv_k);
+                // rstd * (g - a - (x - mean) (rstd b))
+                const float2 c = both(-a[k].x * inv_k * rstd[k]), e = both(-a[k].y * inv_k * rstd[k]);
 #pragma unroll
                 for (int p = 0; p < Sh::kPairs; ++p) {
-                    const float2 h = __ffma2_rn(xs[k].get(p), both(rstd[k]), both(shift[k])),
-                                 g = __fmul2_rn(ds[k].get(p), w.get(p));
+                    const float2 h = __fadd2_rn(xs[k].get(p), both(-mean[k])), g = __fmul2_rn(ds[k].get(p), w.get(p));
                     xs[k].set(p, __ffma2_rn(__ffma2_rn(h, e, g), both(rstd[k]), c));
                 }
                 xs[k].store(dx + here + k * hop, K, base, vec, whole);
