@@ -356,6 +356,12 @@ struct Turns {
     }
 };
 
+// sum / K in one rounding, from the reciprocal of K; infinities and NaN as they are.
+__device__ __forceinline__ float mean_of(float sum, float K, float inv_k) {
+    const float q = div_rn_by(sum, K, inv_k);
+    return fabsf(sum) <= 3.402823466e38f ? q : sum;
+}
+
 // kThreads, here and below: the most threads of a block.
 template <typename T, typename P, int V, int S, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 256 ? 4 : 1)
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 128 ? 5 : kThreads == 25
         float2 a = both(0.f);
 #pragma unroll
         for (int p = 0; p < Sh::kPairs; ++p) a = __fadd2_rn(a, xs.get(p));
-        const float mean = row_sum(a.x + a.y, s[at]) * inv_k;
+        const float mean = mean_of(row_sum(a.x + a.y, s[at]), (float)K, inv_k);
         a = both(0.f);
         if (whole) {
 #pragma unroll

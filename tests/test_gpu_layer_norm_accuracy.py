@@ -37,6 +37,18 @@ def test_gradients_of_rows_far_from_zero(M, K, dtype, shift):
     assert err <= 8 * E, err.item()
 
 
+@pytest.mark.parametrize("K", [96, 1111, 1536, 5000, 9000, 10001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_mean_is_the_quotient(K, dtype):
+    """Rows of small whole numbers: every sum is exact, so that the mean has one rounding."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randint(-8, 9, (4096, K), device="cuda", generator=g).to(dtype)
+    w = torch.ones(K, device="cuda")
+    _, mean, _ = moe.moe_layer_norm(x, w, w)
+    ref = x.double().sum(1) / K
+    assert ((mean.double() - ref).abs() <= E * ref.abs()).all(), ((mean.double() - ref).abs() / ref.abs()).nan_to_num(0).max() / E
+
+
 @pytest.mark.parametrize("K", [64, 2048, 8192, 32768])
 def test_reciprocal_root(K):
     """Rows of +a and -a, a of 8 bits: mean 0 and variance a^2 exactly (no partial sum of the squares has more
@@ -67,3 +79,12 @@ def test_results_do_not_depend_on_alignment(M, K, dtype, shift):
     first = moe.moe_layer_norm_backward(dy, x, w, *first[1:])
     second = moe.moe_layer_norm_backward(moved(dy), moved(x), moved(w), *second[1:])
     assert all(torch.equal(p, q) for p, q in zip(first, second))
+
+
+@pytest.mark.parametrize("K", [1111, 2048, 20000])
+def test_mean_of_rows_that_hold_infinities(K):
+    x = torch.randn(4, K, device="cuda")
+    x[0, 3], x[1, 5], x[2, 7], x[2, 8] = float("inf"), -float("inf"), float("inf"), -float("inf")
+    w = torch.ones(K, device="cuda")
+    mean = moe.moe_layer_norm(x, w, w)[1].tolist()
+    assert mean[0] == float("inf") and mean[1] == -float("inf") and mean[2] != mean[2] and abs(mean[3]) < 1
