@@ -371,7 +371,8 @@ MOE_API int moe_host_wait(moe_stream_t stream);
 MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const void* weight, const void* bias,
                            int param_dtype, float eps, void* y, float* mean, float* rstd, moe_stream_t stream);
 
-/* Scratch bytes moe_layer_norm_backward needs. Returns 0 on bad arguments. */
+/* Scratch bytes moe_layer_norm_backward needs: 2 K floats for every block, of which there are no more
+ * than rows. Returns 0 on bad arguments. */
 MOE_API size_t moe_layer_norm_workspace_size(int64_t M, int K);
 
 /* Its gradients, from x and the mean and rstd of the forward pass. With

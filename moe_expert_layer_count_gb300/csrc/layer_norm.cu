@@ -782,9 +782,11 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
 
 MOE_API size_t moe_layer_norm_workspace_size(int64_t M, int K) {
     if (M < 0 || K < 1 || K > kMostColumns) return 0;
-    // whichever way the rows are divided (by their type and alignment), the looping kernels too
+    // whichever way the rows are divided (by their type and alignment), the looping kernels too; never more
+    // partial sums than rows, and one for no rows, so that there is a workspace to name
     int n = parts_of<1>(K) > parts_of<8>(K) ? parts_of<1>(K) : parts_of<8>(K);
     if (n < kColParts) n = kColParts;
+    if (n > M) n = M > 1 ? (int)M : 1;
     return (size_t)n * 2 * K * sizeof(float);
 }
 
