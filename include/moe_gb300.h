@@ -357,7 +357,9 @@ MOE_API int moe_host_wait(moe_stream_t stream);
  * their gradients, and the clipping of the gradients. (moe_scatter with MOE_QUANT_NONE
  * and moe_gather_weight_reduce permute between them in both directions.)
  * All sums, statistics and products are held in fp32 (the norm of a list of tensors
- * partly in fp64) and rounded once where a result is stored in 16 bits. */
+ * partly in fp64) and rounded once where a result is stored in 16 bits.
+ * Every pointer is aligned to its elements, or further where that is said (MOE_ERR_INVALID_ARG
+ * otherwise). */
 
 /* Layer norm over the last dimension of x [M, K]:
  *   mean = sum x / K;  rstd = 1 / sqrt(sum (x - mean)^2 / K + eps)

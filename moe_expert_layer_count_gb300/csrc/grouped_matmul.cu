@@ -874,7 +874,7 @@ int grouped_impl(const void* a, const void* b, const int32_t* off, const int32_t
         (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16) || (out_dtype != dtype && out_dtype != MOE_DT_F32))
         return MOE_ERR_INVALID_ARG;
     if (((R > 0 || MODE == kWgrad) && !out) || (R > 0 && (!a || !b)) || misaligned(a, 16) || misaligned(b, 16) ||
-        misaligned(out, 16))
+        misaligned(out, 16) || misaligned(off, 4) || misaligned(cnt, 4))
         return MOE_ERR_INVALID_ARG;
     // tiles are counted in 32 bits
     const int64_t m_tiles = ((int64_t)(MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;

@@ -738,7 +738,8 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
     if (!norm_args_ok(M, K, dtype, param_dtype) || !(eps >= 0.f)) return MOE_ERR_INVALID_ARG;
     if (M == 0) return MOE_OK;
     const int z = dtype_bytes(dtype), zp = dtype_bytes(param_dtype);
-    if (!x || !weight || !y || misaligned(x, z) || misaligned(y, z) || misaligned(weight, zp) || misaligned(bias, zp))
+    if (!x || !weight || !y || misaligned(x, z) || misaligned(y, z) || misaligned(weight, zp) || misaligned(bias, zp) ||
+        misaligned(mean, 4) || misaligned(rstd, 4))
         return MOE_ERR_INVALID_ARG;
     const size_t n = (size_t)M * K * z;
     if ((y != x && overlap(y, n, x, n)) || overlap(y, n, weight, (size_t)K * zp) ||
@@ -798,7 +799,7 @@ MOE_API int moe_layer_norm_backward(const void* dy, const void* x, int64_t M, in
     const int z = dtype_bytes(dtype), zp = dtype_bytes(param_dtype);
     if (misaligned(d_weight, zp) || misaligned(d_bias, zp)) return MOE_ERR_INVALID_ARG;
     if (M > 0 && (!dy || !x || !weight || !mean || !rstd || !dx || misaligned(dy, z) || misaligned(x, z) ||
-                  misaligned(dx, z) || misaligned(weight, zp)))
+                  misaligned(dx, z) || misaligned(weight, zp) || misaligned(mean, 4) || misaligned(rstd, 4)))
         return MOE_ERR_INVALID_ARG;
     const size_t n = (size_t)M * K * z;
     if ((dx != dy && overlap(dx, n, dy, n)) || overlap(dx, n, x, n) || overlap(workspace, workspace_bytes, dy, n) ||

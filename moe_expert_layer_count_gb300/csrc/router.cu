@@ -684,7 +684,9 @@ int router_impl(const void* logits, int64_t M, int E, int dtype, int topk, int s
                 float scale, float* w, TId* ids, moe_stream_t stream) {
     if (!router_args_ok(M, E, dtype, topk, scoring)) return MOE_ERR_INVALID_ARG;
     if (M == 0) return MOE_OK;
-    if (!logits || !w || !ids || misaligned(logits, dtype_bytes(dtype))) return MOE_ERR_INVALID_ARG;
+    if (!logits || !w || !ids || misaligned(logits, dtype_bytes(dtype)) || misaligned(bias, 4) || misaligned(w, 4) ||
+        misaligned(ids, sizeof(TId)))
+        return MOE_ERR_INVALID_ARG;
     const size_t nl = (size_t)M * E * dtype_bytes(dtype), nw = (size_t)M * topk * 4, ni = (size_t)M * topk * sizeof(TId);
     if (overlap(w, nw, logits, nl) || overlap(ids, ni, logits, nl) || overlap(w, nw, ids, ni)) return MOE_ERR_INVALID_ARG;
     if (int st = check_device(nullptr)) return st;
@@ -727,7 +729,7 @@ int router_backward_impl(const void* logits, int64_t M, int E, int dtype, const 
     if (!router_args_ok(M, E, dtype, topk, scoring)) return MOE_ERR_INVALID_ARG;
     if (M == 0) return MOE_OK;
     if (!logits || !ids || !dw || !d_logits || misaligned(logits, dtype_bytes(dtype)) ||
-        misaligned(d_logits, dtype_bytes(dtype)))
+        misaligned(d_logits, dtype_bytes(dtype)) || misaligned(ids, sizeof(TId)) || misaligned(dw, 4))
         return MOE_ERR_INVALID_ARG;
     const size_t nl = (size_t)M * E * dtype_bytes(dtype);
     if ((d_logits != logits && overlap(d_logits, nl, logits, nl)) ||

@@ -1,5 +1,19 @@
-"""The scratch memory that the training operators ask for. No GPU needed."""
-from test_train_abi import L  # noqa: F401
+"""The training operators' checks of the memory that a call names, and the scratch memory that they ask for.
+No GPU needed, and none used: the addresses are made up, so that calls are not tried where a kernel
+could be launched on them."""
+import ctypes
+
+import pytest
+import torch
+
+from test_train_abi import BF, FP, INVALID, L, at  # noqa: F401
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up device addresses")
+ACCEPTED = (3, 4)  # past the checks: there is no device here
+
+
+def off(mib, n):
+    return ctypes.c_void_p((mib << 20) + n)
 
 
 def test_layer_norm_workspace_follows_the_rows(L):  # noqa: F811
@@ -10,3 +24,43 @@ def test_layer_norm_workspace_follows_the_rows(L):  # noqa: F811
         assert 0 < size(5, K) <= 5 * 2 * K * 4
         assert size(0, K) <= size(1, K) <= size(100, K) <= size(1 << 20, K)
     assert size(1 << 20, 2048) == size(1 << 30, 2048)
+
+
+# Each call with its pointers, all but the big operands' (their checks are in test_train_abi), and what they
+# point to. The other arguments are small and right.
+def calls(L):  # noqa: F811
+    def layer_norm(mean=at(5), rstd=at(6)):
+        return L.moe_layer_norm(at(1), 64, 512, BF, at(2), at(3), FP, 1e-5, at(4), mean, rstd, None)
+
+    def layer_norm_backward(mean=at(4), rstd=at(5)):
+        return L.moe_layer_norm_backward(at(1), at(2), 64, 512, BF, at(3), FP, mean, rstd, at(6), at(7), at(8), at(64),
+                                         16 << 20, None)
+
+    def router(z):
+        fn = L.moe_router_topk if z == 4 else L.moe_router_topk_i64
+        return lambda bias=at(2), weights=at(3), ids=at(4): fn(at(1), 64, 128, BF, 8, 0, bias, 1, 1.0, weights, ids, None)
+
+    def router_backward(z):
+        fn = L.moe_router_topk_backward if z == 4 else L.moe_router_topk_backward_i64
+        return lambda ids=at(2), weights=at(3): fn(at(1), 64, 128, BF, ids, 8, 0, 1, 1.0, weights, at(4), None)
+
+    def grouped(fn):
+        return lambda offsets=at(3), counts=at(4): fn(at(1), 256, at(2), 4, 64, 64, offsets, counts, BF, BF, at(5), None)
+
+    def wgrad(offsets=at(3), counts=at(4)):
+        return L.moe_grouped_matmul_wgrad(at(1), at(2), 256, 4, 64, 64, offsets, counts, BF, BF, at(5), None, 0, None)
+    return [(layer_norm, dict(mean=4, rstd=4)), (layer_norm_backward, dict(mean=4, rstd=4)),
+            (router(4), dict(bias=4, weights=4, ids=4)), (router(8), dict(bias=4, weights=4, ids=8)),
+            (router_backward(4), dict(ids=4, weights=4)), (router_backward(8), dict(ids=8, weights=4)),
+            (grouped(L.moe_grouped_matmul), dict(offsets=4, counts=4)),
+            (grouped(L.moe_grouped_matmul_dgrad), dict(offsets=4, counts=4)), (wgrad, dict(offsets=4, counts=4))]
+
+
+@no_gpu
+def test_every_pointer_is_aligned_to_its_elements(L):  # noqa: F811
+    for call, sizes in calls(L):
+        assert call() in ACCEPTED
+        for name, z in sizes.items():
+            for shift in (1, z // 2):
+                assert call(**{name: off(30, shift)}) == INVALID, (call, name, shift)
+            assert call(**{name: off(30, z)}) in ACCEPTED
