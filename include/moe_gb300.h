@@ -359,7 +359,8 @@ MOE_API int moe_host_wait(moe_stream_t stream);
  * All sums, statistics and products are held in fp32 (the norm of a list of tensors
  * partly in fp64) and rounded once where a result is stored in 16 bits.
  * Every pointer is aligned to its elements, or further where that is said (MOE_ERR_INVALID_ARG
- * otherwise). */
+ * otherwise). Outputs and workspaces overlap neither one another nor an input that the same
+ * call reads, but where that is said; what would let a kernel read what it has written is refused. */
 
 /* Layer norm over the last dimension of x [M, K]:
  *   mean = sum x / K;  rstd = 1 / sqrt(sum (x - mean)^2 / K + eps)

@@ -885,12 +885,16 @@ int grouped_impl(const void* a, const void* b, const int32_t* off, const int32_t
     const size_t a_bytes = (size_t)R * (MODE == kFwd ? K : N) * 2;
     const size_t b_bytes = MODE == kWgrad ? (size_t)R * K * 2 : wn * 2;
     const size_t o_bytes = (MODE == kWgrad ? wn : (size_t)R * (MODE == kFwd ? N : K)) * dtype_bytes(out_dtype);
-    if (overlap(out, o_bytes, a, a_bytes) || overlap(out, o_bytes, b, b_bytes)) return MOE_ERR_INVALID_ARG;
+    const size_t off_bytes = ((size_t)El + 1) * 4, cnt_bytes = cnt ? (size_t)El * 4 : 0;  // read by every CTA as it starts
+    if (overlap(out, o_bytes, a, a_bytes) || overlap(out, o_bytes, b, b_bytes) || overlap(out, o_bytes, off, off_bytes) ||
+        overlap(out, o_bytes, cnt, cnt_bytes))
+        return MOE_ERR_INVALID_ARG;
     if (MODE == kWgrad) {
         const size_t need = moe_grouped_matmul_wgrad_workspace_size(R, El, N, K);
         if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE_TOO_SMALL;
         if (need > 0 && (misaligned(workspace, 16) || overlap(workspace, need, a, a_bytes) || overlap(workspace, need, b, b_bytes) ||
-                         overlap(workspace, need, out, o_bytes)))
+                         overlap(workspace, need, out, o_bytes) || overlap(workspace, need, off, off_bytes) ||
+                         overlap(workspace, need, cnt, cnt_bytes)))
             return MOE_ERR_INVALID_ARG;
     }
     int sms = 0;

@@ -742,8 +742,12 @@ MOE_API int moe_layer_norm(const void* x, int64_t M, int K, int dtype, const voi
         misaligned(mean, 4) || misaligned(rstd, 4))
         return MOE_ERR_INVALID_ARG;
     const size_t n = (size_t)M * K * z;
-    if ((y != x && overlap(y, n, x, n)) || overlap(y, n, weight, (size_t)K * zp) ||
-        overlap(y, n, bias, bias ? (size_t)K * zp : 0))
+    const size_t nm = mean ? (size_t)M * 4 : 0, nr = rstd ? (size_t)M * 4 : 0, nw = (size_t)K * zp, nb = bias ? nw : 0;
+    if ((y != x && overlap(y, n, x, n)) || overlap(y, n, weight, nw) || overlap(y, n, bias, nb)) return MOE_ERR_INVALID_ARG;
+    // the statistics, too, are written while other blocks still read
+    if (overlap(mean, nm, x, n) || overlap(mean, nm, y, n) || overlap(mean, nm, weight, nw) || overlap(mean, nm, bias, nb) ||
+        overlap(rstd, nr, x, n) || overlap(rstd, nr, y, n) || overlap(rstd, nr, weight, nw) || overlap(rstd, nr, bias, nb) ||
+        overlap(mean, nm, rstd, nr))
         return MOE_ERR_INVALID_ARG;
     int sms = 0;
     if (int st = check_device(&sms)) return st;
@@ -805,7 +809,16 @@ MOE_API int moe_layer_norm_backward(const void* dy, const void* x, int64_t M, in
     if ((dx != dy && overlap(dx, n, dy, n)) || overlap(dx, n, x, n) || overlap(workspace, workspace_bytes, dy, n) ||
         overlap(workspace, workspace_bytes, x, n) || overlap(workspace, workspace_bytes, dx, n))
         return MOE_ERR_INVALID_ARG;
-    if (workspace_bytes < moe_layer_norm_workspace_size(M, K)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const size_t need = moe_layer_norm_workspace_size(M, K);
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    // dx and the partial sums are written while other blocks still read the weight and the statistics, the
+    // column sums (which may lie over any of the inputs) while the partial sums are read
+    const size_t nm = (size_t)M * 4, nw = (size_t)K * zp, nb = d_bias ? nw : 0, nin = M > 0 ? nw : 0;
+    if (overlap(dx, n, weight, nin) || overlap(dx, n, mean, nm) || overlap(dx, n, rstd, nm) || overlap(dx, n, d_weight, nw) ||
+        overlap(dx, n, d_bias, nb) || overlap(workspace, need, weight, nin) || overlap(workspace, need, mean, nm) ||
+        overlap(workspace, need, rstd, nm) || overlap(workspace, need, d_weight, nw) || overlap(workspace, need, d_bias, nb) ||
+        overlap(d_weight, nw, d_bias, nb))
+        return MOE_ERR_INVALID_ARG;
     if (int st = check_device(nullptr)) return st;
     return with_types(dtype, param_dtype, [&](auto* t, auto* p) {
         using T = std::remove_pointer_t<decltype(t)>;

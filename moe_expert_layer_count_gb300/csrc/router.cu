@@ -688,7 +688,10 @@ int router_impl(const void* logits, int64_t M, int E, int dtype, int topk, int s
         misaligned(ids, sizeof(TId)))
         return MOE_ERR_INVALID_ARG;
     const size_t nl = (size_t)M * E * dtype_bytes(dtype), nw = (size_t)M * topk * 4, ni = (size_t)M * topk * sizeof(TId);
-    if (overlap(w, nw, logits, nl) || overlap(ids, ni, logits, nl) || overlap(w, nw, ids, ni)) return MOE_ERR_INVALID_ARG;
+    const size_t nb = bias ? (size_t)E * 4 : 0;
+    if (overlap(w, nw, logits, nl) || overlap(ids, ni, logits, nl) || overlap(w, nw, ids, ni) || overlap(w, nw, bias, nb) ||
+        overlap(ids, ni, bias, nb))
+        return MOE_ERR_INVALID_ARG;
     if (int st = check_device(nullptr)) return st;
     const unsigned grid = (unsigned)((M + kRouterWarps - 1) / kRouterWarps);
     return with_dtype(dtype, [&](auto* p) {

@@ -64,3 +64,55 @@ def test_every_pointer_is_aligned_to_its_elements(L):  # noqa: F811
             for shift in (1, z // 2):
                 assert call(**{name: off(30, shift)}) == INVALID, (call, name, shift)
             assert call(**{name: off(30, z)}) in ACCEPTED
+
+
+@no_gpu
+def test_layer_norm_overlaps(L):  # noqa: F811
+    M, K = 64, 512
+
+    def fwd(x=at(1), w=at(2), b=at(3), y=at(4), mean=at(5), rstd=at(6)):
+        return L.moe_layer_norm(x, M, K, BF, w, b, FP, 1e-5, y, mean, rstd, None)
+    assert fwd() in ACCEPTED and fwd(y=at(1)) in ACCEPTED and fwd(mean=None, rstd=None) in ACCEPTED
+    for bad in (dict(mean=off(1, 64)), dict(rstd=off(1, 64)),                    # rows that other blocks read later
+                dict(mean=off(4, 64)), dict(rstd=off(4, 64)), dict(rstd=off(5, 4)),
+                dict(mean=at(2)), dict(rstd=at(3))):
+        assert fwd(**bad) == INVALID, bad
+
+    def bwd(dy=at(1), x=at(2), w=at(3), mean=at(4), rstd=at(5), dx=at(6), dw=at(7), db=at(8), ws=at(64)):
+        return L.moe_layer_norm_backward(dy, x, M, K, BF, w, FP, mean, rstd, dx, dw, db, ws, 16 << 20, None)
+    assert bwd() in ACCEPTED and bwd(dx=at(1)) in ACCEPTED and bwd(db=None) in ACCEPTED
+    # the column sums are written once everything has been read
+    assert bwd(dw=at(3)) in ACCEPTED and bwd(dw=at(4), db=off(2, 64)) in ACCEPTED
+    for bad in (dict(dx=at(3)), dict(dx=at(4)), dict(dx=at(5)),
+                dict(dw=at(6)), dict(db=off(6, 64)), dict(db=off(7, 64)), dict(dw=off(64, 64)), dict(db=off(64, 64)),
+                dict(w=off(64, 64)), dict(mean=off(64, 64)), dict(rstd=off(64, 64))):
+        assert bwd(**bad) == INVALID, bad
+
+
+@no_gpu
+def test_router_overlaps(L):  # noqa: F811
+    for fn in (L.moe_router_topk, L.moe_router_topk_i64):
+        def fwd(x=at(1), bias=at(2), w=at(3), i=at(4)):
+            return fn(x, 64, 128, BF, 8, 0, bias, 1, 1.0, w, i, None)
+        assert fwd() in ACCEPTED and fwd(bias=None) in ACCEPTED
+        for bad in (dict(w=off(2, 64)), dict(i=off(2, 64))):            # the bias that other blocks read later
+            assert fwd(**bad) == INVALID, bad
+
+
+@no_gpu
+def test_grouped_overlaps(L):  # noqa: F811
+    def fwd(a=at(1), w=at(2), off_=at(3), cnt=at(4), out=at(5), fn=L.moe_grouped_matmul):
+        return fn(a, 256, w, 4, 64, 64, off_, cnt, BF, BF, out, None)
+    for fn in (L.moe_grouped_matmul, L.moe_grouped_matmul_dgrad):
+        assert fwd(fn=fn) in ACCEPTED and fwd(fn=fn, cnt=None) in ACCEPTED
+        for bad in (dict(off_=off(5, 64)), dict(cnt=off(5, 64))):
+            assert fwd(fn=fn, **bad) == INVALID, bad
+    need = L.moe_grouped_matmul_wgrad_workspace_size(8192, 1, 128, 2048)
+    assert need > 0
+
+    def wgrad(off_=at(3), cnt=at(4), out=at(1 << 14), ws=at(1 << 16)):
+        return L.moe_grouped_matmul_wgrad(at(1 << 10), at(1 << 12), 8192, 1, 128, 2048, off_, cnt, BF, FP, out, ws, need, None)
+    assert wgrad() in ACCEPTED and wgrad(cnt=None) in ACCEPTED
+    for bad in (dict(off_=off(1 << 14, 64)), dict(cnt=off(1 << 14, 64)), dict(off_=off(1 << 16, 64)),
+                dict(cnt=off(1 << 16, 64))):
+        assert wgrad(**bad) == INVALID, bad
