@@ -476,7 +476,8 @@ MOE_API int moe_grad_norm(const void* const* tensors, const int64_t* numel, cons
  * else 1; tensors are left as they are (c = 1) when the norm is inf or NaN, which the
  * caller sees in norm[0].
  *   outs     HOST array of n_tensors DEVICE pointers of the tensors' types and lengths, or
- *            NULL: in place. outs[t] may be tensors[t]; otherwise outputs overlap nothing
+ *            NULL: in place. outs[t] may be tensors[t]; otherwise outputs overlap nothing, not one
+ *            another either (in place, a tensor may be there only once)
  *   max_norm >= 0 */
 MOE_API int moe_clip_grad_norm(void* const* tensors, const int64_t* numel, const int32_t* dtypes, int n_tensors,
                                float max_norm, void* const* outs, float* norm, void* workspace,

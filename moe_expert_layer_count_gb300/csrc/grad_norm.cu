@@ -8,6 +8,10 @@
 // of the list is what the first pass has left in L2. 604 M bf16 values, over several GPUs: the
 // norm alone 172-185 us (7.0-6.5 TB/s), with the clipping 545-556 us (6.65-6.5 TB/s over the
 // three passes).
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "elem.cuh"
 
 namespace moe {
@@ -272,6 +276,47 @@ int run(const void* const* in, void* const* outs, const int64_t* numel, const in
     return launch_status();
 }
 
+// Bytes that the clip pass reads or writes.
+struct Span {
+    uintptr_t lo, hi;
+    bool written;
+};
+
+// Whether the clip pass would write what another block reads or writes too: the tensors, their outputs, the
+// norm and the partial sums (a tensor that is its own output is one span). A sweep over the spans in
+// the order of their addresses.
+int check_spans(const void* const* in, void* const* outs, const int64_t* numel, const int32_t* dtypes, int n_tensors,
+                const float* norm, const void* workspace, size_t need) {
+    constexpr int kFew = 130;  // 64 tensors and their outputs
+    Span few[kFew];
+    std::unique_ptr<Span[]> many;
+    const size_t most = 2 * (size_t)n_tensors + 2;
+    if (most > kFew) many.reset(new (std::nothrow) Span[most]);
+    Span* s = most > kFew ? many.get() : few;
+    if (!s) return MOE_ERR_CUDA;  // no host memory for a list of this length
+    size_t n = 0;
+    auto add = [&](const void* p, size_t bytes, bool written) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        if (bytes) s[n++] = Span{lo, lo + bytes, written};
+    };
+    for (int i = 0; i < n_tensors; ++i) {
+        const size_t b = (size_t)numel[i] * dtype_bytes(dtypes[i]);
+        const bool same = !outs || outs[i] == in[i];
+        add(in[i], b, same);
+        if (!same) add(outs[i], b, true);
+    }
+    add(norm, sizeof(float), true);
+    add(workspace, need, true);
+    std::sort(s, s + n, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    uintptr_t end = 0, written_end = 0;  // of the spans so far
+    for (size_t i = 0; i < n; ++i) {
+        if (s[i].lo < (s[i].written ? end : written_end)) return MOE_ERR_INVALID_ARG;
+        end = std::max(end, s[i].hi);
+        if (s[i].written) written_end = std::max(written_end, s[i].hi);
+    }
+    return MOE_OK;
+}
+
 int norm_impl(const void* const* in, const int64_t* numel, const int32_t* dtypes, int n_tensors, bool clip, float max_norm,
               void* const* outs, float* norm, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (n_tensors < 0 || !norm || misaligned(norm, 4) || !workspace || misaligned(workspace, 16) ||
@@ -287,7 +332,10 @@ int norm_impl(const void* const* in, const int64_t* numel, const int32_t* dtypes
             overlap(workspace, workspace_bytes, o, b) || overlap(workspace, workspace_bytes, in[i], b))
             return MOE_ERR_INVALID_ARG;
     }
-    if (workspace_bytes < moe_grad_norm_workspace_size(numel, n_tensors)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const size_t need = moe_grad_norm_workspace_size(numel, n_tensors);
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (clip)
+        if (int st = check_spans(in, outs, numel, dtypes, n_tensors, norm, workspace, need)) return st;
     if (int st = check_device(nullptr)) return st;
     double* parts = static_cast<double*>(workspace);
     if (n_tensors <= kFewTensors)

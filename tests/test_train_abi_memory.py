@@ -116,3 +116,36 @@ def test_grouped_overlaps(L):  # noqa: F811
     for bad in (dict(off_=off(1 << 14, 64)), dict(cnt=off(1 << 14, 64)), dict(off_=off(1 << 16, 64)),
                 dict(cnt=off(1 << 16, 64))):
         assert wgrad(**bad) == INVALID, bad
+
+
+@no_gpu
+def test_clip_overlaps(L):  # noqa: F811
+    def call(ptrs, lens, outs=None, clip=True, norm=at(100), ws=at(101)):
+        n = len(lens)
+        p, c, t = (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*lens), (ctypes.c_int32 * n)(*([FP] * n))
+        if not clip:
+            return L.moe_grad_norm(p, c, t, n, norm, ws, 1 << 20, None)
+        o = None if outs is None else (ctypes.c_void_p * n)(*outs)
+        return L.moe_clip_grad_norm(p, c, t, n, 1.0, o, norm, ws, 1 << 20, None)
+    a, b, c, d = 1 << 20, 2 << 20, 3 << 20, 4 << 20
+    assert call([a, b], [1000, 10]) in ACCEPTED and call([a, b], [1000, 10], [c, d]) in ACCEPTED
+    assert call([a, b], [1000, 10], [a, d]) in ACCEPTED and call([a, b], [1000, 10], [c, b]) in ACCEPTED
+    # neighbours touch but do not overlap; an empty tensor overlaps nothing
+    assert call([a, a + 4000], [1000, 10]) in ACCEPTED and call([a + 4000, a], [10, 1000]) in ACCEPTED
+    assert call([a, a + 40, b], [1000, 0, 5]) in ACCEPTED
+    # read only: a tensor may be there twice
+    assert call([a, a], [1000, 1000], clip=False) in ACCEPTED and call([a, a], [1000, 10], [c, d]) in ACCEPTED
+    # scaled twice, or read after another tensor's output has gone over it
+    assert call([a, a], [1000, 1000]) == INVALID and call([a, a + 400], [1000, 10]) == INVALID
+    assert call([b, a + 400, c, a], [10, 10, 10, 1000]) == INVALID
+    assert call([a, b], [1000, 10], [c, c + 400]) == INVALID and call([a, b], [1000, 10], [b, d]) == INVALID
+    assert call([a, b], [1000, 10], [c, a + 400]) == INVALID and call([a, a], [1000, 1000], [a, c]) == INVALID
+    # the norm is written while tensors and partial sums are still read; moe_grad_norm writes it last
+    for norm in (off(1, 400), off(101, 64)):
+        assert call([a, b], [1000, 10], norm=norm) == INVALID
+        assert call([a, b], [1000, 10], clip=False, norm=norm) in ACCEPTED
+    assert call([a, b], [1000, 10], [c, d], norm=off(3, 400)) == INVALID
+    # a long list
+    many = [a + 64 * i for i in range(1000)]
+    assert call(many, [16] * 1000) in ACCEPTED and call(many[::-1], [16] * 1000) in ACCEPTED
+    assert call(many, [16] * 700 + [17] + [16] * 299) == INVALID
