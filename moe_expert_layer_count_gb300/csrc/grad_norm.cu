@@ -263,6 +263,7 @@ int run(const void* const* in, void* const* outs, const int64_t* numel, const in
         note_launches(1);
         n_parts += grid;
     }
+    if (int st = launch_status()) return st;  // nothing is scaled by sums that were not made
     if (!clip || n_tensors == 0) {
         launch_k(norm_kernel, 1, kNormThreads, 0, stream, parts, n_parts, norm);
         note_launches(1);
