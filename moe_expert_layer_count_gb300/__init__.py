@@ -463,8 +463,9 @@ def moe_layer_norm_workspace_size(M: int, K: int) -> int:
 
 
 def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, d_weight=None, d_bias=None, workspace=None,
-                            stream=None):
-    """Gradients of moe_layer_norm from its inputs and statistics: (dx, d_weight, d_bias)."""
+                            stream=None, has_bias=True):
+    """Gradients of moe_layer_norm from its inputs and statistics: (dx, d_weight, d_bias). d_bias is None for
+    a norm without a bias (has_bias false)."""
     dt = _dtype_code(x, "x")
     pdt = _dtype_code(weight, "weight")
     M, K = x.shape
@@ -476,7 +477,9 @@ def moe_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, d_weight=None, d
         dx = _empty(x.shape, x.dtype, x.device, stream)
     if d_weight is None:
         d_weight = _empty(weight.shape, weight.dtype, weight.device, stream)
-    if d_bias is None:
+    if not has_bias and d_bias is not None:
+        raise ValueError("d_bias: given for a norm without a bias")
+    if d_bias is None and has_bias:
         d_bias = _empty(weight.shape, weight.dtype, weight.device, stream)
     _same(dx, (M, K), x.dtype, "dx")
     _same(d_weight, (K,), weight.dtype, "d_weight")

@@ -26,12 +26,13 @@ class _LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps):
         y, mean, rstd = moe.moe_layer_norm(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.has_bias = bias is not None
         return y
 
     @staticmethod
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
-        dx, dw, db = moe.moe_layer_norm_backward(dy.contiguous(), x, weight, mean, rstd)
+        dx, dw, db = moe.moe_layer_norm_backward(dy.contiguous(), x, weight, mean, rstd, has_bias=ctx.has_bias)
         return dx, dw, db, None
 
 
@@ -104,7 +105,7 @@ class _WeightedGather(torch.autograd.Function):
         return drows, None, torch.where(kept, dots, 0.0), None, None
 
 
-def layer_norm(x, weight, bias, eps=1e-5):
+def layer_norm(x, weight, bias=None, eps=1e-5):
     """moe_layer_norm under autograd: y."""
     return _LayerNorm.apply(x, weight, bias, eps)
 
