@@ -53,17 +53,22 @@ class _RouterTopk(torch.autograd.Function):
 
 class _GroupedMatmul(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, offsets, counts, out_dtype):
+    def forward(ctx, x, w, offsets, counts, out_dtype, gaps):
         ctx.save_for_backward(x, w, offsets, counts)
+        ctx.gaps = gaps
         return moe.moe_grouped_matmul(x, w, offsets, counts, out_dtype=out_dtype)
 
     @staticmethod
     def backward(ctx, dy):
         x, w, offsets, counts = ctx.saved_tensors
         dy = dy.to(w.dtype).contiguous()  # the products' operands have one 16-bit type
-        dx = moe.moe_grouped_matmul_dgrad(dy, w, offsets, counts) if ctx.needs_input_grad[0] else None
+        dx = None
+        if ctx.needs_input_grad[0]:
+            # the product does not write the rows of no group
+            out = torch.zeros_like(x) if ctx.gaps else None
+            dx = moe.moe_grouped_matmul_dgrad(dy, w, offsets, counts, out=out)
         dw = moe.moe_grouped_matmul_wgrad(dy, x, offsets, counts) if ctx.needs_input_grad[1] else None
-        return dx, dw, None, None, None
+        return dx, dw, None, None, None, None
 
 
 class _Permute(torch.autograd.Function):
@@ -115,9 +120,11 @@ def router_topk(logits, topk, scoring=moe.MOE_SCORE_SOFTMAX, renormalize=True, s
     return _RouterTopk.apply(logits, topk, scoring, renormalize, scale, bias)
 
 
-def grouped_matmul(x, w, expert_offsets, expert_num_tokens=None, out_dtype=None):
-    """moe_grouped_matmul under autograd."""
-    return _GroupedMatmul.apply(x, w, expert_offsets, expert_num_tokens, out_dtype)
+def grouped_matmul(x, w, expert_offsets, expert_num_tokens=None, out_dtype=None, gaps=True):
+    """moe_grouped_matmul under autograd. Rows of no group have an undefined result and no influence: their
+    gradient is 0. gaps=False leaves it undefined too, which saves a pass of writing: for callers whose groups
+    hold every row, or who do not use the others'."""
+    return _GroupedMatmul.apply(x, w, expert_offsets, expert_num_tokens, out_dtype, gaps)
 
 
 def init_block(K: int, N: int, E: int, device="cuda", seed: int = 0):
@@ -136,11 +143,12 @@ def moe_block(p, x, topk: int, scoring=moe.MOE_SCORE_SOFTMAX, renormalize=True, 
     E, N2, _ = p["w13"].shape
     h = layer_norm(x, p["norm_weight"], p["norm_bias"], eps)
     everyone = torch.tensor([0, x.shape[0]], dtype=torch.int32, device=x.device)
-    logits = grouped_matmul(h, p["gate"], everyone, out_dtype=torch.float32)
+    logits = grouped_matmul(h, p["gate"], everyone, out_dtype=torch.float32, gaps=False)
     weights, ids = router_topk(logits, topk, scoring, renormalize)
     rows, offsets, src2dst, counts = _Permute.apply(h, ids, weights, E)
-    gate, up = grouped_matmul(rows, p["w13"], offsets, counts).split(N2 // 2, dim=1)
-    out = grouped_matmul(torch.nn.functional.silu(gate) * up, p["w2"], offsets, counts)
+    # the permutation's gradient reads no row between the groups, and everything up to it is row by row
+    gate, up = grouped_matmul(rows, p["w13"], offsets, counts, gaps=False).split(N2 // 2, dim=1)
+    out = grouped_matmul(torch.nn.functional.silu(gate) * up, p["w2"], offsets, counts, gaps=False)
     return x + _WeightedGather.apply(out, src2dst, weights, ids, counts)
 
 

@@ -20,3 +20,28 @@ def test_layer_norm_without_a_bias():
     assert again[2] is None and torch.equal(again[0], dx) and torch.equal(again[1], dw)
     with pytest.raises(ValueError):
         moe.moe_layer_norm_backward(dy, x.detach(), w.detach(), mean, rstd, d_bias=torch.empty_like(dw), has_bias=False)
+
+
+def test_rows_of_no_group_have_no_gradient():
+    """Rows between the groups take no part in the product: their gradient is 0, whatever the memory
+    that it is written to held before."""
+    counts, K, N = [3, 0, 130, 64], 136, 72
+    starts = [5, 133, 140, 300]
+    R = 400
+    off = torch.tensor(starts + [R], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    inside = torch.zeros(R, dtype=torch.bool, device="cuda")
+    for s, c in zip(starts, counts):
+        inside[s:s + c] = True
+    w = torch.randn(4, N, K, device="cuda").bfloat16().requires_grad_()
+    for cnt_or_none, rows in ((cnt, inside), (None, torch.arange(R, device="cuda") >= starts[0])):
+        x = torch.randn(R, K, device="cuda").bfloat16().requires_grad_()
+        y = train.grouped_matmul(x, w, off, cnt_or_none)
+        dy = torch.zeros_like(y)
+        dy[rows] = 1.0
+        poison = [torch.full((R, K), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+        del poison
+        dx, = torch.autograd.grad(y, x, dy)
+        assert (dx[~rows] == 0).all()
+        want = moe.moe_grouped_matmul_dgrad(dy, w.detach(), off, cnt_or_none)
+        assert torch.equal(dx[rows], want[rows])
