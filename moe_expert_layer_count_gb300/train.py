@@ -10,13 +10,14 @@ Nothing of it reads the experts' row counts on the host. The permutation's gradi
 library's own pair again: the gradient of the weighted gather is a scatter of the output's
 gradient that applies the weights, the gradient of the scatter a gather with unit weights.
 The activation between the products and the dot product that gives the gradient of a routing
-weight are plain torch operations.
+weight are plain torch operations. There are no second gradients.
 
 `python -m moe_expert_layer_count_gb300.train` runs a few steps on synthetic data.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 import moe_expert_layer_count_gb300 as moe
 
@@ -30,6 +31,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dw, db = moe.moe_layer_norm_backward(dy.contiguous(), x, weight, mean, rstd, has_bias=ctx.has_bias)
@@ -46,6 +48,7 @@ class _RouterTopk(torch.autograd.Function):
         return weights, ids
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dweights, _):
         logits, ids = ctx.saved_tensors
         return moe.moe_router_topk_backward(logits, ids, dweights.contiguous(), *ctx.how), None, None, None, None, None
@@ -59,6 +62,7 @@ class _GroupedMatmul(torch.autograd.Function):
         return moe.moe_grouped_matmul(x, w, offsets, counts, out_dtype=out_dtype)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, offsets, counts = ctx.saved_tensors
         dy = dy.to(w.dtype).contiguous()  # the products' operands have one 16-bit type
@@ -84,6 +88,7 @@ class _Permute(torch.autograd.Function):
         return rows, offsets, src2dst, counts
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, drows, *_):
         src2dst, weights = ctx.saved_tensors
         # unit weights: every kept slot's row once
@@ -99,6 +104,7 @@ class _WeightedGather(torch.autograd.Function):
         return moe.moe_gather_weight_reduce(rows, src2dst, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         rows, src2dst, weights, ids, counts = ctx.saved_tensors
         dout = dout.contiguous()

@@ -45,3 +45,35 @@ def test_rows_of_no_group_have_no_gradient():
         assert (dx[~rows] == 0).all()
         want = moe.moe_grouped_matmul_dgrad(dy, w.detach(), off, cnt_or_none)
         assert torch.equal(dx[rows], want[rows])
+
+
+def first_gradient(name):
+    """x and a gradient with respect to it that was taken with create_graph."""
+    if name == "layer_norm":
+        x = torch.randn(8, 64, device="cuda").requires_grad_()
+        y = train.layer_norm(x, torch.ones(64, device="cuda"), torch.zeros(64, device="cuda"))
+    elif name == "router_topk":
+        x = torch.randn(8, 64, device="cuda").requires_grad_()
+        y, _ = train.router_topk(x, 4)
+    elif name == "grouped_matmul":
+        x = torch.randn(8, 64, device="cuda").bfloat16().requires_grad_()
+        w = torch.randn(2, 64, 64, device="cuda").bfloat16().requires_grad_()
+        y = train.grouped_matmul(x, w, torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda"))
+    else:
+        x = torch.randn(40, 128, device="cuda").bfloat16().requires_grad_()
+        ids = torch.randint(0, 8, (40, 1), dtype=torch.int32, device="cuda")
+        weights = torch.rand(40, 1, device="cuda")
+        rows, _, src2dst, counts = train._Permute.apply(x, ids, weights, 8)
+        if name == "permute":
+            y = rows
+        else:
+            y = train._WeightedGather.apply(rows, src2dst, weights, ids, counts)
+    return x, torch.autograd.grad(y.float().square().sum(), x, create_graph=True)[0]
+
+
+@pytest.mark.parametrize("name", ["layer_norm", "router_topk", "grouped_matmul", "permute", "weighted_gather"])
+def test_second_gradients_are_refused(name):
+    """The functions have no second gradients; asking for one is an error and not a missing term."""
+    x, g = first_gradient(name)
+    with pytest.raises(RuntimeError):
+        (g.float().square().sum() + x.float().square().sum()).backward()
