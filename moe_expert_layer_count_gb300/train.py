@@ -148,7 +148,8 @@ def moe_block(p, x, topk: int, scoring=moe.MOE_SCORE_SOFTMAX, renormalize=True, 
     """x + MoE(layer_norm(x)) for x bf16 [M, K] and the parameters of init_block."""
     E, N2, _ = p["w13"].shape
     h = layer_norm(x, p["norm_weight"], p["norm_bias"], eps)
-    everyone = torch.tensor([0, x.shape[0]], dtype=torch.int32, device=x.device)
+    # made on the device: the block can be captured in a CUDA graph
+    everyone = torch.arange(2, dtype=torch.int32, device=x.device) * x.shape[0]
     logits = grouped_matmul(h, p["gate"], everyone, out_dtype=torch.float32, gaps=False)
     weights, ids = router_topk(logits, topk, scoring, renormalize)
     rows, offsets, src2dst, counts = _Permute.apply(h, ids, weights, E)

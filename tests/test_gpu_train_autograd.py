@@ -77,3 +77,29 @@ def test_second_gradients_are_refused(name):
     x, g = first_gradient(name)
     with pytest.raises(RuntimeError):
         (g.float().square().sum() + x.float().square().sum()).backward()
+
+
+def test_block_in_a_graph():
+    """The block's forward and backward pass, captured and replayed on other inputs."""
+    M, K, N, E, topk = 200, 256, 128, 8, 2
+    p = train.init_block(K, N, E, seed=5)
+    x = torch.randn(M, K, device="cuda").bfloat16().requires_grad_()
+    dout = torch.randn(M, K, device="cuda").bfloat16()
+
+    def step():
+        out = train.moe_block(p, x, topk)
+        return [out, *torch.autograd.grad(out, [x, *p.values()], dout)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        step()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=s):
+            got = step()
+    with torch.no_grad():
+        x.copy_(torch.randn(M, K, device="cuda"))
+    want = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
