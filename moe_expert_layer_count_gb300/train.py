@@ -111,9 +111,14 @@ class _WeightedGather(torch.autograd.Function):
         n = counts.numel()
         drows, _, _, _ = moe.moe_scatter(dout, ids, weights, n, n, counts, apply_router_weight_on_input=True,
                                          quant=moe.MOE_QUANT_NONE, rp_cap=rows.shape[0])
-        kept = src2dst >= 0
-        dots = (rows[src2dst.clamp(min=0).long()].float() * dout.float()[:, None, :]).sum(-1)
-        return drows, None, torch.where(kept, dots, 0.0), None, None
+        # a few tensors of tokens x hidden size at a time, not of every token's chosen rows
+        M, topk = src2dst.shape
+        dots = torch.empty(M, topk, dtype=torch.float32, device=dout.device)
+        step = max(256, -(-2 * M // topk))
+        for i in range(0, M, step):
+            s = slice(i, i + step)
+            dots[s] = (rows[src2dst[s].clamp(min=0).long()] * dout[s].float()[:, None, :]).sum(-1)  # products in fp32
+        return drows, None, torch.where(src2dst >= 0, dots, 0.0), None, None
 
 
 def layer_norm(x, weight, bias=None, eps=1e-5):

@@ -103,3 +103,28 @@ def test_block_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_memory_of_the_weighted_gathers_backward():
+    """Beside its results the backward pass holds a few tensors of tokens x hidden size, not of every
+    token's chosen rows."""
+    M, K, E, topk = 2048, 2048, 16, 8
+    ids = torch.stack([torch.randperm(E)[:topk] for _ in range(M)]).int().cuda()
+    weights = torch.rand(M, topk, device="cuda").requires_grad_()
+    h = torch.randn(M, K, device="cuda").bfloat16()
+    rows, _, src2dst, counts = train._Permute.apply(h, ids, weights, E)
+    rows = rows.detach().requires_grad_()
+    dout = torch.randn(M, K, device="cuda").bfloat16()
+    out = train._WeightedGather.apply(rows, src2dst, weights, ids, counts)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    drows, dweights = torch.autograd.grad(out, [rows, weights], dout)
+    torch.cuda.synchronize()
+    peak = torch.cuda.max_memory_allocated() - before
+    results = drows.numel() * 2 + dweights.numel() * 4
+    assert peak <= results + 6 * M * K * 4, (peak, results)
+    kept = h.float()[:, None].expand(M, topk, K).double()
+    ref = (kept * dout.double()[:, None]).sum(-1)
+    # fp32 sums of K products, whatever their order
+    assert ((dweights.double() - ref).abs() <= K * 2.0 ** -24 * (kept * dout.double()[:, None]).abs().sum(-1)).all()
