@@ -626,8 +626,8 @@ def moe_clip_grad_norm(tensors, max_norm, out=None, norm=None, workspace=None, s
 def _norm_call(fn, tensors, max_norm, out, norm, workspace, stream):
     tensors = list(tensors)
     n = len(tensors)
-    if n == 0:
-        raise ValueError(f"{fn}: no tensors")
+    if n == 0 and norm is None:
+        raise ValueError(f"{fn}: no tensors, and no norm buffer to say where the norm goes")
     dtypes = list(map(_dtype_of, tensors))
     try:
         types = array("i", map(_DTYPES.__getitem__, dtypes))
@@ -635,7 +635,7 @@ def _norm_call(fn, tensors, max_norm, out, norm, workspace, stream):
         raise TypeError(f"{fn}: expected torch.float32, torch.bfloat16 or torch.float16, got {e.args[0]}") from None
     lens = array("q", map(torch.Tensor.numel, tensors))
     ptrs = _addresses(tensors)
-    dev = tensors[0].device
+    dev = tensors[0].device if n else norm.device
     if norm is None:
         norm = _empty(1, torch.float32, dev, stream)
     _same(norm, (1,), torch.float32, "norm")

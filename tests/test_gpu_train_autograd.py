@@ -128,3 +128,12 @@ def test_memory_of_the_weighted_gathers_backward():
     ref = (kept * dout.double()[:, None]).sum(-1)
     # fp32 sums of K products, whatever their order
     assert ((dweights.double() - ref).abs() <= K * 2.0 ** -24 * (kept * dout.double()[:, None]).abs().sum(-1)).all()
+
+
+def test_an_empty_list_of_gradients():
+    """Without tensors the norm is 0; the buffer for it says where."""
+    norm = torch.ones(1, device="cuda")
+    assert moe.moe_grad_norm([], norm=norm).item() == 0
+    norm.fill_(1)
+    assert moe.moe_clip_grad_norm([], 1.0, norm=norm).item() == 0
+    assert moe.moe_clip_grad_norm([], 1.0, out=[], norm=norm).item() == 0
