@@ -6,7 +6,7 @@
 // their number alone, so the sum's order does not change from call to call. The clip pass
 // adds the partial sums in every block and scales the chunks, last chunk first: the end
 // of the list is what the first pass has left in L2. 604 M bf16 values, over several GPUs: the
-// norm alone 172-185 us (7.0-6.5 TB/s), with the clipping 545-556 us (6.65-6.5 TB/s over the
+// norm alone 172-185 us (7.0-6.5 TB/s), with the clipping 545-569 us (6.65-6.4 TB/s over the
 // three passes).
 #include <algorithm>
 #include <memory>

@@ -22,13 +22,14 @@
 // epilogue runs under the next tile's MMAs. Every pipeline wait gives up after 2 s, sets a device
 // error word and ends the kernel.
 //
-// What it measured (one GB300, times of one call, back to back; 8192 x 8192 x 8192 in the library's
-// dense product: 555 us):
-//   one group of 8192 rows, 8192 x 8192      610 us forward, 597 us wgrad   1.80, 1.84 PFLOP/s
-//   128 groups of 512 rows, 1536 x 2048      250 us forward, 286 us wgrad   1.65, 1.44
-//   65536 rows over 128 groups, Zipf 1.2     285 us forward, 331 us wgrad   1.45, 1.24
-//   512 rows over 128 groups (decode)        127 us forward: 806 MB of weights at 6.3 TB/s
-//                                            130 us wgrad: as much written at 6.2 TB/s
+// What it measured (one GB300, times of one call in bursts of a few tens of ms, SM clock 2070 MHz; in
+// brackets after a second of load, when the power cap holds it at 1290-1575 MHz; 8192 x 8192 x 8192 in the
+// library's dense product: 540-555 us):
+//   one group of 8192 rows, 8192 x 8192      590-610 us forward, 596 us [700] wgrad   1.8, 1.84 PFLOP/s
+//   128 groups of 512 rows, 1536 x 2048      248-257 us [292] forward, 287 us [322] wgrad   1.65, 1.44
+//   65536 rows over 128 groups, Zipf 1.2     285-305 us [327] forward, 343-354 us wgrad   1.4, 1.2
+//   512 rows over 128 groups (decode)        116-127 us forward: 750-806 MB of weights at 6.4 TB/s
+//                                            132 us wgrad: as much written at 6.1 TB/s
 // Where the time goes (variants that leave one part out, 512 rows a group):
 //   forward: without loads 187 us, without MMAs 211 us (DRAM gives 6 TB/s for the 1.27 GB that has
 //   to move), the full kernel 250 us, as the two hide each other only in part;
@@ -36,8 +37,8 @@
 //   and 0.8 GB out of them, 16.4 TB/s, which is about what they take (64 bytes a clock each).
 // What it is sensitive to: the MMA loop has to issue from uniform registers (a loop that one lane
 // runs alone takes 130 clocks an MMA: 750 us dense), the look-up of a tile is on the MMA warp's
-// way between tiles, and a signal to the other CTA must not be a cluster-wide release, which
-// waits for the signalling thread's own stores (2000 clocks).
+// way between tiles, and a signal to the other CTA must not be a cluster-wide release by a thread that
+// stores, which it waits for (2000 clocks).
 
 #include <cudaTypedefs.h>
 
