@@ -466,7 +466,8 @@ MOE_API size_t moe_grad_norm_workspace_size(const int64_t* numel, int n_tensors)
  *   tensors  HOST array of n_tensors DEVICE pointers, aligned to their elements
  *   numel    HOST array of their lengths (0 allowed);  dtypes HOST array of enum moe_dtype
  *   norm     fp32 [1], written. Squares that overflow or vanish in fp32 are taken in fp64,
- *            so the norm is right over the whole range of fp32; inf or NaN if a value is
+ *            so the norm is right over the whole range of fp32; inf or NaN if a value is,
+ *            and inf where it lies above that range
  * The sum has a fixed order. n_tensors = 0 writes 0.
  * workspace >= moe_grad_norm_workspace_size bytes, 16-byte aligned. */
 MOE_API int moe_grad_norm(const void* const* tensors, const int64_t* numel, const int32_t* dtypes, int n_tensors,
