@@ -96,6 +96,17 @@ enum moe_scoring {
     MOE_SCORE_SIGMOID = 1, /* score of expert e: 1 / (1 + exp(-l_e)) */
 };
 
+enum moe_activation {
+    MOE_ACT_SILU = 0,      /* a(g) = g / (1 + exp(-g)) */
+    MOE_ACT_GELU_TANH = 1, /* a(g) = g/2 * (1 + tanh(sqrt(2/pi) * (g + 0.044715 g^3))) */
+};
+
+enum moe_keep { /* how gate and up are kept for the backward pass */
+    MOE_KEEP_NONE = 0,  /* not at all (inference) */
+    MOE_KEEP_16BIT = 1, /* in the operands' type */
+    MOE_KEEP_E4M3 = 2,  /* in 8 bits, as moe_checkpoint_pack makes them of the 16-bit ones */
+};
+
 /* Text of a status code (static storage). */
 MOE_API const char* moe_status_string(int status);
 
@@ -457,6 +468,66 @@ MOE_API int moe_grouped_matmul_wgrad(const void* dy, const void* x, int64_t R, i
                                      int k_in, const int32_t* expert_offsets, const int32_t* expert_num_tokens,
                                      int dtype, int out_dtype, void* dw, void* workspace, size_t workspace_bytes,
                                      moe_stream_t stream);
+
+/* The gated feed-forward part of the experts: both input projections of a ragged row group and the
+ * activation in one product. For the rows r of group l (groups as in moe_grouped_matmul), with W_g
+ * the first N rows of w13[l] and W_u the last N:
+ *   g = W_g x[r],  u = W_u x[r],  h[r] = a(g) * u
+ *   x          `dtype` [R, K];  w13 `dtype` [El, 2N, K] (gate rows, then up rows)
+ *   h          `dtype` [R, N]
+ *   keep       enum moe_keep. MOE_KEEP_16BIT: pre is `dtype` [R, 2N], row r holds g then u.
+ *              MOE_KEEP_E4M3: pre is uint8 codes [R, 2N] and pre_scale uint8 [R, 2N/16], the 8-bit
+ *              form (moe_checkpoint_pack) of the 16-bit pre; N is then a multiple of 16.
+ *              pre and pre_scale are NULL where nothing of them is kept
+ *   activation enum moe_activation
+ * h is made of the fp32 sums, not of what is kept. Rows of no group are neither read as data nor
+ * written, in any output. dtype is MOE_DT_BF16 or MOE_DT_F16; N and K are multiples of 8;
+ * 1 <= El <= 1024; R <= 2^31 - 1; x, w13, h and pre are 16-byte aligned. */
+MOE_API int moe_grouped_gated(const void* x, int64_t R, const void* w13, int local_num_experts, int N, int K,
+                              const int32_t* expert_offsets, const int32_t* expert_num_tokens, int activation, int dtype,
+                              void* h, int keep, void* pre, uint8_t* pre_scale, moe_stream_t stream);
+
+/* Its backward pass from the gradient of the down projection's result y[r] = w2[l] h[r]: with
+ * dh = w2[l]^T dy[r] (held in fp32) and g, u as they were kept,
+ *   d_pre[r] = (dh * u * a'(g), dh * a(g))   `dtype` [R, 2N]
+ *   h[r]     = a(g) * u                      `dtype` [R, N], or NULL: not wanted
+ * The rest of the backward pass is moe_grouped_matmul_wgrad of (dy, h) for w2, and _dgrad and _wgrad
+ * of d_pre for x and w13.
+ *   dy `dtype` [R, K];  w2 `dtype` [El, K, N];  keep MOE_KEEP_16BIT or MOE_KEEP_E4M3, pre and
+ *   pre_scale as moe_grouped_gated wrote them
+ * d_pre may be pre itself where that is in 16 bits. Sizes, types and alignment as above. */
+MOE_API int moe_grouped_gated_backward(const void* dy, int64_t R, const void* w2, int local_num_experts, int N, int K,
+                                       const int32_t* expert_offsets, const int32_t* expert_num_tokens, int activation,
+                                       int dtype, int keep, const void* pre, const uint8_t* pre_scale, void* d_pre, void* h,
+                                       moe_stream_t stream);
+
+/* Activations kept in 8 bits for the backward pass. x [M, K] becomes e4m3 codes [M, K] and, for
+ * every 16 values of a row (the last group of a row may be shorter), one byte s: the group's scale is
+ * 2^(s - 127), the smallest power of two, 2^-126 or more, that brings its values within +-448.
+ *   code = e4m3(x * 2^(127 - s)), rounded to nearest even
+ * A group that holds an infinity or a NaN has s = 255 and every code NaN.
+ *   x `dtype` [M, K], contiguous;  codes uint8 [M, K];  scales uint8 [M, ceil(K / 16)]
+ * 1 <= K <= 2^30; x is aligned to its elements; rows of whole groups on 16-byte boundaries move 16 bytes at a time. */
+MOE_API int moe_checkpoint_pack(const void* x, int64_t M, int K, int dtype, uint8_t* codes, uint8_t* scales,
+                                moe_stream_t stream);
+
+/* And back: x = code * 2^(s - 127) in `dtype` (which need not be the packed one's), values beyond its
+ * range as its largest; NaN where s is 255. Any byte is a scale (0: 2^-127). */
+MOE_API int moe_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, int64_t M, int K, int dtype, void* x,
+                                  moe_stream_t stream);
+
+/* Gradients of moe_gather_weight_reduce. For every slot with a row r = src2dst[t, k] in [0, rows):
+ *   d_y[r]               = bf16(w'[t, k] * dout[t]),  w' = topk_weights, or 1 when
+ *                          apply_router_weight_on_input != 0
+ *   d_topk_weights[t, k] = sum over c of y[r, c] * dout[t, c], fp32; 0 for a slot without a row.
+ *                          NULL: not wanted (and y is not read); NULL when apply_router_weight_on_input
+ *   dout bf16 [M, K];  y, d_y bf16 [rows, K];  rows of no slot are left as they are
+ * No row may belong to two slots (src2dst as moe_scatter writes it). K is a multiple of 128;
+ * 1 <= topk <= 32; dout, y and d_y are 16-byte aligned. */
+MOE_API int moe_gather_weight_reduce_backward(const void* dout, const void* y, int64_t rows, const int32_t* src2dst,
+                                              const float* topk_weights, int64_t M, int topk, int K,
+                                              int apply_router_weight_on_input, void* d_y, float* d_topk_weights,
+                                              moe_stream_t stream);
 
 /* Scratch bytes moe_grad_norm and moe_clip_grad_norm need for these tensors (HOST array of
  * n_tensors lengths). Returns 0 on bad arguments. */

@@ -33,6 +33,8 @@ MOE_QUANT_NONE, MOE_QUANT_FP8_1X128 = 0, 1
 MOE_EPI_BF16, MOE_EPI_F32, MOE_EPI_SILU_MUL_QUANT = 0, 1, 2
 MOE_DT_F32, MOE_DT_BF16, MOE_DT_F16 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ACT_SILU, MOE_ACT_GELU_TANH = 0, 1
+MOE_KEEP_NONE, MOE_KEEP_16BIT, MOE_KEEP_E4M3 = 0, 1, 2
 _DTYPES = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 
 _lib = None
@@ -102,6 +104,11 @@ SIGNATURES = {
     "moe_grouped_matmul_dgrad": ([_p, _i64, _p, _int, _int, _int, _p, _p, _int, _int, _p, _p], _int),
     "moe_grouped_matmul_wgrad": ([_p, _p, _i64, _int, _int, _int, _p, _p, _int, _int, _p, _p, _sz, _p], _int),
     "moe_grouped_matmul_wgrad_workspace_size": ([_i64, _int, _int, _int], _sz),
+    "moe_grouped_gated": ([_p, _i64, _p, _int, _int, _int, _p, _p, _int, _int, _p, _int, _p, _p, _p], _int),
+    "moe_grouped_gated_backward": ([_p, _i64, _p, _int, _int, _int, _p, _p, _int, _int, _int, _p, _p, _p, _p, _p], _int),
+    "moe_checkpoint_pack": ([_p, _i64, _int, _int, _p, _p, _p], _int),
+    "moe_checkpoint_unpack": ([_p, _p, _i64, _int, _int, _p, _p], _int),
+    "moe_gather_weight_reduce_backward": ([_p, _p, _i64, _p, _p, _i64, _int, _int, _int, _p, _p, _p], _int),
     "moe_grad_norm_workspace_size": ([_p, _int], _sz),
     "moe_grad_norm": ([_p, _p, _p, _int, _p, _p, _sz, _p], _int),
     "moe_clip_grad_norm": ([_p, _p, _p, _int, _f, _p, _p, _p, _sz, _p], _int),
@@ -592,6 +599,157 @@ def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=
     _same(x, (R, K), dy.dtype, "x")
     return _grouped("moe_grouped_matmul_wgrad", dy, x, (El, N, K), (El, N, K), expert_offsets, expert_num_tokens, out,
                     out_dtype, stream, workspace)
+
+
+def _one_device(*tensors):
+    """The tensors of one call lie on the current device: a kernel is launched there and reads their addresses."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is not None and t.device != dev:
+                raise ValueError(f"tensors on two devices, {dev} and {t.device}")
+            dev = t.device
+    if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, which is not the current device")
+
+
+def _half(t, name):
+    if t.dtype != torch.bfloat16 and t.dtype != torch.float16:
+        raise TypeError(f"{name}: expected torch.bfloat16 or torch.float16, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _kept(keep, R, N, dtype):
+    """Shape and type of what is kept of gate and up, and of its scales (None: there is none)."""
+    if keep == MOE_KEEP_16BIT:
+        return ((R, 2 * N), dtype), None
+    if keep == MOE_KEEP_E4M3:
+        return ((R, 2 * N), torch.uint8), ((R, 2 * N // 16), torch.uint8)
+    return None, None
+
+
+def moe_grouped_gated(x, w13, expert_offsets, expert_num_tokens=None, activation=MOE_ACT_SILU, keep=MOE_KEEP_NONE, out=None,
+                      pre=None, pre_scale=None, stream=None):
+    """h[r] = a(g) * u with (g, u) = w13[l] @ x[r] for the rows r of every group l: x [R, K] and w13 [El, 2N, K]
+    (gate rows, then up rows) in bf16 or fp16, h [R, N]; groups as in moe_grouped_matmul. `keep`: what is kept of
+    g and u for the backward pass. Returns (h, pre, pre_scale): pre [R, 2N] in x's type (MOE_KEEP_16BIT) or as 8-bit
+    codes with pre_scale [R, 2N / 16] (MOE_KEEP_E4M3), None where nothing is kept."""
+    dt = _half(w13, "w13")
+    El, N2, K = w13.shape
+    R, N = x.shape[0], N2 // 2
+    if N2 % 2:
+        raise ValueError(f"w13: gate and up need an even number of rows, got {N2}")
+    _same(x, (R, K), w13.dtype, "x")
+    _same(expert_offsets, (El + 1,), torch.int32, "expert_offsets")
+    _same(expert_num_tokens, (El,), torch.int32, "expert_num_tokens")
+    of_pre, of_scale = _kept(keep, R, N, x.dtype)
+    for t, of, name in ((pre, of_pre, "pre"), (pre_scale, of_scale, "pre_scale")):
+        if t is not None:
+            if of is None:
+                raise ValueError(f"{name}: given, but not kept")
+            _same(t, *of, name)
+    _one_device(x, w13, expert_offsets, expert_num_tokens, out, pre, pre_scale)
+    if out is None:
+        out = _empty((R, N), x.dtype, x.device, stream)
+    _same(out, (R, N), x.dtype, "out")
+    if pre is None and of_pre is not None:
+        pre = _empty(*of_pre, x.device, stream)
+    if pre_scale is None and of_scale is not None:
+        pre_scale = _empty(*of_scale, x.device, stream)
+    _check("moe_grouped_gated", lib().moe_grouped_gated(
+        _addr(x), R, _addr(w13), El, N, K, _addr(expert_offsets), _addr(expert_num_tokens), activation, dt, _addr(out), keep,
+        _addr(pre), _addr(pre_scale), _raw_stream(stream)))
+    return out, pre, pre_scale
+
+
+def moe_grouped_gated_backward(dy, w2, pre, expert_offsets, expert_num_tokens=None, activation=MOE_ACT_SILU, pre_scale=None,
+                               d_pre=None, h=None, want_h=True, stream=None):
+    """Backward pass of moe_grouped_gated behind a down projection w2 [El, K, N], from that one's gradient dy [R, K]
+    and what was kept (pre; with pre_scale: in 8 bits). Returns (d_pre, h): the gradients of gate and up [R, 2N], and
+    h [R, N] once more for w2's gradient (None with want_h false). d_pre may be a 16-bit pre itself."""
+    dt = _half(w2, "w2")
+    El, K, N = w2.shape
+    R = dy.shape[0]
+    keep = MOE_KEEP_16BIT if pre_scale is None else MOE_KEEP_E4M3
+    of_pre, of_scale = _kept(keep, R, N, w2.dtype)
+    _same(dy, (R, K), w2.dtype, "dy")
+    _same(pre, *of_pre, "pre")
+    if of_scale is not None:
+        _same(pre_scale, *of_scale, "pre_scale")
+    _same(expert_offsets, (El + 1,), torch.int32, "expert_offsets")
+    _same(expert_num_tokens, (El,), torch.int32, "expert_num_tokens")
+    if h is not None and not want_h:
+        raise ValueError("h: given, but not wanted")
+    _one_device(dy, w2, pre, expert_offsets, expert_num_tokens, pre_scale, d_pre, h)
+    if d_pre is None:
+        d_pre = _empty((R, 2 * N), dy.dtype, dy.device, stream)
+    if h is None and want_h:
+        h = _empty((R, N), dy.dtype, dy.device, stream)
+    _same(d_pre, (R, 2 * N), dy.dtype, "d_pre")
+    _same(h, (R, N), dy.dtype, "h")
+    _check("moe_grouped_gated_backward", lib().moe_grouped_gated_backward(
+        _addr(dy), R, _addr(w2), El, N, K, _addr(expert_offsets), _addr(expert_num_tokens), activation, dt, keep, _addr(pre),
+        _addr(pre_scale), _addr(d_pre), _addr(h), _raw_stream(stream)))
+    return d_pre, h
+
+
+def moe_checkpoint_pack(x, codes=None, scales=None, stream=None):
+    """x [M, K] (bf16, fp16 or fp32) in 8 bits: (codes uint8 [M, K], scales uint8 [M, ceil(K / 16)]), e4m3 with a
+    power-of-two scale for every 16 values of a row."""
+    dt = _dtype_code(x, "x")
+    M, K = x.shape
+    of_scales = (M, -(-K // 16))
+    _one_device(x, codes, scales)
+    if codes is None:
+        codes = _empty((M, K), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty(of_scales, torch.uint8, x.device, stream)
+    _same(codes, (M, K), torch.uint8, "codes")
+    _same(scales, of_scales, torch.uint8, "scales")
+    _check("moe_checkpoint_pack", lib().moe_checkpoint_pack(_addr(x), M, K, dt, _addr(codes), _addr(scales), _raw_stream(stream)))
+    return codes, scales
+
+
+def moe_checkpoint_unpack(codes, scales, dtype, out=None, stream=None):
+    """The values that moe_checkpoint_pack kept, [M, K] in `dtype`; beyond its range its largest."""
+    M, K = codes.shape
+    _same(codes, (M, K), torch.uint8, "codes")
+    _same(scales, (M, -(-K // 16)), torch.uint8, "scales")
+    _one_device(codes, scales, out)
+    if out is None:
+        out = _empty((M, K), dtype, codes.device, stream)
+    _same(out, (M, K), dtype, "out")
+    _check("moe_checkpoint_unpack", lib().moe_checkpoint_unpack(
+        _addr(codes), _addr(scales), M, K, _dtype_code(out, "out"), _addr(out), _raw_stream(stream)))
+    return out
+
+
+def moe_gather_weight_reduce_backward(dout, y, src2dst, topk_weights, apply_router_weight_on_input=False, d_y=None,
+                                      d_topk_weights=None, want_weights=True, stream=None):
+    """Gradients of moe_gather_weight_reduce: (d_y bf16 [rows, K], d_topk_weights fp32 [M, topk]). Rows of no slot are
+    left as they are in d_y. The weights' gradient is None with want_weights false or
+    apply_router_weight_on_input."""
+    _dt(dout, torch.bfloat16, "dout")
+    M, topk = src2dst.shape
+    rows, K = y.shape
+    _same(dout, (M, K), dout.dtype, "dout")
+    _same(y, (rows, K), torch.bfloat16, "y")
+    _same(src2dst, (M, topk), torch.int32, "src2dst")
+    _same(topk_weights, (M, topk), torch.float32, "topk_weights")
+    _one_device(dout, y, src2dst, topk_weights, d_y, d_topk_weights)
+    wanted = want_weights and not apply_router_weight_on_input
+    if d_topk_weights is not None and not wanted:
+        raise ValueError("d_topk_weights: given, but there is no such gradient")
+    if d_y is None:
+        d_y = _empty((rows, K), torch.bfloat16, dout.device, stream)
+    if d_topk_weights is None and wanted:
+        d_topk_weights = _empty((M, topk), torch.float32, dout.device, stream)
+    _same(d_y, (rows, K), torch.bfloat16, "d_y")
+    _same(d_topk_weights, (M, topk), torch.float32, "d_topk_weights")
+    _check("moe_gather_weight_reduce_backward", lib().moe_gather_weight_reduce_backward(
+        _addr(dout), _addr(y), rows, _addr(src2dst), _addr(topk_weights), M, topk, K, int(bool(apply_router_weight_on_input)),
+        _addr(d_y), _addr(d_topk_weights), _raw_stream(stream)))
+    return d_y, d_topk_weights
 
 
 _dtype_of, _is_cuda = attrgetter("dtype"), attrgetter("is_cuda")

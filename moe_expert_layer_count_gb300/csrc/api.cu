@@ -100,8 +100,8 @@ MOE_API const char* moe_status_string(int status) {
 MOE_API uint64_t moe_kernel_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
 MOE_API int moe_device_error(int clear) {
-    const int a = read_gemm_error(clear), b = read_grouped_error(clear);
-    return a < 0 || b < 0 ? -1 : a | b;
+    const int a = read_gemm_error(clear), b = read_grouped_error(clear), c = read_gated_error(clear);
+    return a < 0 || b < 0 || c < 0 ? -1 : a | b | c;
 }
 
 MOE_API int64_t moe_rp_cap(int64_t chunk_M, int topk, int local_num_experts) {

@@ -1,0 +1,1110 @@
+// The kernel behind the matrix products of ragged row groups with one 16-bit weight matrix per
+// group, on the 5th-generation tensor cores (tcgen05, sm_103a): forward, its two gradients, and the
+// gated forms with an activation in the epilogue. Included by the files that launch it.
+//
+// Two CTAs (one cluster, two neighbouring SMs) work on one 256-row tile with
+// tcgen05.mma.cta_group::2; each holds 128 rows of A and half of B's columns in shared
+// memory and 128 rows of the fp32 accumulator in TMEM.
+//  * forward and dgrad compute the transposed product: the M side (256 rows) runs over the
+//    weights' outputs, which have no ragged edge, and the N side over a group's rows. N may
+//    be any multiple of 16 up to 256, so a group of c rows costs ceil(c / 16) * 16 columns
+//    and not a multiple of 128, and a group of a few rows (decode) just streams its weights.
+//  * the gated forward product's 256 rows are 128 outputs' gate rows and up rows, 16 and 16 by
+//    turns, so that an epilogue thread has both of an output in its registers.
+//  * wgrad: M over n_out, N over k_in, the sum over the group's rows in steps of 64. The
+//    last step's rows past the group's end are another group's (or anything): a warp of each
+//    CTA zeroes them in shared memory, in both operands (0 * NaN is NaN).
+// The operand that TMA loads with its reduced index outermost (the weights of dgrad, both
+// operands of wgrad) is read as an MN-major tile: 64 x 64 boxes, no transposition in memory.
+// A persistent grid of CTA pairs; per CTA: warps 0-3 epilogue, warp 4 TMA, warp 5 MMA (issued
+// by the pair's first CTA), warps 6 and 7 wgrad's ragged ends. Two TMEM accumulators, so that a tile's
+// epilogue runs under the next tile's MMAs. Every pipeline wait gives up after 2 s, sets a device
+// error word and ends the kernel.
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <climits>
+#include <mutex>
+
+#include "ckpt.cuh"
+#include "elem.cuh"
+#include "route.cuh"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+__device__ int g_grouped_error;  // set to 1 when a pipeline wait ran out of time; one for each file with kernels
+
+// kGated: two forward products of the same rows (gate and up) whose results meet in the epilogue;
+// kGatedBwd: dgrad with the activation's gradients in the epilogue.
+enum { kFwd = 0, kDgrad = 1, kWgrad = 2, kGated = 3, kGatedBwd = 4 };
+__host__ __device__ constexpr bool like_fwd(int mode) { return mode == kFwd || mode == kGated; }
+__host__ __device__ constexpr bool like_dgrad(int mode) { return mode == kDgrad || mode == kGatedBwd; }
+
+constexpr int kPairM = 256;        // rows of a tile (both CTAs)
+constexpr int kMaxN = 256;         // columns of a tile
+constexpr int kDepth = 64;         // reduced index per stage: 64 16-bit values = one 128-byte swizzled row
+constexpr int kOperandBytes = 128 * kDepth * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kMaxStages = 6;
+constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kTailWarp = 6;
+constexpr int kBoxBytes = 4096;    // wgrad output box: 32 rows x 128 bytes
+constexpr int kGatedBytes = 6144;  // kGatedBwd: a warp's 32 rows x 64 bytes of gate, up and h
+constexpr int kBoxes = 2;          // boxes of a warp in turn (four would cost two stages: 302 against 289 us)
+// forward and dgrad stage two 32-row x 64-byte buffers per warp
+template <int MODE>
+__host__ __device__ constexpr int staging_bytes() {
+    return kEpiWarps * (MODE == kGatedBwd ? kGatedBytes : kBoxBytes * (MODE == kWgrad ? kBoxes : 1));
+}
+// results along the M side of a tile: kGated's rows are half gate and half up
+template <int MODE>
+__host__ __device__ constexpr int tile_outputs() { return MODE == kGated ? kPairM / 2 : kPairM; }
+constexpr int kSmemLimit = 232448;
+constexpr int kRowBoxes = 5;       // boxes of 8, 16, 32, 64, 128 rows
+template <int MODE>
+__host__ __device__ constexpr int threads_of() { return MODE == kWgrad ? 256 : 192; }  // the tail warps are wgrad's
+constexpr int kBuckets = 128;      // steps of cost that the groups are sorted by
+constexpr int kSms = 152;           // what a workspace size is computed for
+constexpr int kMaxDevices = 64;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+struct Maps {
+    CUtensorMap a;             // M side: weights (forward, dgrad) or dy (wgrad)
+    CUtensorMap b[kRowBoxes];  // N side: rows in boxes of 8 << i (forward, dgrad); b[0]: x (wgrad)
+    CUtensorMap o;             // wgrad's output
+};
+
+// What the gated epilogues read and write beside `out` (h).
+struct Gated {
+    int act, keep;       // enum moe_activation, enum moe_keep
+    const void* pre_in;  // kGatedBwd: gate and up as they were kept, [R, 2 P] (16 bits or codes)
+    void* pre_out;       // kGated: gate and up to keep, or null; kGatedBwd: their gradients (16 bits)
+    uint8_t* scale;      // the codes' scale bytes [R, 2 P / 16]: written by kGated, read by kGatedBwd
+};
+
+struct __align__(8) Tail {
+    uint64_t full[kMaxStages];   // first CTA: both CTAs' loads of a stage have landed
+    uint64_t empty[kMaxStages];
+    uint64_t land[kMaxStages];   // wgrad: this CTA's loads of a group's ragged last stage have landed
+    uint64_t ready[kMaxStages];  // wgrad, first CTA: both CTAs have zeroed what the stage must not hold
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort;
+    int tiles;
+    int bucket[kBuckets];
+};
+
+// Shared memory without the stages: alignment, staging, the groups, barriers.
+template <int MODE>
+size_t fixed_smem(int El) { return 1024 + staging_bytes<MODE>() + sizeof(Tail) + (size_t)El * 16; }
+
+
+// ------------------------------------------------------------------ PTX of the CTA pair
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared variable `a` in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t map_to(uint32_t a, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+// Arrivals on a barrier of the pair's other CTA. With nothing in memory to publish (an accumulator that
+// has been read, ordered by tcgen05.fence) the arrival is relaxed; without a scope it would be a release
+// among this CTA's threads, which says nothing to the other CTA.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The arrival that makes this warp's shared-memory writes visible to the other CTA's waiter (which takes
+// wait_phase<true>). It waits for the thread's own global stores; the tail warps have none.
+__device__ __forceinline__ void arrive_cluster_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+// Tile loads whose completion may count on the barrier of the pair's other CTA.
+__device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void load_4d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void store_3d(const CUtensorMap* m, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t t, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(cols) : "memory");
+}
+// D[tmem of both CTAs] (+)= A * B^T over 16 values of the reduced index, 16-bit operands.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on `bar` of both CTAs once the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// Shared-memory descriptor of 16 values of the reduced index (the i-th) of an operand tile with
+// the 128-byte swizzle; `addr`: its address / 16. K-major (the reduced index innermost): rows
+// of 128 bytes, groups of 8 rows 1024 bytes apart (stride offset). MN-major: boxes of 64
+// values x kDepth rows of 128 bytes, the boxes 8192 bytes apart (leading offset), groups of 8
+// rows of the reduced index 1024 bytes apart.
+template <bool kMn>
+__device__ __forceinline__ uint64_t operand(uint32_t addr, int i) {
+    const uint32_t lo = addr + (uint32_t)i * (kMn ? 2048 >> 4 : 32 >> 4) | (kMn ? kOperandBytes / 2 >> 4 : 1u) << 16;
+    constexpr uint32_t hi = 1024 >> 4 | 1u << 14 | 2u << 29;  // stride offset, version, 128-byte swizzle
+    return (uint64_t)hi << 32 | lo;
+}
+
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// TMEM columns [t, t + N) of this warp's 32 lanes: thread i gets lane i.
+__device__ __forceinline__ void load_columns(uint32_t t, uint32_t (&r)[32]) { ptx::tmem_ld_32x32b_x32(t, r); }
+__device__ __forceinline__ void load_columns(uint32_t t, uint32_t (&r)[64]) {
+    ptx::tmem_ld_32x32b_x32(t, *reinterpret_cast<uint32_t(*)[32]>(r));
+    ptx::tmem_ld_32x32b_x32(t + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+}
+__device__ __forceinline__ void wait_columns(uint32_t (&r)[32]) { ptx::tmem_wait_ld_regs32(r); }
+__device__ __forceinline__ void wait_columns(uint32_t (&r)[64]) {
+    ptx::tmem_wait_ld_regs32(*reinterpret_cast<uint32_t(*)[32]>(r));
+    ptx::tmem_wait_ld_regs32(*reinterpret_cast<uint32_t(*)[32]>(r + 32));
+}
+// 16 lanes x 32 columns as 8 x 8 fragments: registers 4i .. 4i + 3 of thread T hold columns
+// 8i + 2 (T % 4) and the next of lane T / 4, then of lane T / 4 + 8.
+__device__ __forceinline__ void load_fragments16(uint32_t t, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+}
+// The warp's 32 lanes x 32 columns: lanes 0-15 in r[0..15], lanes 16-31 in r[16..31].
+__device__ __forceinline__ void load_fragments(uint32_t t, uint32_t (&r)[32]) {
+    load_fragments16(t, r);
+    load_fragments16(t + (16u << 16), r + 16);
+}
+// Four 8 x 8 fragments of 16-bit values, transposed; lane i addresses row i % 8 of fragment i / 8.
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+// The other way: four 8 x 8 fragments read from rows of 16 bytes, transposed.
+__device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                 : "r"(addr)
+                 : "memory");
+}
+// Two fp32 rounded to O, the first in the low half.
+template <typename O>
+__device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) {
+    Vec<O, 2> v;
+    v.v[0] = from_f32<O>(__uint_as_float(lo));
+    v.v[1] = from_f32<O>(__uint_as_float(hi));
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Instruction descriptor of kind::f16 for M = 256 without N (N / 8 goes to bit 17).
+uint32_t idesc_base(int mode, int dtype) {
+    const uint32_t f = dtype == MOE_DT_BF16 ? 1u : 0u;
+    return 1u << 4 | f << 7 | f << 10 | (!like_fwd(mode) ? 1u << 15 : 0u) | (mode == kWgrad ? 1u << 16 : 0u) |
+           (uint32_t)(kPairM >> 4) << 24;
+}
+
+// Waits for a phase; false when the kernel was given up or the time ran out. kCluster: the barrier's
+// arrivals come from both CTAs and publish, or hand over, what the waiter uses next.
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort, bool check_abort = true) {
+    auto done = [&] { return kCluster ? try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+    if (done()) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (done()) return true;
+        if ((i & 31) == 0) {
+            if (check_abort && *abort) return false;
+            if (ptx::globaltimer_ns() - t0 > kTimeoutNs) {
+                *abort = 1;
+                atomicExch(&g_grouped_error, 1);
+                return false;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ activations
+constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+// Both activations are a(g) = g s with s = 1 / (1 + exp(-q)): q = g for SiLU and, since
+// (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)), q = 2 sqrt(2 / pi) (g + 0.044715 g^3) for GELU's tanh form,
+// whose cubic is taken at most at |g| = 32, where s is 0 or 1 already. exp(-q) may overflow: the
+// quotient is 0 then. Exponential and quotient are the fast ones, a few fp32 ulp where the result is
+// rounded to 16 bits.
+template <bool kGelu>
+__device__ __forceinline__ float act_exponent(float g) {
+    if (!kGelu) return g;
+    const float c = fminf(fmaxf(g, -32.f), 32.f);
+    return kGeluA * (c + kGeluB * c * c * c);
+}
+template <bool kGelu>
+__device__ __forceinline__ float act_of(float g) { return __fdividef(g, 1.f + __expf(-act_exponent<kGelu>(g))); }
+// a(g) and its derivative s + g q' s (1 - s), q' = 1 or 2 sqrt(2 / pi) (1 + 3 * 0.044715 g^2).
+template <bool kGelu>
+__device__ __forceinline__ void act_and_slope(float g, float& a, float& slope) {
+    const float s = __fdividef(1.f, 1.f + __expf(-act_exponent<kGelu>(g)));
+    a = g * s;
+    float gq = g;
+    if (kGelu) {
+        const float c = fminf(fmaxf(g, -32.f), 32.f);
+        gq = c * (kGeluA * (1.f + 3.f * kGeluB * c * c));
+    }
+    slope = s + s * (1.f - s) * gq;
+}
+
+// ------------------------------------------------------------------ tiles
+// A group of rows: its first row, its row count, its number (low 16 bits of `id`) and, forward
+// and dgrad, its first tile and the rows of each of its tiles (high 16 bits of `id`; equal
+// parts of at most 256, whole 16s). wgrad has the groups in falling order of rows.
+struct __align__(16) Group {
+    int start, lo, rows;
+    uint32_t id;
+};
+// ceil(n / d) for n >= 0, without n + d overflowing.
+__device__ __forceinline__ int ceil_div(int n, int d) { return n > 0 ? (n - 1) / d + 1 : 0; }
+// wgrad: the bucket of a group of so many rows, four buckets an octave, the largest first.
+__device__ __forceinline__ int bucket_of(int rows) {
+    return kBuckets - 1 - ((int)(__float_as_uint((float)rows + 1.f) >> 21) - 508);
+}
+
+// i / d for 0 <= i < 2^31 by a multiplication; magic_of(d) = floor(2^32 / d) + 1 overshoots by
+// less than one.
+uint32_t magic_of(int64_t d) { return d == 1 ? 0 : (uint32_t)((1ull << 32) / (uint64_t)d + 1); }
+struct Divisor {
+    int d;
+    uint32_t magic;
+    __device__ __forceinline__ int of(int i) const {
+        if (d == 1) return i;
+        const int q = (int)__umulhi((uint32_t)i, magic);
+        return q * (int64_t)d > i ? q - 1 : q;
+    }
+};
+struct Shape {
+    Divisor m_tiles;      // tiles along the M side
+    Divisor group_tiles;  // wgrad: tiles of a group, all its parts'
+    Divisor part_tiles;   // wgrad: tiles of one part
+    int parts;            // wgrad: parts that a group's rows are split into
+    int depth;            // forward, dgrad: the reduced length
+};
+
+// Where a tile lies. forward, dgrad: outputs [m0, m0 + 256) x rows [lo, lo + rows) of group
+// l, n = rows rounded up to 16. wgrad: [m0, m0 + 256) x [n0, n0 + 256) of the part-th sum of
+// dW_l, over rows [lo, lo + rows). steps: stages of the reduced index.
+struct Tile {
+    int l, part, lo, rows, m0, n0, n, steps;
+};
+
+// All lanes of a warp call it together (forward and dgrad look the group up with two votes).
+template <int MODE>
+__device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, const Shape& sh) {
+    Tile t;
+    if (MODE == kWgrad) {
+        const int at = sh.group_tiles.of(tile);
+        int i = tile - at * sh.group_tiles.d;
+        t.part = sh.part_tiles.of(i);
+        i -= t.part * sh.part_tiles.d;
+        const int p = sh.m_tiles.of(i);
+        const Group g = groups[at];
+        t.l = g.id & 0xffff;
+        t.m0 = (i - p * sh.m_tiles.d) * kPairM;
+        t.n0 = p * kMaxN;
+        t.n = kMaxN;
+        t.lo = g.lo;
+        t.rows = g.rows;
+        t.steps = ceil_div(t.rows, kDepth);
+        if (sh.parts > 1) {  // whole steps to every part
+            const int from = (int)((int64_t)t.steps * t.part / sh.parts), to = (int)((int64_t)t.steps * (t.part + 1) / sh.parts);
+            t.lo += from * kDepth;
+            t.rows = min(t.rows - from * kDepth, (to - from) * kDepth);
+            t.steps = to - from;
+        }
+    } else {
+        // the last group whose first tile is not past this one (an empty group starts where
+        // the next one does): the block of `stride` groups, then the group
+        const int lane = threadIdx.x & 31, stride = (El + 31) >> 5;
+        int l = lane * stride;
+        l = __popc(__ballot_sync(0xffffffffu, l < El && groups[l].start <= tile)) * stride - stride;
+        l += __popc(__ballot_sync(0xffffffffu, lane < stride && l + lane < El && groups[l + lane].start <= tile)) - 1;
+        const Group g = groups[l];
+        const int i = tile - g.start, per = g.id >> 16;
+        const int p = sh.m_tiles.of(i);
+        t.l = g.id & 0xffff;
+        t.m0 = (i - p * sh.m_tiles.d) * tile_outputs<MODE>();
+        t.lo = g.lo + p * per;
+        t.rows = min(per, g.rows - p * per);
+        t.n = (t.rows + 15) & ~15;
+        t.n0 = t.part = 0;
+        t.steps = ceil_div(sh.depth, kDepth);
+    }
+    return t;
+}
+
+// wgrad: whether stage k of a tile ends between two multiples of 16 rows, so that the MMAs
+// would read rows past the group's end.
+__device__ __forceinline__ bool ragged(const Tile& t, int k) { return k + 1 == t.steps && (t.rows & 15) != 0; }
+
+__device__ __forceinline__ int warp_prefix(int v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)(threadIdx.x & 31) >= o) v += w;
+    }
+    return v;
+}
+
+template <int MODE, typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 1)
+    grouped_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ off, const int32_t* __restrict__ cnt,
+                   int El, int R, int N, int K, Shape sh, uint32_t idesc0, int stages, O* __restrict__ out,
+                   const Gated gated) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* staging = smem + stages * kStageBytes;
+    Group* groups = reinterpret_cast<Group*>(staging + staging_bytes<MODE>());
+    Tail* st = reinterpret_cast<Tail*>(groups + El);
+    volatile int* abort = &st->abort;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    const int P = like_dgrad(MODE) ? K : N;  // length of the M side
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            ptx::mbar_init(ptx::smem_addr(&st->full[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&st->empty[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&st->land[s]), 1);
+            ptx::mbar_init(ptx::smem_addr(&st->ready[s]), 2);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(ptx::smem_addr(&st->tfull[b]), 1);
+            ptx::mbar_init(ptx::smem_addr(&st->tempty[b]), 2 * kEpiWarps);
+        }
+        ptx::mbar_init(ptx::smem_addr(&st->mma_done), 1);
+        st->abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc_pair(ptx::smem_addr(&st->tmem_base), 512);
+        tmem_relinquish_pair();
+        ptx::tc_fence_before();
+    }
+    pdl_wait();
+    pdl_trigger();
+    // the groups' rows, never outside [0, R)
+    Group* unsorted = MODE == kWgrad ? reinterpret_cast<Group*>(smem) : groups;  // in the still unused stages
+    if (MODE == kWgrad) {
+        for (int i = threadIdx.x; i < kBuckets; i += threads_of<MODE>()) st->bucket[i] = 0;
+        __syncthreads();
+    }
+    for (int l = threadIdx.x; l < El; l += threads_of<MODE>()) {
+        const int lo = min(max(__ldg(off + l), 0), R);
+        const int end = cnt ? (int)min((int64_t)lo + max(__ldg(cnt + l), 0), (int64_t)R) : min(__ldg(off + l + 1), R);
+        const int rows = max(end - lo, 0);
+        const int parts = max(ceil_div(rows, kMaxN), 1);
+        const int per = (ceil_div(rows, parts) + 15) & ~15;
+        const int b = MODE == kWgrad ? bucket_of(rows) : 0;
+        unsorted[l] = Group{b, lo, rows, (uint32_t)per << 16 | l};
+        if (MODE == kWgrad) atomicAdd(&st->bucket[b], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        if (MODE == kWgrad) {
+            // a counting sort that every CTA does alike: the first place of every bucket (lane i
+            // has buckets [4i, 4i + 4)), then the groups in their order
+            int n[kBuckets / 32], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kBuckets / 32; ++i) {
+                n[i] = sum;
+                sum += st->bucket[lane * (kBuckets / 32) + i];
+            }
+            const int before = warp_prefix(sum) - sum;
+#pragma unroll
+            for (int i = 0; i < kBuckets / 32; ++i) st->bucket[lane * (kBuckets / 32) + i] = before + n[i];
+            __syncwarp();
+            for (int l0 = 0; l0 < El; l0 += 32) {
+                const bool in = l0 + lane < El;
+                const Group g = in ? unsorted[l0 + lane] : Group{-1, 0, 0, 0};
+                const unsigned same = __match_any_sync(0xffffffffu, g.start);
+                const int place = in ? st->bucket[g.start] + __popc(same & lanemask_lt()) : 0;
+                __syncwarp();
+                if (in) {
+                    groups[place] = g;
+                    if (same >> lane == 1u) st->bucket[g.start] = place + 1;  // the last of its bucket
+                }
+                __syncwarp();
+            }
+        } else {
+            // prefix sums of the groups' tiles
+            int base = 0;
+            for (int l0 = 0; l0 < El; l0 += 32) {
+                const int l = l0 + lane;
+                const int mine = l < El ? ceil_div(groups[l].rows, kMaxN) * sh.m_tiles.d : 0;
+                const int sum = warp_prefix(mine);
+                if (l < El) groups[l].start = base + sum - mine;
+                base += __shfl_sync(0xffffffffu, sum, 31);
+            }
+            if (lane == 0) st->tiles = base;
+        }
+    }
+    if (MODE == kWgrad) ptx::fence_proxy_async_smem();  // TMA writes the stages next
+    __syncthreads();
+    cluster_sync();  // barriers and TMEM of both CTAs are in place
+    ptx::tc_fence_after();
+    const uint32_t tmem = st->tmem_base;
+    const int tiles = MODE == kWgrad ? El * sh.group_tiles.d : st->tiles;
+    // Pair p takes the tiles p, p + pairs, ...; wgrad, whose tiles come from the dearest to the
+    // cheapest, p, 2 * pairs - 1 - p, 2 * pairs + p, ..., so that the pairs' sums stay close
+    // (skewed groups of 65536 rows: 378 -> 345 us). Forward and dgrad are bound by what the SMs
+    // take in from L2, not by the spread of the pairs' work: sorted, they measured no faster.
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int turn = MODE == kWgrad ? 2 * (pairs - pair) - 1 : pairs;
+
+    if (warp == kTmaWarp) {
+        const bool lead = elect_one();
+        const uint32_t pair_full = map_to(ptx::smem_addr(&st->full[0]), 0);  // both CTAs' loads count on the first's
+        int s = 0;
+        uint32_t ph = 0, filled = 0, landed = 0;
+        bool ok = true;
+        for (int tile = pair, gap = turn; ok && tile < tiles; tile += gap, gap = 2 * pairs - gap) {
+            const Tile t = tile_at<MODE>(tile, groups, El, sh);
+            int box = 0;  // the smallest box that holds this CTA's half of the columns
+            while (MODE != kWgrad && (8 << box) < t.n / 2) ++box;
+            const int row = t.lo + (int)rank * (t.n / 2);
+            const int m = t.m0 + (int)rank * 128, n = t.n0 + (int)rank * 128;
+            for (int k = 0; k < t.steps; ++k) {
+                ok = __all_sync(0xffffffffu, wait_phase(ptx::smem_addr(&st->empty[s]), ph ^ 1, abort));
+                if (!ok) break;
+                const uint32_t a = ptx::smem_addr(smem + s * kStageBytes), b = a + kOperandBytes;
+                const uint32_t full = ptx::smem_addr(&st->full[s]), bar = pair_full + 8 * s;
+                const int d = k * kDepth;
+                if (MODE == kWgrad && ragged(t, k)) {  // this CTA's tail warps come first
+                    if (lead) {
+                        const uint32_t land = ptx::smem_addr(&st->land[s]);
+                        ptx::mbar_arrive_expect_tx(land, kStageBytes);
+                        ptx::tma_load_2d(a, &maps.a, m, t.lo + d, land);
+                        ptx::tma_load_2d(a + kOperandBytes / 2, &maps.a, m + 64, t.lo + d, land);
+                        ptx::tma_load_2d(b, &maps.b[0], n, t.lo + d, land);
+                        ptx::tma_load_2d(b + kOperandBytes / 2, &maps.b[0], n + 64, t.lo + d, land);
+                    }
+                    landed ^= 1u << s;
+                } else {
+                    if (lead) {
+                        if (rank == 0)
+                            ptx::mbar_arrive_expect_tx(full, MODE == kWgrad ? 2 * kStageBytes : 2 * (kOperandBytes + (1024u << box)));
+                        if (MODE == kWgrad) {
+                            load_2d_pair(a, &maps.a, m, t.lo + d, bar);
+                            load_2d_pair(a + kOperandBytes / 2, &maps.a, m + 64, t.lo + d, bar);
+                            load_2d_pair(b, &maps.b[0], n, t.lo + d, bar);
+                            load_2d_pair(b + kOperandBytes / 2, &maps.b[0], n + 64, t.lo + d, bar);
+                        } else {
+                            if (MODE == kGated) {
+                                // every warp's 32 lanes of the accumulator: 16 gate rows, then the up rows of
+                                // the same outputs
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    load_4d_pair(a + i * (kOperandBytes / 4), &maps.a, d, t.m0 + (int)rank * 64 + i * 16, 0, t.l, bar);
+                            } else if (MODE == kFwd) {
+                                load_3d_pair(a, &maps.a, d, m, t.l, bar);
+                            } else {
+                                load_3d_pair(a, &maps.a, m, d, t.l, bar);
+                                load_3d_pair(a + kOperandBytes / 2, &maps.a, m + 64, d, t.l, bar);
+                            }
+                            load_2d_pair(b, &maps.b[box], d, row, bar);
+                        }
+                    }
+                    filled ^= 1u << s;
+                }
+                if (++s == stages) s = 0, ph ^= 1;
+            }
+        }
+        // never leave with copies in flight: every stage's last loads must have landed
+        // (`filled`, `landed`: the parity of each barrier's uses, odd after the first)
+        for (int i = 0; i < stages; ++i) {
+            if (rank == 0) wait_phase(ptx::smem_addr(&st->full[i]), (filled >> i & 1) ^ 1, abort, false);
+            if (MODE == kWgrad) wait_phase(ptx::smem_addr(&st->land[i]), (landed >> i & 1) ^ 1, abort, false);
+        }
+    } else if (warp == kMmaWarp) {
+        if (rank == 0) {
+            // the whole warp runs the loop, so that what the MMAs take stays in uniform registers;
+            // one elected lane issues
+            const bool lead = elect_one();
+            const uint32_t base = ptx::smem_addr(smem) >> 4;
+            int s = 0, b = 0;
+            uint32_t tph = 0, filled = 0, landed = 0;
+            bool ok = true;
+            for (int tile = pair, gap = turn; ok && tile < tiles; tile += gap, gap = 2 * pairs - gap) {
+                const Tile t = tile_at<MODE>(tile, groups, El, sh);
+                if (t.steps == 0) continue;
+                const uint32_t idesc = idesc0 | (uint32_t)(t.n >> 3) << 17;
+                const uint32_t d = tmem + (uint32_t)(b * kMaxN);
+                ok = __all_sync(0xffffffffu, wait_phase<true>(ptx::smem_addr(&st->tempty[b]), tph ^ 1, abort));
+                if (!ok) break;
+                for (int k = 0; k < t.steps; ++k) {
+                    bool got;
+                    if (MODE == kWgrad && ragged(t, k)) {
+                        got = wait_phase<true>(ptx::smem_addr(&st->ready[s]), landed >> s & 1, abort);
+                        landed ^= 1u << s;
+                    } else {
+                        got = wait_phase(ptx::smem_addr(&st->full[s]), filled >> s & 1, abort);
+                        filled ^= 1u << s;
+                    }
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t a = base + (uint32_t)s * (kStageBytes >> 4), w = a + (kOperandBytes >> 4);
+                    const int left = (MODE == kWgrad ? t.rows : sh.depth) - k * kDepth;
+                    if (left > kDepth - 16) {
+                        if (lead) {
+#pragma unroll
+                            for (int i = 0; i < kDepth / 16; ++i)
+                                mma_pair(d, operand<!like_fwd(MODE)>(a, i), operand<MODE == kWgrad>(w, i), idesc,
+                                         i > 0 || k > 0 ? 1u : 0u);
+                            commit_pair(ptx::smem_addr(&st->empty[s]));
+                        }
+                    } else if (lead) {
+                        for (int i = 0; i * 16 < left; ++i)
+                            mma_pair(d, operand<!like_fwd(MODE)>(a, i), operand<MODE == kWgrad>(w, i), idesc, (i | k) ? 1u : 0u);
+                        commit_pair(ptx::smem_addr(&st->empty[s]));
+                    }
+                    if (++s == stages) s = 0;
+                }
+                if (ok && lead) commit_pair(ptx::smem_addr(&st->tfull[b]));
+                if (++b == 2) b = 0, tph ^= 1;
+            }
+            // never leave with MMAs in flight
+            if (lead) {
+                commit_pair(ptx::smem_addr(&st->mma_done));
+                wait_phase(ptx::smem_addr(&st->mma_done), 0, abort, false);
+            }
+        }
+    } else if (MODE == kWgrad && warp >= kTailWarp) {
+        // a group's last stage, the first warp's where it lies in an even stage (each warp sees all phases of its
+        // stages' barriers; one warp alone, with the wait for its writes to reach the cluster, took longer than
+        // the rest of a decode-sized tile: 512 rows over 128 groups 143.8 -> 131.6 us): the rows past the group's end within the last 16 that the MMAs
+        // read become zeros in all four boxes of this CTA
+        int s = 0;
+        uint32_t landed = 0;
+        for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
+            const Tile t = tile_at<MODE>(tile, groups, El, sh);
+            if (t.steps == 0) continue;
+            s = (s + t.steps - 1) % stages;
+            if (ragged(t, t.steps - 1) && (s & 1) == warp - kTailWarp) {
+                const bool ok = wait_phase(ptx::smem_addr(&st->land[s]), landed >> s & 1, abort);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                landed ^= 1u << s;
+                uint8_t* p = smem + s * kStageBytes;
+                const int left = t.rows - (t.steps - 1) * kDepth;
+                const int n = (-left & 15) * 8;  // 16-byte pieces of a box
+                p += left * 128 + lane * 16;
+                for (int i = lane; i < n; i += 32, p += 512)
+#pragma unroll
+                    for (int box = 0; box < 4; ++box)
+                        *reinterpret_cast<uint4*>(p + box * (kOperandBytes / 2)) = make_uint4(0, 0, 0, 0);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_cluster_release(map_to(ptx::smem_addr(&st->ready[s]), 0));
+            }
+            if (++s == stages) s = 0;
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        int b = 0, boxes = 0;
+        uint32_t tph = 0;
+        const uint32_t slab = (uint32_t)(warp * 32) << 16;
+        for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
+            const Tile t = tile_at<MODE>(tile, groups, El, sh);
+            const int m = t.m0 + (int)rank * (tile_outputs<MODE>() / 2) + warp * (tile_outputs<MODE>() / 8);  // this warp's first output
+            if (t.steps > 0) {
+                bool ok = wait_phase(ptx::smem_addr(&st->tfull[b]), tph, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ptx::tc_fence_after();
+            }
+            const uint32_t acc = tmem + slab + (uint32_t)(b * kMaxN);
+            // the accumulator is free for the MMAs once this warp has read its last columns
+            auto release = [&] {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(map_to(ptx::smem_addr(&st->tempty[b]), 0));
+            };
+            if constexpr (MODE == kWgrad) {
+                constexpr int kCols = 128 / sizeof(O);  // columns of a 128-byte-wide box
+                const int cols = min(kMaxN, K - t.n0);
+                // 32 rows x 128 bytes in TMA's 128-byte swizzle, kBoxes boxes in turn
+                auto put = [&](const uint32_t (&v)[kCols], int c) {
+                    uint8_t* box = staging + (warp * kBoxes + boxes) * kBoxBytes;
+                    if (++boxes == kBoxes) boxes = 0;
+                    if (lane == 0) bulk_wait_read<kBoxes - 1>();
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        Vec<O, 16 / sizeof(O)> w;
+#pragma unroll
+                        for (int j = 0; j < 16 / (int)sizeof(O); ++j)
+                            w.v[j] = from_f32<O>(__uint_as_float(v[q * (16 / sizeof(O)) + j]));
+                        *reinterpret_cast<Vec<O, 16 / sizeof(O)>*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (m < P) store_3d(&maps.o, ptx::smem_addr(box), t.n0 + c, m, t.part * El + t.l);
+                        ptx::bulk_commit();
+                    }
+                };
+                uint32_t u[kCols], v[kCols];
+                if (t.steps == 0) {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) u[j] = 0;
+                    for (int c = 0; c < cols; c += kCols) put(u, c);
+                } else {
+                    // the next box's columns are on their way while this one's are stored
+                    auto step_box = [&](uint32_t (&now)[kCols], uint32_t (&next)[kCols], int c) {
+                        wait_columns(now);
+                        if (c + kCols < cols)
+                            load_columns(acc + c + kCols, next);
+                        else
+                            release();
+                        put(now, c);
+                    };
+                    load_columns(acc, u);
+                    for (int c = 0; c < cols; c += 2 * kCols) {
+                        step_box(u, v, c);
+                        if (c + kCols < cols) step_box(v, u, c + kCols);
+                    }
+                }
+            } else if constexpr (MODE == kGated) {
+                // 32 rows at a time. Lanes 0-15 of the accumulator are the gates of this warp's 16 outputs,
+                // lanes 16-31 their ups, so that a thread's registers j and 16 + j are the gate and up of one
+                // output. Rounded to 16 bits they are transposed into shared memory, rows of 64 bytes
+                // (16 gates, 16 ups) and of 32 bytes (h), and leave it as 16-byte pieces of rows.
+                uint8_t* stage = staging + warp * kBoxBytes;
+                uint8_t* hbuf = stage + 2048;
+                const uint32_t put_pre = ptx::smem_addr(stage) + (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
+                // two row blocks at once: lanes 16-31 address the second one's rows
+                const uint32_t put_h = ptx::smem_addr(hbuf) + (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * 32 +
+                                                                         ((((lane >> 3) & 1) ^ ((lane >> 2) & 1)) << 4));
+                const int64_t P2 = 2 * (int64_t)P;
+                uint32_t u[32], v[32];
+                auto step_rows = [&](uint32_t (&now)[32], uint32_t (&next)[32], int c) {
+                    __syncwarp();
+                    wait_columns(now);
+                    if (c + 32 < t.rows)
+                        load_fragments(acc + c + 32, next);
+                    else
+                        release();
+                    float h[16];
+                    if (gated.act == MOE_ACT_SILU) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) h[j] = act_of<false>(__uint_as_float(now[j])) * __uint_as_float(now[16 + j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) h[j] = act_of<true>(__uint_as_float(now[j])) * __uint_as_float(now[16 + j]);
+                    }
+                    auto hh = [&](int j) { return pack2<O>(__float_as_uint(h[j]), __float_as_uint(h[j + 1])); };
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) store_transposed(put_h + i * 512, hh(8 * i), hh(8 * i + 2), hh(8 * i + 4), hh(8 * i + 6));
+                    if (gated.keep != MOE_KEEP_NONE) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            store_transposed(put_pre + i * 512, pack2<O>(now[4 * i], now[4 * i + 1]),
+                                             pack2<O>(now[4 * i + 2], now[4 * i + 3]),
+                                             pack2<O>(now[16 + 4 * i], now[16 + 4 * i + 1]),
+                                             pack2<O>(now[16 + 4 * i + 2], now[16 + 4 * i + 3]));
+                    }
+                    __syncwarp();
+                    const int64_t row0 = (int64_t)t.lo + c;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = i * 16 + (lane >> 1), piece = lane & 1;
+                        const uint4 w = *reinterpret_cast<const uint4*>(hbuf + r * 32 + ((piece ^ ((r >> 2) & 1)) << 4));
+                        if (m + piece * 8 < P && c + r < t.rows) *reinterpret_cast<uint4*>(out + (row0 + r) * P + m + piece * 8) = w;
+                    }
+                    if (gated.keep == MOE_KEEP_16BIT) {
+                        O* pre = static_cast<O*>(gated.pre_out);
+                        const int piece = lane & 3, j = m + (piece & 1) * 8;
+                        const int64_t at = (piece >> 1) * (int64_t)P + j;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = i * 8 + (lane >> 2);
+                            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4));
+                            if (j < P && c + r < t.rows) *reinterpret_cast<uint4*>(pre + (row0 + r) * P2 + at) = w;
+                        }
+                    } else if (gated.keep == MOE_KEEP_E4M3) {
+                        // a lane has one row's 16 gates or ups: one group of the 8-bit form, made from the
+                        // 16-bit values so that it equals what packing those gives
+                        uint8_t* codes = static_cast<uint8_t*>(gated.pre_out);
+                        const int half = lane & 1;
+                        const int64_t at = half * (int64_t)P + m;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = i * 16 + (lane >> 1), z = (r >> 1) & 3;
+                            const uint4 lo = *reinterpret_cast<const uint4*>(stage + r * 64 + (((2 * half) ^ z) << 4));
+                            const uint4 hi = *reinterpret_cast<const uint4*>(stage + r * 64 + (((2 * half + 1) ^ z) << 4));
+                            uint32_t byte;
+                            const uint4 w = ckpt_encode16<O>(lo, hi, byte);
+                            if (m < P && c + r < t.rows) {
+                                *reinterpret_cast<uint4*>(codes + (row0 + r) * P2 + at) = w;
+                                gated.scale[((row0 + r) * P2 + at) / kCkptGroup] = (uint8_t)byte;
+                            }
+                        }
+                    }
+                };
+                load_fragments(acc, u);
+                for (int c = 0; c < t.rows; c += 64) {
+                    step_rows(u, v, c);
+                    if (c + 32 < t.rows) step_rows(v, u, c + 32);
+                }
+                __syncwarp();
+            } else if constexpr (MODE == kGatedBwd) {
+                // 32 rows x this warp's 32 outputs at a time: gate and up come in as 16-byte pieces of rows, one
+                // step ahead, are laid into shared memory (64 bytes a row, swizzled) and read as the
+                // accumulator's 8 x 8 fragments; the gradients go back over them and out, h beside them.
+                uint8_t* gbuf = staging + warp * kGatedBytes;
+                const uint32_t frag = ptx::smem_addr(gbuf) + (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
+                const int64_t P2 = 2 * (int64_t)P;
+                const bool eight = gated.keep == MOE_KEEP_E4M3;
+                const int piece = lane & 3, j = m + piece * 8;   // 16 bits: rows 8 i + lane / 4
+                const int group = lane & 1, jg = m + group * 16;  // 8 bits: rows 16 i + lane / 2
+                uint4 in[8];     // 16 bits: gate, up by turns; 8 bits: codes of gate, up by turns in the first four
+                uint32_t sc[4];  // 8 bits: their scales
+                auto fetch = [&](int c) {
+                    const int64_t row0 = (int64_t)t.lo + c;
+                    if (eight) {
+                        const uint8_t* codes = static_cast<const uint8_t*>(gated.pre_in);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = (i >> 1) * 16 + (lane >> 1);
+                            const int64_t at = (row0 + r) * P2 + (i & 1) * (int64_t)P + jg;
+                            const bool live = jg < P && c + r < t.rows;
+                            in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(codes + at)) : make_uint4(0, 0, 0, 0);
+                            sc[i] = live ? __ldcg(gated.scale + at / kCkptGroup) : 127u;
+                        }
+                    } else {
+                        const O* pre = static_cast<const O*>(gated.pre_in);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = (i >> 1) * 8 + (lane >> 2);
+                            const bool live = j < P && c + r < t.rows;
+                            in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(pre + (row0 + r) * P2 + (i & 1) * (int64_t)P + j))
+                                         : make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                };
+                uint32_t u[32], v[32];
+                auto step_rows = [&](uint32_t (&now)[32], uint32_t (&next)[32], int c) {
+                    __syncwarp();
+                    if (eight) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = (i >> 1) * 16 + (lane >> 1), z = (r >> 1) & 3;
+                            uint8_t* row = gbuf + (i & 1) * 2048 + r * 64;
+                            uint4 lo, hi;
+                            ckpt_decode16<O>(in[i], sc[i], lo, hi);
+                            *reinterpret_cast<uint4*>(row + (((2 * group) ^ z) << 4)) = lo;
+                            *reinterpret_cast<uint4*>(row + (((2 * group + 1) ^ z) << 4)) = hi;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = (i >> 1) * 8 + (lane >> 2);
+                            *reinterpret_cast<uint4*>(gbuf + (i & 1) * 2048 + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4)) = in[i];
+                        }
+                    }
+                    if (c + 32 < t.rows) fetch(c + 32);
+                    __syncwarp();
+                    wait_columns(now);
+                    if (c + 32 < t.rows)
+                        load_fragments(acc + c + 32, next);
+                    else
+                        release();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // 8 rows
+                        uint32_t g[4], up[4], h[4];
+                        load_transposed(frag + i * 512, g[0], g[1], g[2], g[3]);
+                        load_transposed(frag + 2048 + i * 512, up[0], up[1], up[2], up[3]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {  // outputs 8 q .. 8 q + 7; two rows each
+                            const float2 gv = unpack2<O>(g[q]), uv = unpack2<O>(up[q]);
+                            const int at = (q >> 1) * 16 + 4 * i + (q & 1) * 2;
+                            const float d0 = __uint_as_float(now[at]), d1 = __uint_as_float(now[at + 1]);
+                            float a0, a1, s0, s1;
+                            if (gated.act == MOE_ACT_SILU) {
+                                act_and_slope<false>(gv.x, a0, s0);
+                                act_and_slope<false>(gv.y, a1, s1);
+                            } else {
+                                act_and_slope<true>(gv.x, a0, s0);
+                                act_and_slope<true>(gv.y, a1, s1);
+                            }
+                            auto two = [](float x, float y) { return pack2<O>(__float_as_uint(x), __float_as_uint(y)); };
+                            g[q] = two(d0 * uv.x * s0, d1 * uv.y * s1);
+                            up[q] = two(d0 * a0, d1 * a1);
+                            h[q] = two(a0 * uv.x, a1 * uv.y);
+                        }
+                        __syncwarp();
+                        store_transposed(frag + i * 512, g[0], g[1], g[2], g[3]);
+                        store_transposed(frag + 2048 + i * 512, up[0], up[1], up[2], up[3]);
+                        store_transposed(frag + 4096 + i * 512, h[0], h[1], h[2], h[3]);
+                    }
+                    __syncwarp();
+                    O* grads = static_cast<O*>(gated.pre_out);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 8 + (lane >> 2);
+                        const uint8_t* row = gbuf + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4);
+                        const int64_t at = (int64_t)t.lo + c + r;
+                        if (j < P && c + r < t.rows) {
+                            *reinterpret_cast<uint4*>(grads + at * P2 + j) = *reinterpret_cast<const uint4*>(row);
+                            *reinterpret_cast<uint4*>(grads + at * P2 + P + j) = *reinterpret_cast<const uint4*>(row + 2048);
+                            if (out) *reinterpret_cast<uint4*>(out + at * P + j) = *reinterpret_cast<const uint4*>(row + 4096);
+                        }
+                    }
+                };
+                if (t.rows > 0) fetch(0);
+                load_fragments(acc, u);
+                for (int c = 0; c < t.rows; c += 64) {
+                    step_rows(u, v, c);
+                    if (c + 32 < t.rows) step_rows(v, u, c + 32);
+                }
+                __syncwarp();
+            } else if constexpr (sizeof(O) == 4) {
+                // lane = output column: 128 bytes of one row per store
+                const bool in = m + lane < P;
+                O* o = out + (int64_t)t.lo * P + m + lane;
+                uint32_t u[32], v[32];
+                auto step_rows = [&](uint32_t (&now)[32], uint32_t (&next)[32], int c) {
+                    __syncwarp();
+                    wait_columns(now);
+                    if (c + 32 < t.rows)
+                        load_columns(acc + c + 32, next);
+                    else
+                        release();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (in && c + j < t.rows) o[(int64_t)(c + j) * P] = __uint_as_float(now[j]);
+                };
+                load_columns(acc, u);
+                for (int c = 0; c < t.rows; c += 64) {
+                    step_rows(u, v, c);
+                    if (c + 32 < t.rows) step_rows(v, u, c + 32);
+                }
+            } else {
+                // 32 rows of the result x this warp's 32 outputs at a time: read as 8 x 8 fragments,
+                // transposed into shared memory (64 bytes a row, 16-byte pieces swizzled so that
+                // neither side has bank conflicts), stored as 64-byte pieces of rows
+                uint8_t* stage = staging + warp * kBoxBytes;
+                const int piece = lane & 3;
+                const bool in = m + piece * 8 < P;
+                O* o = out + ((int64_t)t.lo + (lane >> 2)) * P + m + piece * 8;
+                const uint32_t put_at = (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
+                const uint32_t get_at = (uint32_t)((lane >> 2) * 64 + ((piece ^ ((lane >> 3) & 3)) << 4));
+                uint32_t u[32], v[32];
+                auto step_rows = [&](uint32_t (&now)[32], uint32_t (&next)[32], int c) {
+                    __syncwarp();
+                    wait_columns(now);
+                    if (c + 32 < t.rows)
+                        load_fragments(acc + c + 32, next);
+                    else
+                        release();
+                    uint8_t* buf = stage + (c & 32) * 64;
+                    const uint32_t to = ptx::smem_addr(buf) + put_at;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        store_transposed(to + i * 512, pack2<O>(now[4 * i], now[4 * i + 1]),
+                                         pack2<O>(now[4 * i + 2], now[4 * i + 3]), pack2<O>(now[16 + 4 * i], now[16 + 4 * i + 1]),
+                                         pack2<O>(now[16 + 4 * i + 2], now[16 + 4 * i + 3]));
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(buf + get_at + i * 512);
+                        if (in && c + i * 8 + (lane >> 2) < t.rows) *reinterpret_cast<uint4*>(o + (int64_t)(c + i * 8) * P) = w;
+                    }
+                };
+                load_fragments(acc, u);
+                for (int c = 0; c < t.rows; c += 64) {
+                    step_rows(u, v, c);
+                    if (c + 32 < t.rows) step_rows(v, u, c + 32);
+                }
+                __syncwarp();
+            }
+            if (t.steps > 0)
+                if (++b == 2) b = 0, tph ^= 1;
+        }
+        if (MODE == kWgrad && lane == 0) ptx::bulk_wait0();
+    }
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();  // no CTA leaves while the other still signals its barriers or uses its TMEM
+    if (warp == kMmaWarp) {
+        // The MMAs' completions are signalled to both CTAs by the hardware, outside of any thread's order: the
+        // first CTA has seen the last of them, the second may not leave before it has arrived there too (its
+        // shared memory may by then be another kernel's).
+        if (rank == 1) wait_phase(ptx::smem_addr(&st->mma_done), 0, abort, false);
+        __syncwarp();
+        ptx::tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// kGated's weights [El][2][N][K] of 2-byte elements: boxes of 16 outputs' gate rows and up rows, 128 bytes each.
+bool make_gated_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t N, uint64_t El) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t size[4] = {K, N, 2, El}, stride[3] = {K * 2, K * N * 2, K * N * 4};
+    const cuuint32_t box[4] = {kDepth, 16, 2, 1}, one[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), size, stride, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor [z, y, x] (z = 1: two dimensions) of 2- or 4-byte elements, boxes of box_y rows x 128
+// bytes with the 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, int esize, uint64_t x, uint64_t y, uint64_t z, uint32_t box_y, int dims) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t size[3] = {x, y, z}, stride[2] = {x * esize, x * y * esize};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / esize), box_y, 1}, one[3] = {1, 1, 1};
+    return fn(m, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (cuuint32_t)dims,
+              const_cast<void*>(base), size, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, typename O>
+int launch_grouped(const void* a, const void* b, const int32_t* off, const int32_t* cnt, int El, int64_t R, int N, int K,
+                   int dtype, void* out, int parts, int num_sms, cudaStream_t stream, const Gated& gated = {}) {
+    Maps maps{};
+    bool ok = true;
+    if (MODE == kWgrad) {
+        const uint64_t rows = R > 0 ? (uint64_t)R : 1;  // R = 0: nothing is loaded
+        const void* any = out;
+        ok = make_map(&maps.a, R > 0 ? a : any, 2, N, rows, 1, kDepth, 2) &&
+             make_map(&maps.b[0], R > 0 ? b : any, 2, K, rows, 1, kDepth, 2) &&
+             make_map(&maps.o, out, sizeof(O), K, N, (uint64_t)El * parts, 32, 3);
+    } else {
+        ok = MODE == kGated ? make_gated_map(&maps.a, b, K, N, El) : make_map(&maps.a, b, 2, K, N, El, MODE == kFwd ? 128 : kDepth, 3);
+        for (int i = 0; i < kRowBoxes; ++i) ok = ok && make_map(&maps.b[i], a, 2, like_fwd(MODE) ? K : N, R, 1, 8u << i, 2);
+    }
+    if (!ok) return MOE_ERR_CUDA;
+    int dev = 0;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(grouped_kernel<MODE, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) !=
+            cudaSuccess)
+            return MOE_ERR_CUDA;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    int stages = (int)((kSmemLimit - fixed_smem<MODE>(El)) / kStageBytes);
+    if (stages > kMaxStages) stages = kMaxStages;
+    const size_t smem = fixed_smem<MODE>(El) + (size_t)stages * kStageBytes;
+    const int64_t m_tiles = ((int64_t)(like_dgrad(MODE) ? K : N) + tile_outputs<MODE>() - 1) / tile_outputs<MODE>();
+    const int64_t part_tiles = m_tiles * (((int64_t)K + kMaxN - 1) / kMaxN), group_tiles = part_tiles * parts;
+    const Shape sh{{(int)m_tiles, magic_of(m_tiles)}, {(int)group_tiles, magic_of(group_tiles)},
+                   {(int)part_tiles, magic_of(part_tiles)}, parts, like_dgrad(MODE) ? N : K};
+    // no more pairs than tiles (an upper bound: the groups' sizes are not known here)
+    const int64_t most = MODE == kWgrad ? El * group_tiles : (R / kMaxN + (R < El ? R : El)) * m_tiles;
+    const int pairs = (int)(most < num_sms / 2 ? most : num_sms / 2);
+    launch_k(grouped_kernel<MODE, O>, 2 * pairs, threads_of<MODE>(), smem, stream, maps, off, cnt, El, (int)R, N, K,
+             sh, idesc_base(MODE, dtype), stages, static_cast<O*>(out), gated);
+    note_launches(1);
+    return launch_status();
+}
+
+// The error word of this file's kernels (see moe_device_error).
+int read_error_word(int clear) {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_grouped_error, sizeof(int)) != cudaSuccess) return -1;
+    if (clear && v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_grouped_error, &z, sizeof(int));
+    }
+    return v;
+}
+
+}  // namespace
+}  // namespace moe

@@ -65,7 +65,8 @@ int forward_chunked_impl(const void* hidden_states, const TId* topk_ids, const f
 // Device error word of the grouped GEMM (1: a pipeline wait ran out of time). Reading
 // it synchronises the device; `clear` resets it.
 int read_gemm_error(int clear);
-// The same of the 16-bit grouped products.
+// The same of the 16-bit grouped products, and of their gated forms.
 int read_grouped_error(int clear);
+int read_gated_error(int clear);
 
 }  // namespace moe
