@@ -53,12 +53,15 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kTailWarp = 6;
 constexpr int kBoxBytes = 4096;    // wgrad output box: 32 rows x 128 bytes
-constexpr int kGatedBytes = 6144;  // kGatedBwd: a warp's 32 rows x 64 bytes of gate, up and h
+constexpr int kGatedBytes = 3072;  // kGated, kGatedBwd: a warp's 16 rows x 64 bytes of gate and up (kGatedBwd: each) and of h
 constexpr int kBoxes = 2;          // boxes of a warp in turn (four would cost two stages: 302 against 289 us)
+// The gated forms' epilogues have two warps for each quarter of the accumulator's lanes.
+template <int MODE>
+__host__ __device__ constexpr int epi_warps() { return MODE == kGated || MODE == kGatedBwd ? 2 * kEpiWarps : kEpiWarps; }
 // forward and dgrad stage two 32-row x 64-byte buffers per warp
 template <int MODE>
 __host__ __device__ constexpr int staging_bytes() {
-    return kEpiWarps * (MODE == kGatedBwd ? kGatedBytes : kBoxBytes * (MODE == kWgrad ? kBoxes : 1));
+    return epi_warps<MODE>() * (MODE == kGated || MODE == kGatedBwd ? kGatedBytes : kBoxBytes * (MODE == kWgrad ? kBoxes : 1));
 }
 // results along the M side of a tile: kGated's rows are half gate and half up
 template <int MODE>
@@ -66,7 +69,9 @@ __host__ __device__ constexpr int tile_outputs() { return MODE == kGated ? kPair
 constexpr int kSmemLimit = 232448;
 constexpr int kRowBoxes = 5;       // boxes of 8, 16, 32, 64, 128 rows
 template <int MODE>
-__host__ __device__ constexpr int threads_of() { return MODE == kWgrad ? 256 : 192; }  // the tail warps are wgrad's
+__host__ __device__ constexpr int threads_of() {  // the tail warps are wgrad's
+    return MODE == kWgrad ? 256 : 32 * (epi_warps<MODE>() + 2);
+}
 constexpr int kBuckets = 128;      // steps of cost that the groups are sorted by
 constexpr int kSms = 152;           // what a workspace size is computed for
 constexpr int kMaxDevices = 64;
@@ -235,6 +240,18 @@ __device__ __forceinline__ void load_fragments16(uint32_t t, uint32_t* r) {
         : "r"(t)
         : "memory");
 }
+// 16 lanes x 16 columns in the same way.
+__device__ __forceinline__ void load_fragments8(uint32_t t, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t)
+                 : "memory");
+}
+// The warp's 32 lanes x 16 columns: lanes 0-15 in r[0..7], lanes 16-31 in r[8..15].
+__device__ __forceinline__ void load_fragments(uint32_t t, uint32_t (&r)[16]) {
+    load_fragments8(t, r);
+    load_fragments8(t + (16u << 16), r + 8);
+}
 // The warp's 32 lanes x 32 columns: lanes 0-15 in r[0..15], lanes 16-31 in r[16..31].
 __device__ __forceinline__ void load_fragments(uint32_t t, uint32_t (&r)[32]) {
     load_fragments16(t, r);
@@ -298,31 +315,47 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
 // ------------------------------------------------------------------ activations
 constexpr float kGeluA = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Both activations are a(g) = g s with s = 1 / (1 + exp(-q)): q = g for SiLU and, since
 // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)), q = 2 sqrt(2 / pi) (g + 0.044715 g^3) for GELU's tanh form,
-// whose cubic is taken at most at |g| = 32, where s is 0 or 1 already. exp(-q) may overflow: the
-// quotient is 0 then. Exponential and quotient are the fast ones, a few fp32 ulp where the result is
-// rounded to 16 bits.
+// whose cubic is taken at most at |g| = 32, where s is 0 or 1 already. exp(-q) may overflow: s is 0
+// then. Exponential and reciprocal are the approximate ones, which flush what is subnormal: a few fp32
+// ulp where the result is rounded to 16 bits (the forms that keep subnormals cost another seven
+// instructions a value).
 template <bool kGelu>
-__device__ __forceinline__ float act_exponent(float g) {
-    if (!kGelu) return g;
-    const float c = fminf(fmaxf(g, -32.f), 32.f);
-    return kGeluA * (c + kGeluB * c * c * c);
+__device__ __forceinline__ float act_gate(float g) {
+    float q = -kLog2e * g;
+    if (kGelu) {
+        const float c = fminf(fmaxf(g, -32.f), 32.f);
+        q = c * fmaf(-kLog2e * kGeluA * kGeluB, c * c, -kLog2e * kGeluA);
+    }
+    return rcp_approx(1.f + ex2_approx(q));
 }
 template <bool kGelu>
-__device__ __forceinline__ float act_of(float g) { return __fdividef(g, 1.f + __expf(-act_exponent<kGelu>(g))); }
+__device__ __forceinline__ float act_of(float g) { return g * act_gate<kGelu>(g); }
 // a(g) and its derivative s + g q' s (1 - s), q' = 1 or 2 sqrt(2 / pi) (1 + 3 * 0.044715 g^2).
 template <bool kGelu>
 __device__ __forceinline__ void act_and_slope(float g, float& a, float& slope) {
-    const float s = __fdividef(1.f, 1.f + __expf(-act_exponent<kGelu>(g)));
+    const float s = act_gate<kGelu>(g);
     a = g * s;
     float gq = g;
     if (kGelu) {
         const float c = fminf(fmaxf(g, -32.f), 32.f);
-        gq = c * (kGeluA * (1.f + 3.f * kGeluB * c * c));
+        gq = c * fmaf(3.f * kGeluA * kGeluB, c * c, kGeluA);
     }
-    slope = s + s * (1.f - s) * gq;
+    slope = fmaf(fmaf(-s, s, s), gq, s);
 }
 
 // ------------------------------------------------------------------ tiles
@@ -449,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(ptx::smem_addr(&st->tfull[b]), 1);
-            ptx::mbar_init(ptx::smem_addr(&st->tempty[b]), 2 * kEpiWarps);
+            ptx::mbar_init(ptx::smem_addr(&st->tempty[b]), 2 * epi_warps<MODE>());
         }
         ptx::mbar_init(ptx::smem_addr(&st->mma_done), 1);
         st->abort = 0;
@@ -682,10 +715,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         // ---------------------------------------------------------------- epilogue
         int b = 0, boxes = 0;
         uint32_t tph = 0;
-        const uint32_t slab = (uint32_t)(warp * 32) << 16;
+        const int quarter = warp & 3;  // of the accumulator's lanes: what a warp can read goes by its number
+        const uint32_t slab = (uint32_t)(quarter * 32) << 16;
         for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
             const Tile t = tile_at<MODE>(tile, groups, El, sh);
-            const int m = t.m0 + (int)rank * (tile_outputs<MODE>() / 2) + warp * (tile_outputs<MODE>() / 8);  // this warp's first output
+            const int m = t.m0 + (int)rank * (tile_outputs<MODE>() / 2) + quarter * (tile_outputs<MODE>() / 8);  // this warp's first output
             if (t.steps > 0) {
                 bool ok = wait_phase(ptx::smem_addr(&st->tfull[b]), tph, abort);
                 ok = __all_sync(0xffffffffu, ok);
@@ -745,116 +779,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                     }
                 }
             } else if constexpr (MODE == kGated) {
-                // 32 rows at a time. Lanes 0-15 of the accumulator are the gates of this warp's 16 outputs,
-                // lanes 16-31 their ups, so that a thread's registers j and 16 + j are the gate and up of one
-                // output. Rounded to 16 bits they are transposed into shared memory, rows of 64 bytes
-                // (16 gates, 16 ups) and of 32 bytes (h), and leave it as 16-byte pieces of rows.
-                uint8_t* stage = staging + warp * kBoxBytes;
-                uint8_t* hbuf = stage + 2048;
+                // 16 rows at a time, the quarter's two warps by turns. Lanes 0-15 of the accumulator are the gates
+                // of this warp's 16 outputs, lanes 16-31 their ups, so that a thread's registers j and 8 + j are
+                // the gate and up of one output. Rounded to 16 bits they are transposed into shared memory, rows
+                // of 64 bytes (16 gates, 16 ups) and of 32 bytes (h), and leave it as 16-byte pieces of rows.
+                const int half = warp > 3, first = half * 16;
+                uint8_t* stage = staging + (half * 4 + quarter) * kGatedBytes;
+                uint8_t* hbuf = stage + 1024;
                 const uint32_t put_pre = ptx::smem_addr(stage) + (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
-                // two row blocks at once: lanes 16-31 address the second one's rows
+                // 8 rows and the next 8: lanes 16-31 address the second ones
                 const uint32_t put_h = ptx::smem_addr(hbuf) + (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * 32 +
                                                                          ((((lane >> 3) & 1) ^ ((lane >> 2) & 1)) << 4));
                 const int64_t P2 = 2 * (int64_t)P;
-                uint32_t u[32], v[32];
-                auto step_rows = [&](uint32_t (&now)[32], uint32_t (&next)[32], int c) {
+                uint32_t next[16];
+                if (first < t.rows)
+                    load_fragments(acc + first, next);
+                else
+                    release();
+#pragma unroll 1
+                for (int c = first; c < t.rows; c += 32) {
                     __syncwarp();
-                    wait_columns(now);
+                    ptx::tmem_wait_ld_regs(next);
+                    uint32_t v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = next[j];
                     if (c + 32 < t.rows)
                         load_fragments(acc + c + 32, next);
                     else
                         release();
-                    float h[16];
+                    float h[8];
                     if (gated.act == MOE_ACT_SILU) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) h[j] = act_of<false>(__uint_as_float(now[j])) * __uint_as_float(now[16 + j]);
+                        for (int j = 0; j < 8; ++j) h[j] = act_of<false>(__uint_as_float(v[j])) * __uint_as_float(v[8 + j]);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) h[j] = act_of<true>(__uint_as_float(now[j])) * __uint_as_float(now[16 + j]);
+                        for (int j = 0; j < 8; ++j) h[j] = act_of<true>(__uint_as_float(v[j])) * __uint_as_float(v[8 + j]);
                     }
                     auto hh = [&](int j) { return pack2<O>(__float_as_uint(h[j]), __float_as_uint(h[j + 1])); };
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) store_transposed(put_h + i * 512, hh(8 * i), hh(8 * i + 2), hh(8 * i + 4), hh(8 * i + 6));
+                    store_transposed(put_h, hh(0), hh(2), hh(4), hh(6));
                     if (gated.keep != MOE_KEEP_NONE) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            store_transposed(put_pre + i * 512, pack2<O>(now[4 * i], now[4 * i + 1]),
-                                             pack2<O>(now[4 * i + 2], now[4 * i + 3]),
-                                             pack2<O>(now[16 + 4 * i], now[16 + 4 * i + 1]),
-                                             pack2<O>(now[16 + 4 * i + 2], now[16 + 4 * i + 3]));
+                        for (int i = 0; i < 2; ++i)
+                            store_transposed(put_pre + i * 512, pack2<O>(v[4 * i], v[4 * i + 1]), pack2<O>(v[4 * i + 2], v[4 * i + 3]),
+                                             pack2<O>(v[8 + 4 * i], v[8 + 4 * i + 1]), pack2<O>(v[8 + 4 * i + 2], v[8 + 4 * i + 3]));
                     }
                     __syncwarp();
                     const int64_t row0 = (int64_t)t.lo + c;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = i * 16 + (lane >> 1), piece = lane & 1;
-                        const uint4 w = *reinterpret_cast<const uint4*>(hbuf + r * 32 + ((piece ^ ((r >> 2) & 1)) << 4));
-                        if (m + piece * 8 < P && c + r < t.rows) *reinterpret_cast<uint4*>(out + (row0 + r) * P + m + piece * 8) = w;
+                    const int r = lane >> 1, side = lane & 1;
+                    const bool live = c + r < t.rows;
+                    {
+                        const uint4 w = *reinterpret_cast<const uint4*>(hbuf + r * 32 + ((side ^ ((r >> 2) & 1)) << 4));
+                        if (live && m + side * 8 < P) *reinterpret_cast<uint4*>(out + (row0 + r) * P + m + side * 8) = w;
                     }
                     if (gated.keep == MOE_KEEP_16BIT) {
                         O* pre = static_cast<O*>(gated.pre_out);
                         const int piece = lane & 3, j = m + (piece & 1) * 8;
                         const int64_t at = (piece >> 1) * (int64_t)P + j;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = i * 8 + (lane >> 2);
-                            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4));
-                            if (j < P && c + r < t.rows) *reinterpret_cast<uint4*>(pre + (row0 + r) * P2 + at) = w;
+                        for (int i = 0; i < 2; ++i) {
+                            const int q = i * 8 + (lane >> 2);
+                            const uint4 w = *reinterpret_cast<const uint4*>(stage + q * 64 + ((piece ^ ((q >> 1) & 3)) << 4));
+                            if (j < P && c + q < t.rows) *reinterpret_cast<uint4*>(pre + (row0 + q) * P2 + at) = w;
                         }
                     } else if (gated.keep == MOE_KEEP_E4M3) {
                         // a lane has one row's 16 gates or ups: one group of the 8-bit form, made from the
                         // 16-bit values so that it equals what packing those gives
-                        uint8_t* codes = static_cast<uint8_t*>(gated.pre_out);
-                        const int half = lane & 1;
-                        const int64_t at = half * (int64_t)P + m;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int r = i * 16 + (lane >> 1), z = (r >> 1) & 3;
-                            const uint4 lo = *reinterpret_cast<const uint4*>(stage + r * 64 + (((2 * half) ^ z) << 4));
-                            const uint4 hi = *reinterpret_cast<const uint4*>(stage + r * 64 + (((2 * half + 1) ^ z) << 4));
-                            uint32_t byte;
-                            const uint4 w = ckpt_encode16<O>(lo, hi, byte);
-                            if (m < P && c + r < t.rows) {
-                                *reinterpret_cast<uint4*>(codes + (row0 + r) * P2 + at) = w;
-                                gated.scale[((row0 + r) * P2 + at) / kCkptGroup] = (uint8_t)byte;
-                            }
+                        const int64_t at = (row0 + r) * P2 + side * (int64_t)P + m;
+                        const int z = (r >> 1) & 3;
+                        const uint4 lo = *reinterpret_cast<const uint4*>(stage + r * 64 + (((2 * side) ^ z) << 4));
+                        const uint4 hi = *reinterpret_cast<const uint4*>(stage + r * 64 + (((2 * side + 1) ^ z) << 4));
+                        uint32_t byte;
+                        const uint4 w = ckpt_encode16<O>(lo, hi, byte);
+                        if (live && m < P) {
+                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(gated.pre_out) + at) = w;
+                            gated.scale[at / kCkptGroup] = (uint8_t)byte;
                         }
                     }
-                };
-                load_fragments(acc, u);
-                for (int c = 0; c < t.rows; c += 64) {
-                    step_rows(u, v, c);
-                    if (c + 32 < t.rows) step_rows(v, u, c + 32);
                 }
                 __syncwarp();
             } else if constexpr (MODE == kGatedBwd) {
-                // 32 rows x this warp's 32 outputs at a time: gate and up come in as 16-byte pieces of rows, one
-                // step ahead, are laid into shared memory (64 bytes a row, swizzled) and read as the
-                // accumulator's 8 x 8 fragments; the gradients go back over them and out, h beside them.
-                uint8_t* gbuf = staging + warp * kGatedBytes;
+                // 16 rows x this warp's 32 outputs at a time, the quarter's two warps by turns: gate and up come
+                // in as 16-byte pieces of rows, one step ahead, are laid into shared memory (64 bytes a row,
+                // swizzled) and read as the accumulator's 8 x 8 fragments; the gradients go back over them and
+                // out, h beside them.
+                const int half = warp > 3, first = half * 16;
+                uint8_t* gbuf = staging + (half * 4 + quarter) * kGatedBytes;
                 const uint32_t frag = ptx::smem_addr(gbuf) + (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
                 const int64_t P2 = 2 * (int64_t)P;
                 const bool eight = gated.keep == MOE_KEEP_E4M3;
-                const int piece = lane & 3, j = m + piece * 8;   // 16 bits: rows 8 i + lane / 4
-                const int group = lane & 1, jg = m + group * 16;  // 8 bits: rows 16 i + lane / 2
-                uint4 in[8];     // 16 bits: gate, up by turns; 8 bits: codes of gate, up by turns in the first four
-                uint32_t sc[4];  // 8 bits: their scales
+                const int piece = lane & 3, j = m + piece * 8;     // 16 bits: rows 8 i + lane / 4
+                const int group = lane & 1, jg = m + group * 16;   // 8 bits: row lane / 2
+                uint4 in[4];     // 16 bits: gate, up by turns; 8 bits: codes of gate and up
+                uint32_t sc[2];  // 8 bits: their scales
                 auto fetch = [&](int c) {
                     const int64_t row0 = (int64_t)t.lo + c;
                     if (eight) {
                         const uint8_t* codes = static_cast<const uint8_t*>(gated.pre_in);
+                        const int r = lane >> 1;
+                        const bool live = jg < P && c + r < t.rows;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = (i >> 1) * 16 + (lane >> 1);
-                            const int64_t at = (row0 + r) * P2 + (i & 1) * (int64_t)P + jg;
-                            const bool live = jg < P && c + r < t.rows;
+                        for (int i = 0; i < 2; ++i) {
+                            const int64_t at = (row0 + r) * P2 + i * (int64_t)P + jg;
                             in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(codes + at)) : make_uint4(0, 0, 0, 0);
                             sc[i] = live ? __ldcg(gated.scale + at / kCkptGroup) : 127u;
                         }
                     } else {
                         const O* pre = static_cast<const O*>(gated.pre_in);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < 4; ++i) {
                             const int r = (i >> 1) * 8 + (lane >> 2);
                             const bool live = j < P && c + r < t.rows;
                             in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(pre + (row0 + r) * P2 + (i & 1) * (int64_t)P + j))
@@ -862,14 +894,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                         }
                     }
                 };
-                uint32_t u[32], v[32];
-                auto step_rows = [&](uint32_t (&now)[32], uint32_t (&next)[32], int c) {
+                uint32_t next[16];
+                if (first < t.rows) {
+                    fetch(first);
+                    load_fragments(acc + first, next);
+                } else {
+                    release();
+                }
+#pragma unroll 1
+                for (int c = first; c < t.rows; c += 32) {
                     __syncwarp();
                     if (eight) {
+                        const int r = lane >> 1, z = (r >> 1) & 3;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = (i >> 1) * 16 + (lane >> 1), z = (r >> 1) & 3;
-                            uint8_t* row = gbuf + (i & 1) * 2048 + r * 64;
+                        for (int i = 0; i < 2; ++i) {
+                            uint8_t* row = gbuf + i * 1024 + r * 64;
                             uint4 lo, hi;
                             ckpt_decode16<O>(in[i], sc[i], lo, hi);
                             *reinterpret_cast<uint4*>(row + (((2 * group) ^ z) << 4)) = lo;
@@ -877,28 +916,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < 4; ++i) {
                             const int r = (i >> 1) * 8 + (lane >> 2);
-                            *reinterpret_cast<uint4*>(gbuf + (i & 1) * 2048 + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4)) = in[i];
+                            *reinterpret_cast<uint4*>(gbuf + (i & 1) * 1024 + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4)) = in[i];
                         }
                     }
                     if (c + 32 < t.rows) fetch(c + 32);
                     __syncwarp();
-                    wait_columns(now);
+                    ptx::tmem_wait_ld_regs(next);
+                    uint32_t v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = next[i];
                     if (c + 32 < t.rows)
                         load_fragments(acc + c + 32, next);
                     else
                         release();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // 8 rows
+                    for (int i = 0; i < 2; ++i) {  // 8 rows
                         uint32_t g[4], up[4], h[4];
                         load_transposed(frag + i * 512, g[0], g[1], g[2], g[3]);
-                        load_transposed(frag + 2048 + i * 512, up[0], up[1], up[2], up[3]);
+                        load_transposed(frag + 1024 + i * 512, up[0], up[1], up[2], up[3]);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {  // outputs 8 q .. 8 q + 7; two rows each
                             const float2 gv = unpack2<O>(g[q]), uv = unpack2<O>(up[q]);
-                            const int at = (q >> 1) * 16 + 4 * i + (q & 1) * 2;
-                            const float d0 = __uint_as_float(now[at]), d1 = __uint_as_float(now[at + 1]);
+                            const int at = (q >> 1) * 8 + 4 * i + (q & 1) * 2;
+                            const float d0 = __uint_as_float(v[at]), d1 = __uint_as_float(v[at + 1]);
                             float a0, a1, s0, s1;
                             if (gated.act == MOE_ACT_SILU) {
                                 act_and_slope<false>(gv.x, a0, s0);
@@ -914,28 +956,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                         }
                         __syncwarp();
                         store_transposed(frag + i * 512, g[0], g[1], g[2], g[3]);
-                        store_transposed(frag + 2048 + i * 512, up[0], up[1], up[2], up[3]);
-                        store_transposed(frag + 4096 + i * 512, h[0], h[1], h[2], h[3]);
+                        store_transposed(frag + 1024 + i * 512, up[0], up[1], up[2], up[3]);
+                        store_transposed(frag + 2048 + i * 512, h[0], h[1], h[2], h[3]);
                     }
                     __syncwarp();
                     O* grads = static_cast<O*>(gated.pre_out);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const int r = i * 8 + (lane >> 2);
                         const uint8_t* row = gbuf + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4);
                         const int64_t at = (int64_t)t.lo + c + r;
                         if (j < P && c + r < t.rows) {
                             *reinterpret_cast<uint4*>(grads + at * P2 + j) = *reinterpret_cast<const uint4*>(row);
-                            *reinterpret_cast<uint4*>(grads + at * P2 + P + j) = *reinterpret_cast<const uint4*>(row + 2048);
-                            if (out) *reinterpret_cast<uint4*>(out + at * P + j) = *reinterpret_cast<const uint4*>(row + 4096);
+                            *reinterpret_cast<uint4*>(grads + at * P2 + P + j) = *reinterpret_cast<const uint4*>(row + 1024);
+                            if (out) *reinterpret_cast<uint4*>(out + at * P + j) = *reinterpret_cast<const uint4*>(row + 2048);
                         }
                     }
-                };
-                if (t.rows > 0) fetch(0);
-                load_fragments(acc, u);
-                for (int c = 0; c < t.rows; c += 64) {
-                    step_rows(u, v, c);
-                    if (c + 32 < t.rows) step_rows(v, u, c + 32);
                 }
                 __syncwarp();
             } else if constexpr (sizeof(O) == 4) {
