@@ -720,6 +720,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
             const Tile t = tile_at<MODE>(tile, groups, El, sh);
             const int m = t.m0 + (int)rank * (tile_outputs<MODE>() / 2) + quarter * (tile_outputs<MODE>() / 8);  // this warp's first output
+            if constexpr (MODE == kGatedBwd) {
+                // ask for what this warp will read of gate and up while the tile's product is under way
+                const bool eight = gated.keep == MOE_KEEP_E4M3;
+                const uint8_t* p = static_cast<const uint8_t*>(gated.pre_in);
+                const int64_t P2 = 2 * (int64_t)P;
+                const int r = lane >> 1, z = eight ? 1 : 2;
+                if (m < P)
+                    for (int c = warp > 3 ? 16 : 0; c + r < t.rows; c += 32) {
+                        const int64_t at = (t.lo + (int64_t)c + r) * P2 + (lane & 1) * (int64_t)P + m;
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + at * z) : "memory");
+                        if (eight) asm volatile("prefetch.global.L2 [%0];" ::"l"(gated.scale + at / kCkptGroup) : "memory");
+                    }
+            }
             if (t.steps > 0) {
                 bool ok = wait_phase(ptx::smem_addr(&st->tfull[b]), tph, abort);
                 ok = __all_sync(0xffffffffu, ok);
