@@ -606,11 +606,12 @@ def _one_device(*tensors):
     dev = None
     for t in tensors:
         if t is not None:
-            if dev is not None and t.device != dev:
-                raise ValueError(f"tensors on two devices, {dev} and {t.device}")
-            dev = t.device
-    if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, which is not the current device")
+            at = t.get_device()  # -1: host
+            if dev is not None and at != dev:
+                raise ValueError(f"tensors on two devices, {dev} and {at} (-1: the host)")
+            dev = at
+    if dev is not None and dev >= 0 and dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on device {dev}, which is not the current one")
 
 
 def _half(t, name):

@@ -48,57 +48,79 @@ __global__ void __launch_bounds__(kThreads) unpack_groups_kernel(const uint8_t* 
                                                                  int64_t groups, T* __restrict__ x) {
     pdl_wait();
     pdl_trigger();
-    const int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (g >= groups) return;
-    const uint4 c = reinterpret_cast<const uint4*>(codes)[g];
-    const uint32_t byte = scales[g];
-    uint4* o = reinterpret_cast<uint4*>(x + g * kCkptGroup);
     if constexpr (sizeof(T) == 2) {
+        const int64_t g = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+        if (g >= groups) return;
         uint4 lo, hi;
-        ckpt_decode16<T>(c, byte, lo, hi);
+        ckpt_decode16<T>(reinterpret_cast<const uint4*>(codes)[g], scales[g], lo, hi);
+        uint4* o = reinterpret_cast<uint4*>(x) + 2 * g;
         o[0] = lo;
         o[1] = hi;
     } else {
-        const float scale = ckpt_scale(byte);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        // four values at a time, so that a warp writes 512 bytes in a row (65536 x 2048: 64 bytes a thread 130 us)
+        const int64_t q0 = (int64_t)blockIdx.x * (4 * kThreads) + threadIdx.x;
+        uint32_t c[4], byte[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t q = q0 + i * kThreads;
+            const bool live = q < 4 * groups;
+            c[i] = live ? reinterpret_cast<const uint32_t*>(codes)[q] : 0;
+            byte[i] = live ? scales[q >> 2] : 0;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float v[4];
-            ckpt_decode4<T>(w[i], scale, v);
-            o[i] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            ckpt_decode4<T>(c[i], ckpt_scale(byte[i]), v);
+            const int64_t q = q0 + i * kThreads;
+            if (q < 4 * groups) reinterpret_cast<float4*>(x)[q] = make_float4(v[0], v[1], v[2], v[3]);
         }
     }
 }
 
-// `bytes` bytes between global and shared memory by all threads of the block, 16 at a time but for the
-// ends. Both addresses have the same offset from a 16-byte boundary; a value's size divides them.
-template <int kSize>
-__device__ __forceinline__ void move_flat(uint8_t* to, const uint8_t* from, int bytes) {
+// `bytes` bytes from global to shared memory or back by all threads of the block, 16 at a time but for the
+// ends. Shared memory holds them at the address's offset from a 16-byte boundary; kSize, a value's size,
+// divides them. At most 16 * kTurns bytes a thread.
+template <int kSize, bool kIn, int kTurns>
+__device__ __forceinline__ void move_flat(uint4 (&mem)[kTurns * kThreads + kTurns + 1], uint8_t* global, int bytes) {
     using U = std::conditional_t<kSize == 4, uint32_t, std::conditional_t<kSize == 2, uint16_t, uint8_t>>;
-    const int head = min((int)(-reinterpret_cast<uintptr_t>(from) & 15), bytes), whole = (bytes - head) & ~15, tail = head + whole;
-    for (int i = threadIdx.x * 16; i < whole; i += kThreads * 16)
-        *reinterpret_cast<uint4*>(to + head + i) = *reinterpret_cast<const uint4*>(from + head + i);
-    const int i = threadIdx.x * kSize;
-    if (i < head) *reinterpret_cast<U*>(to + i) = *reinterpret_cast<const U*>(from + i);
-    if (tail + i < bytes) *reinterpret_cast<U*>(to + tail + i) = *reinterpret_cast<const U*>(from + tail + i);
+    const int skew = (int)(reinterpret_cast<uintptr_t>(global) & 15), end = skew + bytes;
+    uint4* g = reinterpret_cast<uint4*>(global - skew);
+    // whole vectors [lo, hi)
+    const int lo = skew ? 1 : 0, hi = end >> 4;
+#pragma unroll
+    for (int k = 0; k < kTurns + 1; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        if (i >= lo && i < hi) kIn ? mem[i] = g[i] : g[i] = mem[i];
+    }
+    // the ends: the first threads have the values before lo and from hi on
+    U* m = reinterpret_cast<U*>(mem);
+    U* v = reinterpret_cast<U*>(g);
+    constexpr int kPer = 16 / kSize;
+    if (threadIdx.x < 2 * kPer) {
+        const int vec = threadIdx.x < kPer ? 0 : hi, i = vec * kPer + (threadIdx.x & (kPer - 1));
+        // a first vector that is no whole one, and the last one's part (once, where both are the same)
+        if ((threadIdx.x < kPer ? lo == 1 : hi >= lo) && i * kSize >= skew && i * kSize < end) kIn ? m[i] = v[i] : v[i] = m[i];
+    }
 }
 
 // Any width and alignment. A block has kThreads groups one after the other, whose values are contiguous in
 // memory whatever the rows' length: they go through shared memory, so that global memory is moved 16 bytes
-// at a time, and a thread has one group there. Lane l takes its values from the (l / 2)-th on, which spreads
-// the lanes over the banks for values of 1, 2 and 4 bytes alike. `per_row`: groups of a row.
+// at a time, and a thread has one group there, which starts anywhere. It takes the group's quads, and the
+// values of a quad, in an order that goes by its lane, so that the lanes' values lie in different banks.
+// `per_row`: groups of a row.
 template <typename T, bool kPack>
 __global__ void __launch_bounds__(kThreads) rows_kernel(T* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                                                        int64_t groups, int K, int per_row) {
-    __shared__ __align__(16) uint8_t x_mem[kThreads * kCkptGroup * sizeof(T) + 16];
-    __shared__ __align__(16) uint8_t c_mem[kThreads * kCkptGroup + 16];
+                                                        int64_t groups, int K, Divisor per_row) {
+    // one vector for the offset from a boundary; a short last group is looked at as a whole one
+    __shared__ uint4 x_mem[sizeof(T) * kThreads + sizeof(T) + 1], c_mem[kThreads + 2];
+    static_assert(kCkptGroup == sizeof(uint4), "a thread's codes are one vector");
     pdl_wait();
     pdl_trigger();
-    const int64_t g0 = (int64_t)blockIdx.x * kThreads, row0 = g0 / per_row;
-    const int first = (int)(g0 - row0 * per_row), n = (int)min((int64_t)kThreads, groups - g0);
+    const int64_t g0 = (int64_t)blockIdx.x * kThreads, row0 = groups <= INT32_MAX ? per_row.of((int)g0) : g0 / per_row.d;
+    const int first = (int)(g0 - row0 * per_row.d), n = (int)min((int64_t)kThreads, groups - g0);
     // the i-th group's first value from the first group's, and its length
     auto start = [&](int i, int& length) {
-        const int row = (first + i) / per_row, col = (first + i - row * per_row) * kCkptGroup;
+        const int row = per_row.of(first + i), col = (first + i - row * per_row.d) * kCkptGroup;
         length = min(kCkptGroup, K - col);
         return row * K + col - first * kCkptGroup;
     };
@@ -107,66 +129,133 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(T* __restrict__ x, uint8
     const int64_t at = row0 * K + (int64_t)first * kCkptGroup;
     uint8_t* xg = reinterpret_cast<uint8_t*>(x + at);
     uint8_t* cg = codes + at;
-    uint8_t* xr = x_mem + (reinterpret_cast<uintptr_t>(xg) & 15);
-    uint8_t* cs = c_mem + (reinterpret_cast<uintptr_t>(cg) & 15);
-    T* xs = reinterpret_cast<T*>(xr);
-    if (kPack)
-        move_flat<sizeof(T)>(xr, xg, values * (int)sizeof(T));
-    else
-        move_flat<1>(cs, cg, values);
+    const int i = threadIdx.x, lane = threadIdx.x & 31;
+    uint32_t byte = 0;
+    if (kPack) {
+        move_flat<sizeof(T), true, sizeof(T)>(x_mem, xg, values * (int)sizeof(T));
+    } else {
+        if (i < n) byte = scales[g0 + i];
+        move_flat<1, true, 1>(c_mem, cg, values);
+    }
     __syncthreads();
-    const int i = threadIdx.x;
-    if (i < n) {
-        const int s = start(i, length), turn = (threadIdx.x & 31) >> 1;
-        if (kPack) {
-            float v[kCkptGroup];
-            uint32_t amax = 0;
+    {
+        const int s = start(i, length);
+        if (i >= n) length = 0;
+        // indices, and not pointers, so that every access is one of shared memory
+        T* xm = reinterpret_cast<T*>(x_mem);
+        uint8_t* cm = reinterpret_cast<uint8_t*>(c_mem);
+        const int xs = (int)(reinterpret_cast<uintptr_t>(xg) & 15) / (int)sizeof(T) + s;
+        const int cs = (int)(reinterpret_cast<uintptr_t>(cg) & 15) + s;
+        // fp32: groups are 16 words apart, so lanes 0, 2, 4, 6 take different quads, lanes 8 apart other values of
+        // a quad; 16 bits, 8 words apart: lanes 0, 4, 8, 12 and lanes 16 apart take different quads. The codes'
+        // groups are 4 words apart: lanes 8 apart take different quads
+        const int quad = sizeof(T) == 4 ? (lane >> 1) + (lane >> 3) : (lane >> 2) + (lane >> 4);
+        const int turn = sizeof(T) == 4 ? lane >> 3 : 0;
+        const int in_quad[4] = {turn, (turn + 1) & 3, (turn + 2) & 3, (turn + 3) & 3};
+        // whole: no lane of the warp has a short group, so that nothing is compared with its length
+        auto group = [&](auto whole) {
+            auto in = [&](int e) { return decltype(whole)::value || e < length; };
+            if (kPack) {
+                uint32_t amax = 0;
+                float v[kCkptGroup];
+                if constexpr (sizeof(T) == 2) {
+                    // words, and the next one where the group starts in the middle of one, in order; the
+                    // values' bits are compared two at a time
+                    const uint32_t* words = reinterpret_cast<const uint32_t*>(x_mem);
+                    const uint32_t shift = 16 * (uint32_t)(xs & 1);
 #pragma unroll
-            for (int j = 0; j < kCkptGroup; ++j) {
-                const int e = (j + turn) & (kCkptGroup - 1);
-                v[j] = e < length ? to_f32(xs[s + e]) : 0.f;
-                amax = max(amax, abs_bits(v[j]));
-            }
-            const uint32_t byte = ckpt_byte(amax);
-            const float inv = ckpt_inverse(byte);
+                    for (int q = 0; q < 4; ++q) {
+                        const int base = ((quad + q) & 3) * 4;
+                        const uint32_t* w = words + ((xs + base) >> 1);
+                        const uint32_t w0 = w[0], w1 = w[1], w2 = w[2];
 #pragma unroll
-            for (int j = 0; j < kCkptGroup; j += 2) {
-                const uint32_t two = f32x2_to_e4m3x2(v[j] * inv, v[j + 1] * inv);
-                const int e = (j + turn) & (kCkptGroup - 1), f = (j + 1 + turn) & (kCkptGroup - 1);
-                if (e < length) cs[s + e] = (uint8_t)two;
-                if (f < length) cs[s + f] = (uint8_t)(two >> 8);
-            }
-            scales[g0 + i] = (uint8_t)byte;
-        } else {
-            const float scale = ckpt_scale(scales[g0 + i]);
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t two = __funnelshift_r(j ? w1 : w0, j ? w2 : w1, shift);
+                            if (!in(base + 2 * j)) two = 0;
+                            if (!in(base + 2 * j + 1)) two &= 0xffff;
+                            amax = __vmaxu2(amax, two & 0x7fff7fffu);
+                            const float2 f = unpack2<T>(two);
+                            v[4 * q + 2 * j] = f.x;
+                            v[4 * q + 2 * j + 1] = f.y;
+                        }
+                    }
+                    amax = max(amax >> 16, amax & 0xffff);
+                    amax = abs_bits(unpack2<T>(amax).x);
+                } else {
 #pragma unroll
-            for (int j = 0; j < kCkptGroup; j += 4) {
-                uint32_t four = 0;
+                    for (int q = 0; q < 4; ++q) {
+                        const int base = ((quad + q) & 3) * 4;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float u = to_f32(xm[xs + base + in_quad[j]]);
+                            v[4 * q + j] = in(base + in_quad[j]) ? u : 0.f;
+                            amax = max(amax, abs_bits(v[4 * q + j]));
+                        }
+                    }
+                }
+                byte = ckpt_byte(amax);
+                const float inv = ckpt_inverse(byte);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int e = (j + q + turn) & (kCkptGroup - 1);
-                    if (e < length) four |= (uint32_t)cs[s + e] << 8 * q;
+                    const int base = ((quad + q) & 3) * 4;
+                    uint32_t c = ckpt_encode4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3], inv);
+                    if (sizeof(T) == 4) c = __funnelshift_l(c, c, 8 * turn);  // back in order
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (in(base + j)) cm[cs + base + j] = (uint8_t)(c >> 8 * j);
                 }
-                float v[4];
-                ckpt_decode4<T>(four, scale, v);
+            } else {
+                const float scale = ckpt_scale(byte);
+                const uint32_t* words = reinterpret_cast<const uint32_t*>(c_mem);
+                const uint32_t shift = 8 * (uint32_t)(cs & 3);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int e = (j + q + turn) & (kCkptGroup - 1);
-                    if (e < length) xs[s + e] = from_f32<T>(v[q]);
+                    const int at_quad = (quad + q) & 3, base = at_quad * 4;
+                    uint32_t c = __funnelshift_r(words[(cs >> 2) + at_quad], words[(cs >> 2) + at_quad + 1], shift);
+                    if (sizeof(T) == 4) c = __funnelshift_r(c, c, 8 * turn);
+                    float v[4];
+                    ckpt_decode4<T>(c, scale, v);
+                    bool stored = false;
+                    if constexpr (sizeof(T) == 2) if (decltype(whole)::value) {
+                        // two words, or half a word, a word and half a word
+                        stored = true;
+                        const uint32_t lo = pack2_f32<T>(v[0], v[1]), hi = pack2_f32<T>(v[2], v[3]);
+                        const int to = xs + base;
+                        uint16_t* halves = reinterpret_cast<uint16_t*>(x_mem);
+                        uint32_t* pairs = reinterpret_cast<uint32_t*>(x_mem) + (to >> 1);
+                        if (to & 1) {
+                            halves[to] = (uint16_t)lo;
+                            pairs[1] = __funnelshift_r(lo, hi, 16);
+                            halves[to + 3] = (uint16_t)(hi >> 16);
+                        } else {
+                            pairs[0] = lo;
+                            pairs[1] = hi;
+                        }
+                    }
+                    if (!stored) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (in(base + in_quad[j])) xm[xs + base + in_quad[j]] = from_f32<T>(v[j]);
+                    }
                 }
             }
-        }
+        };
+        if (__all_sync(0xffffffffu, length == kCkptGroup))
+            group(std::true_type());
+        else
+            group(std::false_type());
+        if (kPack && i < n) scales[g0 + i] = (uint8_t)byte;
     }
     __syncthreads();
     if (kPack)
-        move_flat<1>(cg, cs, values);
+        move_flat<1, false, 1>(c_mem, cg, values);
     else
-        move_flat<sizeof(T)>(xg, xr, values * (int)sizeof(T));
+        move_flat<sizeof(T), false, sizeof(T)>(x_mem, xg, values * (int)sizeof(T));
 }
 
 // Sizes of both directions; the groups' number.
 bool sizes_ok(int64_t M, int K, int dtype, int64_t& groups) {
-    if (M < 0 || K < 1 || K > 1 << 30 || !dtype_bytes(dtype) || M > ((int64_t)1 << 46) / K) return false;
+    if (M < 0 || K < 1 || K > 1 << 30 || !dtype_bytes(dtype) || M > ((int64_t)1 << 40) / K) return false;  // grids
     groups = M * ((K + kCkptGroup - 1) / kCkptGroup);
     return groups <= (int64_t)INT32_MAX * kThreads;  // one grid
 }
@@ -194,8 +283,9 @@ MOE_API int moe_checkpoint_pack(const void* x, int64_t M, int K, int dtype, uint
         if (K % kCkptGroup == 0 && !misaligned(x, 16) && !misaligned(codes, 16)) {
             launch_k(pack_groups_kernel<T>, (unsigned)((groups + kThreads - 1) / kThreads), kThreads, 0, s, in, groups, codes, scales);
         } else {
+            const int per_row = (K + kCkptGroup - 1) / kCkptGroup;
             launch_k(rows_kernel<T, true>, (unsigned)((groups + kThreads - 1) / kThreads), kThreads, 0, s, const_cast<T*>(in), codes, scales,
-                     groups, K, (K + kCkptGroup - 1) / kCkptGroup);
+                     groups, K, Divisor{per_row, magic_of(per_row)});
         }
         note_launches(1);
         return launch_status();
@@ -218,8 +308,9 @@ MOE_API int moe_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, i
         if (K % kCkptGroup == 0 && !misaligned(x, 16) && !misaligned(codes, 16)) {
             launch_k(unpack_groups_kernel<T>, (unsigned)((groups + kThreads - 1) / kThreads), kThreads, 0, s, codes, scales, groups, out);
         } else {
+            const int per_row = (K + kCkptGroup - 1) / kCkptGroup;
             launch_k(rows_kernel<T, false>, (unsigned)((groups + kThreads - 1) / kThreads), kThreads, 0, s, out, const_cast<uint8_t*>(codes),
-                     const_cast<uint8_t*>(scales), groups, K, (K + kCkptGroup - 1) / kCkptGroup);
+                     const_cast<uint8_t*>(scales), groups, K, Divisor{per_row, magic_of(per_row)});
         }
         note_launches(1);
         return launch_status();

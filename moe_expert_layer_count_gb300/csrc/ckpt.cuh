@@ -50,8 +50,9 @@ __device__ __forceinline__ float largest<fp16>() { return 65504.f; }
 // The value of a code under its scale, within T's range (NaN stays NaN). Exact in T but where it is subnormal.
 template <typename T>
 __device__ __forceinline__ float ckpt_value(float code, float scale) {
-    const float v = code * scale, top = largest<T>();
-    return v > top ? top : v < -top ? -top : v;
+    float v;  // the smaller magnitude with the first one's sign
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(v) : "f"(code * scale), "f"(largest<T>()));
+    return v;
 }
 template <typename T>
 __device__ __forceinline__ void ckpt_decode4(uint32_t codes, float scale, float (&v)[4]) {
@@ -79,9 +80,9 @@ __device__ __forceinline__ uint4 ckpt_encode16(const uint4& lo, const uint4& hi,
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         v[i] = unpack2<T>(w[i]);
-        amax = max(amax, max(abs_bits(v[i].x), abs_bits(v[i].y)));
+        amax = __vmaxu2(amax, w[i] & 0x7fff7fffu);  // magnitudes of one type order as their bits
     }
-    byte = ckpt_byte(amax);
+    byte = ckpt_byte(abs_bits(unpack2<T>(max(amax >> 16, amax & 0xffff)).x));
     const float inv = ckpt_inverse(byte);
     uint32_t c[4];
 #pragma unroll
@@ -100,12 +101,7 @@ __device__ __forceinline__ void ckpt_decode16(const uint4& codes, uint32_t byte,
         float v[4];
         ckpt_decode4<T>(c[i], scale, v);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            Vec<T, 2> p;
-            p.v[0] = from_f32<T>(v[2 * j]);
-            p.v[1] = from_f32<T>(v[2 * j + 1]);
-            w[2 * i + j] = *reinterpret_cast<uint32_t*>(&p);
-        }
+        for (int j = 0; j < 2; ++j) w[2 * i + j] = pack2_f32<T>(v[2 * j], v[2 * j + 1]);
     }
     lo = make_uint4(w[0], w[1], w[2], w[3]);
     hi = make_uint4(w[4], w[5], w[6], w[7]);

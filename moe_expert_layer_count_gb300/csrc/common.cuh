@@ -78,6 +78,19 @@ __device__ __forceinline__ int local_expert(TId id, const int32_t* __restrict__ 
     return (l >= 0 && l < El) ? l : -1;
 }
 
+// i / d for 0 <= i < 2^31 by a multiplication; magic_of(d) = floor(2^32 / d) + 1 overshoots by
+// less than one.
+inline uint32_t magic_of(int64_t d) { return d == 1 ? 0 : (uint32_t)((1ull << 32) / (uint64_t)d + 1); }
+struct Divisor {
+    int d;
+    uint32_t magic;
+    __device__ __forceinline__ int of(int i) const {
+        if (d == 1) return i;
+        const int q = (int)__umulhi((uint32_t)i, magic);
+        return q * (int64_t)d > i ? q - 1 : q;
+    }
+};
+
 __device__ __forceinline__ unsigned lanemask_lt() {
     unsigned m;
     asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));

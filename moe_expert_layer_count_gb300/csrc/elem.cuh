@@ -27,6 +27,20 @@ __device__ __forceinline__ bf16 from_f32<bf16>(float v) { return __float2bfloat1
 template <>
 __device__ __forceinline__ fp16 from_f32<fp16>(float v) { return __float2half_rn(v); }
 
+// Two values rounded to T in one conversion, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2_f32(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2_f32<bf16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2_f32<fp16>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // V consecutive values of T, moved with one load or store where V * sizeof(T) is 16.
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Vec {

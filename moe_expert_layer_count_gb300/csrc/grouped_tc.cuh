@@ -273,10 +273,7 @@ __device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t& a, uint
 // Two fp32 rounded to O, the first in the low half.
 template <typename O>
 __device__ __forceinline__ uint32_t pack2(uint32_t lo, uint32_t hi) {
-    Vec<O, 2> v;
-    v.v[0] = from_f32<O>(__uint_as_float(lo));
-    v.v[1] = from_f32<O>(__uint_as_float(hi));
-    return *reinterpret_cast<uint32_t*>(&v);
+    return pack2_f32<O>(__uint_as_float(lo), __uint_as_float(hi));
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -373,18 +370,6 @@ __device__ __forceinline__ int bucket_of(int rows) {
     return kBuckets - 1 - ((int)(__float_as_uint((float)rows + 1.f) >> 21) - 508);
 }
 
-// i / d for 0 <= i < 2^31 by a multiplication; magic_of(d) = floor(2^32 / d) + 1 overshoots by
-// less than one.
-uint32_t magic_of(int64_t d) { return d == 1 ? 0 : (uint32_t)((1ull << 32) / (uint64_t)d + 1); }
-struct Divisor {
-    int d;
-    uint32_t magic;
-    __device__ __forceinline__ int of(int i) const {
-        if (d == 1) return i;
-        const int q = (int)__umulhi((uint32_t)i, magic);
-        return q * (int64_t)d > i ? q - 1 : q;
-    }
-};
 struct Shape {
     Divisor m_tiles;      // tiles along the M side
     Divisor group_tiles;  // wgrad: tiles of a group, all its parts'

@@ -147,7 +147,7 @@ def test_tensors_on_two_devices_are_refused(L, monkeypatch):  # noqa: F811
     import types
 
     import moe_expert_layer_count_gb300 as moe
-    fake = lambda i: types.SimpleNamespace(device=torch.device("cuda", i))  # noqa: E731
+    fake = lambda i: types.SimpleNamespace(get_device=lambda: i)  # noqa: E731
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     moe._one_device(fake(0), None, fake(0))
     with pytest.raises(ValueError):
