@@ -27,6 +27,7 @@
 #include <atomic>
 #include <climits>
 #include <mutex>
+#include <type_traits>
 
 #include "ckpt.cuh"
 #include "elem.cuh"
@@ -53,7 +54,10 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kTailWarp = 6;
 constexpr int kBoxBytes = 4096;    // wgrad output box: 32 rows x 128 bytes
-constexpr int kGatedBytes = 3072;  // kGated, kGatedBwd: a warp's 16 rows x 64 bytes of gate and up (kGatedBwd: each) and of h
+// a warp's 16 rows of the gated forms: 64 bytes of gate and up (kGatedBwd: of each) and h of 32 (kGatedBwd: 64)
+template <int MODE>
+__host__ __device__ constexpr int gated_bytes() { return MODE == kGatedBwd ? 3072 : 1536; }
+constexpr int kScaleBytes = 256 * 8;  // kGated: a tile's scale bytes, 4 of gate and 4 of up a row
 constexpr int kBoxes = 2;          // boxes of a warp in turn (four would cost two stages: 302 against 289 us)
 // The gated forms' epilogues have two warps for each quarter of the accumulator's lanes.
 template <int MODE>
@@ -61,7 +65,8 @@ __host__ __device__ constexpr int epi_warps() { return MODE == kGated || MODE ==
 // forward and dgrad stage two 32-row x 64-byte buffers per warp
 template <int MODE>
 __host__ __device__ constexpr int staging_bytes() {
-    return epi_warps<MODE>() * (MODE == kGated || MODE == kGatedBwd ? kGatedBytes : kBoxBytes * (MODE == kWgrad ? kBoxes : 1));
+    if (MODE == kGated) return epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 2 * 8;  // and two barriers
+    return epi_warps<MODE>() * (MODE == kGatedBwd ? gated_bytes<MODE>() : kBoxBytes * (MODE == kWgrad ? kBoxes : 1));
 }
 // results along the M side of a tile: kGated's rows are half gate and half up
 template <int MODE>
@@ -89,6 +94,7 @@ struct Gated {
     const void* pre_in;  // kGatedBwd: gate and up as they were kept, [R, 2 P] (16 bits or codes)
     void* pre_out;       // kGated: gate and up to keep, or null; kGatedBwd: their gradients (16 bits)
     uint8_t* scale;      // the codes' scale bytes [R, 2 P / 16]: written by kGated, read by kGatedBwd
+    int wide_scales;     // kGated: P is a multiple of 64 and `scale` of 4, so that four outputs groups' bytes are a word
 };
 
 struct __align__(8) Tail {
@@ -331,28 +337,33 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // then. Exponential and reciprocal are the approximate ones, which flush what is subnormal: a few fp32
 // ulp where the result is rounded to 16 bits (the forms that keep subnormals cost another seven
 // instructions a value).
+// Two values at once: products and sums in packed instructions.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 template <bool kGelu>
-__device__ __forceinline__ float act_gate(float g) {
-    float q = -kLog2e * g;
+__device__ __forceinline__ float2 act_gate(float2 g) {
+    float2 q;
     if (kGelu) {
-        const float c = fminf(fmaxf(g, -32.f), 32.f);
-        q = c * fmaf(-kLog2e * kGeluA * kGeluB, c * c, -kLog2e * kGeluA);
+        const float2 c = make_float2(fminf(fmaxf(g.x, -32.f), 32.f), fminf(fmaxf(g.y, -32.f), 32.f));
+        q = __fmul2_rn(c, __ffma2_rn(both(-kLog2e * kGeluA * kGeluB), __fmul2_rn(c, c), both(-kLog2e * kGeluA)));
+    } else {
+        q = __fmul2_rn(both(-kLog2e), g);
     }
-    return rcp_approx(1.f + ex2_approx(q));
+    const float2 d = __fadd2_rn(both(1.f), make_float2(ex2_approx(q.x), ex2_approx(q.y)));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 template <bool kGelu>
-__device__ __forceinline__ float act_of(float g) { return g * act_gate<kGelu>(g); }
+__device__ __forceinline__ float2 act_of(float2 g) { return __fmul2_rn(g, act_gate<kGelu>(g)); }
 // a(g) and its derivative s + g q' s (1 - s), q' = 1 or 2 sqrt(2 / pi) (1 + 3 * 0.044715 g^2).
 template <bool kGelu>
-__device__ __forceinline__ void act_and_slope(float g, float& a, float& slope) {
-    const float s = act_gate<kGelu>(g);
-    a = g * s;
-    float gq = g;
+__device__ __forceinline__ void act_and_slope(float2 g, float2& a, float2& slope) {
+    const float2 s = act_gate<kGelu>(g);
+    a = __fmul2_rn(g, s);
+    float2 gq = g;
     if (kGelu) {
-        const float c = fminf(fmaxf(g, -32.f), 32.f);
-        gq = c * fmaf(3.f * kGeluA * kGeluB, c * c, kGeluA);
+        const float2 c = make_float2(fminf(fmaxf(g.x, -32.f), 32.f), fminf(fmaxf(g.y, -32.f), 32.f));
+        gq = __fmul2_rn(c, __ffma2_rn(both(3.f * kGeluA * kGeluB), __fmul2_rn(c, c), both(kGeluA)));
     }
-    slope = fmaf(fmaf(-s, s, s), gq, s);
+    slope = __ffma2_rn(__ffma2_rn(make_float2(-s.x, -s.y), s, s), gq, s);
 }
 
 // ------------------------------------------------------------------ tiles
@@ -470,6 +481,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             ptx::mbar_init(ptx::smem_addr(&st->tempty[b]), 2 * epi_warps<MODE>());
         }
         ptx::mbar_init(ptx::smem_addr(&st->mma_done), 1);
+        if (MODE == kGated)
+            for (int half = 0; half < 2; ++half)
+                ptx::mbar_init(ptx::smem_addr(staging + epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 8 * half), 4);
         st->abort = 0;
         ptx::fence_mbar_init();
     }
@@ -699,20 +713,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
     } else {
         // ---------------------------------------------------------------- epilogue
         int b = 0, boxes = 0;
-        uint32_t tph = 0;
+        uint32_t tph = 0, turns = 0;
         const int quarter = warp & 3;  // of the accumulator's lanes: what a warp can read goes by its number
         const uint32_t slab = (uint32_t)(quarter * 32) << 16;
         for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
             const Tile t = tile_at<MODE>(tile, groups, El, sh);
             const int m = t.m0 + (int)rank * (tile_outputs<MODE>() / 2) + quarter * (tile_outputs<MODE>() / 8);  // this warp's first output
+            // kGatedBwd: gate and up as 16-byte pieces of rows, or of 8-bit groups
+            uint4 in[4];     // 16 bits: gate, up by turns, rows 8 i + lane / 4; 8 bits: codes of gate and up, row lane / 2
+            uint32_t sc[2];  // 8 bits: their scales
+            auto fetch = [&](int c) {
+                const int64_t row0 = (int64_t)t.lo + c, P2 = 2 * (int64_t)P;
+                if (gated.keep == MOE_KEEP_E4M3) {
+                    const uint8_t* codes = static_cast<const uint8_t*>(gated.pre_in);
+                    const int r = lane >> 1, j = m + (lane & 1) * 16;
+                    const bool live = j < P && c + r < t.rows;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int64_t at = (row0 + r) * P2 + i * (int64_t)P + j;
+                        in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(codes + at)) : make_uint4(0, 0, 0, 0);
+                        sc[i] = live ? __ldcg(gated.scale + at / kCkptGroup) : 127u;
+                    }
+                } else {
+                    const O* pre = static_cast<const O*>(gated.pre_in);
+                    const int j = m + (lane & 3) * 8;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = (i >> 1) * 8 + (lane >> 2);
+                        const bool live = j < P && c + r < t.rows;
+                        in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(pre + (row0 + r) * P2 + (i & 1) * (int64_t)P + j))
+                                     : make_uint4(0, 0, 0, 0);
+                    }
+                }
+            };
             if constexpr (MODE == kGatedBwd) {
-                // ask for what this warp will read of gate and up while the tile's product is under way
+                // ask for what this warp will read while the tile's product is under way
                 const bool eight = gated.keep == MOE_KEEP_E4M3;
                 const uint8_t* p = static_cast<const uint8_t*>(gated.pre_in);
                 const int64_t P2 = 2 * (int64_t)P;
-                const int r = lane >> 1, z = eight ? 1 : 2;
+                const int r = lane >> 1, z = eight ? 1 : 2, first = warp > 3 ? 16 : 0;
+                if (first < t.rows) fetch(first);
                 if (m < P)
-                    for (int c = warp > 3 ? 16 : 0; c + r < t.rows; c += 32) {
+                    for (int c = first + 32; c + r < t.rows; c += 32) {
                         const int64_t at = (t.lo + (int64_t)c + r) * P2 + (lane & 1) * (int64_t)P + m;
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(p + at * z) : "memory");
                         if (eight) asm volatile("prefetch.global.L2 [%0];" ::"l"(gated.scale + at / kCkptGroup) : "memory");
@@ -782,13 +824,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 // the gate and up of one output. Rounded to 16 bits they are transposed into shared memory, rows
                 // of 64 bytes (16 gates, 16 ups) and of 32 bytes (h), and leave it as 16-byte pieces of rows.
                 const int half = warp > 3, first = half * 16;
-                uint8_t* stage = staging + (half * 4 + quarter) * kGatedBytes;
+                uint8_t* stage = staging + (half * 4 + quarter) * gated_bytes<MODE>();
                 uint8_t* hbuf = stage + 1024;
                 const uint32_t put_pre = ptx::smem_addr(stage) + (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
                 // 8 rows and the next 8: lanes 16-31 address the second ones
                 const uint32_t put_h = ptx::smem_addr(hbuf) + (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * 32 +
                                                                          ((((lane >> 3) & 1) ^ ((lane >> 2) & 1)) << 4));
                 const int64_t P2 = 2 * (int64_t)P;
+                uint8_t* bytes = staging + epi_warps<MODE>() * gated_bytes<MODE>() + (turns & 1) * kScaleBytes;
                 uint32_t next[16];
                 if (first < t.rows)
                     load_fragments(acc + first, next);
@@ -805,16 +848,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                         load_fragments(acc + c + 32, next);
                     else
                         release();
-                    float h[8];
-                    if (gated.act == MOE_ACT_SILU) {
+                    uint32_t h[4];
+                    auto activate = [&](auto gelu) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) h[j] = act_of<false>(__uint_as_float(v[j])) * __uint_as_float(v[8 + j]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) h[j] = act_of<true>(__uint_as_float(v[j])) * __uint_as_float(v[8 + j]);
-                    }
-                    auto hh = [&](int j) { return pack2<O>(__float_as_uint(h[j]), __float_as_uint(h[j + 1])); };
-                    store_transposed(put_h, hh(0), hh(2), hh(4), hh(6));
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 g = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                            const float2 u = make_float2(__uint_as_float(v[8 + 2 * j]), __uint_as_float(v[9 + 2 * j]));
+                            const float2 w = __fmul2_rn(act_of<decltype(gelu)::value>(g), u);
+                            h[j] = pack2_f32<O>(w.x, w.y);
+                        }
+                    };
+                    if (gated.act == MOE_ACT_SILU)
+                        activate(std::false_type());
+                    else
+                        activate(std::true_type());
+                    store_transposed(put_h, h[0], h[1], h[2], h[3]);
                     if (gated.keep != MOE_KEEP_NONE) {
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
@@ -850,55 +898,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                         const uint4 w = ckpt_encode16<O>(lo, hi, byte);
                         if (live && m < P) {
                             *reinterpret_cast<uint4*>(static_cast<uint8_t*>(gated.pre_out) + at) = w;
-                            gated.scale[at / kCkptGroup] = (uint8_t)byte;
                         }
+                        bytes[(c + r) * 8 + side * 4 + quarter] = (uint8_t)byte;
                     }
                 }
                 __syncwarp();
+                if (gated.keep == MOE_KEEP_E4M3) {
+                    // The four quarters' bytes of a row lie side by side: the warps of this half meet, and each
+                    // writes every fourth chunk's, 8 bytes a row (single bytes, each in a sector of its own, cost 14 of
+                    // 285 us at 512 rows a group). The next tile but one uses the same buffer: by then all four
+                    // have been at the next one's meeting, after they had read this one's.
+                    const uint32_t met = ptx::smem_addr(staging + epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 8 * half);
+                    if (lane == 0) ptx::mbar_arrive(met);
+                    if (!__all_sync(0xffffffffu, wait_phase(met, turns & 1, abort))) break;
+                    ++turns;
+                    const int j = t.m0 + (int)rank * 64, n = min((P - j) / kCkptGroup, 4);
+                    for (int c = first + quarter * 32; c < t.rows; c += 128) {
+                        if (gated.wide_scales) {
+                            const int r = lane >> 1, side = lane & 1;
+                            const int64_t at = (((int64_t)t.lo + c + r) * P2 + side * (int64_t)P + j) / kCkptGroup;
+                            if (n == 4 && c + r < t.rows)
+                                *reinterpret_cast<uint32_t*>(gated.scale + at) = *reinterpret_cast<const uint32_t*>(bytes + c * 8 + lane * 4);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = i * 4 + (lane >> 3), side = (lane >> 2) & 1, q = lane & 3;
+                                const int64_t at = (((int64_t)t.lo + c + r) * P2 + side * (int64_t)P + j) / kCkptGroup + q;
+                                if (q < n && c + r < t.rows) gated.scale[at] = bytes[c * 8 + i * 32 + lane];
+                            }
+                        }
+                    }
+                }
             } else if constexpr (MODE == kGatedBwd) {
                 // 16 rows x this warp's 32 outputs at a time, the quarter's two warps by turns: gate and up come
                 // in as 16-byte pieces of rows, one step ahead, are laid into shared memory (64 bytes a row,
                 // swizzled) and read as the accumulator's 8 x 8 fragments; the gradients go back over them and
                 // out, h beside them.
                 const int half = warp > 3, first = half * 16;
-                uint8_t* gbuf = staging + (half * 4 + quarter) * kGatedBytes;
+                uint8_t* gbuf = staging + (half * 4 + quarter) * gated_bytes<MODE>();
                 const uint32_t frag = ptx::smem_addr(gbuf) + (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
                 const int64_t P2 = 2 * (int64_t)P;
                 const bool eight = gated.keep == MOE_KEEP_E4M3;
-                const int piece = lane & 3, j = m + piece * 8;     // 16 bits: rows 8 i + lane / 4
-                const int group = lane & 1, jg = m + group * 16;   // 8 bits: row lane / 2
-                uint4 in[4];     // 16 bits: gate, up by turns; 8 bits: codes of gate and up
-                uint32_t sc[2];  // 8 bits: their scales
-                auto fetch = [&](int c) {
-                    const int64_t row0 = (int64_t)t.lo + c;
-                    if (eight) {
-                        const uint8_t* codes = static_cast<const uint8_t*>(gated.pre_in);
-                        const int r = lane >> 1;
-                        const bool live = jg < P && c + r < t.rows;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int64_t at = (row0 + r) * P2 + i * (int64_t)P + jg;
-                            in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(codes + at)) : make_uint4(0, 0, 0, 0);
-                            sc[i] = live ? __ldcg(gated.scale + at / kCkptGroup) : 127u;
-                        }
-                    } else {
-                        const O* pre = static_cast<const O*>(gated.pre_in);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = (i >> 1) * 8 + (lane >> 2);
-                            const bool live = j < P && c + r < t.rows;
-                            in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(pre + (row0 + r) * P2 + (i & 1) * (int64_t)P + j))
-                                         : make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                };
+                const int piece = lane & 3, j = m + piece * 8, group = lane & 1;
                 uint32_t next[16];
-                if (first < t.rows) {
-                    fetch(first);
+                if (first < t.rows)
                     load_fragments(acc + first, next);
-                } else {
+                else
                     release();
-                }
 #pragma unroll 1
                 for (int c = first; c < t.rows; c += 32) {
                     __syncwarp();
@@ -929,33 +975,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                         load_fragments(acc + c + 32, next);
                     else
                         release();
+                    // all of the step's fragments at once, so that their chains overlap: g[4 i + q]: rows 8 i ..,
+                    // outputs 8 q ..
+                    uint32_t g[8], up[8], h[8];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {  // 8 rows
-                        uint32_t g[4], up[4], h[4];
-                        load_transposed(frag + i * 512, g[0], g[1], g[2], g[3]);
-                        load_transposed(frag + 1024 + i * 512, up[0], up[1], up[2], up[3]);
+                    for (int i = 0; i < 2; ++i) {
+                        load_transposed(frag + i * 512, g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
+                        load_transposed(frag + 1024 + i * 512, up[4 * i], up[4 * i + 1], up[4 * i + 2], up[4 * i + 3]);
+                    }
+                    auto gradients = [&](auto gelu) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {  // outputs 8 q .. 8 q + 7; two rows each
-                            const float2 gv = unpack2<O>(g[q]), uv = unpack2<O>(up[q]);
-                            const int at = (q >> 1) * 8 + 4 * i + (q & 1) * 2;
-                            const float d0 = __uint_as_float(v[at]), d1 = __uint_as_float(v[at + 1]);
-                            float a0, a1, s0, s1;
-                            if (gated.act == MOE_ACT_SILU) {
-                                act_and_slope<false>(gv.x, a0, s0);
-                                act_and_slope<false>(gv.y, a1, s1);
-                            } else {
-                                act_and_slope<true>(gv.x, a0, s0);
-                                act_and_slope<true>(gv.y, a1, s1);
-                            }
-                            auto two = [](float x, float y) { return pack2<O>(__float_as_uint(x), __float_as_uint(y)); };
-                            g[q] = two(d0 * uv.x * s0, d1 * uv.y * s1);
-                            up[q] = two(d0 * a0, d1 * a1);
-                            h[q] = two(a0 * uv.x, a1 * uv.y);
+                        for (int k = 0; k < 8; ++k) {  // two rows each
+                            const float2 uv = unpack2<O>(up[k]);
+                            const int at = ((k >> 1) & 1) * 8 + 4 * (k >> 2) + (k & 1) * 2;
+                            const float2 d = make_float2(__uint_as_float(v[at]), __uint_as_float(v[at + 1]));
+                            float2 a, slope;
+                            act_and_slope<decltype(gelu)::value>(unpack2<O>(g[k]), a, slope);
+                            const float2 dg = __fmul2_rn(__fmul2_rn(d, uv), slope), du = __fmul2_rn(d, a), hv = __fmul2_rn(a, uv);
+                            g[k] = pack2_f32<O>(dg.x, dg.y);
+                            up[k] = pack2_f32<O>(du.x, du.y);
+                            h[k] = pack2_f32<O>(hv.x, hv.y);
                         }
-                        __syncwarp();
-                        store_transposed(frag + i * 512, g[0], g[1], g[2], g[3]);
-                        store_transposed(frag + 1024 + i * 512, up[0], up[1], up[2], up[3]);
-                        store_transposed(frag + 2048 + i * 512, h[0], h[1], h[2], h[3]);
+                    };
+                    if (gated.act == MOE_ACT_SILU)
+                        gradients(std::false_type());
+                    else
+                        gradients(std::true_type());
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        store_transposed(frag + i * 512, g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
+                        store_transposed(frag + 1024 + i * 512, up[4 * i], up[4 * i + 1], up[4 * i + 2], up[4 * i + 3]);
+                        store_transposed(frag + 2048 + i * 512, h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
                     }
                     __syncwarp();
                     O* grads = static_cast<O*>(gated.pre_out);
