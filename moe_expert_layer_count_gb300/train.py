@@ -10,11 +10,18 @@ Nothing of it reads the experts' row counts on the host. The permutation's gradi
 library's own pair again: the gradient of the weighted gather is a scatter of the output's
 gradient that applies the weights, the gradient of the scatter a gather with unit weights.
 The activation between the products and the dot product that gives the gradient of a routing
-weight are plain torch operations. There are no second gradients.
+weight are plain torch operations, unless the block is told what to keep for its backward pass
+(moe_block's `keep`): then the first product and the activation are one kernel, forward and backward
+(moe_grouped_gated), the weighted sum's backward pass is one kernel too
+(moe_gather_weight_reduce_backward), and what the backward pass needs of the experts' part (its rows,
+gate and up, its results) is kept in 16 or in 8 bits. There are no second gradients.
 
-`python -m moe_expert_layer_count_gb300.train` runs a few steps on synthetic data.
+`python -m moe_expert_layer_count_gb300.train` runs a few steps on synthetic data
+(`--keep 16bit` or `--keep 8bit` with the fused kernels).
 """
 from __future__ import annotations
+
+import argparse
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -121,6 +128,72 @@ class _WeightedGather(torch.autograd.Function):
         return drows, None, torch.where(src2dst >= 0, dots, 0.0), None, None
 
 
+class _Kept:
+    """A tensor of rows for the backward pass, as it is or in 8 bits."""
+
+    def __init__(self, rows, keep):
+        self.dtype = rows.dtype
+        self.tensors = moe.moe_checkpoint_pack(rows) if keep == moe.MOE_KEEP_E4M3 else (rows, None)
+
+    @staticmethod
+    def back(values, scales, dtype):
+        return values if scales is None else moe.moe_checkpoint_unpack(values, scales, dtype)
+
+
+class _GatedExperts(torch.autograd.Function):
+    """y[r] = w2[l] (a(g) * u) with (g, u) = w13[l] x[r]. h = a(g) * u is not kept: the backward pass makes it again."""
+
+    @staticmethod
+    def forward(ctx, x, w13, w2, offsets, counts, activation, keep, gaps):
+        h, pre, scale = moe.moe_grouped_gated(x, w13, offsets, counts, activation=activation, keep=keep)
+        kept = _Kept(x, keep)
+        ctx.save_for_backward(*kept.tensors, pre, scale, w13, w2, offsets, counts)
+        ctx.how = (activation, gaps, x.dtype)
+        return moe.moe_grouped_matmul(h, w2, offsets, counts)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        values, scales, pre, scale, w13, w2, offsets, counts = ctx.saved_tensors
+        activation, gaps, dtype = ctx.how
+        need_x, need_w13, need_w2 = ctx.needs_input_grad[:3]
+        dy = dy.contiguous()
+        d_pre, h = moe.moe_grouped_gated_backward(dy, w2, pre, offsets, counts, activation=activation, pre_scale=scale,
+                                                  want_h=need_w2)
+        dw2 = moe.moe_grouped_matmul_wgrad(dy, h, offsets, counts) if need_w2 else None
+        del h
+        dx = dw13 = None
+        if need_w13:
+            dw13 = moe.moe_grouped_matmul_wgrad(d_pre, _Kept.back(values, scales, dtype), offsets, counts)
+        if need_x:
+            # the product does not write the rows of no group
+            out = torch.zeros(values.shape, dtype=dtype, device=dy.device) if gaps else None
+            dx = moe.moe_grouped_matmul_dgrad(d_pre, w13, offsets, counts, out=out)
+        return dx, dw13, dw2, None, None, None, None, None
+
+
+class _WeightedSum(torch.autograd.Function):
+    """_WeightedGather with its backward pass in one kernel, and its rows kept as they are or in 8 bits."""
+
+    @staticmethod
+    def forward(ctx, rows, src2dst, weights, keep, gaps):
+        kept = _Kept(rows, keep)
+        ctx.save_for_backward(*kept.tensors, src2dst, weights)
+        ctx.gaps = gaps
+        return moe.moe_gather_weight_reduce(rows, src2dst, weights)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        values, scales, src2dst, weights = ctx.saved_tensors
+        make = torch.zeros if ctx.gaps else torch.empty
+        drows = make(values.shape, dtype=torch.bfloat16, device=dout.device)
+        drows, dweights = moe.moe_gather_weight_reduce_backward(
+            dout.contiguous(), _Kept.back(values, scales, torch.bfloat16), src2dst, weights, d_y=drows,
+            want_weights=ctx.needs_input_grad[2])
+        return drows, None, dweights, None, None
+
+
 def layer_norm(x, weight, bias=None, eps=1e-5):
     """moe_layer_norm under autograd: y."""
     return _LayerNorm.apply(x, weight, bias, eps)
@@ -138,6 +211,21 @@ def grouped_matmul(x, w, expert_offsets, expert_num_tokens=None, out_dtype=None,
     return _GroupedMatmul.apply(x, w, expert_offsets, expert_num_tokens, out_dtype, gaps)
 
 
+def gated_experts(x, w13, w2, expert_offsets, expert_num_tokens=None, activation=moe.MOE_ACT_SILU, keep=moe.MOE_KEEP_16BIT,
+                  gaps=True):
+    """The experts' feed-forward part under autograd: w2[l] (a(g) * u) with (g, u) = w13[l] x[r] for the rows r of every
+    group l (moe_grouped_gated, moe_grouped_matmul). `keep`: whether x and (g, u) are kept for the backward pass in
+    16 bits (MOE_KEEP_16BIT) or in 8 (MOE_KEEP_E4M3: half the memory; what the gradients are made of is off by up to
+    2^-4). Rows of no group as in grouped_matmul."""
+    return _GatedExperts.apply(x, w13, w2, expert_offsets, expert_num_tokens, activation, keep, gaps)
+
+
+def weighted_sum(rows, src2dst, weights, keep=moe.MOE_KEEP_16BIT, gaps=True):
+    """moe_gather_weight_reduce under autograd: out[t] = sum over k of weights[t, k] * rows[src2dst[t, k]]. `keep`: how the
+    rows are kept for the weights' gradient. The gradient of rows of no slot is 0, or undefined with gaps=False."""
+    return _WeightedSum.apply(rows, src2dst, weights, keep, gaps)
+
+
 def init_block(K: int, N: int, E: int, device="cuda", seed: int = 0):
     """Parameters of a block: hidden size K and intermediate size N (multiples of 128), E experts
     (a multiple of 8: the gate is one of the 16-bit products)."""
@@ -149,8 +237,10 @@ def init_block(K: int, N: int, E: int, device="cuda", seed: int = 0):
             "gate": normal(1, E, K), "w13": normal(E, 2 * N, K), "w2": normal(E, K, N)}
 
 
-def moe_block(p, x, topk: int, scoring=moe.MOE_SCORE_SOFTMAX, renormalize=True, eps=1e-5):
-    """x + MoE(layer_norm(x)) for x bf16 [M, K] and the parameters of init_block."""
+def moe_block(p, x, topk: int, scoring=moe.MOE_SCORE_SOFTMAX, renormalize=True, eps=1e-5, keep=None):
+    """x + MoE(layer_norm(x)) for x bf16 [M, K] and the parameters of init_block. `keep`: MOE_KEEP_16BIT or MOE_KEEP_E4M3
+    runs the experts' part in gated_experts and weighted_sum, which keep what they need in 16 or 8 bits; None has
+    the activation in torch operations, which keep each of their inputs."""
     E, N2, _ = p["w13"].shape
     h = layer_norm(x, p["norm_weight"], p["norm_bias"], eps)
     # made on the device: the block can be captured in a CUDA graph
@@ -159,17 +249,20 @@ def moe_block(p, x, topk: int, scoring=moe.MOE_SCORE_SOFTMAX, renormalize=True, 
     weights, ids = router_topk(logits, topk, scoring, renormalize)
     rows, offsets, src2dst, counts = _Permute.apply(h, ids, weights, E)
     # the permutation's gradient reads no row between the groups, and everything up to it is row by row
+    if keep is not None:
+        out = gated_experts(rows, p["w13"], p["w2"], offsets, counts, keep=keep, gaps=False)
+        return x + weighted_sum(out, src2dst, weights, keep=keep, gaps=False)
     gate, up = grouped_matmul(rows, p["w13"], offsets, counts, gaps=False).split(N2 // 2, dim=1)
     out = grouped_matmul(torch.nn.functional.silu(gate) * up, p["w2"], offsets, counts, gaps=False)
     return x + _WeightedGather.apply(out, src2dst, weights, ids, counts)
 
 
-def train_step(p, x, target, topk: int, lr: float, max_norm: float):
+def train_step(p, x, target, topk: int, lr: float, max_norm: float, keep=None):
     """One step of gradient descent on the tokens' mean squared distance to `target`: backward pass, clipping of all gradients by their common norm, update. Returns the loss
     and the norm before clipping, as device tensors."""
     for v in p.values():
         v.grad = None
-    loss = (moe_block(p, x, topk).float() - target.float()).square().sum(1).mean()
+    loss = (moe_block(p, x, topk, keep=keep).float() - target.float()).square().sum(1).mean()
     loss.backward()
     grads = [v.grad for v in p.values()]
     norm = moe.moe_clip_grad_norm(grads, max_norm)
@@ -179,13 +272,19 @@ def train_step(p, x, target, topk: int, lr: float, max_norm: float):
     return loss.detach(), norm
 
 
-def main():
+KEEP = {"torch": None, "16bit": moe.MOE_KEEP_16BIT, "8bit": moe.MOE_KEEP_E4M3}
+
+
+def main(argv=None):
+    a = argparse.ArgumentParser(description="a few training steps of an MoE block on synthetic data")
+    a.add_argument("--keep", choices=sorted(KEEP), default="torch", help="what the experts' part keeps for its backward pass")
+    keep = KEEP[a.parse_args(argv).keep]
     M, K, N, E, topk = 4096, 2048, 768, 128, 8
     p = init_block(K, N, E)
     x = torch.randn(M, K, device="cuda").bfloat16()
     target = x + 0.1 * torch.roll(x, 1, dims=1)
     for i in range(5):
-        loss, norm = train_step(p, x, target, topk, lr=2.0, max_norm=1.0)
+        loss, norm = train_step(p, x, target, topk, lr=2.0, max_norm=1.0, keep=keep)
         print(f"step {i}: loss {loss.item():.6f}, gradient norm {norm.item():.4f}")
 
 
