@@ -97,6 +97,21 @@ struct Gated {
     int wide_scales;     // kGated: P is a multiple of 64 and `scale` of 4, so that four outputs groups' bytes are a word
 };
 
+// Forward and dgrad go through the parts, all tiles along the M side of one after the other, and take
+// the two kinds by turns in proportion. A part of a long group finds its weights in L2, where the group's
+// other parts have left them, and is bound by the MMAs; a group of one part is bound by its weights' way
+// from DRAM: one kind after the other, each leaves idle what bounds the other.
+struct Order {
+    int singles, several;       // groups
+    int single_parts, parts;    // parts of the former; of all groups
+    uint32_t step;              // about 2^32 * single_parts / parts
+    // How many of the first `part` parts are groups of their own: it grows by 0 or 1 a part and leaves, at
+    // either end, as many of each kind as there are.
+    __device__ __forceinline__ int singles_before(int part) const {
+        return min(max((int)__umulhi((uint32_t)part, step), part - (parts - single_parts)), single_parts);
+    }
+};
+
 struct __align__(8) Tail {
     uint64_t full[kMaxStages];   // first CTA: both CTAs' loads of a stage have landed
     uint64_t empty[kMaxStages];
@@ -107,7 +122,7 @@ struct __align__(8) Tail {
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
-    int tiles;
+    Order order;
     int bucket[kBuckets];
 };
 
@@ -368,8 +383,10 @@ __device__ __forceinline__ void act_and_slope(float2 g, float2& a, float2& slope
 
 // ------------------------------------------------------------------ tiles
 // A group of rows: its first row, its row count, its number (low 16 bits of `id`) and, forward
-// and dgrad, its first tile and the rows of each of its tiles (high 16 bits of `id`; equal
-// parts of at most 256, whole 16s). wgrad has the groups in falling order of rows.
+// and dgrad, its first part and the rows of each of its parts (high 16 bits of `id`; equal
+// parts of at most 256, whole 16s). wgrad has the groups in falling order of rows; forward and dgrad
+// have the groups of several parts in front of the others, in their own order, and count both kinds'
+// parts from 0.
 struct __align__(16) Group {
     int start, lo, rows;
     uint32_t id;
@@ -398,7 +415,7 @@ struct Tile {
 
 // All lanes of a warp call it together (forward and dgrad look the group up with two votes).
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, const Shape& sh) {
+__device__ __forceinline__ Tile tile_at(int tile, const Group* groups, const Order& order, const Shape& sh) {
     Tile t;
     if (MODE == kWgrad) {
         const int at = sh.group_tiles.of(tile);
@@ -421,17 +438,21 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, int El, c
             t.steps = to - from;
         }
     } else {
-        // the last group whose first tile is not past this one (an empty group starts where
+        const int part = sh.m_tiles.of(tile), i = tile - part * sh.m_tiles.d;
+        const int before = order.singles_before(part);
+        const bool single = order.singles_before(part + 1) > before;
+        const int at = single ? before : part - before, n = single ? order.singles : order.several;
+        const Group* of = single ? groups + order.several : groups;
+        // the last group whose first part is not past this one (an empty group starts where
         // the next one does): the block of `stride` groups, then the group
-        const int lane = threadIdx.x & 31, stride = (El + 31) >> 5;
+        const int lane = threadIdx.x & 31, stride = (n + 31) >> 5;
         int l = lane * stride;
-        l = __popc(__ballot_sync(0xffffffffu, l < El && groups[l].start <= tile)) * stride - stride;
-        l += __popc(__ballot_sync(0xffffffffu, lane < stride && l + lane < El && groups[l + lane].start <= tile)) - 1;
-        const Group g = groups[l];
-        const int i = tile - g.start, per = g.id >> 16;
-        const int p = sh.m_tiles.of(i);
+        l = __popc(__ballot_sync(0xffffffffu, l < n && of[l].start <= at)) * stride - stride;
+        l += __popc(__ballot_sync(0xffffffffu, lane < stride && l + lane < n && of[l + lane].start <= at)) - 1;
+        const Group g = of[l];
+        const int p = at - g.start, per = g.id >> 16;
         t.l = g.id & 0xffff;
-        t.m0 = (i - p * sh.m_tiles.d) * tile_outputs<MODE>();
+        t.m0 = i * tile_outputs<MODE>();
         t.lo = g.lo + p * per;
         t.rows = min(per, g.rows - p * per);
         t.n = (t.rows + 15) & ~15;
@@ -495,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
     pdl_wait();
     pdl_trigger();
     // the groups' rows, never outside [0, R)
-    Group* unsorted = MODE == kWgrad ? reinterpret_cast<Group*>(smem) : groups;  // in the still unused stages
+    Group* unsorted = reinterpret_cast<Group*>(smem);  // in the still unused stages
     if (MODE == kWgrad) {
         for (int i = threadIdx.x; i < kBuckets; i += threads_of<MODE>()) st->bucket[i] = 0;
         __syncthreads();
@@ -538,24 +559,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 __syncwarp();
             }
         } else {
-            // prefix sums of the groups' tiles
-            int base = 0;
+            // groups of several parts, then the others; prefix sums of each kind's parts
+            int many = 0;
+            for (int l0 = 0; l0 < El; l0 += 32)
+                many += __popc(__ballot_sync(0xffffffffu, l0 + lane < El && unsorted[l0 + lane].rows > kMaxN));
+            int place = 0, single_place = many;
+            int64_t parts = 0, single_parts = 0;
             for (int l0 = 0; l0 < El; l0 += 32) {
                 const int l = l0 + lane;
-                const int mine = l < El ? ceil_div(groups[l].rows, kMaxN) * sh.m_tiles.d : 0;
-                const int sum = warp_prefix(mine);
-                if (l < El) groups[l].start = base + sum - mine;
-                base += __shfl_sync(0xffffffffu, sum, 31);
+                Group g = l < El ? unsorted[l] : Group{0, 0, 0, 0};
+                const bool several = g.rows > kMaxN;
+                const unsigned those = __ballot_sync(0xffffffffu, several), others = __ballot_sync(0xffffffffu, l < El && !several);
+                const int mine = ceil_div(g.rows, kMaxN), a = warp_prefix(several ? mine : 0), b = warp_prefix(several ? 0 : mine);
+                g.start = several ? (int)parts + a - mine : (int)single_parts + b - mine;
+                if (l < El) groups[several ? place + __popc(those & lanemask_lt()) : single_place + __popc(others & lanemask_lt())] = g;
+                place += __popc(those);
+                single_place += __popc(others);
+                parts += __shfl_sync(0xffffffffu, a, 31);
+                single_parts += __shfl_sync(0xffffffffu, b, 31);
             }
-            if (lane == 0) st->tiles = base;
+            if (lane == 0) {
+                // more tiles than 32 bits count come of groups that lie over one another only: none, then
+                const int64_t all = (parts + single_parts) * sh.m_tiles.d <= INT_MAX / 2 ? parts + single_parts : 0;
+                const float step = __fdividef((float)single_parts, (float)max(all, (int64_t)1)) * 4294967296.f;
+                st->order = Order{El - many, many, (int)single_parts, (int)all, __float2uint_rz(fminf(step, 4294967040.f))};
+            }
         }
     }
-    if (MODE == kWgrad) ptx::fence_proxy_async_smem();  // TMA writes the stages next
+    ptx::fence_proxy_async_smem();  // TMA writes the stages next
     __syncthreads();
     cluster_sync();  // barriers and TMEM of both CTAs are in place
     ptx::tc_fence_after();
     const uint32_t tmem = st->tmem_base;
-    const int tiles = MODE == kWgrad ? El * sh.group_tiles.d : st->tiles;
+    Order order;
+    if (MODE != kWgrad) order = st->order;
+    const int tiles = MODE == kWgrad ? El * sh.group_tiles.d : order.parts * sh.m_tiles.d;
     // Pair p takes the tiles p, p + pairs, ...; wgrad, whose tiles come from the dearest to the
     // cheapest, p, 2 * pairs - 1 - p, 2 * pairs + p, ..., so that the pairs' sums stay close
     // (skewed groups of 65536 rows: 378 -> 345 us). Forward and dgrad are bound by what the SMs
@@ -570,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         uint32_t ph = 0, filled = 0, landed = 0;
         bool ok = true;
         for (int tile = pair, gap = turn; ok && tile < tiles; tile += gap, gap = 2 * pairs - gap) {
-            const Tile t = tile_at<MODE>(tile, groups, El, sh);
+            const Tile t = tile_at<MODE>(tile, groups, order, sh);
             int box = 0;  // the smallest box that holds this CTA's half of the columns
             while (MODE != kWgrad && (8 << box) < t.n / 2) ++box;
             const int row = t.lo + (int)rank * (t.n / 2);
@@ -637,7 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             uint32_t tph = 0, filled = 0, landed = 0;
             bool ok = true;
             for (int tile = pair, gap = turn; ok && tile < tiles; tile += gap, gap = 2 * pairs - gap) {
-                const Tile t = tile_at<MODE>(tile, groups, El, sh);
+                const Tile t = tile_at<MODE>(tile, groups, order, sh);
                 if (t.steps == 0) continue;
                 const uint32_t idesc = idesc0 | (uint32_t)(t.n >> 3) << 17;
                 const uint32_t d = tmem + (uint32_t)(b * kMaxN);
@@ -689,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         int s = 0;
         uint32_t landed = 0;
         for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
-            const Tile t = tile_at<MODE>(tile, groups, El, sh);
+            const Tile t = tile_at<MODE>(tile, groups, order, sh);
             if (t.steps == 0) continue;
             s = (s + t.steps - 1) % stages;
             if (ragged(t, t.steps - 1) && (s & 1) == warp - kTailWarp) {
@@ -717,7 +755,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         const int quarter = warp & 3;  // of the accumulator's lanes: what a warp can read goes by its number
         const uint32_t slab = (uint32_t)(quarter * 32) << 16;
         for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
-            const Tile t = tile_at<MODE>(tile, groups, El, sh);
+            const Tile t = tile_at<MODE>(tile, groups, order, sh);
             const int m = t.m0 + (int)rank * (tile_outputs<MODE>() / 2) + quarter * (tile_outputs<MODE>() / 8);  // this warp's first output
             // kGatedBwd: gate and up as 16-byte pieces of rows, or of 8-bit groups
             uint4 in[4];     // 16 bits: gate, up by turns, rows 8 i + lane / 4; 8 bits: codes of gate and up, row lane / 2
