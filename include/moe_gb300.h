@@ -522,8 +522,8 @@ MOE_API int moe_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, i
  *   d_topk_weights[t, k] = sum over c of y[r, c] * dout[t, c], fp32; 0 for a slot without a row.
  *                          NULL: not wanted (and y is not read); NULL when apply_router_weight_on_input
  *   dout bf16 [M, K];  y, d_y bf16 [rows, K];  rows of no slot are left as they are
- * No row may belong to two slots (src2dst as moe_scatter writes it). K is a multiple of 128;
- * 1 <= topk <= 32; dout, y and d_y are 16-byte aligned. */
+ * No row may belong to two slots (src2dst as moe_scatter writes it). K is a multiple of 128, at most
+ * 2^30; 1 <= topk <= 32; dout, y and d_y are 16-byte aligned. */
 MOE_API int moe_gather_weight_reduce_backward(const void* dout, const void* y, int64_t rows, const int32_t* src2dst,
                                               const float* topk_weights, int64_t M, int topk, int K,
                                               int apply_router_weight_on_input, void* d_y, float* d_topk_weights,

@@ -601,17 +601,25 @@ def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=
                     out_dtype, stream, workspace)
 
 
-def _one_device(*tensors):
-    """The tensors of one call lie on the current device: a kernel is launched there and reads their addresses."""
-    dev = None
+def _addresses_here(*tensors):
+    """The device addresses of one call's contiguous CUDA tensors (None for None), all of which lie on the current
+    device: a kernel is launched there and reads them."""
+    here, out = None, []
     for t in tensors:
-        if t is not None:
-            at = t.get_device()  # -1: host
-            if dev is not None and at != dev:
-                raise ValueError(f"tensors on two devices, {dev} and {at} (-1: the host)")
-            dev = at
-    if dev is not None and dev >= 0 and dev != torch.cuda.current_device():
-        raise ValueError(f"tensors on device {dev}, which is not the current one")
+        if t is None:
+            out.append(None)
+            continue
+        at = t.get_device()  # -1: host
+        if at != here:
+            if at < 0:
+                raise ValueError("expected a CUDA tensor")
+            here = torch.cuda.current_device()
+            if at != here:
+                raise ValueError(f"tensor on device {at}, which is not the current one, {here}")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        out.append(t.data_ptr())
+    return out
 
 
 def _half(t, name):
@@ -649,7 +657,6 @@ def moe_grouped_gated(x, w13, expert_offsets, expert_num_tokens=None, activation
             if of is None:
                 raise ValueError(f"{name}: given, but not kept")
             _same(t, *of, name)
-    _one_device(x, w13, expert_offsets, expert_num_tokens, out, pre, pre_scale)
     if out is None:
         out = _empty((R, N), x.dtype, x.device, stream)
     _same(out, (R, N), x.dtype, "out")
@@ -657,9 +664,9 @@ def moe_grouped_gated(x, w13, expert_offsets, expert_num_tokens=None, activation
         pre = _empty(*of_pre, x.device, stream)
     if pre_scale is None and of_scale is not None:
         pre_scale = _empty(*of_scale, x.device, stream)
-    _check("moe_grouped_gated", lib().moe_grouped_gated(
-        _addr(x), R, _addr(w13), El, N, K, _addr(expert_offsets), _addr(expert_num_tokens), activation, dt, _addr(out), keep,
-        _addr(pre), _addr(pre_scale), _raw_stream(stream)))
+    px, pw, po, pc, ph, pp, ps = _addresses_here(x, w13, expert_offsets, expert_num_tokens, out, pre, pre_scale)
+    _check("moe_grouped_gated", lib().moe_grouped_gated(px, R, pw, El, N, K, po, pc, activation, dt, ph, keep, pp, ps,
+                                                        _raw_stream(stream)))
     return out, pre, pre_scale
 
 
@@ -681,16 +688,15 @@ def moe_grouped_gated_backward(dy, w2, pre, expert_offsets, expert_num_tokens=No
     _same(expert_num_tokens, (El,), torch.int32, "expert_num_tokens")
     if h is not None and not want_h:
         raise ValueError("h: given, but not wanted")
-    _one_device(dy, w2, pre, expert_offsets, expert_num_tokens, pre_scale, d_pre, h)
     if d_pre is None:
         d_pre = _empty((R, 2 * N), dy.dtype, dy.device, stream)
     if h is None and want_h:
         h = _empty((R, N), dy.dtype, dy.device, stream)
     _same(d_pre, (R, 2 * N), dy.dtype, "d_pre")
     _same(h, (R, N), dy.dtype, "h")
+    py, pw, po, pc, pp, ps, pd, ph = _addresses_here(dy, w2, expert_offsets, expert_num_tokens, pre, pre_scale, d_pre, h)
     _check("moe_grouped_gated_backward", lib().moe_grouped_gated_backward(
-        _addr(dy), R, _addr(w2), El, N, K, _addr(expert_offsets), _addr(expert_num_tokens), activation, dt, keep, _addr(pre),
-        _addr(pre_scale), _addr(d_pre), _addr(h), _raw_stream(stream)))
+        py, R, pw, El, N, K, po, pc, activation, dt, keep, pp, ps, pd, ph, _raw_stream(stream)))
     return d_pre, h
 
 
@@ -700,14 +706,14 @@ def moe_checkpoint_pack(x, codes=None, scales=None, stream=None):
     dt = _dtype_code(x, "x")
     M, K = x.shape
     of_scales = (M, -(-K // 16))
-    _one_device(x, codes, scales)
     if codes is None:
         codes = _empty((M, K), torch.uint8, x.device, stream)
     if scales is None:
         scales = _empty(of_scales, torch.uint8, x.device, stream)
     _same(codes, (M, K), torch.uint8, "codes")
     _same(scales, of_scales, torch.uint8, "scales")
-    _check("moe_checkpoint_pack", lib().moe_checkpoint_pack(_addr(x), M, K, dt, _addr(codes), _addr(scales), _raw_stream(stream)))
+    px, pc, ps = _addresses_here(x, codes, scales)
+    _check("moe_checkpoint_pack", lib().moe_checkpoint_pack(px, M, K, dt, pc, ps, _raw_stream(stream)))
     return codes, scales
 
 
@@ -716,12 +722,12 @@ def moe_checkpoint_unpack(codes, scales, dtype, out=None, stream=None):
     M, K = codes.shape
     _same(codes, (M, K), torch.uint8, "codes")
     _same(scales, (M, -(-K // 16)), torch.uint8, "scales")
-    _one_device(codes, scales, out)
     if out is None:
         out = _empty((M, K), dtype, codes.device, stream)
     _same(out, (M, K), dtype, "out")
-    _check("moe_checkpoint_unpack", lib().moe_checkpoint_unpack(
-        _addr(codes), _addr(scales), M, K, _dtype_code(out, "out"), _addr(out), _raw_stream(stream)))
+    dt = _dtype_code(out, "out")
+    pc, ps, px = _addresses_here(codes, scales, out)
+    _check("moe_checkpoint_unpack", lib().moe_checkpoint_unpack(pc, ps, M, K, dt, px, _raw_stream(stream)))
     return out
 
 
@@ -737,7 +743,6 @@ def moe_gather_weight_reduce_backward(dout, y, src2dst, topk_weights, apply_rout
     _same(y, (rows, K), torch.bfloat16, "y")
     _same(src2dst, (M, topk), torch.int32, "src2dst")
     _same(topk_weights, (M, topk), torch.float32, "topk_weights")
-    _one_device(dout, y, src2dst, topk_weights, d_y, d_topk_weights)
     wanted = want_weights and not apply_router_weight_on_input
     if d_topk_weights is not None and not wanted:
         raise ValueError("d_topk_weights: given, but there is no such gradient")
@@ -747,9 +752,9 @@ def moe_gather_weight_reduce_backward(dout, y, src2dst, topk_weights, apply_rout
         d_topk_weights = _empty((M, topk), torch.float32, dout.device, stream)
     _same(d_y, (rows, K), torch.bfloat16, "d_y")
     _same(d_topk_weights, (M, topk), torch.float32, "d_topk_weights")
+    po, py, ps, pw, pd, pg = _addresses_here(dout, y, src2dst, topk_weights, d_y, d_topk_weights)
     _check("moe_gather_weight_reduce_backward", lib().moe_gather_weight_reduce_backward(
-        _addr(dout), _addr(y), rows, _addr(src2dst), _addr(topk_weights), M, topk, K, int(bool(apply_router_weight_on_input)),
-        _addr(d_y), _addr(d_topk_weights), _raw_stream(stream)))
+        po, py, rows, ps, pw, M, topk, K, int(bool(apply_router_weight_on_input)), pd, pg, _raw_stream(stream)))
     return d_y, d_topk_weights
 
 

@@ -53,7 +53,7 @@ extern "C" MOE_API int moe_gather_weight_reduce_backward(const void* dout, const
                                                          int apply_router_weight_on_input, void* d_y, float* d_topk_weights,
                                                          moe_stream_t stream) {
     const bool unit = apply_router_weight_on_input != 0;
-    if (M < 0 || topk < 1 || topk > 32 || M > INT32_MAX / topk || K < 128 || K % 128 || rows < 0 || rows > INT32_MAX)
+    if (M < 0 || topk < 1 || topk > 32 || M > INT32_MAX / topk || K < 128 || K % 128 || K > 1 << 30 || rows < 0 || rows > INT32_MAX)
         return MOE_ERR_INVALID_ARG;
     if (M > 0 && (!dout || !src2dst || (rows > 0 && !d_y) || (!unit && !topk_weights) || (d_topk_weights && rows > 0 && !y)))
         return MOE_ERR_INVALID_ARG;

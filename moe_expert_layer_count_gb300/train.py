@@ -211,19 +211,28 @@ def grouped_matmul(x, w, expert_offsets, expert_num_tokens=None, out_dtype=None,
     return _GroupedMatmul.apply(x, w, expert_offsets, expert_num_tokens, out_dtype, gaps)
 
 
+def _needed(keep, *inputs):
+    """Nothing is kept where there will be no backward pass."""
+    return keep if torch.is_grad_enabled() and any(t.requires_grad for t in inputs) else moe.MOE_KEEP_NONE
+
+
 def gated_experts(x, w13, w2, expert_offsets, expert_num_tokens=None, activation=moe.MOE_ACT_SILU, keep=moe.MOE_KEEP_16BIT,
                   gaps=True):
     """The experts' feed-forward part under autograd: w2[l] (a(g) * u) with (g, u) = w13[l] x[r] for the rows r of every
     group l (moe_grouped_gated, moe_grouped_matmul). `keep`: whether x and (g, u) are kept for the backward pass in
     16 bits (MOE_KEEP_16BIT) or in 8 (MOE_KEEP_E4M3: half the memory; what the gradients are made of is off by up to
     2^-4). Rows of no group as in grouped_matmul."""
-    return _GatedExperts.apply(x, w13, w2, expert_offsets, expert_num_tokens, activation, keep, gaps)
+    if keep not in (moe.MOE_KEEP_16BIT, moe.MOE_KEEP_E4M3):
+        raise ValueError(f"keep: expected MOE_KEEP_16BIT or MOE_KEEP_E4M3, got {keep}")
+    return _GatedExperts.apply(x, w13, w2, expert_offsets, expert_num_tokens, activation, _needed(keep, x, w13, w2), gaps)
 
 
 def weighted_sum(rows, src2dst, weights, keep=moe.MOE_KEEP_16BIT, gaps=True):
     """moe_gather_weight_reduce under autograd: out[t] = sum over k of weights[t, k] * rows[src2dst[t, k]]. `keep`: how the
     rows are kept for the weights' gradient. The gradient of rows of no slot is 0, or undefined with gaps=False."""
-    return _WeightedSum.apply(rows, src2dst, weights, keep, gaps)
+    if keep not in (moe.MOE_KEEP_16BIT, moe.MOE_KEEP_E4M3):
+        raise ValueError(f"keep: expected MOE_KEEP_16BIT or MOE_KEEP_E4M3, got {keep}")
+    return _WeightedSum.apply(rows, src2dst, weights, _needed(keep, rows, weights), gaps)
 
 
 def init_block(K: int, N: int, E: int, device="cuda", seed: int = 0):

@@ -91,7 +91,7 @@ def combine(L, dout=at(1), y=at(2), rows=64, s=at(3), w=at(4), M=16, topk=4, K=1
 
 def test_gather_backward_refusals(L):  # noqa: F811
     assert combine(L, M=0) == 0
-    for bad in (dict(M=-1), dict(topk=0), dict(topk=33), dict(K=0), dict(K=64), dict(K=130), dict(rows=-1), dict(rows=1 << 31),
+    for bad in (dict(M=-1), dict(topk=0), dict(topk=33), dict(K=0), dict(K=64), dict(K=130), dict(K=(1 << 30) + 128), dict(rows=-1), dict(rows=1 << 31),
                 dict(M=1 << 30), dict(dout=None), dict(y=None), dict(s=None), dict(w=None), dict(d=None), dict(unit=1),
                 dict(dout=off(1, 8)), dict(y=off(2, 8)), dict(d=off(5, 8)), dict(s=off(3, 2)), dict(w=off(4, 2)), dict(dw=off(6, 2)),
                 dict(d=at(1)), dict(d=at(2)), dict(d=at(3)), dict(d=at(4)), dict(dw=at(1)), dict(dw=at(2)), dict(dw=at(3)), dict(dw=at(4)),
@@ -143,14 +143,13 @@ def test_binding_refusals(L):  # noqa: F811
         g(d.float(), y, s, w)
 
 
-def test_tensors_on_two_devices_are_refused(L, monkeypatch):  # noqa: F811
+def test_tensors_of_another_device_are_refused(L, monkeypatch):  # noqa: F811
     import types
 
     import moe_expert_layer_count_gb300 as moe
-    fake = lambda i: types.SimpleNamespace(get_device=lambda: i)  # noqa: E731
+    fake = lambda i: types.SimpleNamespace(get_device=lambda: i, is_contiguous=lambda: True, data_ptr=lambda: 64 + i)  # noqa: E731
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    moe._one_device(fake(0), None, fake(0))
-    with pytest.raises(ValueError):
-        moe._one_device(fake(0), fake(1))
-    with pytest.raises(ValueError):
-        moe._one_device(fake(1), None)
+    assert moe._addresses_here(fake(0), None, fake(0)) == [64, None, 64]
+    for bad in ((fake(0), fake(1)), (fake(1), None), (fake(0), fake(-1))):
+        with pytest.raises(ValueError):
+            moe._addresses_here(*bad)

@@ -225,3 +225,20 @@ def test_command(keep, capsys):
     train.main(["--keep", keep])
     lines = capsys.readouterr().out.strip().splitlines()
     assert len(lines) == 5 and all("loss" in x for x in lines)
+
+
+def test_without_gradients_nothing_is_kept():
+    counts, N, K = [40, 24], 64, 128
+    x, _, w13, w2, _, off = make(counts, N, K, torch.bfloat16, seed=3)
+    w13.requires_grad_()
+    want = train.gated_experts(x, w13, w2, off)
+    with torch.no_grad():
+        launches = moe.moe_kernel_launch_count()
+        y = train.gated_experts(x, w13, w2, off, keep=moe.MOE_KEEP_E4M3)
+        z = train.weighted_sum(y, torch.arange(64, dtype=torch.int32, device="cuda").view(32, 2), torch.ones(32, 2, device="cuda"),
+                               keep=moe.MOE_KEEP_E4M3)
+        assert moe.moe_kernel_launch_count() - launches == 3  # two products and the sum
+    assert torch.equal(y, want) and not z.requires_grad
+    for bad in (moe.MOE_KEEP_NONE, 7, None):
+        with pytest.raises(ValueError):
+            train.gated_experts(x, w13, w2, off, keep=bad)
