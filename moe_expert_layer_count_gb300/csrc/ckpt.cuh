@@ -90,6 +90,26 @@ __device__ __forceinline__ uint4 ckpt_encode16(const uint4& lo, const uint4& hi,
     return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
+// The same of a group that two neighbouring lanes hold a half of each: this lane's eight codes.
+template <typename T>
+__device__ __forceinline__ uint2 ckpt_encode8(const uint4& piece, uint32_t& byte) {
+    const uint32_t w[4] = {piece.x, piece.y, piece.z, piece.w};
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) amax = __vmaxu2(amax, w[i] & 0x7fff7fffu);
+    amax = max(amax >> 16, amax & 0xffff);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    byte = ckpt_byte(abs_bits(unpack2<T>(amax).x));
+    const float inv = ckpt_inverse(byte);
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 a = unpack2<T>(w[2 * i]), b = unpack2<T>(w[2 * i + 1]);
+        c[i] = ckpt_encode4(a.x, a.y, b.x, b.y, inv);
+    }
+    return make_uint2(c[0], c[1]);
+}
+
 // And back.
 template <typename T>
 __device__ __forceinline__ void ckpt_decode16(const uint4& codes, uint32_t byte, uint4& lo, uint4& hi) {

@@ -54,18 +54,20 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMaxStages = 6;
 constexpr int kEpiWarps = 4, kTmaWarp = 4, kMmaWarp = 5, kTailWarp = 6;
 constexpr int kBoxBytes = 4096;    // wgrad output box: 32 rows x 128 bytes
-// a warp's 16 rows of the gated forms: 64 bytes of gate and up (kGatedBwd: of each) and h of 32 (kGatedBwd: 64)
-template <int MODE>
-__host__ __device__ constexpr int gated_bytes() { return MODE == kGatedBwd ? 3072 : 1536; }
 constexpr int kScaleBytes = 256 * 8;  // kGated: a tile's scale bytes, 4 of gate and 4 of up a row
 constexpr int kBoxes = 2;          // boxes of a warp in turn (four would cost two stages: 302 against 289 us)
-// The gated forms' epilogues have two warps for each quarter of the accumulator's lanes.
+// The gated forms' epilogues take kStep rows at a time and have kSets warps for each quarter of the
+// accumulator's lanes, whose steps' chains of loads, special functions and exchanges overlap.
+constexpr int kStep = 8, kSets = 4;
 template <int MODE>
-__host__ __device__ constexpr int epi_warps() { return MODE == kGated || MODE == kGatedBwd ? 2 * kEpiWarps : kEpiWarps; }
+__host__ __device__ constexpr int epi_warps() { return MODE == kGated || MODE == kGatedBwd ? kSets * kEpiWarps : kEpiWarps; }
+// a warp's kStep rows of the gated forms: 64 bytes of gate and up (kGatedBwd: of each) and h of 32 (kGatedBwd: 64)
+template <int MODE>
+__host__ __device__ constexpr int gated_bytes() { return kStep * (MODE == kGatedBwd ? 192 : 96); }
 // forward and dgrad stage two 32-row x 64-byte buffers per warp
 template <int MODE>
 __host__ __device__ constexpr int staging_bytes() {
-    if (MODE == kGated) return epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 2 * 8;  // and two barriers
+    if (MODE == kGated) return epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + kSets * 8;  // and a barrier for each set
     return epi_warps<MODE>() * (MODE == kGatedBwd ? gated_bytes<MODE>() : kBoxBytes * (MODE == kWgrad ? kBoxes : 1));
 }
 // results along the M side of a tile: kGated's rows are half gate and half up
@@ -261,17 +263,22 @@ __device__ __forceinline__ void load_fragments16(uint32_t t, uint32_t* r) {
         : "r"(t)
         : "memory");
 }
-// 16 lanes x 16 columns in the same way.
-__device__ __forceinline__ void load_fragments8(uint32_t t, uint32_t* r) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+// The warp's 32 lanes x 8 columns: lanes 0-15 in r[0..3], lanes 16-31 in r[4..7].
+__device__ __forceinline__ void load_fragments(uint32_t t, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(t)
                  : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t + (16u << 16))
+                 : "memory");
 }
-// The warp's 32 lanes x 16 columns: lanes 0-15 in r[0..7], lanes 16-31 in r[8..15].
-__device__ __forceinline__ void load_fragments(uint32_t t, uint32_t (&r)[16]) {
-    load_fragments8(t, r);
-    load_fragments8(t + (16u << 16), r + 8);
+__device__ __forceinline__ void wait_columns(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
 }
 // The warp's 32 lanes x 32 columns: lanes 0-15 in r[0..15], lanes 16-31 in r[16..31].
 __device__ __forceinline__ void load_fragments(uint32_t t, uint32_t (&r)[32]) {
@@ -283,6 +290,10 @@ __device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
                  "r"(c), "r"(d)
                  : "memory");
+}
+// Two of them; lanes 0-15 give the addresses.
+__device__ __forceinline__ void store_transposed(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 // The other way: four 8 x 8 fragments read from rows of 16 bytes, transposed.
 __device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
@@ -503,8 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         }
         ptx::mbar_init(ptx::smem_addr(&st->mma_done), 1);
         if (MODE == kGated)
-            for (int half = 0; half < 2; ++half)
-                ptx::mbar_init(ptx::smem_addr(staging + epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 8 * half), 4);
+            for (int set = 0; set < kSets; ++set)
+                ptx::mbar_init(ptx::smem_addr(staging + epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 8 * set), 4);
         st->abort = 0;
         ptx::fence_mbar_init();
     }
@@ -753,35 +764,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         int b = 0, boxes = 0;
         uint32_t tph = 0, turns = 0;
         const int quarter = warp & 3;  // of the accumulator's lanes: what a warp can read goes by its number
+        const int set = warp < 4 ? 0 : (warp - 2) >> 2;
         const uint32_t slab = (uint32_t)(quarter * 32) << 16;
         for (int tile = pair, gap = turn; tile < tiles; tile += gap, gap = 2 * pairs - gap) {
             const Tile t = tile_at<MODE>(tile, groups, order, sh);
             const int m = t.m0 + (int)rank * (tile_outputs<MODE>() / 2) + quarter * (tile_outputs<MODE>() / 8);  // this warp's first output
-            // kGatedBwd: gate and up as 16-byte pieces of rows, or of 8-bit groups
-            uint4 in[4];     // 16 bits: gate, up by turns, rows 8 i + lane / 4; 8 bits: codes of gate and up, row lane / 2
-            uint32_t sc[2];  // 8 bits: their scales
+            // kGatedBwd: a step's gate and up, row lane / 4; 16 bits: the lane's 16-byte piece of each; 8 bits: one
+            // group's codes and scale, of gate or up
+            uint4 in[2];
+            uint32_t sc;
             auto fetch = [&](int c) {
-                const int64_t row0 = (int64_t)t.lo + c, P2 = 2 * (int64_t)P;
+                const int r = lane >> 2;
+                const int64_t P2 = 2 * (int64_t)P, row = ((int64_t)t.lo + c + r) * P2;
                 if (gated.keep == MOE_KEEP_E4M3) {
-                    const uint8_t* codes = static_cast<const uint8_t*>(gated.pre_in);
-                    const int r = lane >> 1, j = m + (lane & 1) * 16;
+                    const int j = m + (lane & 1) * 16;
+                    const bool live = j < P && c + r < t.rows;
+                    const int64_t at = row + ((lane >> 1) & 1) * (int64_t)P + j;
+                    in[0] = live ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(gated.pre_in) + at)) : make_uint4(0, 0, 0, 0);
+                    sc = live ? __ldcg(gated.scale + at / kCkptGroup) : 127u;
+                } else {
+                    const int j = m + (lane & 3) * 8;
                     const bool live = j < P && c + r < t.rows;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int64_t at = (row0 + r) * P2 + i * (int64_t)P + j;
-                        in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(codes + at)) : make_uint4(0, 0, 0, 0);
-                        sc[i] = live ? __ldcg(gated.scale + at / kCkptGroup) : 127u;
-                    }
-                } else {
-                    const O* pre = static_cast<const O*>(gated.pre_in);
-                    const int j = m + (lane & 3) * 8;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = (i >> 1) * 8 + (lane >> 2);
-                        const bool live = j < P && c + r < t.rows;
-                        in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(pre + (row0 + r) * P2 + (i & 1) * (int64_t)P + j))
+                    for (int i = 0; i < 2; ++i)
+                        in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const O*>(gated.pre_in) + row + i * (int64_t)P + j))
                                      : make_uint4(0, 0, 0, 0);
-                    }
                 }
             };
             if constexpr (MODE == kGatedBwd) {
@@ -789,10 +796,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 const bool eight = gated.keep == MOE_KEEP_E4M3;
                 const uint8_t* p = static_cast<const uint8_t*>(gated.pre_in);
                 const int64_t P2 = 2 * (int64_t)P;
-                const int r = lane >> 1, z = eight ? 1 : 2, first = warp > 3 ? 16 : 0;
+                const int z = eight ? 1 : 2, first = set * kStep, r = (lane >> 1) & 7;
                 if (first < t.rows) fetch(first);
-                if (m < P)
-                    for (int c = first + 32; c + r < t.rows; c += 32) {
+                if (m < P)  // two steps' rows at a time
+                    for (int c = first + kSets * kStep * (1 + (lane >> 4)); c + r < t.rows; c += 2 * kSets * kStep) {
                         const int64_t at = (t.lo + (int64_t)c + r) * P2 + (lane & 1) * (int64_t)P + m;
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(p + at * z) : "memory");
                         if (eight) asm volatile("prefetch.global.L2 [%0];" ::"l"(gated.scale + at / kCkptGroup) : "memory");
@@ -857,41 +864,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                     }
                 }
             } else if constexpr (MODE == kGated) {
-                // 16 rows at a time, the quarter's two warps by turns. Lanes 0-15 of the accumulator are the gates
-                // of this warp's 16 outputs, lanes 16-31 their ups, so that a thread's registers j and 8 + j are
-                // the gate and up of one output. Rounded to 16 bits they are transposed into shared memory, rows
-                // of 64 bytes (16 gates, 16 ups) and of 32 bytes (h), and leave it as 16-byte pieces of rows.
-                const int half = warp > 3, first = half * 16;
-                uint8_t* stage = staging + (half * 4 + quarter) * gated_bytes<MODE>();
-                uint8_t* hbuf = stage + 1024;
+                // Lanes 0-15 of the accumulator are the gates of this warp's 16 outputs, lanes 16-31 their ups, so
+                // that a thread's registers j and 4 + j are the gate and up of one output. Rounded to 16 bits they
+                // are transposed into shared memory, rows of 64 bytes (16 gates, 16 ups) and of 32 bytes (h), and
+                // leave it as 16-byte pieces of rows.
+                uint8_t* stage = staging + (set * 4 + quarter) * gated_bytes<MODE>();
+                uint8_t* hbuf = stage + kStep * 64;
                 const uint32_t put_pre = ptx::smem_addr(stage) + (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
-                // 8 rows and the next 8: lanes 16-31 address the second ones
-                const uint32_t put_h = ptx::smem_addr(hbuf) + (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * 32 +
-                                                                         ((((lane >> 3) & 1) ^ ((lane >> 2) & 1)) << 4));
+                const uint32_t put_h = ptx::smem_addr(hbuf) + (uint32_t)((lane & 7) * 32 + ((((lane >> 3) & 1) ^ ((lane >> 2) & 1)) << 4));
                 const int64_t P2 = 2 * (int64_t)P;
                 uint8_t* bytes = staging + epi_warps<MODE>() * gated_bytes<MODE>() + (turns & 1) * kScaleBytes;
-                uint32_t next[16];
-                if (first < t.rows)
-                    load_fragments(acc + first, next);
-                else
-                    release();
+                const int r = lane >> 2, piece = lane & 3;             // of gate and up
+                const int hr = (lane >> 1) & 7, side = lane & 1;       // of h
+                if (set * kStep >= t.rows) release();
 #pragma unroll 1
-                for (int c = first; c < t.rows; c += 32) {
+                for (int c = set * kStep; c < t.rows; c += kSets * kStep) {
+                    uint32_t v[8], h[2];
+                    load_fragments(acc + c, v);
                     __syncwarp();
-                    ptx::tmem_wait_ld_regs(next);
-                    uint32_t v[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = next[j];
-                    if (c + 32 < t.rows)
-                        load_fragments(acc + c + 32, next);
-                    else
-                        release();
-                    uint32_t h[4];
+                    wait_columns(v);
+                    if (c + kSets * kStep >= t.rows) release();
                     auto activate = [&](auto gelu) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < 2; ++j) {
                             const float2 g = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                            const float2 u = make_float2(__uint_as_float(v[8 + 2 * j]), __uint_as_float(v[9 + 2 * j]));
+                            const float2 u = make_float2(__uint_as_float(v[4 + 2 * j]), __uint_as_float(v[5 + 2 * j]));
                             const float2 w = __fmul2_rn(act_of<decltype(gelu)::value>(g), u);
                             h[j] = pack2_f32<O>(w.x, w.y);
                         }
@@ -900,139 +897,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                         activate(std::false_type());
                     else
                         activate(std::true_type());
-                    store_transposed(put_h, h[0], h[1], h[2], h[3]);
-                    if (gated.keep != MOE_KEEP_NONE) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            store_transposed(put_pre + i * 512, pack2<O>(v[4 * i], v[4 * i + 1]), pack2<O>(v[4 * i + 2], v[4 * i + 3]),
-                                             pack2<O>(v[8 + 4 * i], v[8 + 4 * i + 1]), pack2<O>(v[8 + 4 * i + 2], v[8 + 4 * i + 3]));
-                    }
+                    store_transposed(put_h, h[0], h[1]);
+                    if (gated.keep != MOE_KEEP_NONE)
+                        store_transposed(put_pre, pack2<O>(v[0], v[1]), pack2<O>(v[2], v[3]), pack2<O>(v[4], v[5]), pack2<O>(v[6], v[7]));
                     __syncwarp();
                     const int64_t row0 = (int64_t)t.lo + c;
-                    const int r = lane >> 1, side = lane & 1;
-                    const bool live = c + r < t.rows;
-                    {
-                        const uint4 w = *reinterpret_cast<const uint4*>(hbuf + r * 32 + ((side ^ ((r >> 2) & 1)) << 4));
-                        if (live && m + side * 8 < P) *reinterpret_cast<uint4*>(out + (row0 + r) * P + m + side * 8) = w;
-                    }
-                    if (gated.keep == MOE_KEEP_16BIT) {
-                        O* pre = static_cast<O*>(gated.pre_out);
-                        const int piece = lane & 3, j = m + (piece & 1) * 8;
-                        const int64_t at = (piece >> 1) * (int64_t)P + j;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int q = i * 8 + (lane >> 2);
-                            const uint4 w = *reinterpret_cast<const uint4*>(stage + q * 64 + ((piece ^ ((q >> 1) & 3)) << 4));
-                            if (j < P && c + q < t.rows) *reinterpret_cast<uint4*>(pre + (row0 + q) * P2 + at) = w;
+                    if (lane < 16 && c + hr < t.rows && m + side * 8 < P)
+                        *reinterpret_cast<uint4*>(out + (row0 + hr) * P + m + side * 8) =
+                            *reinterpret_cast<const uint4*>(hbuf + hr * 32 + ((side ^ ((hr >> 2) & 1)) << 4));
+                    if (gated.keep != MOE_KEEP_NONE) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4));
+                        const int j = m + (piece & 1) * 8;
+                        const int64_t at = (row0 + r) * P2 + (piece >> 1) * (int64_t)P + j;
+                        const bool live = j < P && c + r < t.rows;
+                        if (gated.keep == MOE_KEEP_16BIT) {
+                            if (live) *reinterpret_cast<uint4*>(static_cast<O*>(gated.pre_out) + at) = w;
+                        } else {
+                            // two lanes have a group of the 8-bit form, made from the 16-bit values so that it
+                            // equals what packing those gives
+                            uint32_t byte;
+                            const uint2 codes = ckpt_encode8<O>(w, byte);
+                            if (live) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(gated.pre_out) + at) = codes;
+                            if ((lane & 1) == 0) bytes[(c + r) * 8 + (piece >> 1) * 4 + quarter] = (uint8_t)byte;
                         }
-                    } else if (gated.keep == MOE_KEEP_E4M3) {
-                        // a lane has one row's 16 gates or ups: one group of the 8-bit form, made from the
-                        // 16-bit values so that it equals what packing those gives
-                        const int64_t at = (row0 + r) * P2 + side * (int64_t)P + m;
-                        const int z = (r >> 1) & 3;
-                        const uint4 lo = *reinterpret_cast<const uint4*>(stage + r * 64 + (((2 * side) ^ z) << 4));
-                        const uint4 hi = *reinterpret_cast<const uint4*>(stage + r * 64 + (((2 * side + 1) ^ z) << 4));
-                        uint32_t byte;
-                        const uint4 w = ckpt_encode16<O>(lo, hi, byte);
-                        if (live && m < P) {
-                            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(gated.pre_out) + at) = w;
-                        }
-                        bytes[(c + r) * 8 + side * 4 + quarter] = (uint8_t)byte;
                     }
                 }
                 __syncwarp();
                 if (gated.keep == MOE_KEEP_E4M3) {
-                    // The four quarters' bytes of a row lie side by side: the warps of this half meet, and each
-                    // writes every fourth chunk's, 8 bytes a row (single bytes, each in a sector of its own, cost 14 of
-                    // 285 us at 512 rows a group). The next tile but one uses the same buffer: by then all four
-                    // have been at the next one's meeting, after they had read this one's.
-                    const uint32_t met = ptx::smem_addr(staging + epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 8 * half);
+                    // The four quarters' bytes of a row lie side by side: the set's warps meet, and each writes every
+                    // fourth step's, 8 bytes a row (single bytes, each in a sector of its own, cost 14 of 285 us at
+                    // 512 rows a group). The next tile but one uses the same buffer: by then all four have been at the
+                    // next one's meeting, after they had read this one's.
+                    const uint32_t met = ptx::smem_addr(staging + epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 8 * set);
                     if (lane == 0) ptx::mbar_arrive(met);
                     if (!__all_sync(0xffffffffu, wait_phase(met, turns & 1, abort))) break;
                     ++turns;
                     const int j = t.m0 + (int)rank * 64, n = min((P - j) / kCkptGroup, 4);
-                    for (int c = first + quarter * 32; c < t.rows; c += 128) {
+                    for (int c = set * kStep + quarter * (kSets * kStep); c < t.rows; c += 4 * kSets * kStep) {
                         if (gated.wide_scales) {
-                            const int r = lane >> 1, side = lane & 1;
-                            const int64_t at = (((int64_t)t.lo + c + r) * P2 + side * (int64_t)P + j) / kCkptGroup;
-                            if (n == 4 && c + r < t.rows)
+                            const int64_t at = (((int64_t)t.lo + c + hr) * P2 + side * (int64_t)P + j) / kCkptGroup;
+                            if (lane < 16 && n == 4 && c + hr < t.rows)
                                 *reinterpret_cast<uint32_t*>(gated.scale + at) = *reinterpret_cast<const uint32_t*>(bytes + c * 8 + lane * 4);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int r = i * 4 + (lane >> 3), side = (lane >> 2) & 1, q = lane & 3;
-                                const int64_t at = (((int64_t)t.lo + c + r) * P2 + side * (int64_t)P + j) / kCkptGroup + q;
-                                if (q < n && c + r < t.rows) gated.scale[at] = bytes[c * 8 + i * 32 + lane];
+                            for (int i = 0; i < 2; ++i) {
+                                const int br = i * 4 + (lane >> 3), q = lane & 3;
+                                const int64_t at = (((int64_t)t.lo + c + br) * P2 + ((lane >> 2) & 1) * (int64_t)P + j) / kCkptGroup + q;
+                                if (q < n && c + br < t.rows) gated.scale[at] = bytes[c * 8 + i * 32 + lane];
                             }
                         }
                     }
                 }
             } else if constexpr (MODE == kGatedBwd) {
-                // 16 rows x this warp's 32 outputs at a time, the quarter's two warps by turns: gate and up come
-                // in as 16-byte pieces of rows, one step ahead, are laid into shared memory (64 bytes a row,
-                // swizzled) and read as the accumulator's 8 x 8 fragments; the gradients go back over them and
-                // out, h beside them.
-                const int half = warp > 3, first = half * 16;
-                uint8_t* gbuf = staging + (half * 4 + quarter) * gated_bytes<MODE>();
+                // 8 rows x this warp's 32 outputs at a time: gate and up come in as 16-byte pieces of rows, one step
+                // ahead, are laid into shared memory (64 bytes a row, swizzled) and read as the accumulator's
+                // 8 x 8 fragments; the gradients go back over them and out, h beside them.
+                uint8_t* gbuf = staging + (set * 4 + quarter) * gated_bytes<MODE>();
+                constexpr int kUp = kStep * 64;  // up's buffer behind gate's, h's behind that
                 const uint32_t frag = ptx::smem_addr(gbuf) + (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
                 const int64_t P2 = 2 * (int64_t)P;
-                const bool eight = gated.keep == MOE_KEEP_E4M3;
-                const int piece = lane & 3, j = m + piece * 8, group = lane & 1;
-                uint32_t next[16];
-                if (first < t.rows)
-                    load_fragments(acc + first, next);
-                else
-                    release();
+                const int r = lane >> 2, piece = lane & 3, j = m + piece * 8;
+                uint8_t* own = gbuf + r * 64;
+                const int z = (r >> 1) & 3;  // row r's swizzle
+                if (set * kStep >= t.rows) release();
 #pragma unroll 1
-                for (int c = first; c < t.rows; c += 32) {
+                for (int c = set * kStep; c < t.rows; c += kSets * kStep) {
+                    uint32_t v[8], g[4], up[4], h[4];
+                    load_fragments(acc + c, v);
                     __syncwarp();
-                    if (eight) {
-                        const int r = lane >> 1, z = (r >> 1) & 3;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint8_t* row = gbuf + i * 1024 + r * 64;
-                            uint4 lo, hi;
-                            ckpt_decode16<O>(in[i], sc[i], lo, hi);
-                            *reinterpret_cast<uint4*>(row + (((2 * group) ^ z) << 4)) = lo;
-                            *reinterpret_cast<uint4*>(row + (((2 * group + 1) ^ z) << 4)) = hi;
-                        }
+                    if (gated.keep == MOE_KEEP_E4M3) {
+                        uint8_t* row = own + (piece >> 1) * kUp;
+                        uint4 lo, hi;
+                        ckpt_decode16<O>(in[0], sc, lo, hi);
+                        *reinterpret_cast<uint4*>(row + (((2 * (piece & 1)) ^ z) << 4)) = lo;
+                        *reinterpret_cast<uint4*>(row + (((2 * (piece & 1) + 1) ^ z) << 4)) = hi;
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = (i >> 1) * 8 + (lane >> 2);
-                            *reinterpret_cast<uint4*>(gbuf + (i & 1) * 1024 + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4)) = in[i];
-                        }
+                        for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(own + i * kUp + ((piece ^ z) << 4)) = in[i];
                     }
-                    if (c + 32 < t.rows) fetch(c + 32);
+                    if (c + kSets * kStep < t.rows) fetch(c + kSets * kStep);
                     __syncwarp();
-                    ptx::tmem_wait_ld_regs(next);
-                    uint32_t v[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = next[i];
-                    if (c + 32 < t.rows)
-                        load_fragments(acc + c + 32, next);
-                    else
-                        release();
-                    // all of the step's fragments at once, so that their chains overlap: g[4 i + q]: rows 8 i ..,
-                    // outputs 8 q ..
-                    uint32_t g[8], up[8], h[8];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        load_transposed(frag + i * 512, g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
-                        load_transposed(frag + 1024 + i * 512, up[4 * i], up[4 * i + 1], up[4 * i + 2], up[4 * i + 3]);
-                    }
+                    load_transposed(frag, g[0], g[1], g[2], g[3]);
+                    load_transposed(frag + kUp, up[0], up[1], up[2], up[3]);
+                    wait_columns(v);
+                    if (c + kSets * kStep >= t.rows) release();
                     auto gradients = [&](auto gelu) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {  // two rows each
-                            const float2 uv = unpack2<O>(up[k]);
-                            const int at = ((k >> 1) & 1) * 8 + 4 * (k >> 2) + (k & 1) * 2;
-                            const float2 d = make_float2(__uint_as_float(v[at]), __uint_as_float(v[at + 1]));
+                        for (int q = 0; q < 4; ++q) {  // outputs 8 q .. 8 q + 7; two rows each
+                            const float2 uv = unpack2<O>(up[q]), d = make_float2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
                             float2 a, slope;
-                            act_and_slope<decltype(gelu)::value>(unpack2<O>(g[k]), a, slope);
+                            act_and_slope<decltype(gelu)::value>(unpack2<O>(g[q]), a, slope);
                             const float2 dg = __fmul2_rn(__fmul2_rn(d, uv), slope), du = __fmul2_rn(d, a), hv = __fmul2_rn(a, uv);
-                            g[k] = pack2_f32<O>(dg.x, dg.y);
-                            up[k] = pack2_f32<O>(du.x, du.y);
-                            h[k] = pack2_f32<O>(hv.x, hv.y);
+                            g[q] = pack2_f32<O>(dg.x, dg.y);
+                            up[q] = pack2_f32<O>(du.x, du.y);
+                            h[q] = pack2_f32<O>(hv.x, hv.y);
                         }
                     };
                     if (gated.act == MOE_ACT_SILU)
@@ -1040,24 +998,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                     else
                         gradients(std::true_type());
                     __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        store_transposed(frag + i * 512, g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
-                        store_transposed(frag + 1024 + i * 512, up[4 * i], up[4 * i + 1], up[4 * i + 2], up[4 * i + 3]);
-                        store_transposed(frag + 2048 + i * 512, h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-                    }
+                    store_transposed(frag, g[0], g[1], g[2], g[3]);
+                    store_transposed(frag + kUp, up[0], up[1], up[2], up[3]);
+                    store_transposed(frag + 2 * kUp, h[0], h[1], h[2], h[3]);
                     __syncwarp();
-                    O* grads = static_cast<O*>(gated.pre_out);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = i * 8 + (lane >> 2);
-                        const uint8_t* row = gbuf + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4);
+                    if (j < P && c + r < t.rows) {
+                        O* grads = static_cast<O*>(gated.pre_out);
+                        const uint8_t* from = own + ((piece ^ z) << 4);
                         const int64_t at = (int64_t)t.lo + c + r;
-                        if (j < P && c + r < t.rows) {
-                            *reinterpret_cast<uint4*>(grads + at * P2 + j) = *reinterpret_cast<const uint4*>(row);
-                            *reinterpret_cast<uint4*>(grads + at * P2 + P + j) = *reinterpret_cast<const uint4*>(row + 1024);
-                            if (out) *reinterpret_cast<uint4*>(out + at * P + j) = *reinterpret_cast<const uint4*>(row + 2048);
-                        }
+                        *reinterpret_cast<uint4*>(grads + at * P2 + j) = *reinterpret_cast<const uint4*>(from);
+                        *reinterpret_cast<uint4*>(grads + at * P2 + P + j) = *reinterpret_cast<const uint4*>(from + kUp);
+                        if (out) *reinterpret_cast<uint4*>(out + at * P + j) = *reinterpret_cast<const uint4*>(from + 2 * kUp);
                     }
                 }
                 __syncwarp();
