@@ -365,7 +365,8 @@ MOE_API int moe_host_wait(moe_stream_t stream);
 /* ---------------------------------------------------------------------------------
  * One training step of a pre-norm MoE block with 16-bit expert weights: the norm in
  * front of the layer, the router that chooses the experts, the experts' products with
- * their gradients, and the clipping of the gradients. (moe_scatter with MOE_QUANT_NONE
+ * their gradients, alone or with the activation between them, what is kept for the backward
+ * pass in 8 bits, and the clipping of the gradients. (moe_scatter with MOE_QUANT_NONE
  * and moe_gather_weight_reduce permute between them in both directions.)
  * All sums, statistics and products are held in fp32 (the norm of a list of tensors
  * partly in fp64) and rounded once where a result is stored in 16 bits.

@@ -12,8 +12,11 @@ SiLU-and-mul requantisation -> grouped GEMM (w2) -> ep_gather with the top-k
 weight-and-reduce, under a chunking loop that sizes the workspace per chunk.
 
 Beside it, the operators of one training step of a pre-norm MoE block with 16-bit expert
-weights, each with its gradient: moe_layer_norm, moe_router_topk, moe_grouped_matmul, and
-moe_clip_grad_norm over the gradients (``train.py`` runs them together under autograd).
+weights, each with its gradient: moe_layer_norm, moe_router_topk, moe_grouped_matmul,
+moe_grouped_gated (both input projections with the activation between the experts' products),
+moe_gather_weight_reduce_backward, and moe_clip_grad_norm over the gradients; moe_checkpoint_pack
+and _unpack keep activations in 8 bits for the backward pass (``train.py`` runs them together under
+autograd).
 """
 from __future__ import annotations
 
@@ -601,10 +604,14 @@ def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=
                     out_dtype, stream, workspace)
 
 
-def _addresses_here(*tensors):
-    """The device addresses of one call's contiguous CUDA tensors (None for None), all of which lie on the current
-    device: a kernel is launched there and reads them."""
-    here, out = None, []
+# the index of the current device, without a look whether CUDA has been initialised
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _here(stream, *tensors):
+    """The handle of the stream (None: the current one), then the device addresses of one call's contiguous CUDA
+    tensors (None for None), all of which lie on the current device: a kernel is launched there and reads them."""
+    here, out = None, [None]
     for t in tensors:
         if t is None:
             out.append(None)
@@ -613,12 +620,13 @@ def _addresses_here(*tensors):
         if at != here:
             if at < 0:
                 raise ValueError("expected a CUDA tensor")
-            here = torch.cuda.current_device()
+            here = _current_device()
             if at != here:
                 raise ValueError(f"tensor on device {at}, which is not the current one, {here}")
         if not t.is_contiguous():
             raise ValueError("expected a contiguous tensor")
         out.append(t.data_ptr())
+    out[0] = _raw_stream(stream) if stream is not None or _current_raw is None else _current_raw(here)
     return out
 
 
@@ -637,6 +645,18 @@ def _kept(keep, R, N, dtype):
     return None, None
 
 
+def _buffer(t, of, device, stream, name):
+    """The caller's buffer `t` of the shape and type `of`, or a new one; None where there is no such result."""
+    if of is None:
+        if t is not None:
+            raise ValueError(f"{name}: given, but there is no such result")
+    elif t is None:
+        t = _empty(*of, device, stream)
+    else:
+        _same(t, *of, name)
+    return t
+
+
 def moe_grouped_gated(x, w13, expert_offsets, expert_num_tokens=None, activation=MOE_ACT_SILU, keep=MOE_KEEP_NONE, out=None,
                       pre=None, pre_scale=None, stream=None):
     """h[r] = a(g) * u with (g, u) = w13[l] @ x[r] for the rows r of every group l: x [R, K] and w13 [El, 2N, K]
@@ -651,22 +671,15 @@ def moe_grouped_gated(x, w13, expert_offsets, expert_num_tokens=None, activation
     _same(x, (R, K), w13.dtype, "x")
     _same(expert_offsets, (El + 1,), torch.int32, "expert_offsets")
     _same(expert_num_tokens, (El,), torch.int32, "expert_num_tokens")
-    of_pre, of_scale = _kept(keep, R, N, x.dtype)
-    for t, of, name in ((pre, of_pre, "pre"), (pre_scale, of_scale, "pre_scale")):
-        if t is not None:
-            if of is None:
-                raise ValueError(f"{name}: given, but not kept")
-            _same(t, *of, name)
     if out is None:
         out = _empty((R, N), x.dtype, x.device, stream)
-    _same(out, (R, N), x.dtype, "out")
-    if pre is None and of_pre is not None:
-        pre = _empty(*of_pre, x.device, stream)
-    if pre_scale is None and of_scale is not None:
-        pre_scale = _empty(*of_scale, x.device, stream)
-    px, pw, po, pc, ph, pp, ps = _addresses_here(x, w13, expert_offsets, expert_num_tokens, out, pre, pre_scale)
-    _check("moe_grouped_gated", lib().moe_grouped_gated(px, R, pw, El, N, K, po, pc, activation, dt, ph, keep, pp, ps,
-                                                        _raw_stream(stream)))
+    else:
+        _same(out, (R, N), x.dtype, "out")
+    of_pre, of_scale = _kept(keep, R, N, x.dtype)
+    pre = _buffer(pre, of_pre, x.device, stream, "pre")
+    pre_scale = _buffer(pre_scale, of_scale, x.device, stream, "pre_scale")
+    on, px, pw, po, pc, ph, pp, ps = _here(stream, x, w13, expert_offsets, expert_num_tokens, out, pre, pre_scale)
+    _check("moe_grouped_gated", lib().moe_grouped_gated(px, R, pw, El, N, K, po, pc, activation, dt, ph, keep, pp, ps, on))
     return out, pre, pre_scale
 
 
@@ -686,17 +699,11 @@ def moe_grouped_gated_backward(dy, w2, pre, expert_offsets, expert_num_tokens=No
         _same(pre_scale, *of_scale, "pre_scale")
     _same(expert_offsets, (El + 1,), torch.int32, "expert_offsets")
     _same(expert_num_tokens, (El,), torch.int32, "expert_num_tokens")
-    if h is not None and not want_h:
-        raise ValueError("h: given, but not wanted")
-    if d_pre is None:
-        d_pre = _empty((R, 2 * N), dy.dtype, dy.device, stream)
-    if h is None and want_h:
-        h = _empty((R, N), dy.dtype, dy.device, stream)
-    _same(d_pre, (R, 2 * N), dy.dtype, "d_pre")
-    _same(h, (R, N), dy.dtype, "h")
-    py, pw, po, pc, pp, ps, pd, ph = _addresses_here(dy, w2, expert_offsets, expert_num_tokens, pre, pre_scale, d_pre, h)
+    d_pre = _buffer(d_pre, ((R, 2 * N), dy.dtype), dy.device, stream, "d_pre")
+    h = _buffer(h, ((R, N), dy.dtype) if want_h else None, dy.device, stream, "h")
+    on, py, pw, po, pc, pp, ps, pd, ph = _here(stream, dy, w2, expert_offsets, expert_num_tokens, pre, pre_scale, d_pre, h)
     _check("moe_grouped_gated_backward", lib().moe_grouped_gated_backward(
-        py, R, pw, El, N, K, po, pc, activation, dt, keep, pp, ps, pd, ph, _raw_stream(stream)))
+        py, R, pw, El, N, K, po, pc, activation, dt, keep, pp, ps, pd, ph, on))
     return d_pre, h
 
 
@@ -706,14 +713,10 @@ def moe_checkpoint_pack(x, codes=None, scales=None, stream=None):
     dt = _dtype_code(x, "x")
     M, K = x.shape
     of_scales = (M, -(-K // 16))
-    if codes is None:
-        codes = _empty((M, K), torch.uint8, x.device, stream)
-    if scales is None:
-        scales = _empty(of_scales, torch.uint8, x.device, stream)
-    _same(codes, (M, K), torch.uint8, "codes")
-    _same(scales, of_scales, torch.uint8, "scales")
-    px, pc, ps = _addresses_here(x, codes, scales)
-    _check("moe_checkpoint_pack", lib().moe_checkpoint_pack(px, M, K, dt, pc, ps, _raw_stream(stream)))
+    codes = _buffer(codes, ((M, K), torch.uint8), x.device, stream, "codes")
+    scales = _buffer(scales, (of_scales, torch.uint8), x.device, stream, "scales")
+    on, px, pc, ps = _here(stream, x, codes, scales)
+    _check("moe_checkpoint_pack", lib().moe_checkpoint_pack(px, M, K, dt, pc, ps, on))
     return codes, scales
 
 
@@ -722,12 +725,10 @@ def moe_checkpoint_unpack(codes, scales, dtype, out=None, stream=None):
     M, K = codes.shape
     _same(codes, (M, K), torch.uint8, "codes")
     _same(scales, (M, -(-K // 16)), torch.uint8, "scales")
-    if out is None:
-        out = _empty((M, K), dtype, codes.device, stream)
-    _same(out, (M, K), dtype, "out")
+    out = _buffer(out, ((M, K), dtype), codes.device, stream, "out")
     dt = _dtype_code(out, "out")
-    pc, ps, px = _addresses_here(codes, scales, out)
-    _check("moe_checkpoint_unpack", lib().moe_checkpoint_unpack(pc, ps, M, K, dt, px, _raw_stream(stream)))
+    on, pc, ps, px = _here(stream, codes, scales, out)
+    _check("moe_checkpoint_unpack", lib().moe_checkpoint_unpack(pc, ps, M, K, dt, px, on))
     return out
 
 
@@ -744,17 +745,12 @@ def moe_gather_weight_reduce_backward(dout, y, src2dst, topk_weights, apply_rout
     _same(src2dst, (M, topk), torch.int32, "src2dst")
     _same(topk_weights, (M, topk), torch.float32, "topk_weights")
     wanted = want_weights and not apply_router_weight_on_input
-    if d_topk_weights is not None and not wanted:
-        raise ValueError("d_topk_weights: given, but there is no such gradient")
-    if d_y is None:
-        d_y = _empty((rows, K), torch.bfloat16, dout.device, stream)
-    if d_topk_weights is None and wanted:
-        d_topk_weights = _empty((M, topk), torch.float32, dout.device, stream)
-    _same(d_y, (rows, K), torch.bfloat16, "d_y")
-    _same(d_topk_weights, (M, topk), torch.float32, "d_topk_weights")
-    po, py, ps, pw, pd, pg = _addresses_here(dout, y, src2dst, topk_weights, d_y, d_topk_weights)
+    d_y = _buffer(d_y, ((rows, K), torch.bfloat16), dout.device, stream, "d_y")
+    d_topk_weights = _buffer(d_topk_weights, ((M, topk), torch.float32) if wanted else None, dout.device, stream,
+                                  "d_topk_weights")
+    on, po, py, ps, pw, pd, pg = _here(stream, dout, y, src2dst, topk_weights, d_y, d_topk_weights)
     _check("moe_gather_weight_reduce_backward", lib().moe_gather_weight_reduce_backward(
-        po, py, rows, ps, pw, M, topk, K, int(bool(apply_router_weight_on_input)), pd, pg, _raw_stream(stream)))
+        po, py, rows, ps, pw, M, topk, K, 1 if apply_router_weight_on_input else 0, pd, pg, on))
     return d_y, d_topk_weights
 
 

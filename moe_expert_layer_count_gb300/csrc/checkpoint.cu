@@ -1,4 +1,8 @@
-// Activations kept in 8 bits for the backward pass (the form of ckpt.cuh), and read back.
+// Activations kept in 8 bits for the backward pass (the form of ckpt.cuh), and read back: x * 2^-e rounded to
+// e4m3, e one exponent for 16 values. Each value is read and written once, so DRAM bounds it where rows are
+// whole groups: 65536 x 2048 bf16 58 us packed and 60 read back, 6.8-7.1 TB/s (its floor at the copy rate: 61), fp32
+// 99 and 97 (100). Rows of other widths cost instructions instead (an issue in 72-84 % of the slots, DRAM at a
+// third to a half): 30011 x 1111 bf16 22 us both ways (floor 15), fp32 32 and 28 (25).
 #include <climits>
 #include <type_traits>
 

@@ -1,5 +1,8 @@
 // Gradients of the gather with the top-k weight-and-reduce: with r = src2dst[t, k],
 //   d_y[r] = w[t, k] * dout[t],   d_w[t, k] = sum over c of y[r, c] * dout[t, c].
+// DRAM bounds it: dout, y and d_y once each, 84 us for 8192 tokens, top-8, of 2048 columns (571 MB at
+// 6.77 TB/s, the copy rate).
+// Small calls are the host's: 1.6-3.3 us on the device for 17 to 1023 tokens, 7-9 us a call.
 #include <climits>
 
 #include "elem.cuh"
@@ -10,7 +13,8 @@ namespace {
 
 constexpr int kMaxWarps = 8;
 
-// A block has a token, a warp one of its slots at a time: a lane holds pieces of 8 columns.
+// A block has a token, a warp one of its slots at a time, so that dout's row comes from DRAM once and from L1
+// for the other slots, and no sum crosses a warp: a lane holds pieces of 8 columns.
 // Products and sums in fp32; w * dout is rounded once.
 __global__ void __launch_bounds__(32 * kMaxWarps)
     gather_backward_kernel(const bf16* __restrict__ dout, const bf16* __restrict__ y, const int32_t* __restrict__ src2dst,

@@ -5,6 +5,19 @@
 //   backward  dh = w2[l]^T dy[r], dg = dh * u * a'(g), du = dh * a(g), h[r] = a(g) * u again
 // The kernel is in grouped_tc.cuh. What is kept of g and u for the backward pass leaves the same
 // epilogue, in 16 bits or in the 8-bit form of ckpt.cuh.
+//
+// What it measured (one GB300, times of one call with L2 flushed; sizes N = 768, K = 2048, 128 groups):
+//   512 rows a group       forward 250-261 us, 265-277 with g and u kept in 16 bits or in 8 (the ungated product of
+//                          the same weights: 252-259); backward 214-222 us from either
+//   65536 rows, Zipf 1.2   forward 271-283 us, 285-300 with g and u kept; backward 210-214 us from either
+//   512 rows, decode       forward 122-126 us: 790 MB at 6.3-6.5 TB/s
+// What bounds it. Forward: as the ungated product (tensor pipe active 81 %, 74 % with g and u stored): MMAs
+// and the weights' way from DRAM hide each other only in part; without an epilogue 247 us at 512 rows a
+// group. Backward: 1.17 GB from and to DRAM at 5.3-5.5 TB/s (its floor at the copy rate is 174 us); without
+// MMAs it takes as long, without its stores or without reading g and u 181 us each, without both 156.
+// What did not help: asking for the next tile's weights in L2 (258 -> 306-330 us by either kind of prefetch: what the
+// SMs take in is short, not time), asking for g and u by TMA (220 -> 240 us), streaming stores (equal) and loads
+// (214 -> 222 us).
 #include "grouped_tc.cuh"
 
 namespace moe {

@@ -11,7 +11,7 @@
 // library's dense product: 540-555 us):
 //   one group of 8192 rows, 8192 x 8192      590-610 us forward, 596 us [700] wgrad   1.8, 1.84 PFLOP/s
 //   128 groups of 512 rows, 1536 x 2048      248-257 us [292] forward, 287 us [322] wgrad   1.65, 1.44
-//   65536 rows over 128 groups, Zipf 1.2     285-305 us [327] forward, 343-354 us wgrad   1.4, 1.2
+//   65536 rows over 128 groups, Zipf 1.2     275-279 us forward, 343-354 us wgrad   1.5, 1.2
 //   512 rows over 128 groups (decode)        116-127 us forward: 750-806 MB of weights at 6.4 TB/s
 //                                            132 us wgrad: as much written at 6.1 TB/s
 // Where the time goes (variants that leave one part out, 512 rows a group):

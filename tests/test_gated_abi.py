@@ -148,8 +148,9 @@ def test_tensors_of_another_device_are_refused(L, monkeypatch):  # noqa: F811
 
     import moe_expert_layer_count_gb300 as moe
     fake = lambda i: types.SimpleNamespace(get_device=lambda: i, is_contiguous=lambda: True, data_ptr=lambda: 64 + i)  # noqa: E731
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    assert moe._addresses_here(fake(0), None, fake(0)) == [64, None, 64]
+    monkeypatch.setattr(moe, "_current_device", lambda: 0)
+    monkeypatch.setattr(moe, "_current_raw", lambda i: 7 + i)
+    assert moe._here(None, fake(0), None, fake(0)) == [7, 64, None, 64]
     for bad in ((fake(0), fake(1)), (fake(1), None), (fake(0), fake(-1))):
         with pytest.raises(ValueError):
-            moe._addresses_here(*bad)
+            moe._here(None, *bad)
