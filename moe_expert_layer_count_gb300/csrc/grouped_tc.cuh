@@ -48,6 +48,8 @@ __host__ __device__ constexpr bool like_dgrad(int mode) { return mode == kDgrad 
 
 constexpr int kPairM = 256;        // rows of a tile (both CTAs)
 constexpr int kMaxN = 256;         // columns of a tile
+// Forward and dgrad: the most rows that a tile gets are one of these, kMaxN >> c, chosen by choose_rows
+constexpr int kRowChoices = 3, kLeastN = kMaxN >> (kRowChoices - 1);
 constexpr int kDepth = 64;         // reduced index per stage: 64 16-bit values = one 128-byte swizzled row
 constexpr int kOperandBytes = 128 * kDepth * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
@@ -425,6 +427,28 @@ struct Tile {
     int l, part, lo, rows, m0, n0, n, steps;
 };
 
+// Forward and dgrad: the shift c that makes kMaxN >> c the most rows of a tile. A stage of a tile of n rows takes
+// about the time of 256 + n rows on their way into the SM (its MMAs that of 2 n at most); its epilogue, under the next
+// tile's stages but for the last one's, takes some 16 clocks a row (32 with the activation's gradients) and 1000; and
+// the pairs take the tiles in rounds, so that smaller tiles pay where 256 rows leave pairs without one: one group of 2048 rows, 512 x 512, backward
+// 14.0 -> 8.7 us; 8192 rows of 128 x 2048 forward 14.5 -> 12.3 us. With many rounds 256 rows win by their smaller
+// sum. (Sizes between, whose halves are no box of the row maps, measured slower: 4096 rows in tiles of 224 instead
+// of 256, 2048 x 2048, 41.9 -> 45.3 us.) parts: of all groups, for each choice.
+template <int MODE>
+__device__ __forceinline__ int choose_rows(const unsigned (&parts)[kRowChoices], const Shape& sh) {
+    const float pairs = (float)(gridDim.x >> 1), steps = (float)ceil_div(sh.depth, kDepth), tiles = (float)sh.m_tiles.d;
+    int best = 0;
+    float least = 0.f;
+#pragma unroll
+    for (int c = 0; c < kRowChoices; ++c) {
+        const float rows = (float)(kMaxN >> c);
+        const float epilogue = (MODE == kGatedBwd ? 32.f : 16.f) * rows, round = fmaxf(steps * (256.f + rows), 1000.f + epilogue);
+        const float clocks = ceilf(__fdividef((float)parts[c] * tiles, pairs)) * round + epilogue;
+        if (c == 0 || clocks < least) best = c, least = clocks;
+    }
+    return best;
+}
+
 // All lanes of a warp call it together (forward and dgrad look the group up with two votes).
 template <int MODE>
 __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, const Order& order, const Shape& sh) {
@@ -537,10 +561,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         const int lo = min(max(__ldg(off + l), 0), R);
         const int end = cnt ? (int)min((int64_t)lo + max(__ldg(cnt + l), 0), (int64_t)R) : min(__ldg(off + l + 1), R);
         const int rows = max(end - lo, 0);
-        const int parts = max(ceil_div(rows, kMaxN), 1);
-        const int per = (ceil_div(rows, parts) + 15) & ~15;
         const int b = MODE == kWgrad ? bucket_of(rows) : 0;
-        unsorted[l] = Group{b, lo, rows, (uint32_t)per << 16 | l};
+        unsorted[l] = Group{b, lo, rows, (uint32_t)l};
         if (MODE == kWgrad) atomicAdd(&st->bucket[b], 1);
     }
     __syncthreads();
@@ -571,18 +593,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 __syncwarp();
             }
         } else {
+            unsigned of_choice[kRowChoices] = {};
+            for (int l = lane; l < El; l += 32)
+#pragma unroll
+                for (int c = 0; c < kRowChoices; ++c) of_choice[c] += ((unsigned)unsorted[l].rows + (kMaxN >> c) - 1) / (kMaxN >> c);
+#pragma unroll
+            for (int c = 0; c < kRowChoices; ++c) of_choice[c] = __reduce_add_sync(0xffffffffu, of_choice[c]);
+            const int down = choose_rows<MODE>(of_choice, sh), cap = kMaxN >> down;
             // groups of several parts, then the others; prefix sums of each kind's parts
             int many = 0;
             for (int l0 = 0; l0 < El; l0 += 32)
-                many += __popc(__ballot_sync(0xffffffffu, l0 + lane < El && unsorted[l0 + lane].rows > kMaxN));
+                many += __popc(__ballot_sync(0xffffffffu, l0 + lane < El && unsorted[l0 + lane].rows > cap));
             int place = 0, single_place = many;
             int64_t parts = 0, single_parts = 0;
             for (int l0 = 0; l0 < El; l0 += 32) {
                 const int l = l0 + lane;
                 Group g = l < El ? unsorted[l] : Group{0, 0, 0, 0};
-                const bool several = g.rows > kMaxN;
+                const bool several = g.rows > cap;
                 const unsigned those = __ballot_sync(0xffffffffu, several), others = __ballot_sync(0xffffffffu, l < El && !several);
-                const int mine = ceil_div(g.rows, kMaxN), a = warp_prefix(several ? mine : 0), b = warp_prefix(several ? 0 : mine);
+                const int mine = (int)(((unsigned)g.rows + cap - 1) >> (8 - down));
+                const int per = several ? ceil_div(g.rows, mine) : g.rows;
+                g.id |= (uint32_t)((per + 15) & ~15) << 16;
+                const int a = warp_prefix(several ? mine : 0), b = warp_prefix(several ? 0 : mine);
                 g.start = several ? (int)parts + a - mine : (int)single_parts + b - mine;
                 if (l < El) groups[several ? place + __popc(those & lanemask_lt()) : single_place + __popc(others & lanemask_lt())] = g;
                 place += __popc(those);
@@ -592,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             }
             if (lane == 0) {
                 // more tiles than 32 bits count come of groups that lie over one another only: none, then
-                const int64_t all = (parts + single_parts) * sh.m_tiles.d <= INT_MAX / 2 ? parts + single_parts : 0;
+                const int64_t all = (parts + single_parts) * sh.m_tiles.d <= INT_MAX - 4096 ? parts + single_parts : 0;
                 const float step = __fdividef((float)single_parts, (float)max(all, (int64_t)1)) * 4294967296.f;
                 st->order = Order{El - many, many, (int)single_parts, (int)all, __float2uint_rz(fminf(step, 4294967040.f))};
             }
@@ -621,9 +653,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         bool ok = true;
         for (int tile = pair, gap = turn; ok && tile < tiles; tile += gap, gap = 2 * pairs - gap) {
             const Tile t = tile_at<MODE>(tile, groups, order, sh);
-            int box = 0;  // the smallest box that holds this CTA's half of the columns
-            while (MODE != kWgrad && (8 << box) < t.n / 2) ++box;
-            const int row = t.lo + (int)rank * (t.n / 2);
+            const int half = t.n / 2;  // this CTA's rows on the N side
+            int box = 0;               // the smallest box that holds them (exact ones, several a stage, measured slower)
+            while (MODE != kWgrad && (8 << box) < half) ++box;
+            const int row = t.lo + (int)rank * half;
             const int m = t.m0 + (int)rank * 128, n = t.n0 + (int)rank * 128;
             for (int k = 0; k < t.steps; ++k) {
                 ok = __all_sync(0xffffffffu, wait_phase(ptx::smem_addr(&st->empty[s]), ph ^ 1, abort));
@@ -1162,7 +1195,7 @@ int launch_grouped(const void* a, const void* b, const int32_t* off, const int32
     const Shape sh{{(int)m_tiles, magic_of(m_tiles)}, {(int)group_tiles, magic_of(group_tiles)},
                    {(int)part_tiles, magic_of(part_tiles)}, parts, like_dgrad(MODE) ? N : K};
     // no more pairs than tiles (an upper bound: the groups' sizes are not known here)
-    const int64_t most = MODE == kWgrad ? El * group_tiles : (R / kMaxN + (R < El ? R : El)) * m_tiles;
+    const int64_t most = MODE == kWgrad ? El * group_tiles : (R / kLeastN + (R < El ? R : El)) * m_tiles;
     const int pairs = (int)(most < num_sms / 2 ? most : num_sms / 2);
     launch_k(grouped_kernel<MODE, O>, 2 * pairs, threads_of<MODE>(), smem, stream, maps, off, cnt, El, (int)R, N, K,
              sh, idesc_base(MODE, dtype), stages, static_cast<O*>(out), gated);
