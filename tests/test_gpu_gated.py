@@ -306,3 +306,48 @@ def test_captured_replayed_and_on_another_stream():
     h, _, _ = moe.moe_grouped_gated(x, w13, off, stream=s)
     s.synchronize()
     assert torch.equal(h, want[0])
+
+
+@pytest.mark.parametrize("counts,N,K", [
+    ([5000, 3, 0, 700, 40, 1, 257, 64] * 3, 128, 64),   # long groups' parts and short groups by turns, many rounds
+    ([300] + [1] * 200 + [4000], 40, 72),               # few long ones
+    ([1] * 300, 64, 64), ([257] * 90, 64, 64),          # one kind only
+    ([2048], 256, 128), ([65, 129, 193], 136, 64),      # tiles of 128 and of 64 rows
+])
+def test_long_and_short_groups(counts, N, K):
+    x, dy, w13, w2, pre, off = make(counts, N, K, torch.bfloat16, seed=13)
+    h, kept, _ = moe.moe_grouped_gated(x, w13, off, keep=moe.MOE_KEEP_16BIT)
+    check_forward(h, kept, x, w13, off, counts, "silu")
+    check_backward(*moe.moe_grouped_gated_backward(dy, w2, pre, off), dy, w2, pre, off, counts, "silu")
+    # a group's results do not depend on the others, which decide how the rows are cut into tiles
+    for l in (0, len(counts) // 2, len(counts) - 1):
+        s = slice(int(off[l]), int(off[l]) + counts[l])
+        one = torch.tensor([0, counts[l]], dtype=torch.int32, device="cuda")
+        alone, again, _ = moe.moe_grouped_gated(x[s], w13[l:l + 1], one, keep=moe.MOE_KEEP_16BIT)
+        assert torch.equal(alone, h[s]) and torch.equal(again, kept[s])
+    assert moe.moe_device_error() == 0
+
+
+def test_calls_from_two_threads_on_two_streams():
+    import threading
+    work = [make([333, 0, 90], 96 + 32 * i, 128, torch.bfloat16, seed=20 + i) for i in range(2)]
+
+    def both(x, dy, w13, w2, pre, off, stream=None):
+        h, codes, scale = moe.moe_grouped_gated(x, w13, off, keep=moe.MOE_KEEP_E4M3, stream=stream)
+        return [h, codes, scale, *moe.moe_grouped_gated_backward(dy, w2, codes, off, pre_scale=scale, stream=stream)]
+    want = [[t.clone() for t in both(*w)] for w in work]
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def run(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i] = both(*work[i], stream=s)
+        s.synchronize()
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
