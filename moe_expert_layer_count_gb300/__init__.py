@@ -608,26 +608,29 @@ def moe_grouped_matmul_wgrad(dy, x, expert_offsets, expert_num_tokens=None, out=
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _here(stream, *tensors):
-    """The handle of the stream (None: the current one), then the device addresses of one call's contiguous CUDA
-    tensors (None for None), all of which lie on the current device: a kernel is launched there and reads them."""
-    here, out = None, [None]
-    for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        at = t.get_device()  # -1: host
-        if at != here:
-            if at < 0:
-                raise ValueError("expected a CUDA tensor")
-            here = _current_device()
-            if at != here:
-                raise ValueError(f"tensor on device {at}, which is not the current one, {here}")
-        if not t.is_contiguous():
-            raise ValueError("expected a contiguous tensor")
-        out.append(t.data_ptr())
-    out[0] = _raw_stream(stream) if stream is not None or _current_raw is None else _current_raw(here)
-    return out
+def _here(t) -> int:
+    """The device of a call's first tensor, which has to be the current one: a kernel is launched there."""
+    here = t.get_device()  # -1: host
+    if here < 0:
+        raise ValueError("expected a CUDA tensor")
+    if here != _current_device():
+        raise ValueError(f"tensor on device {here}, which is not the current one, {_current_device()}")
+    return here
+
+
+def _take(t, shape, dtype, here, name) -> int:
+    """The address of a contiguous tensor of this shape and type on the device `here`."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != here:
+        raise ValueError(f"{name}: expected a CUDA tensor on device {here}, got one on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _stream_on(here, stream) -> int:
+    return _raw_stream(stream) if stream is not None or _current_raw is None else _current_raw(here)
 
 
 def _half(t, name):
@@ -636,50 +639,41 @@ def _half(t, name):
     return _DTYPES[t.dtype]
 
 
-def _kept(keep, R, N, dtype):
-    """Shape and type of what is kept of gate and up, and of its scales (None: there is none)."""
-    if keep == MOE_KEEP_16BIT:
-        return ((R, 2 * N), dtype), None
-    if keep == MOE_KEEP_E4M3:
-        return ((R, 2 * N), torch.uint8), ((R, 2 * N // 16), torch.uint8)
-    return None, None
-
-
-def _buffer(t, of, device, stream, name):
-    """The caller's buffer `t` of the shape and type `of`, or a new one; None where there is no such result."""
-    if of is None:
-        if t is not None:
-            raise ValueError(f"{name}: given, but there is no such result")
-    elif t is None:
-        t = _empty(*of, device, stream)
-    else:
-        _same(t, *of, name)
-    return t
-
-
 def moe_grouped_gated(x, w13, expert_offsets, expert_num_tokens=None, activation=MOE_ACT_SILU, keep=MOE_KEEP_NONE, out=None,
                       pre=None, pre_scale=None, stream=None):
     """h[r] = a(g) * u with (g, u) = w13[l] @ x[r] for the rows r of every group l: x [R, K] and w13 [El, 2N, K]
     (gate rows, then up rows) in bf16 or fp16, h [R, N]; groups as in moe_grouped_matmul. `keep`: what is kept of
     g and u for the backward pass. Returns (h, pre, pre_scale): pre [R, 2N] in x's type (MOE_KEEP_16BIT) or as 8-bit
     codes with pre_scale [R, 2N / 16] (MOE_KEEP_E4M3), None where nothing is kept."""
+    dtype = w13.dtype
     dt = _half(w13, "w13")
     El, N2, K = w13.shape
     R, N = x.shape[0], N2 // 2
     if N2 % 2:
         raise ValueError(f"w13: gate and up need an even number of rows, got {N2}")
-    _same(x, (R, K), w13.dtype, "x")
-    _same(expert_offsets, (El + 1,), torch.int32, "expert_offsets")
-    _same(expert_num_tokens, (El,), torch.int32, "expert_num_tokens")
+    here = _here(x)
     if out is None:
-        out = _empty((R, N), x.dtype, x.device, stream)
+        out = _empty((R, N), dtype, x.device, stream)
+    pp = ps = None
+    if keep == MOE_KEEP_NONE:
+        if pre is not None:
+            raise ValueError("pre: given, but nothing is kept")
     else:
-        _same(out, (R, N), x.dtype, "out")
-    of_pre, of_scale = _kept(keep, R, N, x.dtype)
-    pre = _buffer(pre, of_pre, x.device, stream, "pre")
-    pre_scale = _buffer(pre_scale, of_scale, x.device, stream, "pre_scale")
-    on, px, pw, po, pc, ph, pp, ps = _here(stream, x, w13, expert_offsets, expert_num_tokens, out, pre, pre_scale)
-    _check("moe_grouped_gated", lib().moe_grouped_gated(px, R, pw, El, N, K, po, pc, activation, dt, ph, keep, pp, ps, on))
+        of = torch.uint8 if keep == MOE_KEEP_E4M3 else dtype
+        if pre is None:
+            pre = _empty((R, N2), of, x.device, stream)
+        pp = _take(pre, (R, N2), of, here, "pre")
+    if keep == MOE_KEEP_E4M3:
+        if pre_scale is None:
+            pre_scale = _empty((R, N2 // 16), torch.uint8, x.device, stream)
+        ps = _take(pre_scale, (R, N2 // 16), torch.uint8, here, "pre_scale")
+    elif pre_scale is not None:
+        raise ValueError("pre_scale: given, but nothing is kept in 8 bits")
+    _check("moe_grouped_gated", lib().moe_grouped_gated(
+        _take(x, (R, K), dtype, here, "x"), R, _take(w13, (El, N2, K), dtype, here, "w13"), El, N, K,
+        _take(expert_offsets, (El + 1,), torch.int32, here, "expert_offsets"),
+        None if expert_num_tokens is None else _take(expert_num_tokens, (El,), torch.int32, here, "expert_num_tokens"),
+        activation, dt, _take(out, (R, N), dtype, here, "out"), keep, pp, ps, _stream_on(here, stream)))
     return out, pre, pre_scale
 
 
@@ -688,22 +682,28 @@ def moe_grouped_gated_backward(dy, w2, pre, expert_offsets, expert_num_tokens=No
     """Backward pass of moe_grouped_gated behind a down projection w2 [El, K, N], from that one's gradient dy [R, K]
     and what was kept (pre; with pre_scale: in 8 bits). Returns (d_pre, h): the gradients of gate and up [R, 2N], and
     h [R, N] once more for w2's gradient (None with want_h false). d_pre may be a 16-bit pre itself."""
+    dtype = w2.dtype
     dt = _half(w2, "w2")
     El, K, N = w2.shape
     R = dy.shape[0]
-    keep = MOE_KEEP_16BIT if pre_scale is None else MOE_KEEP_E4M3
-    of_pre, of_scale = _kept(keep, R, N, w2.dtype)
-    _same(dy, (R, K), w2.dtype, "dy")
-    _same(pre, *of_pre, "pre")
-    if of_scale is not None:
-        _same(pre_scale, *of_scale, "pre_scale")
-    _same(expert_offsets, (El + 1,), torch.int32, "expert_offsets")
-    _same(expert_num_tokens, (El,), torch.int32, "expert_num_tokens")
-    d_pre = _buffer(d_pre, ((R, 2 * N), dy.dtype), dy.device, stream, "d_pre")
-    h = _buffer(h, ((R, N), dy.dtype) if want_h else None, dy.device, stream, "h")
-    on, py, pw, po, pc, pp, ps, pd, ph = _here(stream, dy, w2, expert_offsets, expert_num_tokens, pre, pre_scale, d_pre, h)
+    here = _here(dy)
+    if d_pre is None:
+        d_pre = _empty((R, 2 * N), dtype, dy.device, stream)
+    if h is None:
+        if want_h:
+            h = _empty((R, N), dtype, dy.device, stream)
+    elif not want_h:
+        raise ValueError("h: given, but not wanted")
+    if pre_scale is None:
+        keep, of, ps = MOE_KEEP_16BIT, dtype, None
+    else:
+        keep, of, ps = MOE_KEEP_E4M3, torch.uint8, _take(pre_scale, (R, 2 * N // 16), torch.uint8, here, "pre_scale")
     _check("moe_grouped_gated_backward", lib().moe_grouped_gated_backward(
-        py, R, pw, El, N, K, po, pc, activation, dt, keep, pp, ps, pd, ph, on))
+        _take(dy, (R, K), dtype, here, "dy"), R, _take(w2, (El, K, N), dtype, here, "w2"), El, N, K,
+        _take(expert_offsets, (El + 1,), torch.int32, here, "expert_offsets"),
+        None if expert_num_tokens is None else _take(expert_num_tokens, (El,), torch.int32, here, "expert_num_tokens"),
+        activation, dt, keep, _take(pre, (R, 2 * N), of, here, "pre"), ps, _take(d_pre, (R, 2 * N), dtype, here, "d_pre"),
+        None if h is None else _take(h, (R, N), dtype, here, "h"), _stream_on(here, stream)))
     return d_pre, h
 
 
@@ -712,23 +712,28 @@ def moe_checkpoint_pack(x, codes=None, scales=None, stream=None):
     power-of-two scale for every 16 values of a row."""
     dt = _dtype_code(x, "x")
     M, K = x.shape
-    of_scales = (M, -(-K // 16))
-    codes = _buffer(codes, ((M, K), torch.uint8), x.device, stream, "codes")
-    scales = _buffer(scales, (of_scales, torch.uint8), x.device, stream, "scales")
-    on, px, pc, ps = _here(stream, x, codes, scales)
-    _check("moe_checkpoint_pack", lib().moe_checkpoint_pack(px, M, K, dt, pc, ps, on))
+    groups = (K + 15) // 16
+    here = _here(x)
+    if codes is None:
+        codes = _empty((M, K), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty((M, groups), torch.uint8, x.device, stream)
+    _check("moe_checkpoint_pack", lib().moe_checkpoint_pack(
+        _take(x, (M, K), x.dtype, here, "x"), M, K, dt, _take(codes, (M, K), torch.uint8, here, "codes"),
+        _take(scales, (M, groups), torch.uint8, here, "scales"), _stream_on(here, stream)))
     return codes, scales
 
 
 def moe_checkpoint_unpack(codes, scales, dtype, out=None, stream=None):
     """The values that moe_checkpoint_pack kept, [M, K] in `dtype`; beyond its range its largest."""
     M, K = codes.shape
-    _same(codes, (M, K), torch.uint8, "codes")
-    _same(scales, (M, -(-K // 16)), torch.uint8, "scales")
-    out = _buffer(out, ((M, K), dtype), codes.device, stream, "out")
+    here = _here(codes)
+    if out is None:
+        out = _empty((M, K), dtype, codes.device, stream)
     dt = _dtype_code(out, "out")
-    on, pc, ps, px = _here(stream, codes, scales, out)
-    _check("moe_checkpoint_unpack", lib().moe_checkpoint_unpack(pc, ps, M, K, dt, px, on))
+    _check("moe_checkpoint_unpack", lib().moe_checkpoint_unpack(
+        _take(codes, (M, K), torch.uint8, here, "codes"), _take(scales, (M, (K + 15) // 16), torch.uint8, here, "scales"), M, K,
+        dt, _take(out, (M, K), dtype, here, "out"), _stream_on(here, stream)))
     return out
 
 
@@ -738,19 +743,24 @@ def moe_gather_weight_reduce_backward(dout, y, src2dst, topk_weights, apply_rout
     left as they are in d_y. The weights' gradient is None with want_weights false or
     apply_router_weight_on_input."""
     _dt(dout, torch.bfloat16, "dout")
-    M, topk = src2dst.shape
-    rows, K = y.shape
-    _same(dout, (M, K), dout.dtype, "dout")
-    _same(y, (rows, K), torch.bfloat16, "y")
-    _same(src2dst, (M, topk), torch.int32, "src2dst")
-    _same(topk_weights, (M, topk), torch.float32, "topk_weights")
-    wanted = want_weights and not apply_router_weight_on_input
-    d_y = _buffer(d_y, ((rows, K), torch.bfloat16), dout.device, stream, "d_y")
-    d_topk_weights = _buffer(d_topk_weights, ((M, topk), torch.float32) if wanted else None, dout.device, stream,
-                                  "d_topk_weights")
-    on, po, py, ps, pw, pd, pg = _here(stream, dout, y, src2dst, topk_weights, d_y, d_topk_weights)
+    bf16, f32 = torch.bfloat16, torch.float32
+    slots, of_y = src2dst.shape, y.shape
+    M, topk = slots
+    rows, K = of_y
+    here = _here(dout)
+    if d_y is None:
+        d_y = _empty(of_y, bf16, dout.device, stream)
+    pg = None
+    if want_weights and not apply_router_weight_on_input:
+        if d_topk_weights is None:
+            d_topk_weights = _empty(slots, f32, dout.device, stream)
+        pg = _take(d_topk_weights, slots, f32, here, "d_topk_weights")
+    elif d_topk_weights is not None:
+        raise ValueError("d_topk_weights: given, but there is no such gradient")
     _check("moe_gather_weight_reduce_backward", lib().moe_gather_weight_reduce_backward(
-        po, py, rows, ps, pw, M, topk, K, 1 if apply_router_weight_on_input else 0, pd, pg, on))
+        _take(dout, (M, K), bf16, here, "dout"), _take(y, of_y, bf16, here, "y"), rows,
+        _take(src2dst, slots, torch.int32, here, "src2dst"), _take(topk_weights, slots, f32, here, "topk_weights"), M, topk, K,
+        1 if apply_router_weight_on_input else 0, _take(d_y, of_y, bf16, here, "d_y"), pg, _stream_on(here, stream)))
     return d_y, d_topk_weights
 
 

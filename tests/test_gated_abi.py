@@ -147,10 +147,14 @@ def test_tensors_of_another_device_are_refused(L, monkeypatch):  # noqa: F811
     import types
 
     import moe_expert_layer_count_gb300 as moe
-    fake = lambda i: types.SimpleNamespace(get_device=lambda: i, is_contiguous=lambda: True, data_ptr=lambda: 64 + i)  # noqa: E731
+
+    def fake(i):
+        return types.SimpleNamespace(get_device=lambda: i, device=f"cuda:{i}", shape=(4,), dtype=torch.int32, is_contiguous=lambda: True,
+                                     data_ptr=lambda: 64 + i)
     monkeypatch.setattr(moe, "_current_device", lambda: 0)
-    monkeypatch.setattr(moe, "_current_raw", lambda i: 7 + i)
-    assert moe._here(None, fake(0), None, fake(0)) == [7, 64, None, 64]
-    for bad in ((fake(0), fake(1)), (fake(1), None), (fake(0), fake(-1))):
+    assert moe._here(fake(0)) == 0 and moe._take(fake(0), (4,), torch.int32, 0, "t") == 64
+    for bad in (fake(1), fake(-1)):
         with pytest.raises(ValueError):
-            moe._here(None, *bad)
+            moe._here(bad)
+        with pytest.raises(ValueError):
+            moe._take(bad, (4,), torch.int32, 0, "t")
