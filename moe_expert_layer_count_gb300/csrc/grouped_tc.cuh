@@ -1175,7 +1175,10 @@ int launch_grouped(const void* a, const void* b, const int32_t* off, const int32
              make_map(&maps.o, out, sizeof(O), K, N, (uint64_t)El * parts, 32, 3);
     } else {
         ok = MODE == kGated ? make_gated_map(&maps.a, b, K, N, El) : make_map(&maps.a, b, 2, K, N, El, MODE == kFwd ? 128 : kDepth, 3);
-        for (int i = 0; i < kRowBoxes; ++i) ok = ok && make_map(&maps.b[i], a, 2, like_fwd(MODE) ? K : N, R, 1, 8u << i, 2);
+        // a CTA has half of a tile's columns, and no group has more than R rows: up to the first box that holds them
+        const int half = (int)(R < kMaxN ? (R + 15) / 16 * 8 : kMaxN / 2);
+        for (int i = 0; i < kRowBoxes && (i == 0 || (8 << (i - 1)) < half); ++i)
+            ok = ok && make_map(&maps.b[i], a, 2, like_fwd(MODE) ? K : N, R, 1, 8u << i, 2);
     }
     if (!ok) return MOE_ERR_CUDA;
     int dev = 0;
