@@ -17,8 +17,8 @@
 // The operand that TMA loads with its reduced index outermost (the weights of dgrad, both
 // operands of wgrad) is read as an MN-major tile: 64 x 64 boxes, no transposition in memory.
 // A persistent grid of CTA pairs; per CTA: warps 0-3 epilogue, warp 4 TMA, warp 5 MMA (issued
-// by the pair's first CTA), warps 6 and 7 wgrad's ragged ends. Two TMEM accumulators, so that a tile's
-// epilogue runs under the next tile's MMAs. Every pipeline wait gives up after 2 s, sets a device
+// by the pair's first CTA), warps 6 and 7 wgrad's ragged ends, or warps 6-17 the gated forms' epilogues
+// too. Two TMEM accumulators, so that a tile's epilogue runs under the next tile's MMAs. Every pipeline wait gives up after 2 s, sets a device
 // error word and ends the kernel.
 #pragma once
 
@@ -430,10 +430,11 @@ struct Tile {
 // Forward and dgrad: the shift c that makes kMaxN >> c the most rows of a tile. A stage of a tile of n rows takes
 // about the time of 256 + n rows on their way into the SM (its MMAs that of 2 n at most); its epilogue, under the next
 // tile's stages but for the last one's, takes some 16 clocks a row (32 with the activation's gradients) and 1000; and
-// the pairs take the tiles in rounds, so that smaller tiles pay where 256 rows leave pairs without one: one group of 2048 rows, 512 x 512, backward
-// 14.0 -> 8.7 us; 8192 rows of 128 x 2048 forward 14.5 -> 12.3 us. With many rounds 256 rows win by their smaller
-// sum. (Sizes between, whose halves are no box of the row maps, measured slower: 4096 rows in tiles of 224 instead
-// of 256, 2048 x 2048, 41.9 -> 45.3 us.) parts: of all groups, for each choice.
+// the pairs take the tiles in rounds, so that smaller tiles pay where 256 rows leave pairs without one: one group
+// of 2048 rows, 512 x 512, gated backward 14.0 -> 8.5 us; 8192 rows of 128 x 2048 forward 14.4 -> 12.2 us. With many
+// rounds 256 rows win by their smaller sum. (Sizes between, whose halves are no box of the row maps, measured
+// slower: 4096 rows in tiles of 224 instead of 256, 2048 x 2048, 41.9 -> 45.3 us.) parts: of all groups, for each
+// choice.
 template <int MODE>
 __device__ __forceinline__ int choose_rows(const unsigned (&parts)[kRowChoices], const Shape& sh) {
     const float pairs = (float)(gridDim.x >> 1), steps = (float)ceil_div(sh.depth, kDepth), tiles = (float)sh.m_tiles.d;
@@ -826,7 +827,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 }
             };
             if constexpr (MODE == kGatedBwd) {
-                // ask for what this warp will read while the tile's product is under way
+                // ask for what this warp will read while the tile's product is under way (not at all: 28940 rows of
+                // 1376 x 512 102 -> 118 us; a tile ahead: 116)
                 const bool eight = gated.keep == MOE_KEEP_E4M3;
                 const uint8_t* p = static_cast<const uint8_t*>(gated.pre_in);
                 const int64_t P2 = 2 * (int64_t)P;
