@@ -128,16 +128,13 @@ class _WeightedGather(torch.autograd.Function):
         return drows, None, torch.where(src2dst >= 0, dots, 0.0), None, None
 
 
-class _Kept:
-    """A tensor of rows for the backward pass, as it is or in 8 bits."""
+def _pack(rows, keep):
+    """What is saved of rows for the backward pass: they themselves, or codes and scales."""
+    return moe.moe_checkpoint_pack(rows) if keep == moe.MOE_KEEP_E4M3 else (rows, None)
 
-    def __init__(self, rows, keep):
-        self.dtype = rows.dtype
-        self.tensors = moe.moe_checkpoint_pack(rows) if keep == moe.MOE_KEEP_E4M3 else (rows, None)
 
-    @staticmethod
-    def back(values, scales, dtype):
-        return values if scales is None else moe.moe_checkpoint_unpack(values, scales, dtype)
+def _unpack(values, scales, dtype):
+    return values if scales is None else moe.moe_checkpoint_unpack(values, scales, dtype)
 
 
 class _GatedExperts(torch.autograd.Function):
@@ -146,16 +143,16 @@ class _GatedExperts(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w13, w2, offsets, counts, activation, keep, gaps):
         h, pre, scale = moe.moe_grouped_gated(x, w13, offsets, counts, activation=activation, keep=keep)
-        kept = _Kept(x, keep)
-        ctx.save_for_backward(*kept.tensors, pre, scale, w13, w2, offsets, counts)
-        ctx.how = (activation, gaps, x.dtype)
+        kept = _pack(x, keep) if ctx.needs_input_grad[1] else (None, None)  # x is for w13's gradient
+        ctx.save_for_backward(*kept, pre, scale, w13, w2, offsets, counts)
+        ctx.how = (activation, gaps)
         return moe.moe_grouped_matmul(h, w2, offsets, counts)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         values, scales, pre, scale, w13, w2, offsets, counts = ctx.saved_tensors
-        activation, gaps, dtype = ctx.how
+        activation, gaps = ctx.how
         need_x, need_w13, need_w2 = ctx.needs_input_grad[:3]
         dy = dy.contiguous()
         d_pre, h = moe.moe_grouped_gated_backward(dy, w2, pre, offsets, counts, activation=activation, pre_scale=scale,
@@ -164,10 +161,10 @@ class _GatedExperts(torch.autograd.Function):
         del h
         dx = dw13 = None
         if need_w13:
-            dw13 = moe.moe_grouped_matmul_wgrad(d_pre, _Kept.back(values, scales, dtype), offsets, counts)
+            dw13 = moe.moe_grouped_matmul_wgrad(d_pre, _unpack(values, scales, w13.dtype), offsets, counts)
         if need_x:
             # the product does not write the rows of no group
-            out = torch.zeros(values.shape, dtype=dtype, device=dy.device) if gaps else None
+            out = torch.zeros_like(dy) if gaps else None  # x and y have one shape
             dx = moe.moe_grouped_matmul_dgrad(d_pre, w13, offsets, counts, out=out)
         return dx, dw13, dw2, None, None, None, None, None
 
@@ -177,20 +174,21 @@ class _WeightedSum(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, rows, src2dst, weights, keep, gaps):
-        kept = _Kept(rows, keep)
-        ctx.save_for_backward(*kept.tensors, src2dst, weights)
-        ctx.gaps = gaps
+        kept = _pack(rows, keep) if ctx.needs_input_grad[2] else (None, None)  # the rows are for the weights' gradient
+        ctx.save_for_backward(*kept, src2dst, weights)
+        ctx.how = (rows.shape, gaps)
         return moe.moe_gather_weight_reduce(rows, src2dst, weights)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
         values, scales, src2dst, weights = ctx.saved_tensors
-        make = torch.zeros if ctx.gaps else torch.empty
-        drows = make(values.shape, dtype=torch.bfloat16, device=dout.device)
-        drows, dweights = moe.moe_gather_weight_reduce_backward(
-            dout.contiguous(), _Kept.back(values, scales, torch.bfloat16), src2dst, weights, d_y=drows,
-            want_weights=ctx.needs_input_grad[2])
+        shape, gaps = ctx.how
+        need_weights = ctx.needs_input_grad[2]
+        drows = (torch.zeros if gaps else torch.empty)(shape, dtype=torch.bfloat16, device=dout.device)
+        rows = _unpack(values, scales, torch.bfloat16) if need_weights else drows  # not read where they are not wanted
+        drows, dweights = moe.moe_gather_weight_reduce_backward(dout.contiguous(), rows, src2dst, weights, d_y=drows,
+                                                                want_weights=need_weights)
         return drows, None, dweights, None, None
 
 

@@ -118,6 +118,28 @@ def test_only_what_is_asked_for():
 
 
 @pytest.mark.parametrize("keep", KEEPS)
+def test_frozen_weights_keep_no_rows(keep):
+    """What only a frozen input's gradient would need is not kept, and the other gradients are the same."""
+    M, K, N, E, topk = 512, 256, 128, 8, 4
+    p = train.init_block(K, N, E, seed=9)
+    x = torch.randn(M, K, device="cuda").bfloat16()
+    ids = torch.topk(torch.rand(M, E, device="cuda"), topk, dim=1).indices.int()
+    rows, offsets, src2dst, counts = train._Permute.apply(x, ids, torch.rand(M, topk, device="cuda"), E)
+    grads, held = {}, {}
+    for frozen in (False, True):
+        r = rows.detach().clone().requires_grad_()
+        w13 = p["w13"].detach().clone().requires_grad_(not frozen)
+        weights = torch.full((M, topk), 0.25, device="cuda", requires_grad=not frozen)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        out = train.weighted_sum(train.gated_experts(r, w13, p["w2"], offsets, counts, keep=keep), src2dst, weights, keep=keep)
+        held[frozen] = torch.cuda.memory_allocated() - before
+        grads[frozen] = torch.autograd.grad(out, [r, p["w2"]], torch.ones_like(out))
+    assert all(torch.equal(a, b) for a, b in zip(grads[False], grads[True]))
+    assert held[True] < held[False]
+
+
+@pytest.mark.parametrize("keep", KEEPS)
 def test_weighted_sum(keep):
     """The rows' gradient is that of the scatter; a weight's gradient is made of the rows as they were kept."""
     M, K, E, topk = 90, 256, 8, 3
