@@ -78,7 +78,7 @@ MOE_API int moe_grouped_gated(const void* x, int64_t R, const void* w13, int loc
         return MOE_ERR_INVALID_ARG;
     int sms = 0;
     if (int st = check_device(&sms)) return st;
-    const Gated gated{activation, keep, nullptr, pre, pre_scale, N % (4 * kCkptGroup) == 0 && !misaligned(pre_scale, 4)};
+    const Gated gated{activation, keep, nullptr, pre, pre_scale};
     cudaStream_t s = (cudaStream_t)stream;
     if (dtype == MOE_DT_BF16)
         return launch_grouped<kGated, bf16>(x, w13, expert_offsets, expert_num_tokens, El, R, N, K, dtype, h, 1, sms, s, gated);
@@ -110,7 +110,7 @@ MOE_API int moe_grouped_gated_backward(const void* dy, int64_t R, const void* w2
         return MOE_ERR_INVALID_ARG;
     int sms = 0;
     if (int st = check_device(&sms)) return st;
-    const Gated gated{activation, keep, pre, d_pre, const_cast<uint8_t*>(pre_scale), 0};
+    const Gated gated{activation, keep, pre, d_pre, const_cast<uint8_t*>(pre_scale)};
     cudaStream_t s = (cudaStream_t)stream;
     // w2 [El, K, N]: dgrad's n_out is K, its k_in N
     if (dtype == MOE_DT_BF16)

@@ -98,7 +98,6 @@ struct Gated {
     const void* pre_in;  // kGatedBwd: gate and up as they were kept, [R, 2 P] (16 bits or codes)
     void* pre_out;       // kGated: gate and up to keep, or null; kGatedBwd: their gradients (16 bits)
     uint8_t* scale;      // the codes' scale bytes [R, 2 P / 16]: written by kGated, read by kGatedBwd
-    int wide_scales;     // kGated: P is a multiple of 64 and `scale` of 4, so that four outputs groups' bytes are a word
 };
 
 // Forward and dgrad go through the parts, all tiles along the M side of one after the other, and take
@@ -961,26 +960,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 __syncwarp();
                 if (gated.keep == MOE_KEEP_E4M3) {
                     // The four quarters' bytes of a row lie side by side: the set's warps meet, and each writes every
-                    // fourth step's, 8 bytes a row (single bytes, each in a sector of its own, cost 14 of 285 us at
-                    // 512 rows a group). The next tile but one uses the same buffer: by then all four have been at the
-                    // next one's meeting, after they had read this one's.
+                    // fourth step's, four bytes in a row (each in a sector of its own, as they come, they cost 14 of
+                    // 285 us at 512 rows a group; a word for four is no faster). The next tile but one uses the same
+                    // buffer: by then all four have been at the next one's meeting, after they had read this one's.
                     const uint32_t met = ptx::smem_addr(staging + epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 8 * set);
                     if (lane == 0) ptx::mbar_arrive(met);
                     if (!__all_sync(0xffffffffu, wait_phase(met, turns & 1, abort))) break;
                     ++turns;
                     const int j = t.m0 + (int)rank * 64, n = min((P - j) / kCkptGroup, 4);
                     for (int c = set * kStep + quarter * (kSets * kStep); c < t.rows; c += 4 * kSets * kStep) {
-                        if (gated.wide_scales) {
-                            const int64_t at = (((int64_t)t.lo + c + hr) * P2 + side * (int64_t)P + j) / kCkptGroup;
-                            if (lane < 16 && n == 4 && c + hr < t.rows)
-                                *reinterpret_cast<uint32_t*>(gated.scale + at) = *reinterpret_cast<const uint32_t*>(bytes + c * 8 + lane * 4);
-                        } else {
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int br = i * 4 + (lane >> 3), q = lane & 3;
-                                const int64_t at = (((int64_t)t.lo + c + br) * P2 + ((lane >> 2) & 1) * (int64_t)P + j) / kCkptGroup + q;
-                                if (q < n && c + br < t.rows) gated.scale[at] = bytes[c * 8 + i * 32 + lane];
-                            }
+                        for (int i = 0; i < 2; ++i) {
+                            const int br = i * 4 + (lane >> 3), q = lane & 3;
+                            const int64_t at = (((int64_t)t.lo + c + br) * P2 + ((lane >> 2) & 1) * (int64_t)P + j) / kCkptGroup + q;
+                            if (q < n && c + br < t.rows) gated.scale[at] = bytes[c * 8 + i * 32 + lane];
                         }
                     }
                 }
