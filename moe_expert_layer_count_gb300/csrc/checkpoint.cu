@@ -119,8 +119,8 @@ __device__ __forceinline__ void move_flat(uint4 (&mem)[kTurns * kRowGroups + kTu
 // values of a quad, in an order that goes by its lane, so that the lanes' values lie in different banks.
 // `per_row`: groups of a row.
 template <typename T, bool kPack>
-__global__ void __launch_bounds__(kRowGroups / per_thread<T, kPack>()) rows_kernel(T* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                                                        int64_t groups, int K, Divisor per_row) {
+__global__ void __launch_bounds__(kRowGroups / per_thread<T, kPack>())
+    rows_kernel(T* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t groups, int K, Divisor per_row) {
     constexpr int kPer = per_thread<T, kPack>(), kRowThreads = kRowGroups / kPer;
     // one vector for the offset from a boundary; a short last group is looked at as a whole one
     __shared__ uint4 x_mem[sizeof(T) * kRowGroups + sizeof(T) + 1], c_mem[kRowGroups + 2];
@@ -300,8 +300,8 @@ MOE_API int moe_checkpoint_pack(const void* x, int64_t M, int K, int dtype, uint
             launch_k(pack_groups_kernel<T>, (unsigned)((groups + kThreads - 1) / kThreads), kThreads, 0, s, in, groups, codes, scales);
         } else {
             const int per_row = (K + kCkptGroup - 1) / kCkptGroup;
-            launch_k(rows_kernel<T, true>, (unsigned)((groups + kRowGroups - 1) / kRowGroups), kRowGroups / per_thread<T, true>(), 0, s, const_cast<T*>(in), codes, scales,
-                     groups, K, Divisor{per_row, magic_of(per_row)});
+            launch_k(rows_kernel<T, true>, (unsigned)((groups + kRowGroups - 1) / kRowGroups),
+                     kRowGroups / per_thread<T, true>(), 0, s, const_cast<T*>(in), codes, scales, groups, K, Divisor{per_row, magic_of(per_row)});
         }
         note_launches(1);
         return launch_status();
@@ -325,8 +325,8 @@ MOE_API int moe_checkpoint_unpack(const uint8_t* codes, const uint8_t* scales, i
             launch_k(unpack_groups_kernel<T>, (unsigned)((groups + kThreads - 1) / kThreads), kThreads, 0, s, codes, scales, groups, out);
         } else {
             const int per_row = (K + kCkptGroup - 1) / kCkptGroup;
-            launch_k(rows_kernel<T, false>, (unsigned)((groups + kRowGroups - 1) / kRowGroups), kRowGroups / per_thread<T, false>(), 0, s, out, const_cast<uint8_t*>(codes),
-                     const_cast<uint8_t*>(scales), groups, K, Divisor{per_row, magic_of(per_row)});
+            launch_k(rows_kernel<T, false>, (unsigned)((groups + kRowGroups - 1) / kRowGroups),
+                     kRowGroups / per_thread<T, false>(), 0, s, out, const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales), groups, K, Divisor{per_row, magic_of(per_row)});
         }
         note_launches(1);
         return launch_status();

@@ -18,8 +18,8 @@
 // operands of wgrad) is read as an MN-major tile: 64 x 64 boxes, no transposition in memory.
 // A persistent grid of CTA pairs; per CTA: warps 0-3 epilogue, warp 4 TMA, warp 5 MMA (issued
 // by the pair's first CTA), warps 6 and 7 wgrad's ragged ends, or warps 6-17 the gated forms' epilogues
-// too. Two TMEM accumulators, so that a tile's epilogue runs under the next tile's MMAs. Every pipeline wait gives up after 2 s, sets a device
-// error word and ends the kernel.
+// too. Two TMEM accumulators, so that a tile's epilogue runs under the next tile's MMAs. Every pipeline
+// wait gives up after 2 s, sets a device error word and ends the kernel.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -814,15 +814,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                     const int j = m + (lane & 1) * 16;
                     const bool live = j < P && c + r < t.rows;
                     const int64_t at = row + ((lane >> 1) & 1) * (int64_t)P + j;
-                    in[0] = live ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(gated.pre_in) + at)) : make_uint4(0, 0, 0, 0);
+                    const uint8_t* codes = static_cast<const uint8_t*>(gated.pre_in) + at;
+                    in[0] = live ? __ldcg(reinterpret_cast<const uint4*>(codes)) : make_uint4(0, 0, 0, 0);
                     sc = live ? __ldcg(gated.scale + at / kCkptGroup) : 127u;
                 } else {
                     const int j = m + (lane & 3) * 8;
                     const bool live = j < P && c + r < t.rows;
+                    const O* pre = static_cast<const O*>(gated.pre_in) + row + j;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const O*>(gated.pre_in) + row + i * (int64_t)P + j))
-                                     : make_uint4(0, 0, 0, 0);
+                        in[i] = live ? __ldcg(reinterpret_cast<const uint4*>(pre + i * (int64_t)P)) : make_uint4(0, 0, 0, 0);
                 }
             };
             if constexpr (MODE == kGatedBwd) {
