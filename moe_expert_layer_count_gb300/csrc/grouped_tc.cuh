@@ -827,18 +827,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 }
             };
             if constexpr (MODE == kGatedBwd) {
-                // ask for what this warp will read while the tile's product is under way (not at all: 28940 rows of
-                // 1376 x 512 102 -> 118 us; a tile ahead: 116)
+                // ask for what the quarters will read while the tile's product is under way, one of them for each
+                // line of 128 bytes (not at all: 28940 rows of 1376 x 512 100 -> 118 us; each quarter for itself: 102;
+                // a tile ahead: 116)
                 const bool eight = gated.keep == MOE_KEEP_E4M3;
                 const uint8_t* p = static_cast<const uint8_t*>(gated.pre_in);
                 const int64_t P2 = 2 * (int64_t)P;
                 const int z = eight ? 1 : 2, first = set * kStep, r = (lane >> 1) & 7;
                 if (first < t.rows) fetch(first);
-                if (m < P)  // two steps' rows at a time
+                if (m < P && (quarter & (eight ? 3 : 1)) == 0)  // two steps' rows at a time
                     for (int c = first + kSets * kStep * (1 + (lane >> 4)); c + r < t.rows; c += 2 * kSets * kStep) {
                         const int64_t at = (t.lo + (int64_t)c + r) * P2 + (lane & 1) * (int64_t)P + m;
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(p + at * z) : "memory");
-                        if (eight) asm volatile("prefetch.global.L2 [%0];" ::"l"(gated.scale + at / kCkptGroup) : "memory");
                     }
             }
             if (t.steps > 0) {
