@@ -481,9 +481,10 @@ MOE_API int moe_grouped_matmul_wgrad(const void* dy, const void* x, int64_t R, i
  *              form (moe_checkpoint_pack) of the 16-bit pre; N is then a multiple of 16.
  *              pre and pre_scale are NULL where nothing of them is kept
  *   activation enum moe_activation
- * h is made of the fp32 sums, not of what is kept. Rows of no group are neither read as data nor
- * written, in any output. dtype is MOE_DT_BF16 or MOE_DT_F16; N and K are multiples of 8;
- * 1 <= El <= 1024; R <= 2^31 - 1; x, w13, h and pre are 16-byte aligned. */
+ * h is made of the fp32 sums, not of what is kept. A NaN gate makes h NaN; where |a(g)| is below 2^-119
+ * it may be taken as 0. Rows of no group are neither read as data nor written, in any output. dtype is
+ * MOE_DT_BF16 or MOE_DT_F16; N and K are multiples of 8; 1 <= El <= 1024; R <= 2^31 - 1; x, w13, h and
+ * pre are 16-byte aligned. */
 MOE_API int moe_grouped_gated(const void* x, int64_t R, const void* w13, int local_num_experts, int N, int K,
                               const int32_t* expert_offsets, const int32_t* expert_num_tokens, int activation, int dtype,
                               void* h, int keep, void* pre, uint8_t* pre_scale, moe_stream_t stream);
@@ -496,7 +497,9 @@ MOE_API int moe_grouped_gated(const void* x, int64_t R, const void* w13, int loc
  * of d_pre for x and w13.
  *   dy `dtype` [R, K];  w2 `dtype` [El, K, N];  keep MOE_KEEP_16BIT or MOE_KEEP_E4M3, pre and
  *   pre_scale as moe_grouped_gated wrote them
- * d_pre may be pre itself where that is in 16 bits. Sizes, types and alignment as above. */
+ * Where g is NaN (in 8 bits: any of its group's 16 values was NaN or infinite), d_pre and h are NaN
+ * there; a'(g) is NaN where g is infinite, as its formula is. d_pre may be pre itself where that is in
+ * 16 bits. Sizes, types and alignment as above. */
 MOE_API int moe_grouped_gated_backward(const void* dy, int64_t R, const void* w2, int local_num_experts, int N, int K,
                                        const int32_t* expert_offsets, const int32_t* expert_num_tokens, int activation,
                                        int dtype, int keep, const void* pre, const uint8_t* pre_scale, void* d_pre, void* h,

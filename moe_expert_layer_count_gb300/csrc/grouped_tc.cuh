@@ -360,28 +360,28 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // Both activations are a(g) = g s with s = 1 / (1 + exp(-q)): q = g for SiLU and, since
-// (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)), q = 2 sqrt(2 / pi) (g + 0.044715 g^3) for GELU's tanh form,
-// whose cubic is taken at most at |g| = 32, where s is 0 or 1 already. exp(-q) may overflow: s is 0
-// then. Exponential and reciprocal are the approximate ones, which flush what is subnormal: a few fp32
-// ulp where the result is rounded to 16 bits (the forms that keep subnormals cost another seven
-// instructions a value).
+// (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)), q = 2 sqrt(2 / pi) (g + 0.044715 g^3) for GELU's tanh form. The cubic and
+// exp(-q) may overflow: s is 0 or 1 then, as it should be. A NaN gate makes s NaN, so no step of this may take its
+// place by a number (the smaller or larger of NaN and a bound is the bound). Exponential and reciprocal are the
+// approximate ones, which flush what is subnormal: a few fp32 ulp where the result is rounded to 16 bits (the forms that
+// keep subnormals cost another seven instructions a value), but s below 2^-126 is 0: |a| below 2^-119 may be 0.
 // Two values at once: products and sums in packed instructions.
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 template <bool kGelu>
 __device__ __forceinline__ float2 act_gate(float2 g) {
     float2 q;
-    if (kGelu) {
-        const float2 c = make_float2(fminf(fmaxf(g.x, -32.f), 32.f), fminf(fmaxf(g.y, -32.f), 32.f));
-        q = __fmul2_rn(c, __ffma2_rn(both(-kLog2e * kGeluA * kGeluB), __fmul2_rn(c, c), both(-kLog2e * kGeluA)));
-    } else {
+    if (kGelu)
+        q = __fmul2_rn(g, __ffma2_rn(both(-kLog2e * kGeluA * kGeluB), __fmul2_rn(g, g), both(-kLog2e * kGeluA)));
+    else
         q = __fmul2_rn(both(-kLog2e), g);
-    }
     const float2 d = __fadd2_rn(both(1.f), make_float2(ex2_approx(q.x), ex2_approx(q.y)));
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
 template <bool kGelu>
 __device__ __forceinline__ float2 act_of(float2 g) { return __fmul2_rn(g, act_gate<kGelu>(g)); }
-// a(g) and its derivative s + g q' s (1 - s), q' = 1 or 2 sqrt(2 / pi) (1 + 3 * 0.044715 g^2).
+// a(g) and its derivative s + g q' s (1 - s), q' = 1 or 2 sqrt(2 / pi) (1 + 3 * 0.044715 g^2). GELU's g q' is taken at
+// most at |g| = 32, where s (1 - s) is 0 already, since infinity times that were NaN; 0 * g leaves it as it is but where g
+// is infinite or NaN: there the derivative is NaN, as by its formula, for both activations.
 template <bool kGelu>
 __device__ __forceinline__ void act_and_slope(float2 g, float2& a, float2& slope) {
     const float2 s = act_gate<kGelu>(g);
@@ -389,7 +389,7 @@ __device__ __forceinline__ void act_and_slope(float2 g, float2& a, float2& slope
     float2 gq = g;
     if (kGelu) {
         const float2 c = make_float2(fminf(fmaxf(g.x, -32.f), 32.f), fminf(fmaxf(g.y, -32.f), 32.f));
-        gq = __fmul2_rn(c, __ffma2_rn(both(3.f * kGeluA * kGeluB), __fmul2_rn(c, c), both(kGeluA)));
+        gq = __ffma2_rn(both(0.f), g, __fmul2_rn(c, __ffma2_rn(both(3.f * kGeluA * kGeluB), __fmul2_rn(c, c), both(kGeluA))));
     }
     slope = __ffma2_rn(__ffma2_rn(make_float2(-s.x, -s.y), s, s), gq, s);
 }
