@@ -35,14 +35,12 @@
 // abort flag seen by all roles, waits (bounded) for its own copies and MMAs in flight,
 // and the CTA frees its TMEM and returns. An epilogue warp that gives up arrives on the
 // named barrier of the tile it leaves, so the exchange never waits for it.
-#include <cudaTypedefs.h>
-
 #include <atomic>
-#include <mutex>
 
 #include "common.cuh"
 #include "route.cuh"
 #include "sm100_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace moe {
 
@@ -585,49 +583,25 @@ __global__ void __launch_bounds__(threads_of<EPI>(), 1)
 }
 
 // ------------------------------------------------------------------ host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // 2D uint8 tensor [rows, inner] (row-major), boxes of box_rows x 128 bytes, 128-byte swizzle.
 bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {inner, rows};
-    const cuuint64_t strides[1] = {inner};
+    const cuuint64_t dims[2] = {inner, rows}, strides[1] = {inner};
     const cuuint32_t box[2] = {(cuuint32_t)kBK, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // Output tensor [rows, cols] of `esize`-byte elements. Output map: bf16 in 32-row x 128-byte boxes with the 128-byte swizzle, fp8 and fp32
 // in 32-row x 64-byte boxes with the 64-byte swizzle (the staging layouts above).
 bool make_out_tmap(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, int esize) {
-    auto fn = encode_fn();
-    if (!fn) return false;
     const CUtensorMapDataType dt = esize == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    const cuuint64_t dims[2] = {cols, rows};
-    const cuuint64_t strides[1] = {cols * (uint64_t)esize};
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * (uint64_t)esize};
     const bool wide = esize == 2;
     const cuuint32_t box[2] = {(cuuint32_t)((wide ? 128 : kStageRowBytes) / esize), 32};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(m, dt, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_map(m, dt, 2, base, dims, strides, box, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 template <int BN, int EPI, bool kSkip>

@@ -22,17 +22,15 @@
 // wait gives up after 2 s, sets a device error word and ends the kernel.
 #pragma once
 
-#include <cudaTypedefs.h>
-
 #include <atomic>
 #include <climits>
-#include <mutex>
 #include <type_traits>
 
 #include "ckpt.cuh"
 #include "elem.cuh"
 #include "route.cuh"
 #include "sm100_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace moe {
 
@@ -1122,40 +1120,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
 }
 
 // ------------------------------------------------------------------ host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
 // kGated's weights [El][2][N][K] of 2-byte elements: boxes of 16 outputs' gate rows and up rows, 128 bytes each.
 bool make_gated_map(CUtensorMap* m, const void* base, uint64_t K, uint64_t N, uint64_t El) {
-    auto fn = encode_fn();
-    if (!fn) return false;
     const cuuint64_t size[4] = {K, N, 2, El}, stride[3] = {K * 2, K * N * 2, K * N * 4};
-    const cuuint32_t box[4] = {kDepth, 16, 2, 1}, one[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), size, stride, box, one,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[4] = {kDepth, 16, 2, 1};
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, base, size, stride, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // Tensor [z, y, x] (z = 1: two dimensions) of 2- or 4-byte elements, boxes of box_y rows x 128
 // bytes with the 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, int esize, uint64_t x, uint64_t y, uint64_t z, uint32_t box_y, int dims) {
-    auto fn = encode_fn();
-    if (!fn) return false;
     const cuuint64_t size[3] = {x, y, z}, stride[2] = {x * esize, x * y * esize};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / esize), box_y, 1}, one[3] = {1, 1, 1};
-    return fn(m, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (cuuint32_t)dims,
-              const_cast<void*>(base), size, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / esize), box_y, 1};
+    return encode_map(m, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dims, base, size, stride, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 template <int MODE, typename O>
