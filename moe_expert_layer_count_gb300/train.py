@@ -164,7 +164,7 @@ class _GatedExperts(torch.autograd.Function):
             dw13 = moe.moe_grouped_matmul_wgrad(d_pre, _unpack(values, scales, w13.dtype), offsets, counts)
         if need_x:
             # the product does not write the rows of no group
-            out = torch.zeros_like(dy) if gaps else None  # x and y have one shape
+            out = dy.new_zeros(dy.shape[0], w13.shape[2]) if gaps else None
             dx = moe.moe_grouped_matmul_dgrad(d_pre, w13, offsets, counts, out=out)
         return dx, dw13, dw2, None, None, None, None, None
 
