@@ -741,25 +741,35 @@ def moe_gather_weight_reduce_backward(dout, y, src2dst, topk_weights, apply_rout
                                       d_topk_weights=None, want_weights=True, stream=None):
     """Gradients of moe_gather_weight_reduce: (d_y bf16 [rows, K], d_topk_weights fp32 [M, topk]). Rows of no slot are
     left as they are in d_y. The weights' gradient is None with want_weights false or
-    apply_router_weight_on_input."""
+    apply_router_weight_on_input; y is not read then and may be None where d_y is given. With
+    apply_router_weight_on_input topk_weights is not read either and may be None."""
     _dt(dout, torch.bfloat16, "dout")
     bf16, f32 = torch.bfloat16, torch.float32
-    slots, of_y = src2dst.shape, y.shape
+    wanted = want_weights and not apply_router_weight_on_input
+    like = d_y if y is None else y
+    if like is None:
+        raise ValueError("y: needed where d_y is not given")
+    if y is None and wanted:
+        raise ValueError("y: needed for the weights' gradient")
+    slots, of_y = src2dst.shape, like.shape
     M, topk = slots
     rows, K = of_y
     here = _here(dout)
     if d_y is None:
         d_y = _empty(of_y, bf16, dout.device, stream)
     pg = None
-    if want_weights and not apply_router_weight_on_input:
+    if wanted:
         if d_topk_weights is None:
             d_topk_weights = _empty(slots, f32, dout.device, stream)
         pg = _take(d_topk_weights, slots, f32, here, "d_topk_weights")
     elif d_topk_weights is not None:
         raise ValueError("d_topk_weights: given, but there is no such gradient")
+    if topk_weights is None and not apply_router_weight_on_input:
+        raise ValueError("topk_weights: needed where they were not applied to the input")
     _check("moe_gather_weight_reduce_backward", lib().moe_gather_weight_reduce_backward(
-        _take(dout, (M, K), bf16, here, "dout"), _take(y, of_y, bf16, here, "y"), rows,
-        _take(src2dst, slots, torch.int32, here, "src2dst"), _take(topk_weights, slots, f32, here, "topk_weights"), M, topk, K,
+        _take(dout, (M, K), bf16, here, "dout"), None if y is None else _take(y, of_y, bf16, here, "y"), rows,
+        _take(src2dst, slots, torch.int32, here, "src2dst"),
+        None if topk_weights is None else _take(topk_weights, slots, f32, here, "topk_weights"), M, topk, K,
         1 if apply_router_weight_on_input else 0, _take(d_y, of_y, bf16, here, "d_y"), pg, _stream_on(here, stream)))
     return d_y, d_topk_weights
 

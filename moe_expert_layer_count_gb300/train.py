@@ -186,7 +186,7 @@ class _WeightedSum(torch.autograd.Function):
         shape, gaps = ctx.how
         need_weights = ctx.needs_input_grad[2]
         drows = (torch.zeros if gaps else torch.empty)(shape, dtype=torch.bfloat16, device=dout.device)
-        rows = _unpack(values, scales, torch.bfloat16) if need_weights else drows  # not read where they are not wanted
+        rows = _unpack(values, scales, torch.bfloat16) if need_weights else None
         drows, dweights = moe.moe_gather_weight_reduce_backward(dout.contiguous(), rows, src2dst, weights, d_y=drows,
                                                                 want_weights=need_weights)
         return drows, None, dweights, None, None
