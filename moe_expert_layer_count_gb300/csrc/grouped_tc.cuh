@@ -31,6 +31,7 @@
 #include "route.cuh"
 #include "sm100_ptx.cuh"
 #include "tensor_map.cuh"
+#include "tile_rows.cuh"
 
 namespace moe {
 
@@ -45,9 +46,6 @@ __host__ __device__ constexpr bool like_fwd(int mode) { return mode == kFwd || m
 __host__ __device__ constexpr bool like_dgrad(int mode) { return mode == kDgrad || mode == kGatedBwd; }
 
 constexpr int kPairM = 256;        // rows of a tile (both CTAs)
-constexpr int kMaxN = 256;         // columns of a tile
-// Forward and dgrad: the most rows that a tile gets are one of these, kMaxN >> c, chosen by choose_rows
-constexpr int kRowChoices = 3, kLeastN = kMaxN >> (kRowChoices - 1);
 constexpr int kDepth = 64;         // reduced index per stage: 64 16-bit values = one 128-byte swizzled row
 constexpr int kOperandBytes = 128 * kDepth * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
@@ -415,6 +413,7 @@ struct Shape {
     Divisor part_tiles;   // wgrad: tiles of one part
     int parts;            // wgrad: parts that a group's rows are split into
     int depth;            // forward, dgrad: the reduced length
+    float share;          // forward, dgrad: tiles along the M side for each pair of CTAs
 };
 
 // Where a tile lies. forward, dgrad: outputs [m0, m0 + 256) x rows [lo, lo + rows) of group
@@ -423,29 +422,6 @@ struct Shape {
 struct Tile {
     int l, part, lo, rows, m0, n0, n, steps;
 };
-
-// Forward and dgrad: the shift c that makes kMaxN >> c the most rows of a tile. A stage of a tile of n rows takes
-// about the time of 256 + n rows on their way into the SM (its MMAs that of 2 n at most); its epilogue, under the next
-// tile's stages but for the last one's, takes some 16 clocks a row (32 with the activation's gradients) and 1000; and
-// the pairs take the tiles in rounds, so that smaller tiles pay where 256 rows leave pairs without one: one group
-// of 2048 rows, 512 x 512, gated backward 14.0 -> 8.5 us; 8192 rows of 128 x 2048 forward 14.4 -> 12.2 us. With many
-// rounds 256 rows win by their smaller sum. (Sizes between, whose halves are no box of the row maps, measured
-// slower: 4096 rows in tiles of 224 instead of 256, 2048 x 2048, 41.9 -> 45.3 us.) parts: of all groups, for each
-// choice.
-template <int MODE>
-__device__ __forceinline__ int choose_rows(const unsigned (&parts)[kRowChoices], const Shape& sh) {
-    const float pairs = (float)(gridDim.x >> 1), steps = (float)ceil_div(sh.depth, kDepth), tiles = (float)sh.m_tiles.d;
-    int best = 0;
-    float least = 0.f;
-#pragma unroll
-    for (int c = 0; c < kRowChoices; ++c) {
-        const float rows = (float)(kMaxN >> c);
-        const float epilogue = (MODE == kGatedBwd ? 32.f : 16.f) * rows, round = fmaxf(steps * (256.f + rows), 1000.f + epilogue);
-        const float clocks = ceilf(__fdividef((float)parts[c] * tiles, pairs)) * round + epilogue;
-        if (c == 0 || clocks < least) best = c, least = clocks;
-    }
-    return best;
-}
 
 // All lanes of a warp call it together (forward and dgrad look the group up with two votes).
 template <int MODE>
@@ -591,13 +567,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 __syncwarp();
             }
         } else {
-            unsigned of_choice[kRowChoices] = {};
-            for (int l = lane; l < El; l += 32)
+            RowSums sums{};
+            for (int l = lane; l < El; l += 32) {
+                const unsigned rows = (unsigned)unsorted[l].rows;
 #pragma unroll
-                for (int c = 0; c < kRowChoices; ++c) of_choice[c] += ((unsigned)unsorted[l].rows + (kMaxN >> c) - 1) / (kMaxN >> c);
+                for (int c = 0; c < kRowChoices; ++c) sums.parts[c] += (rows + (kMaxN >> c) - 1) / (kMaxN >> c);
+                sums.rows16 += (rows + 15) / 16;
+                sums.longest = max(sums.longest, rows);
+            }
 #pragma unroll
-            for (int c = 0; c < kRowChoices; ++c) of_choice[c] = __reduce_add_sync(0xffffffffu, of_choice[c]);
-            const int down = choose_rows<MODE>(of_choice, sh), cap = kMaxN >> down;
+            for (int c = 0; c < kRowChoices; ++c) sums.parts[c] = __reduce_add_sync(0xffffffffu, sums.parts[c]);
+            sums.rows16 = __reduce_add_sync(0xffffffffu, sums.rows16);
+            sums.longest = __reduce_max_sync(0xffffffffu, sums.longest);
+            const int down = choose_rows<MODE == kGatedBwd>(sums, (float)ceil_div(sh.depth, kDepth), sh.share);
+            const int cap = kMaxN >> down;
             // groups of several parts, then the others; prefix sums of each kind's parts
             int many = 0;
             for (int l0 = 0; l0 < El; l0 += 32)
@@ -1170,11 +1153,11 @@ int launch_grouped(const void* a, const void* b, const int32_t* off, const int32
     const size_t smem = fixed_smem<MODE>(El) + (size_t)stages * kStageBytes;
     const int64_t m_tiles = ((int64_t)(like_dgrad(MODE) ? K : N) + tile_outputs<MODE>() - 1) / tile_outputs<MODE>();
     const int64_t part_tiles = m_tiles * (((int64_t)K + kMaxN - 1) / kMaxN), group_tiles = part_tiles * parts;
-    const Shape sh{{(int)m_tiles, magic_of(m_tiles)}, {(int)group_tiles, magic_of(group_tiles)},
-                   {(int)part_tiles, magic_of(part_tiles)}, parts, like_dgrad(MODE) ? N : K};
     // no more pairs than tiles (an upper bound: the groups' sizes are not known here)
     const int64_t most = MODE == kWgrad ? El * group_tiles : (R / kLeastN + (R < El ? R : El)) * m_tiles;
     const int pairs = (int)(most < num_sms / 2 ? most : num_sms / 2);
+    const Shape sh{{(int)m_tiles, magic_of(m_tiles)}, {(int)group_tiles, magic_of(group_tiles)},
+                   {(int)part_tiles, magic_of(part_tiles)}, parts, like_dgrad(MODE) ? N : K, (float)m_tiles / (float)pairs};
     launch_k(grouped_kernel<MODE, O>, 2 * pairs, threads_of<MODE>(), smem, stream, maps, off, cnt, El, (int)R, N, K,
              sh, idesc_base(MODE, dtype), stages, static_cast<O*>(out), gated);
     note_launches(1);
