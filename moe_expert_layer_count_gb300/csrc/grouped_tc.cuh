@@ -123,7 +123,8 @@ struct __align__(8) Tail {
     uint32_t tmem_base;
     int abort;
     Order order;
-    int bucket[kBuckets];
+    RowSums sums;            // forward, dgrad
+    int bucket[kBuckets];    // wgrad
 };
 
 // Shared memory without the stages: alignment, staging, the groups, barriers.
@@ -394,8 +395,8 @@ __device__ __forceinline__ void act_and_slope(float2 g, float2& a, float2& slope
 // A group of rows: its first row, its row count, its number (low 16 bits of `id`) and, forward
 // and dgrad, its first part and the rows of each of its parts (high 16 bits of `id`; equal
 // parts of at most 256, whole 16s). wgrad has the groups in falling order of rows; forward and dgrad
-// have the groups of several parts in front of the others, in their own order, and count both kinds'
-// parts from 0.
+// have the groups of several parts in their own order from the front, the others from the back, and
+// count both kinds' parts from 0.
 struct __align__(16) Group {
     int start, lo, rows;
     uint32_t id;
@@ -452,14 +453,15 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, const Ord
         const int before = order.singles_before(part);
         const bool single = order.singles_before(part + 1) > before;
         const int at = single ? before : part - before, n = single ? order.singles : order.several;
-        const Group* of = single ? groups + order.several : groups;
+        const Group* of = single ? groups + (order.singles + order.several - 1) : groups;
+        const int way = single ? -1 : 1;
         // the last group whose first part is not past this one (an empty group starts where
         // the next one does): the block of `stride` groups, then the group
         const int lane = threadIdx.x & 31, stride = (n + 31) >> 5;
         int l = lane * stride;
-        l = __popc(__ballot_sync(0xffffffffu, l < n && of[l].start <= at)) * stride - stride;
-        l += __popc(__ballot_sync(0xffffffffu, lane < stride && l + lane < n && of[l + lane].start <= at)) - 1;
-        const Group g = of[l];
+        l = __popc(__ballot_sync(0xffffffffu, l < n && of[way * l].start <= at)) * stride - stride;
+        l += __popc(__ballot_sync(0xffffffffu, lane < stride && l + lane < n && of[way * (l + lane)].start <= at)) - 1;
+        const Group g = of[way * l];
         const int p = at - g.start, per = g.id >> 16;
         t.l = g.id & 0xffff;
         t.m0 = i * tile_outputs<MODE>();
@@ -516,6 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             for (int set = 0; set < kSets; ++set)
                 ptx::mbar_init(ptx::smem_addr(staging + epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 8 * set), 4);
         st->abort = 0;
+        st->sums = RowSums{};
         ptx::fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -523,21 +526,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
         tmem_relinquish_pair();
         ptx::tc_fence_before();
     }
+    if (MODE == kWgrad)
+        for (int i = threadIdx.x; i < kBuckets; i += threads_of<MODE>()) st->bucket[i] = 0;
+    __syncthreads();
     pdl_wait();
     pdl_trigger();
     // the groups' rows, never outside [0, R)
     Group* unsorted = reinterpret_cast<Group*>(smem);  // in the still unused stages
-    if (MODE == kWgrad) {
-        for (int i = threadIdx.x; i < kBuckets; i += threads_of<MODE>()) st->bucket[i] = 0;
-        __syncthreads();
-    }
-    for (int l = threadIdx.x; l < El; l += threads_of<MODE>()) {
-        const int lo = min(max(__ldg(off + l), 0), R);
-        const int end = cnt ? (int)min((int64_t)lo + max(__ldg(cnt + l), 0), (int64_t)R) : min(__ldg(off + l + 1), R);
-        const int rows = max(end - lo, 0);
-        const int b = MODE == kWgrad ? bucket_of(rows) : 0;
-        unsorted[l] = Group{b, lo, rows, (uint32_t)l};
-        if (MODE == kWgrad) atomicAdd(&st->bucket[b], 1);
+    for (int l0 = warp * 32; l0 < El; l0 += threads_of<MODE>()) {
+        const int l = l0 + lane;
+        int rows = 0;
+        if (l < El) {
+            const int lo = min(max(__ldg(off + l), 0), R);
+            const int end = cnt ? (int)min((int64_t)lo + max(__ldg(cnt + l), 0), (int64_t)R) : min(__ldg(off + l + 1), R);
+            rows = max(end - lo, 0);
+            const int b = MODE == kWgrad ? bucket_of(rows) : 0;
+            unsorted[l] = Group{b, lo, rows, (uint32_t)l};
+            if (MODE == kWgrad) atomicAdd(&st->bucket[b], 1);
+        }
+        if (MODE != kWgrad) {
+            // whole numbers: both CTAs, and every other pair, come to the same sums
+            unsigned mine = __reduce_max_sync(0xffffffffu, (unsigned)rows);
+            if (lane == 0) atomicMax(&st->sums.longest, mine);
+#pragma unroll
+            for (int c = 0; c <= kRowChoices; ++c) {
+                const int shift = c < kRowChoices ? 8 - c : 4;
+                const unsigned sum = __reduce_add_sync(0xffffffffu, ((unsigned)rows + (1u << shift) - 1) >> shift);
+                if (lane == c) mine = sum;
+            }
+            if (lane <= kRowChoices) atomicAdd(lane < kRowChoices ? &st->sums.parts[lane] : &st->sums.rows16, mine);
+        }
     }
     __syncthreads();
     if (warp == 0) {
@@ -567,47 +585,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 __syncwarp();
             }
         } else {
-            RowSums sums{};
-            for (int l = lane; l < El; l += 32) {
-                const unsigned rows = (unsigned)unsorted[l].rows;
-#pragma unroll
-                for (int c = 0; c < kRowChoices; ++c) sums.parts[c] += (rows + (kMaxN >> c) - 1) / (kMaxN >> c);
-                sums.rows16 += (rows + 15) / 16;
-                sums.longest = max(sums.longest, rows);
-            }
-#pragma unroll
-            for (int c = 0; c < kRowChoices; ++c) sums.parts[c] = __reduce_add_sync(0xffffffffu, sums.parts[c]);
-            sums.rows16 = __reduce_add_sync(0xffffffffu, sums.rows16);
-            sums.longest = __reduce_max_sync(0xffffffffu, sums.longest);
-            const int down = choose_rows<MODE == kGatedBwd>(sums, (float)ceil_div(sh.depth, kDepth), sh.share);
+            const RowSums sums = st->sums;
+            // (no group is longer than the fewest rows: all choices are one)
+            const int down = sums.longest <= kLeastN ? 0 : choose_rows<MODE == kGatedBwd>(sums, (float)ceil_div(sh.depth, kDepth), sh.share);
             const int cap = kMaxN >> down;
-            // groups of several parts, then the others; prefix sums of each kind's parts
-            int many = 0;
-            for (int l0 = 0; l0 < El; l0 += 32)
-                many += __popc(__ballot_sync(0xffffffffu, l0 + lane < El && unsorted[l0 + lane].rows > cap));
-            int place = 0, single_place = many;
-            int64_t parts = 0, single_parts = 0;
+            int several_at = 0, single_at = El - 1, single_parts = 0;
+            int64_t parts = 0;
             for (int l0 = 0; l0 < El; l0 += 32) {
                 const int l = l0 + lane;
                 Group g = l < El ? unsorted[l] : Group{0, 0, 0, 0};
                 const bool several = g.rows > cap;
                 const unsigned those = __ballot_sync(0xffffffffu, several), others = __ballot_sync(0xffffffffu, l < El && !several);
-                const int mine = (int)(((unsigned)g.rows + cap - 1) >> (8 - down));
-                const int per = several ? ceil_div(g.rows, mine) : g.rows;
+                const unsigned ones = __ballot_sync(0xffffffffu, !several && g.rows > 0), before = lanemask_lt();
+                int per = g.rows;
+                g.start = single_parts + __popc(ones & before);
+                if (those) {
+                    const int mine = several ? (int)(((unsigned)g.rows + cap - 1) >> (8 - down)) : 0, sum = warp_prefix(mine);
+                    if (several) per = ceil_div(g.rows, mine), g.start = (int)parts + sum - mine;
+                    parts += __shfl_sync(0xffffffffu, sum, 31);
+                }
                 g.id |= (uint32_t)((per + 15) & ~15) << 16;
-                const int a = warp_prefix(several ? mine : 0), b = warp_prefix(several ? 0 : mine);
-                g.start = several ? (int)parts + a - mine : (int)single_parts + b - mine;
-                if (l < El) groups[several ? place + __popc(those & lanemask_lt()) : single_place + __popc(others & lanemask_lt())] = g;
-                place += __popc(those);
-                single_place += __popc(others);
-                parts += __shfl_sync(0xffffffffu, a, 31);
-                single_parts += __shfl_sync(0xffffffffu, b, 31);
+                if (l < El) groups[several ? several_at + __popc(those & before) : single_at - __popc(others & before)] = g;
+                several_at += __popc(those);
+                single_at -= __popc(others);
+                single_parts += __popc(ones);
             }
             if (lane == 0) {
                 // more tiles than 32 bits count come of groups that lie over one another only: none, then
                 const int64_t all = (parts + single_parts) * sh.m_tiles.d <= INT_MAX - 4096 ? parts + single_parts : 0;
                 const float step = __fdividef((float)single_parts, (float)max(all, (int64_t)1)) * 4294967296.f;
-                st->order = Order{El - many, many, (int)single_parts, (int)all, __float2uint_rz(fminf(step, 4294967040.f))};
+                st->order = Order{El - several_at, several_at, single_parts, (int)all, __float2uint_rz(fminf(step, 4294967040.f))};
             }
         }
     }
