@@ -122,9 +122,7 @@ struct __align__(8) Tail {
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
-    Order order;
-    RowSums sums;            // forward, dgrad
-    int bucket[kBuckets];    // wgrad
+    int bucket[kBuckets];        // wgrad
 };
 
 // Shared memory without the stages: alignment, staging, the groups, barriers.
@@ -450,8 +448,12 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, const Ord
         }
     } else {
         const int part = sh.m_tiles.of(tile), i = tile - part * sh.m_tiles.d;
-        const int before = order.singles_before(part);
-        const bool single = order.singles_before(part + 1) > before;
+        int before = part;
+        bool single = order.several == 0;  // all are
+        if (!single) {
+            before = order.singles_before(part);
+            single = order.singles_before(part + 1) > before;
+        }
         const int at = single ? before : part - before, n = single ? order.singles : order.several;
         const Group* of = single ? groups + (order.singles + order.several - 1) : groups;
         const int way = single ? -1 : 1;
@@ -487,6 +489,77 @@ __device__ __forceinline__ int warp_prefix(int v) {
     return v;
 }
 
+// Forward and dgrad put the groups in place in two steps, in each of which every warp has 32 groups at a time (one warp
+// alone for all takes 200 clocks for every 32). First, for each choice of a tile's rows, how many parts of each kind
+// these groups have; then, once all are known, the choice, and the groups behind those of the other warps.
+struct __align__(16) Block {
+    // x: groups of several parts and, in the high 16 bits, the parts of the others; y: the former's parts
+    uint2 of[kRowChoices];
+    unsigned rows16, longest;  // as in RowSums
+};
+// More parts come only of groups that lie over one another; 32 bits might not count them.
+constexpr unsigned kPartsLimit = 1u << 26;
+
+__device__ __forceinline__ void sum_groups(int rows, Block* block) {
+    const unsigned any = __ballot_sync(0xffffffffu, rows > 0);
+    Block b;
+#pragma unroll
+    for (int c = 0; c < kRowChoices; ++c) {
+        const bool mine = rows > kMaxN >> c;
+        const unsigned several = __ballot_sync(0xffffffffu, mine);
+        b.of[c] = make_uint2(__popc(several) | __popc(any & ~several) << 16, 0);
+        if (several)
+            b.of[c].y = min(__reduce_add_sync(0xffffffffu, mine ? ((unsigned)rows + (kMaxN >> c) - 1) >> (8 - c) : 0), kPartsLimit);
+    }
+    b.rows16 = __reduce_add_sync(0xffffffffu, ((unsigned)rows + 15) >> 4);
+    b.longest = __reduce_max_sync(0xffffffffu, (unsigned)rows);
+    if ((threadIdx.x & 31) == 0) *block = b;
+}
+
+template <int MODE>
+__device__ __forceinline__ Order place_groups(const Group* unsorted, const Block* blocks, Group* groups, int El, const Shape& sh) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Block block{};
+    if (lane < (El + 31) >> 5) block = blocks[lane];
+    const unsigned longest = __reduce_max_sync(0xffffffffu, block.longest);
+    int down = 0;
+    if (longest > kLeastN) {  // where no group is longer than the fewest rows all choices are one
+        RowSums sums;
+#pragma unroll
+        for (int c = 0; c < kRowChoices; ++c) sums.parts[c] = __reduce_add_sync(0xffffffffu, block.of[c].y + (block.of[c].x >> 16));
+        sums.rows16 = __reduce_add_sync(0xffffffffu, block.rows16);
+        sums.longest = longest;
+        down = choose_rows<MODE == kGatedBwd>(sums, (float)ceil_div(sh.depth, kDepth), sh.share);
+    }
+    const int cap = kMaxN >> down;
+    const uint2 of = down == 0 ? block.of[0] : down == 1 ? block.of[1] : block.of[2];
+    for (int l0 = warp * 32; l0 < El; l0 += threads_of<MODE>()) {
+        const int l = l0 + lane;
+        const unsigned before = __reduce_add_sync(0xffffffffu, lane < l0 >> 5 ? of.x : 0);
+        Group g = l < El ? unsorted[l] : Group{0, 0, 0, 0};
+        const bool several = g.rows > cap;
+        const unsigned those = __ballot_sync(0xffffffffu, several), ones = __ballot_sync(0xffffffffu, g.rows > 0 && !several);
+        const int several_before = (int)(before & 0xffff) + __popc(those & lanemask_lt());
+        int per = g.rows;
+        g.start = (int)(before >> 16) + __popc(ones & lanemask_lt());
+        if (those) {
+            const int mine = several ? (int)(((unsigned)g.rows + cap - 1) >> (8 - down)) : 0, sum = warp_prefix(mine);
+            const int parts_before = (int)__reduce_add_sync(0xffffffffu, lane < l0 >> 5 ? of.y : 0);
+            if (several) per = ceil_div(g.rows, mine), g.start = parts_before + sum - mine;
+        }
+        g.id |= (uint32_t)((per + 15) & ~15) << 16;
+        if (l < El) groups[several ? several_before : El - 1 - (l - several_before)] = g;
+    }
+    const unsigned counts = __reduce_add_sync(0xffffffffu, of.x), several_parts = __reduce_add_sync(0xffffffffu, of.y);
+    const int several = (int)(counts & 0xffff), single_parts = (int)(counts >> 16);
+    const unsigned all = several_parts + single_parts;
+    const bool fits = several_parts < kPartsLimit && (uint64_t)all * (unsigned)sh.m_tiles.d <= INT_MAX - 4096u;  // else no tiles
+    Order order{El - several, several, single_parts, fits ? (int)all : 0, 0};
+    if (several > 0 && single_parts > 0)
+        order.step = __float2uint_rz(fminf(__fdividef((float)single_parts, (float)all) * 4294967296.f, 4294967040.f));
+    return order;
+}
+
 template <int MODE, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 1)
     grouped_kernel(const __grid_constant__ Maps maps, const int32_t* __restrict__ off, const int32_t* __restrict__ cnt,
@@ -518,7 +591,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             for (int set = 0; set < kSets; ++set)
                 ptx::mbar_init(ptx::smem_addr(staging + epi_warps<MODE>() * gated_bytes<MODE>() + 2 * kScaleBytes + 8 * set), 4);
         st->abort = 0;
-        st->sums = RowSums{};
         ptx::fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -528,11 +600,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
     }
     if (MODE == kWgrad)
         for (int i = threadIdx.x; i < kBuckets; i += threads_of<MODE>()) st->bucket[i] = 0;
-    __syncthreads();
+    // barriers and TMEM of both CTAs are in place; before the wait for the kernel before this one, whose last CTAs this
+    // is hidden under (900 clocks)
+    cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem = st->tmem_base;
     pdl_wait();
     pdl_trigger();
     // the groups' rows, never outside [0, R)
     Group* unsorted = reinterpret_cast<Group*>(smem);  // in the still unused stages
+    Block* blocks = reinterpret_cast<Block*>(unsorted + kMaxLocalExperts);
     for (int l0 = warp * 32; l0 < El; l0 += threads_of<MODE>()) {
         const int l = l0 + lane;
         int rows = 0;
@@ -544,18 +621,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
             unsorted[l] = Group{b, lo, rows, (uint32_t)l};
             if (MODE == kWgrad) atomicAdd(&st->bucket[b], 1);
         }
-        if (MODE != kWgrad) {
-            // whole numbers: both CTAs, and every other pair, come to the same sums
-            unsigned mine = __reduce_max_sync(0xffffffffu, (unsigned)rows);
-            if (lane == 0) atomicMax(&st->sums.longest, mine);
-#pragma unroll
-            for (int c = 0; c <= kRowChoices; ++c) {
-                const int shift = c < kRowChoices ? 8 - c : 4;
-                const unsigned sum = __reduce_add_sync(0xffffffffu, ((unsigned)rows + (1u << shift) - 1) >> shift);
-                if (lane == c) mine = sum;
-            }
-            if (lane <= kRowChoices) atomicAdd(lane < kRowChoices ? &st->sums.parts[lane] : &st->sums.rows16, mine);
-        }
+        if (MODE != kWgrad) sum_groups(rows, blocks + (l0 >> 5));
     }
     __syncthreads();
     if (warp == 0) {
@@ -584,47 +650,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<MODE>(), 
                 }
                 __syncwarp();
             }
-        } else {
-            const RowSums sums = st->sums;
-            // (no group is longer than the fewest rows: all choices are one)
-            const int down = sums.longest <= kLeastN ? 0 : choose_rows<MODE == kGatedBwd>(sums, (float)ceil_div(sh.depth, kDepth), sh.share);
-            const int cap = kMaxN >> down;
-            int several_at = 0, single_at = El - 1, single_parts = 0;
-            int64_t parts = 0;
-            for (int l0 = 0; l0 < El; l0 += 32) {
-                const int l = l0 + lane;
-                Group g = l < El ? unsorted[l] : Group{0, 0, 0, 0};
-                const bool several = g.rows > cap;
-                const unsigned those = __ballot_sync(0xffffffffu, several), others = __ballot_sync(0xffffffffu, l < El && !several);
-                const unsigned ones = __ballot_sync(0xffffffffu, !several && g.rows > 0), before = lanemask_lt();
-                int per = g.rows;
-                g.start = single_parts + __popc(ones & before);
-                if (those) {
-                    const int mine = several ? (int)(((unsigned)g.rows + cap - 1) >> (8 - down)) : 0, sum = warp_prefix(mine);
-                    if (several) per = ceil_div(g.rows, mine), g.start = (int)parts + sum - mine;
-                    parts += __shfl_sync(0xffffffffu, sum, 31);
-                }
-                g.id |= (uint32_t)((per + 15) & ~15) << 16;
-                if (l < El) groups[several ? several_at + __popc(those & before) : single_at - __popc(others & before)] = g;
-                several_at += __popc(those);
-                single_at -= __popc(others);
-                single_parts += __popc(ones);
-            }
-            if (lane == 0) {
-                // more tiles than 32 bits count come of groups that lie over one another only: none, then
-                const int64_t all = (parts + single_parts) * sh.m_tiles.d <= INT_MAX - 4096 ? parts + single_parts : 0;
-                const float step = __fdividef((float)single_parts, (float)max(all, (int64_t)1)) * 4294967296.f;
-                st->order = Order{El - several_at, several_at, single_parts, (int)all, __float2uint_rz(fminf(step, 4294967040.f))};
-            }
         }
     }
+    Order order;
+    if (MODE != kWgrad) order = place_groups<MODE>(unsorted, blocks, groups, El, sh);
     ptx::fence_proxy_async_smem();  // TMA writes the stages next
     __syncthreads();
-    cluster_sync();  // barriers and TMEM of both CTAs are in place
-    ptx::tc_fence_after();
-    const uint32_t tmem = st->tmem_base;
-    Order order;
-    if (MODE != kWgrad) order = st->order;
     const int tiles = MODE == kWgrad ? El * sh.group_tiles.d : order.parts * sh.m_tiles.d;
     // Pair p takes the tiles p, p + pairs, ...; wgrad, whose tiles come from the dearest to the
     // cheapest, p, 2 * pairs - 1 - p, 2 * pairs + p, ..., so that the pairs' sums stay close
