@@ -96,11 +96,11 @@ struct Gated {
     uint8_t* scale;      // the codes' scale bytes [R, 2 P / 16]: written by kGated, read by kGatedBwd
 };
 
-// Forward and dgrad go through the parts, all tiles along the M side of one after the other, and take
-// the two kinds by turns in proportion. A part of a long group finds its weights in L2, where the group's
-// other parts have left them, and is bound by the MMAs; a group of one part is bound by its weights' way
-// from DRAM: one kind after the other, each leaves idle what bounds the other (65536 rows, Zipf 1.2:
-// forward 291 -> 275 us; groups of one length, all of one kind, are not touched by it).
+// Forward and dgrad go through the parts, all tiles along the M side of one after the other. A part of a long
+// group finds its weights in L2, where the group's other parts have left them, and is bound by the MMAs; a group of one
+// part is bound by its weights' way from DRAM: one kind after the other, each leaves idle what bounds the other. So
+// the two kinds are taken by turns in proportion, where there is enough of both (by_turns); else all groups are
+// taken in their own order, as groups of several parts.
 struct Order {
     int singles, several;       // groups
     int single_parts, parts;    // parts of the former; of all groups
@@ -448,9 +448,9 @@ __device__ __forceinline__ Tile tile_at(int tile, const Group* groups, const Ord
         }
     } else {
         const int part = sh.m_tiles.of(tile), i = tile - part * sh.m_tiles.d;
-        int before = part;
-        bool single = order.several == 0;  // all are
-        if (!single) {
+        bool single = order.several == 0;
+        int before = single ? part : 0;
+        if (order.several > 0 && order.single_parts > 0) {
             before = order.singles_before(part);
             single = order.singles_before(part + 1) > before;
         }
@@ -532,12 +532,20 @@ __device__ __forceinline__ Order place_groups(const Group* unsorted, const Block
         down = choose_rows<MODE == kGatedBwd>(sums, (float)ceil_div(sh.depth, kDepth), sh.share);
     }
     const int cap = kMaxN >> down;
-    const uint2 of = down == 0 ? block.of[0] : down == 1 ? block.of[1] : block.of[2];
+    uint2 of = down == 0 ? block.of[0] : down == 1 ? block.of[1] : block.of[2];
+    unsigned counts = __reduce_add_sync(0xffffffffu, of.x), several_parts = __reduce_add_sync(0xffffffffu, of.y);
+    // by turns (see Order), or all groups in their own order, as groups of several parts
+    const bool turns = several_parts == 0 || by_turns(several_parts, counts & 0xffff, counts >> 16);
+    if (!turns) {
+        of = make_uint2(min(32, max(El - 32 * lane, 0)), of.y + (of.x >> 16));
+        several_parts += counts >> 16;
+        counts = (unsigned)El;
+    }
     for (int l0 = warp * 32; l0 < El; l0 += threads_of<MODE>()) {
         const int l = l0 + lane;
         const unsigned before = __reduce_add_sync(0xffffffffu, lane < l0 >> 5 ? of.x : 0);
         Group g = l < El ? unsorted[l] : Group{0, 0, 0, 0};
-        const bool several = g.rows > cap;
+        const bool several = turns ? g.rows > cap : l < El;
         const unsigned those = __ballot_sync(0xffffffffu, several), ones = __ballot_sync(0xffffffffu, g.rows > 0 && !several);
         const int several_before = (int)(before & 0xffff) + __popc(those & lanemask_lt());
         int per = g.rows;
@@ -550,7 +558,6 @@ __device__ __forceinline__ Order place_groups(const Group* unsorted, const Block
         g.id |= (uint32_t)((per + 15) & ~15) << 16;
         if (l < El) groups[several ? several_before : El - 1 - (l - several_before)] = g;
     }
-    const unsigned counts = __reduce_add_sync(0xffffffffu, of.x), several_parts = __reduce_add_sync(0xffffffffu, of.y);
     const int several = (int)(counts & 0xffff), single_parts = (int)(counts >> 16);
     const unsigned all = several_parts + single_parts;
     const bool fits = several_parts < kPartsLimit && (uint64_t)all * (unsigned)sh.m_tiles.d <= INT_MAX - 4096u;  // else no tiles

@@ -18,6 +18,9 @@ extern "C" int choose(const unsigned* parts, unsigned rows16, unsigned longest, 
     const float share = (float)tiles / (float)pairs;
     return slope ? choose_rows<true>(s, (float)steps, share) : choose_rows<false>(s, (float)steps, share);
 }
+extern "C" int turns(unsigned several_parts, unsigned several_groups, unsigned single_parts) {
+    return by_turns(several_parts, several_groups, single_parts);
+}
 """
 
 
@@ -30,12 +33,15 @@ def rule(tmp_path_factory):
     (d / "rule.cpp").write_text(SOURCE)
     subprocess.run([gxx, "-std=c++17", "-O2", "-shared", "-fPIC", "-I", os.path.join(ROOT, "moe_expert_layer_count_gb300", "csrc"),
                     str(d / "rule.cpp"), "-o", str(d / "rule.so")], check=True)
-    f = ctypes.CDLL(str(d / "rule.so")).choose
+    lib = ctypes.CDLL(str(d / "rule.so"))
+    lib.turns.argtypes = [ctypes.c_uint] * 3
+    f = lib.choose
     f.argtypes = [ctypes.POINTER(ctypes.c_uint), ctypes.c_uint, ctypes.c_uint, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]
 
     def choose(counts, outputs, tile_outputs, depth, slope=False, pairs=76):
         parts = (ctypes.c_uint * 3)(*(sum(-(-r // (256 >> c)) for r in counts) for c in range(3)))
         return f(parts, sum((r + 15) // 16 for r in counts), max(counts, default=0), -(-outputs // tile_outputs), -(-depth // 64), pairs, slope)
+    choose.lib = lib
     return choose
 
 
@@ -91,3 +97,19 @@ def test_choice_is_always_one(rule):
         for slope in (False, True):
             assert rule(counts, 8, 256, 8, slope) in (0, 1, 2)
     assert rule([64] * 128, 1536, 256, 2048) == 0 and rule([1] * 128, 1536, 256, 2048) == 0
+
+
+# 128 experts, top-8, 768 x 2048, forward products: us in the groups' own order and by turns
+@pytest.mark.parametrize("tokens,s,seed,own,turns", [
+    (1024, 1.2, 2, 141.8, 141.7), (1024, 1.2, 3, 135.5, 138.8), (1024, 0.6, 3, 138.2, 139.3), (2048, 0.6, 2, 151.2, 152.8),
+    (2048, 0.6, 4, 149.8, 154.2), (2048, 1.2, 4, 150.7, 151.2), (4096, 1.2, 2, 189.7, 179.5), (4096, 1.2, 3, 185.3, 181.1),
+    (8192, 1.2, 3, 289.1, 278.4), (8192, 1.2, 4, 291.9, 278.7)])
+def test_order_that_measured_fast(rule, tokens, s, seed, own, turns):
+    counts = zipf(128, 8, tokens, s, seed)
+    several = [r for r in counts if r > 256]
+    taken = rule.lib.turns(sum(-(-r // 256) for r in several), len(several), sum(0 < r <= 256 for r in counts))
+    assert (turns if taken else own) <= 1.01 * min(own, turns)
+
+
+def test_order_of_groups_of_one_kind(rule):
+    assert rule.lib.turns(2 ** 31, 1, 0) and rule.lib.turns(256, 128, 0) and not rule.lib.turns(1, 1, 1000)
