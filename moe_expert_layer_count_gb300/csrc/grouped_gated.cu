@@ -36,13 +36,13 @@ bool apart(const Span& a, std::initializer_list<Span> others) {
     return true;
 }
 
-// What both directions check of their sizes; P: the width of h, `tile`: outputs of a tile.
+// What both directions check of their sizes; tile: outputs of a tile.
 bool sizes_ok(int El, int64_t R, int N, int K, int act, int keep, int dtype, const int32_t* off, int tile) {
     if (El < 1 || El > kMaxLocalExperts || R < 0 || R > INT32_MAX || N < 8 || N > INT32_MAX / 2 || K < 8 || N % 8 || K % 8 ||
         !off || (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16) || (act != MOE_ACT_SILU && act != MOE_ACT_GELU_TANH) ||
         keep < MOE_KEEP_NONE || keep > MOE_KEEP_E4M3 || (keep == MOE_KEEP_E4M3 && N % kCkptGroup))
         return false;
-    // tiles are counted in 32 bits
+    // tiles are counted in 32 bits (choose_rows takes fewer rows only where that makes few more)
     return (R / kMaxN + El) * (((int64_t)N + tile - 1) / tile) <= INT32_MAX / 2 && fits(El, 2 * (int64_t)N, K) &&
            fits(R, 2 * (int64_t)N, 1) && fits(R, K, 1);
 }

@@ -68,7 +68,7 @@ int grouped_impl(const void* a, const void* b, const int32_t* off, const int32_t
     if (((R > 0 || MODE == kWgrad) && !out) || (R > 0 && (!a || !b)) || misaligned(a, 16) || misaligned(b, 16) ||
         misaligned(out, 16) || misaligned(off, 4) || misaligned(cnt, 4))
         return MOE_ERR_INVALID_ARG;
-    // tiles are counted in 32 bits
+    // tiles are counted in 32 bits (choose_rows takes fewer rows only where that makes few more)
     const int64_t m_tiles = ((int64_t)(MODE == kDgrad ? K : N) + kPairM - 1) / kPairM;
     if ((MODE == kWgrad ? El * m_tiles * (((int64_t)K + kMaxN - 1) / kMaxN) : (R / kMaxN + El) * m_tiles) > INT32_MAX / 2)
         return MOE_ERR_INVALID_ARG;

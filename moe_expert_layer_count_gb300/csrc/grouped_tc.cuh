@@ -497,7 +497,7 @@ struct __align__(16) Block {
     uint2 of[kRowChoices];
     unsigned rows16, longest;  // as in RowSums
 };
-// More parts come only of groups that lie over one another; 32 bits might not count them.
+// More parts come only of groups that lie over one another (rows are fewer than 2^31); 32 bits might not count them.
 constexpr unsigned kPartsLimit = 1u << 26;
 
 __device__ __forceinline__ void sum_groups(int rows, Block* block) {

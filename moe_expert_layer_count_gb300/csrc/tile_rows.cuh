@@ -44,6 +44,8 @@ __host__ __device__ __forceinline__ float quotient(float a, float b) {
 //   128 groups of 2048 rows, Zipf 1.2, 768x2048  forward 124 / 132 / 128             dgrad 63 / 69 / 66
 //   16 groups of 300 rows, 768 x 2048            forward 33 / 37 / 55                gated backward 30 / 28 / 38
 // Over 47 such batches its choice takes 0.2 % longer than the best one (at most 9 %); 256 rows throughout 6 % (66 %).
+// Tiles are counted in 32 bits, and the entry points refuse sizes whose tiles of 256 rows might be more than 2^30. Fewer rows
+// never make more of them: with many rounds the largest tiles win, as each part costs the 256 rows' time of its own.
 // (Sizes between, whose halves are no box of the row maps, measured slower: 4096 rows in tiles of 224 instead of 256,
 // 2048 x 2048, 41.9 -> 45.3 us.)
 template <bool kSlope>

@@ -113,3 +113,23 @@ def test_order_that_measured_fast(rule, tokens, s, seed, own, turns):
 
 def test_order_of_groups_of_one_kind(rule):
     assert rule.lib.turns(2 ** 31, 1, 0) and rule.lib.turns(256, 128, 0) and not rule.lib.turns(1, 1, 1000)
+
+
+def test_tiles_stay_within_32_bits(rule):
+    """Whatever the groups: where the largest tiles are at most 2^30, those of the choice are."""
+    r = random.Random(3)
+    worst = 0
+    for _ in range(20000):
+        parts0 = int(2 ** r.uniform(0, 23))
+        tiles = int(2 ** r.uniform(0, 30)) // parts0 + 1
+        if parts0 * tiles > 2 ** 30:
+            continue
+        longest = int(2 ** r.uniform(0, 12)) if r.random() < 0.5 else r.randint(1, 300)
+        # each group's rows between one more than a multiple of 256 and the multiple: up to two and four times the parts
+        parts = (parts0, r.randint(parts0, 2 * parts0), 0)
+        parts = (parts[0], parts[1], r.randint(parts[1], 2 * parts[1]))
+        rows16 = r.randint(parts0, 16 * parts0)
+        for slope in (0, 1):
+            c = rule.lib.choose((ctypes.c_uint * 3)(*parts), rows16, longest, tiles, int(2 ** r.uniform(0, 10)), min(76, parts[2] * tiles), slope)
+            worst = max(worst, parts[c] * tiles)
+    assert 2 ** 28 < worst <= 2 ** 30
