@@ -1,8 +1,9 @@
 // Activations kept in 8 bits for the backward pass (the form of ckpt.cuh), and read back: x * 2^-e rounded to
 // e4m3, e one exponent for 16 values. Each value is read and written once, so DRAM bounds it where rows are
 // whole groups: 65536 x 2048 bf16 58 us packed and 60 read back, 6.8-7.1 TB/s (its floor at the copy rate: 61), fp32
-// 99 and 97 (100). Rows of other widths cost instructions instead (an issue in 72-84 % of the slots, DRAM at a
-// third to a half): 30011 x 1111 bf16 22 us both ways (floor 15), fp32 32 and 28 (25).
+// 99 and 97 (100). Rows of other widths cost instructions and shared memory's queue instead (an issue in 73 % of
+// the slots from and to 16 bits, in 59 % to fp32, DRAM at a quarter to a half): 30011 x 1111 bf16 22 us both ways (floor 15),
+// fp32 32 and 28-29 (25).
 #include <climits>
 #include <type_traits>
 
@@ -115,7 +116,7 @@ __device__ __forceinline__ void move_flat(uint4 (&mem)[kTurns * kRowGroups + kTu
 
 // Any width and alignment. A block has kRowGroups groups one after the other, whose values are contiguous in
 // memory whatever the rows' length: they go through shared memory, so that global memory is moved 16 bytes
-// at a time, and a thread has one group there, which starts anywhere. It takes the group's quads, and the
+// at a time, and a thread has one group there or two (per_thread), which start anywhere. It takes a group's quads, and the
 // values of a quad, in an order that goes by its lane, so that the lanes' values lie in different banks.
 // `per_row`: groups of a row.
 template <typename T, bool kPack>

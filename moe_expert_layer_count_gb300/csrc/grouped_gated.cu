@@ -6,10 +6,13 @@
 // The kernel is in grouped_tc.cuh. What is kept of g and u for the backward pass leaves the same
 // epilogue, in 16 bits or in the 8-bit form of ckpt.cuh.
 //
-// What it measured (one GB300, times of one call with L2 flushed; sizes N = 768, K = 2048, 128 groups):
+// What it measured (one GB300, times of one call with L2 flushed, in short runs at the full clock; sizes N = 768,
+// K = 2048, 128 groups):
 //   512 rows a group       forward 250-261 us, 265-277 with g and u kept in 16 bits or in 8 (the ungated product of
 //                          the same weights: 252-259); backward 214-222 us from either
-//   65536 rows, Zipf 1.2   forward 271-283 us, 285-300 with g and u kept; backward 210-214 us from either
+//   65536 rows, Zipf 1.2   forward 271-283 us, 285-300 with g and u kept; backward 210-214 us from either. Passes that
+//                          follow one another for seconds, where the power cap holds the clock at 1290-1575 MHz:
+//                          322-342 us with g and u kept in 16 bits, backward 212-227
 //   512 rows, decode       forward 122-126 us: 790 MB at 6.3-6.5 TB/s
 // What bounds it. Forward: as the ungated product (tensor pipe active 81 %, 74 % with g and u stored): MMAs
 // and the weights' way from DRAM hide each other only in part; without an epilogue 247 us at 512 rows a

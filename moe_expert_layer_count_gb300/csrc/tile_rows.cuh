@@ -38,12 +38,12 @@ __host__ __device__ __forceinline__ float quotient(float a, float b) {
 // rounds, each about as long as the average tile, which has the rows that the groups have and not the most that it
 // may; some pair gets more of the long ones (half of what one is longer by), and the last epilogue is under nothing.
 // What it decides, in us of 256 / 128 / 64 rows (one GB300, calls back to back):
-//   one group of 2048 rows, 512 x 512            gated backward 15.3 / 11.2 / 9.2    dgrad 8.3 / 6.8 / 6.5
-//   one group of 8192 rows, 128 outputs of 2048  forward 15.7 / 13.6 / 19.1
-//   128 groups of 16384 rows, Zipf 1.2, 768x2048 forward 151 / 160 / 203             gated backward 106 / 103 / 117
-//   128 groups of 2048 rows, Zipf 1.2, 768x2048  forward 124 / 132 / 128             dgrad 63 / 69 / 66
-//   16 groups of 300 rows, 768 x 2048            forward 33 / 37 / 55                gated backward 30 / 28 / 38
-// Over 47 such batches its choice takes 0.2 % longer than the best one (at most 9 %); 256 rows throughout 6 % (66 %).
+//   one group of 2048 rows, 512 x 512            gated backward 15.1 / 10.8 / 9.1    dgrad 8.0 / 6.5 / 6.3
+//   one group of 8192 rows, 128 outputs of 2048  forward 15.3 / 13.2 / 18.8
+//   128 groups of 16384 rows, Zipf 1.2, 768x2048 forward 150 / 159 / 203             gated backward 105 / 102 / 116
+//   128 groups of 2048 rows, Zipf 1.2, 768x2048  forward 123 / 127 / 125             dgrad 62 / 67 / 65
+//   16 groups of 300 rows, 768 x 2048            forward 33 / 36 / 54                gated backward 30 / 27 / 38
+// Over 47 such batches its choice takes 0.2 % longer than the best one (at most 9 %); 256 rows throughout 5.5 % (67 %).
 // Tiles are counted in 32 bits, and the entry points refuse sizes whose tiles of 256 rows might be more than 2^30. Fewer rows
 // never make more of them: with many rounds the largest tiles win, as each part costs the 256 rows' time of its own.
 // (Sizes between, whose halves are no box of the row maps, measured slower: 4096 rows in tiles of 224 instead of 256,

@@ -14,7 +14,9 @@ weight are plain torch operations, unless the block is told what to keep for its
 (moe_block's `keep`): then the first product and the activation are one kernel, forward and backward
 (moe_grouped_gated), the weighted sum's backward pass is one kernel too
 (moe_gather_weight_reduce_backward), and what the backward pass needs of the experts' part (its rows,
-gate and up, its results) is kept in 16 or in 8 bits. There are no second gradients.
+gate and up, its results) is kept in 16 or in 8 bits. That is faster and has fewer roundings; it is asked for, and
+not what happens by itself, because its results are not those of the torch operations bit for bit, and
+programs that train with those keep theirs. There are no second gradients.
 
 `python -m moe_expert_layer_count_gb300.train` runs a few steps on synthetic data
 (`--keep 16bit` or `--keep 8bit` with the fused kernels).
@@ -129,7 +131,8 @@ class _WeightedGather(torch.autograd.Function):
 
 
 def _pack(rows, keep):
-    """What is saved of rows for the backward pass: they themselves, or codes and scales."""
+    """What is saved of rows for the backward pass: they themselves, or codes and scales. All rows are packed, those of
+    no group too (they hold anything, and nothing reads their codes): how many there are the host does not know."""
     return moe.moe_checkpoint_pack(rows) if keep == moe.MOE_KEEP_E4M3 else (rows, None)
 
 
@@ -219,7 +222,8 @@ def gated_experts(x, w13, w2, expert_offsets, expert_num_tokens=None, activation
     """The experts' feed-forward part under autograd: w2[l] (a(g) * u) with (g, u) = w13[l] x[r] for the rows r of every
     group l (moe_grouped_gated, moe_grouped_matmul). `keep`: whether x and (g, u) are kept for the backward pass in
     16 bits (MOE_KEEP_16BIT) or in 8 (MOE_KEEP_E4M3: half the memory; what the gradients are made of is off by up to
-    2^-4). Rows of no group as in grouped_matmul."""
+    2^-4, and packing all rows of x, those of no group too, costs more than it saves where few tokens meet many experts).
+    Rows of no group as in grouped_matmul. w2's results may have another width than x."""
     if keep not in (moe.MOE_KEEP_16BIT, moe.MOE_KEEP_E4M3):
         raise ValueError(f"keep: expected MOE_KEEP_16BIT or MOE_KEEP_E4M3, got {keep}")
     return _GatedExperts.apply(x, w13, w2, expert_offsets, expert_num_tokens, activation, _needed(keep, x, w13, w2), gaps)
